@@ -20,6 +20,8 @@ TT_OK, TT_ERR_INVALID_ARG, TT_ERR_BAD_VOCAB, TT_ERR_BAD_FAMILY, TT_ERR_INVALID_U
     TT_ERR_CAPACITY, TT_ERR_OOM, TT_ERR_CUDA, TT_ERR_TIMEOUT = range(9)
 TT_FAMILY_CL100K_STYLE, TT_FAMILY_O200K_STYLE, TT_FAMILY_DEEPSEEK_STYLE = 1, 2, 3
 TT_NOALLOC_MAX_BYTES, TT_NOALLOC_MAX_REQUESTS = 256 * 1024, 1024
+TT_F32, TT_F16, TT_BF16 = range(3)
+TT_MAX_IDS = 1 << 29
 
 _lib = None
 _lock = threading.Lock()
@@ -62,11 +64,20 @@ def lib():
             L.tt_launch_count.restype = i64
             L.tt_table_digest.restype = ctypes.c_char_p
             L.tt_debug_lookback.argtypes = [p, i32, i32]
+            f32 = ctypes.c_float
+            L.tt_embed.argtypes = [p, i64, p, p, i32, i64, i64, i64, f32, p, i32, i64, p, p]
+            L.tt_embed_grad.argtypes = [p, i64, p, p, i32, i64, i64, f32, p, i32, i64, i64, i32, p, i64, p, p]
+            L.tt_embed_grad_workspace.argtypes = [i64, i64, i64]
+            L.tt_embed_grad_workspace.restype = i64
+            L.tt_token_loss.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, i64, p, p]
+            L.tt_token_loss_grad.argtypes = [p, i32, i64, i64, i64, p, p, p, p, i64, p, p]
+            L.tt_sample.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, p, p, p, p]
             for name in ("tt_create", "tt_encode_batch", "tt_encode_batch_bounded", "tt_encode_batch_spans",
                          "tt_set_added_tokens",
                          "tt_encode_batch_noalloc",
                          "tt_encode_host",
-                         "tt_get_status", "tt_pretokenize_batch", "tt_profile_read", "tt_debug_lookback"):
+                         "tt_get_status", "tt_pretokenize_batch", "tt_profile_read", "tt_debug_lookback",
+                         "tt_embed", "tt_embed_grad", "tt_token_loss", "tt_token_loss_grad", "tt_sample"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -213,6 +224,191 @@ def tt_debug_lookback(h, spin_limit, withhold_tile=-1):
     """Test setting: poll limit of the pre-tokenizer's look-back waits (0: the
     default) and a tile that publishes nothing (-1: none)."""
     _check(lib().tt_debug_lookback(h, int(spin_limit), int(withhold_tile)), "tt_debug_lookback")
+
+
+# ---- operators around token IDs: the C calls
+
+def tt_embed(d_ids, max_ids, d_n_ids, d_table, table_type, n_vocab, dim, table_stride, scale, d_out, out_type,
+             out_stride, d_status=None, stream=None):
+    _check(lib().tt_embed(_ptr(d_ids), max_ids, _ptr(d_n_ids), _ptr(d_table), table_type, n_vocab, dim, table_stride,
+                          scale, _ptr(d_out), out_type, out_stride, _ptr(d_status), _stream(stream)), "tt_embed")
+
+
+def tt_embed_grad(d_ids, max_ids, d_n_ids, d_dout, dout_type, dim, dout_stride, scale, d_dtable, dtable_type, n_vocab,
+                  dtable_stride, accumulate, d_workspace, workspace_bytes, d_status=None, stream=None):
+    _check(lib().tt_embed_grad(_ptr(d_ids), max_ids, _ptr(d_n_ids), _ptr(d_dout), dout_type, dim, dout_stride, scale,
+                               _ptr(d_dtable), dtable_type, n_vocab, dtable_stride, int(accumulate),
+                               _ptr(d_workspace), workspace_bytes, _ptr(d_status), _stream(stream)), "tt_embed_grad")
+
+
+def tt_embed_grad_workspace(max_ids, n_vocab, dim):
+    """Bytes of scratch, or -1 for sizes that tt_embed_grad rejects."""
+    return lib().tt_embed_grad_workspace(int(max_ids), int(n_vocab), int(dim))
+
+
+def tt_token_loss(d_logits, dtype, n_rows, n_vocab, logits_stride, d_targets, d_loss, d_lse, d_row_grads, d_dlogits,
+                  dlogits_stride, d_status=None, stream=None):
+    _check(lib().tt_token_loss(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_targets), _ptr(d_loss),
+                               _ptr(d_lse), _ptr(d_row_grads), _ptr(d_dlogits), dlogits_stride, _ptr(d_status),
+                               _stream(stream)), "tt_token_loss")
+
+
+def tt_token_loss_grad(d_logits, dtype, n_rows, n_vocab, logits_stride, d_targets, d_lse, d_row_grads, d_dlogits,
+                       dlogits_stride, d_status=None, stream=None):
+    _check(lib().tt_token_loss_grad(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_targets),
+                                    _ptr(d_lse), _ptr(d_row_grads), _ptr(d_dlogits), dlogits_stride, _ptr(d_status),
+                                    _stream(stream)), "tt_token_loss_grad")
+
+
+def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temperature, d_top_k, d_top_p, d_min_p,
+              d_out_ids, d_out_logprobs, d_status=None, stream=None):
+    _check(lib().tt_sample(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_uniform),
+                           _ptr(d_temperature), _ptr(d_top_k), _ptr(d_top_p), _ptr(d_min_p), _ptr(d_out_ids),
+                           _ptr(d_out_logprobs), _ptr(d_status), _stream(stream)), "tt_sample")
+
+
+# ---- the same on torch CUDA tensors: outputs and scratch allocated where they
+# are not given, shapes and types checked.  The kernels run on `stream` (the
+# current one if None); what is allocated here is handed to that stream.
+
+_DTYPES = {"torch.float32": TT_F32, "torch.float16": TT_F16, "torch.bfloat16": TT_BF16}
+
+
+def _matrix(x, what, rows=None, cols=None):
+    """(dtype code, row stride) of a 2-D CUDA tensor with unit column stride."""
+    code = _DTYPES.get(str(x.dtype))
+    if code is None:
+        raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
+    n, d = x.shape if x.dim() == 2 else (None, None)
+    if n is None or not x.is_cuda or (rows is not None and n != rows) or (cols is not None and d != cols):
+        raise ValueError("%s: a CUDA tensor [%s, %s] wanted, got %s on %s" % (what, rows or "n", cols or "n",
+                                                                            list(x.shape), x.device))
+    if d > 1 and x.stride(1) != 1:
+        raise ValueError("%s: columns must be contiguous" % what)
+    return code, (x.stride(0) if n > 1 else d)
+
+
+def _vector(x, what, dtype, n=None):
+    """A contiguous 1-D CUDA tensor of `dtype`, or None."""
+    if x is not None and (not x.is_cuda or x.dim() != 1 or str(x.dtype) != dtype or not x.is_contiguous() or
+                          (n is not None and x.shape[0] != n)):
+        raise ValueError("%s: a contiguous CUDA tensor %s [%s] wanted, got %s %s on %s" % (
+            what, dtype, "n" if n is None else n, x.dtype, list(x.shape), x.device))
+    return x
+
+
+def _handed(stream, *tensors):
+    """Tensors allocated on the current stream but used on another."""
+    import torch
+    if stream is not None:
+        raw = _stream(stream)
+        if raw != torch.cuda.current_stream().cuda_stream:
+            s = torch.cuda.ExternalStream(raw)
+            s.wait_stream(torch.cuda.current_stream())     # the block may still be in use there
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+
+
+def embed(ids, table, scale=1.0, n_ids=None, dtype=None, out=None, status=None, stream=None):
+    """scale * table[ids] (zero rows for padding): out [len(ids), dim] of
+    `dtype` (the table's if None).  n_ids: a device int64 count."""
+    import torch
+    _vector(ids, "ids", "torch.int32")
+    t, ts = _matrix(table, "table")
+    n, (vocab, dim) = ids.shape[0], table.shape
+    if out is None:
+        out = torch.empty((n, dim), dtype=dtype or table.dtype, device=table.device)
+        _handed(stream, out)
+    o, os_ = _matrix(out, "out", n, dim)
+    tt_embed(ids, n, n_ids, table, t, vocab, dim, ts, scale, out, o, os_, status, stream)
+    return out
+
+
+def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, accumulate=False, workspace=None,
+               status=None, stream=None):
+    """The gradient of embed: [n_vocab, dim] of `dtype` (float32 if None), the
+    scaled sums of dout's rows by ID; with accumulate, added to `out`."""
+    import torch
+    _vector(ids, "ids", "torch.int32")
+    n = ids.shape[0]
+    d, ds = _matrix(dout, "dout", n)
+    dim = dout.shape[1]
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    need = tt_embed_grad_workspace(n, n_vocab, dim)
+    mine = []
+    if out is None:
+        out = torch.empty((n_vocab, dim), dtype=dtype or torch.float32, device=dout.device)
+        mine.append(out)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dout.device)
+        mine.append(workspace)
+    if mine:
+        _handed(stream, *mine)
+    o, os_ = _matrix(out, "out", n_vocab, dim)
+    tt_embed_grad(ids, n, n_ids, dout, d, dim, ds, scale, out, o, n_vocab, os_, accumulate, workspace,
+                  workspace.numel() * workspace.element_size(), status, stream)
+    return out
+
+
+def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, status=None, stream=None):
+    """Next-token loss of each row: (loss, lse), and with want_grad or dlogits
+    (which may be logits itself) the logits' gradient as a third."""
+    import torch
+    t, ls = _matrix(logits, "logits")
+    n, vocab = logits.shape
+    _vector(targets, "targets", "torch.int32", n)
+    _vector(row_grads, "row_grads", "torch.float32", n)
+    loss, lse = torch.empty((2, n), dtype=torch.float32, device=logits.device)
+    mine = None
+    if dlogits is None and want_grad:
+        dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
+    _handed(stream, loss, mine)
+    d, ds = t, vocab
+    if dlogits is not None:
+        d, ds = _matrix(dlogits, "dlogits", n, vocab)
+    if d != t:
+        raise ValueError("dlogits: the type of logits wanted")
+    tt_token_loss(logits, t, n, vocab, ls, targets, loss, lse, row_grads, dlogits, ds, status, stream)
+    return (loss, lse) if dlogits is None else (loss, lse, dlogits)
+
+
+def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=None, stream=None):
+    """The gradient of token_loss from the lse that it returned."""
+    import torch
+    t, ls = _matrix(logits, "logits")
+    n, vocab = logits.shape
+    _vector(targets, "targets", "torch.int32", n)
+    _vector(lse, "lse", "torch.float32", n)
+    _vector(row_grads, "row_grads", "torch.float32", n)
+    if dlogits is None:
+        dlogits = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
+        _handed(stream, dlogits)
+    d, ds = _matrix(dlogits, "dlogits", n, vocab)
+    if d != t:
+        raise ValueError("dlogits: the type of logits wanted")
+    tt_token_loss_grad(logits, t, n, vocab, ls, targets, lse, row_grads, dlogits, ds, status, stream)
+    return dlogits
+
+
+def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, status=None, stream=None):
+    """One token ID drawn from each row: (ids int32, logprobs float32).  The
+    parameters are device tensors with an entry a row, or None (off)."""
+    import torch
+    t, ls = _matrix(logits, "logits")
+    n, vocab = logits.shape
+    for x, what, kind in ((uniform, "uniform", "torch.float32"), (temperature, "temperature", "torch.float32"),
+                          (top_k, "top_k", "torch.int32"), (top_p, "top_p", "torch.float32"),
+                          (min_p, "min_p", "torch.float32")):
+        _vector(x, what, kind, n)
+    if uniform is None:
+        raise ValueError("uniform: a tensor wanted")
+    ids = torch.empty(n, dtype=torch.int32, device=logits.device)
+    logprobs = torch.empty(n, dtype=torch.float32, device=logits.device)
+    _handed(stream, ids, logprobs)
+    tt_sample(logits, t, n, vocab, ls, uniform, temperature, top_k, top_p, min_p, ids, logprobs, status, stream)
+    return ids, logprobs
 
 
 class Tokenizer:

@@ -1,0 +1,115 @@
+// tt_ops.cuh - what the operators around token IDs share: element types,
+// 16-byte vector loads and stores, argument checks and block reductions.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "../../include/toktier.h"
+
+namespace tt {
+namespace ops {
+
+constexpr int64_t MAX_VOCAB = 1 << 20;
+constexpr float INF = __builtin_huge_valf();
+
+// ------------------------------------------------------------ elements
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// eight elements at a 16-byte aligned address, read through the cache for
+// data that no kernel in flight writes
+__device__ __forceinline__ void load8(const float *p, float v[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <class T2, class T> __device__ __forceinline__ void load8_16(const T *p, float v[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const T *h = reinterpret_cast<const T *>(&w[i]);
+    v[2 * i] = to_f32(h[0]);
+    v[2 * i + 1] = to_f32(h[1]);
+  }
+}
+__device__ __forceinline__ void load8(const __half *p, float v[8]) { load8_16<__half2>(p, v); }
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float v[8]) { load8_16<__nv_bfloat162>(p, v); }
+
+// eight elements to a 16-byte aligned address, marked as not to be read soon
+__device__ __forceinline__ void store8(float *p, const float v[8]) {
+  __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+template <class T> __device__ __forceinline__ void store8(T *p, const float v[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    T h[2] = {from_f32<T>(v[2 * i]), from_f32<T>(v[2 * i + 1])};
+    w[i] = *reinterpret_cast<uint32_t *>(h);
+  }
+  __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+__device__ __forceinline__ void op_status(int32_t *st, int code) {
+  if (st) atomicCAS(st, TT_OK, code);
+}
+
+// ------------------------------------------------------------ checks
+inline size_t type_size(int32_t t) { return t == TT_F32 ? 4 : 2; }
+inline bool type_ok(int32_t t) { return t == TT_F32 || t == TT_F16 || t == TT_BF16; }
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool array_ok(const void *p, size_t elem) { return p && aligned(p, elem); }
+inline bool optional_ok(const void *p, size_t elem) { return !p || aligned(p, elem); }
+inline bool vocab_ok(int64_t n_vocab) { return n_vocab >= 1 && n_vocab <= MAX_VOCAB; }
+// rows of whole 16-byte groups of eight elements
+inline bool rows_vector(const void *p, int64_t stride, int64_t dim) {
+  return aligned(p, 16) && stride % 8 == 0 && dim % 8 == 0;
+}
+
+inline tt_status launched(const char *what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return TT_OK;
+  fprintf(stderr, "toktier: %s failed: %s\n", what, cudaGetErrorString(e));
+  return TT_ERR_CUDA;
+}
+
+// call f(T{}) with the element type of a tt_dtype
+template <class F> void with_type(int32_t t, F f) {
+  if (t == TT_F32) f(float{});
+  else if (t == TT_F16) f(__half{});
+  else f(__nv_bfloat16{});
+}
+
+// ------------------------------------------------------------ block reductions
+struct OpMax { template <class V> __device__ V operator()(V a, V b) const { return a > b ? a : b; } };
+struct OpSum { template <class V> __device__ V operator()(V a, V b) const { return a + b; } };
+
+template <class V, class Op> __device__ __forceinline__ V warp_all(V v, Op op) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(~0u, v, o));
+  return v;
+}
+
+// every thread gets the reduction over the block; `box` holds one V per warp
+template <class V, class Op> __device__ V block_all(V v, Op op, V *box) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5;
+  v = warp_all(v, op);
+  __syncthreads();
+  if (lane == 0) box[warp] = v;
+  __syncthreads();
+  v = box[0];
+  for (int i = 1; i < n; ++i) v = op(v, box[i]);
+  return v;
+}
+
+}  // namespace ops
+}  // namespace tt

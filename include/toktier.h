@@ -317,6 +317,161 @@ tt_status tt_pretokenize_batch(tt_tokenizer *h,
                                const uint8_t *d_utf8, const int64_t *d_byte_offsets, int64_t n_requests,
                                int64_t *d_piece_starts, int64_t *d_piece_offsets, tt_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around token IDs
+ *
+ * What a model does with the IDs on either side of it: looks up their vectors
+ * (tt_embed, and tt_embed_grad for training), scores its predictions against
+ * them (tt_token_loss, tt_token_loss_grad) and draws new ones (tt_sample).
+ * The paper has no counterpart.  They need no handle and keep no state:
+ * everything a call reads or writes is the caller's, scratch included, so
+ * calls on different streams are independent as long as their buffers are.
+ *
+ * Beside the conventions above:
+ *   - Matrices are row-major with unit column stride; a *_stride argument is
+ *     the distance between rows in elements (>= the row's length).  Any
+ *     stride and any element-aligned address work; 16-byte aligned rows are
+ *     the fastest.  A buffer that a call writes overlaps no other buffer of
+ *     the call, but for d_dlogits == d_logits with equal strides (in place).
+ *   - Values are TT_F32, TT_F16 or TT_BF16; arithmetic, sums and softmax
+ *     statistics are in 32 bits or more, and results are rounded from there
+ *     to their type (to nearest even).
+ *   - IDs are int32.  A negative ID is padding: it stands for no token.
+ *     n_vocab is 1 .. 2^20, as in tt_create.
+ *   - d_status (device, int32, may be NULL): a kernel that meets a value this
+ *     header does not allow writes its tt_status there if the word is
+ *     TT_OK (0); it is never cleared.  Such an ID, target or sampling row is
+ *     treated as padding; no other result is affected.
+ *   - Results do not depend on the order in which the hardware runs the
+ *     blocks: the same call gives the same bits.
+ *   - Calls never allocate and never wait; they may be captured in a graph.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { TT_F32 = 0, TT_F16 = 1, TT_BF16 = 2 } tt_dtype;
+
+/* The most IDs of one tt_embed or tt_embed_grad call and the most rows of one
+ * tt_token_loss, tt_token_loss_grad or tt_sample call; more are rejected with
+ * TT_ERR_CAPACITY. */
+#define TT_MAX_IDS (1 << 29)
+
+/*
+ * tt_embed - look up and scale the vectors of token IDs:
+ *   out[i][:] = scale * table[ids[i]][:], a zero row where ids[i] is padding.
+ *
+ *   d_ids      device, int32 [max_ids].
+ *   max_ids    0 .. TT_MAX_IDS, host-known bound on the number of IDs.
+ *   d_n_ids    device, int64, or NULL: the number of IDs if it is below
+ *              max_ids (e.g. &out_id_offsets[n_requests] of an encode on the
+ *              same stream); rows of d_out beyond it are left untouched.
+ *   d_table    device, table_type [n_vocab][dim], rows table_stride apart.
+ *   d_out      device, out_type [max_ids][dim], rows out_stride apart.
+ * An ID >= n_vocab: a zero row and TT_ERR_INVALID_ARG in d_status.
+ */
+tt_status tt_embed(const int32_t *d_ids, int64_t max_ids, const int64_t *d_n_ids,
+                   const void *d_table, int32_t table_type, int64_t n_vocab, int64_t dim, int64_t table_stride,
+                   float scale, void *d_out, int32_t out_type, int64_t out_stride,
+                   int32_t *d_status, tt_stream_t stream);
+
+/*
+ * tt_embed_grad - the gradient of tt_embed with respect to its table:
+ *   dtable[v][:] = scale * (sum of dout[i][:] over the i with ids[i] = v),
+ * every row of the table written (IDs that do not occur get zeros), or with
+ * accumulate != 0 added to what d_dtable holds.
+ *
+ * The tokens are sorted by ID, keeping their order, and each row's terms are
+ * summed in 32 bits in a fixed order (no floating-point atomics).
+ *
+ *   d_ids, max_ids, d_n_ids   as in tt_embed.
+ *   d_dout     device, dout_type [max_ids][dim], rows dout_stride apart.
+ *   d_dtable   device, dtable_type [n_vocab][dim], rows dtable_stride apart.
+ *   d_workspace  device, 16-byte aligned, workspace_bytes >=
+ *              tt_embed_grad_workspace(max_ids, n_vocab, dim), else
+ *              TT_ERR_CAPACITY; its contents before and after mean nothing.
+ * An ID >= n_vocab adds to no row and sets TT_ERR_INVALID_ARG in d_status.
+ */
+tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const int64_t *d_n_ids,
+                        const void *d_dout, int32_t dout_type, int64_t dim, int64_t dout_stride, float scale,
+                        void *d_dtable, int32_t dtable_type, int64_t n_vocab, int64_t dtable_stride,
+                        int32_t accumulate, void *d_workspace, int64_t workspace_bytes,
+                        int32_t *d_status, tt_stream_t stream);
+
+/* tt_embed_grad_workspace - bytes of scratch tt_embed_grad needs (host-side
+ * arithmetic only); -1 for sizes that it rejects. */
+int64_t tt_embed_grad_workspace(int64_t max_ids, int64_t n_vocab, int64_t dim);
+
+/*
+ * tt_token_loss - next-token loss of each row of logits, and its gradient:
+ *   lse[i]        = log(sum_j exp(logits[i][j]))
+ *   loss[i]       = lse[i] - logits[i][targets[i]]
+ *   dlogits[i][j] = row_grads[i] * (exp(logits[i][j] - lse[i]) - (j == targets[i]))
+ *
+ *   d_logits   device, type [n_rows][n_vocab], rows logits_stride apart.
+ *   n_rows     0 .. TT_MAX_IDS.
+ *   d_targets  device, int32 [n_rows]; padding: the row's loss and its row of
+ *              dlogits are zero (its lse is computed).
+ *   d_loss     device, float [n_rows].    d_lse  the same, or NULL.
+ *   d_row_grads  device, float [n_rows]: the gradient that arrives at each
+ *              loss (1 / count for a mean); NULL: 1 for every row.
+ *   d_dlogits  device, type [n_rows][n_vocab], rows dlogits_stride apart, or
+ *              NULL: no gradient.  May be d_logits itself with equal strides.
+ * -inf logits have probability 0: a target there has loss +inf.  A row that
+ * is -inf throughout has lse -inf, loss +inf and a zero gradient.  NaN or
+ * +inf in a row makes its lse NaN or +inf, and its loss and gradient what the
+ * formulas then give in IEEE arithmetic.  A target >= n_vocab is padding and
+ * sets TT_ERR_INVALID_ARG in d_status.
+ */
+tt_status tt_token_loss(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
+                        const int32_t *d_targets, float *d_loss, float *d_lse, const float *d_row_grads,
+                        void *d_dlogits, int64_t dlogits_stride, int32_t *d_status, tt_stream_t stream);
+
+/* tt_token_loss_grad - the gradient of tt_token_loss alone, from the lse that
+ * it returned (for a gradient that is known only later); arguments and
+ * results as there. */
+tt_status tt_token_loss_grad(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab,
+                             int64_t logits_stride, const int32_t *d_targets, const float *d_lse,
+                             const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,
+                             int32_t *d_status, tt_stream_t stream);
+
+/*
+ * tt_sample - draw one token ID from each row of logits, with given random
+ * numbers.
+ *
+ * With M the row's largest logit and T its temperature, token j has the
+ * weight w[j] = rint(2^40 * 2^(-(M - logits[j]) * (log2(e) / T))), the
+ * exponent and the power in 32-bit arithmetic: the softmax's numerators as
+ * whole numbers of 2^-40 of the largest, so that their 64-bit sums are the
+ * same in every order and the drawn ID depends on nothing but the row.
+ * Tokens are ranked by weight, equal ones by lower ID first.  Kept are those
+ * with w > 0 among
+ *   top-k   the first top_k;
+ *   min-p   those with w >= min_p * 2^40 (2^40 is the largest weight);
+ *   top-p   of what the two leave, with sum S, the shortest run of first
+ *           tokens whose sum is >= ceil(top_p * S) (at least one).
+ * With K the sum of what is kept, the drawn ID is the least one for which the
+ * kept weights of IDs up to and including it sum to more than
+ * floor(uniform * K) (the products with S and K rounded to 64-bit floats).
+ *
+ *   d_logits       device, type [n_rows][n_vocab], rows logits_stride apart;
+ *                  -inf and NaN are never drawn; +inf takes all the weight.
+ *   n_rows         0 .. TT_MAX_IDS.
+ *   d_uniform      device, float [n_rows], each in [0, 1).
+ *   d_temperature  device, float [n_rows], each finite and >= 0; 0: the
+ *                  largest logit's lowest ID.  NULL: 1.
+ *   d_top_k        device, int32 [n_rows]; <= 0 or >= n_vocab: off.  NULL: off.
+ *   d_top_p        device, float [n_rows], each in [0, 1]; 1: off.  NULL: off.
+ *   d_min_p        device, float [n_rows], each in [0, 1]; 0: off.  NULL: off.
+ *   d_out_ids      device, int32 [n_rows].
+ *   d_out_logprobs device, float [n_rows], or NULL: log(w[id] / K), the
+ *                  logarithm of the probability with which it was drawn.
+ * A row with nothing to draw (all -inf or NaN) gives ID -1 and logprob -inf.
+ * A row with a parameter outside these ranges gives the same and sets
+ * TT_ERR_INVALID_ARG in d_status.
+ */
+tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
+                    const float *d_uniform, const float *d_temperature, const int32_t *d_top_k,
+                    const float *d_top_p, const float *d_min_p, int32_t *d_out_ids, float *d_out_logprobs,
+                    int32_t *d_status, tt_stream_t stream);
+
 /* tt_status_string - static English text for a status code. */
 const char *tt_status_string(tt_status s);
 
