@@ -1,4 +1,6 @@
 // tt_embed.cu - token embedding and its gradient (include/toktier.h).
+#include <algorithm>
+
 #include "tt_ops.cuh"
 
 using namespace tt::ops;
@@ -33,7 +35,7 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
   const int64_t rows_per_block = 8 * (wide ? 1 : rows_per_warp * R);
   for (int64_t row0 = blockIdx.x * rows_per_block + (threadIdx.x >> 5) * (wide ? 1 : rows_per_warp * R) + (lane >> a.lanes_log2);
        row0 < n; row0 += gridDim.x * rows_per_block) {
-    float v[R][8];
+    Raw8<TI> v[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t row = row0 + j * row_step;
@@ -41,10 +43,9 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
       if (row < n && unit < units) {
         const int32_t id = __ldg(a.ids + row);
         if ((uint32_t)id < (uint32_t)a.n_vocab) {
-          load8(table + id * a.table_stride + unit * 8, v[j]);
+          load_raw(table + id * a.table_stride + unit * 8, v[j]);
         } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[j][k] = 0;
+          v[j] = Raw8<TI>{};
           if (id >= 0 && unit == 0) op_status(a.status, TT_ERR_INVALID_ARG);
         }
       }
@@ -54,9 +55,11 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
       const int64_t row = row0 + j * row_step;
       const int unit = unit0 + j * unit_step;
       if (row < n && unit < units) {
+        float f[8];
+        raw_f32(v[j], f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] *= a.scale;
-        store8(out + row * a.out_stride + unit * 8, v[j]);
+        for (int k = 0; k < 8; ++k) f[k] *= a.scale;
+        store8(out + row * a.out_stride + unit * 8, f);
       }
     }
   }
@@ -94,6 +97,7 @@ struct SortArgs {
   uint32_t *hist;           // [bins][tiles]
   uint32_t *total;          // [bins]
   int32_t *status;
+  int32_t *cut_count;       // cleared for the sums
 };
 
 __device__ __forceinline__ int64_t count_of(const int64_t *n_ids, int64_t max_ids) {
@@ -111,6 +115,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_sort_count(SortArgs a, const i
   __shared__ uint32_t count[MAX_BINS];
   const int64_t n = count_of(a.n_ids, a.max_ids), base = (int64_t)blockIdx.x * SORT_TILE;
   for (int i = threadIdx.x; i < a.bins; i += SORT_THREADS) count[i] = 0;
+  if (FIRST && blockIdx.x == 0 && threadIdx.x == 0) *a.cut_count = 0;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < SORT_KEYS; ++k) {
@@ -233,55 +238,304 @@ k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__rest
   }
 }
 
+// The sums.  Rows and sorted tokens are one list of items, the tokens of a row
+// before the row's end: token i stands at place i + key[i], the end of row r
+// behind the tokens of rows 0 .. r.  The list is cut into equal parts, one for
+// a worker (a group of threads that covers up to 2048 columns); a token costs
+// a row read and a row's end a row written, so the parts cost the same however
+// the tokens are spread: absent rows, rows of one token and rows of a tenth of
+// all tokens.  A row that ends where it began is written at once; one that is
+// cut leaves its pieces in the workspace, and k_grad_join adds them in order.
 struct GradArgs {
   const int64_t *n_ids;
   int64_t max_ids, n_vocab, dim, dout_stride, dtable_stride;
   float scale;
   int accumulate;
   const int32_t *keys, *pos;     // sorted
+  int items, workers;            // items a worker, workers a block
+  int group, cols;               // threads a worker, columns of its tile
+  int64_t carry_stride;          // dim rounded up to whole float4
+  float *heads, *tails;          // [workers in all][carry_stride]
+  int whole;                     // rows of at most so many tokens are not cut
+  int32_t *row_first;            // [n_vocab]: the worker where a cut row begins
+  int32_t *cut_count;
+  int2 *cut;                     // the worker where a cut row ends, and the row
 };
 
-__device__ __forceinline__ int64_t lower_bound(const int32_t *keys, int64_t n, int32_t v) {
-  int64_t lo = 0, hi = n;
+// how many of 0 .. n-1, from the first on, satisfy `pred` (a prefix does): a
+// 33-ary search by a warp
+template <class P> __device__ __forceinline__ int64_t warp_search(int64_t n, P pred) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = n;        // lo - 1 does, hi does not
   while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (keys[mid] < v) lo = mid + 1; else hi = mid;
+    const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const int c = __popc(__ballot_sync(~0u, i < hi && pred(i)));       // probes 0 .. c-1 do
+    if (c < 32) hi = min(hi, lo + c * step);
+    if (c > 0) lo = lo + (c - 1) * step + 1;
   }
   return lo;
 }
 
-// a block a row of the table
-template <class TI, class TO>
-__global__ void __launch_bounds__(256) k_grad_rows(GradArgs a, const TI *__restrict__ dout, TO *__restrict__ dtable) {
+// the number of tokens that stand before `place`
+__device__ __forceinline__ int64_t tokens_before(const int32_t *keys, int64_t n, int64_t place) {
+  return warp_search(n, [&](int64_t i) { return i + keys[i] < place; });
+}
+
+// how a thread's columns lie: eight side by side, or four `group` apart
+template <class T, int COLS> struct Cols;
+template <class T> struct Cols<T, 8> {
+  Raw8<T> raw;
+  __device__ __forceinline__ void load(const T *row, int c, int, int) { load_raw(row + c, raw); }
+  __device__ __forceinline__ void f32(float v[8]) const { raw_f32(raw, v); }
+  static __device__ __forceinline__ void store(T *row, int c, int, int, float v[8], bool accumulate) {
+    if (accumulate) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = to_f32(row[c + j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += o[j];
+    }
+    store8(row + c, v);
+  }
+};
+template <class T> struct Cols<T, 4> {
+  T raw[4];
+  __device__ __forceinline__ void load(const T *row, int c, int group, int dim) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw[j] = c + j * group < dim ? row[c + j * group] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void f32(float v[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = to_f32(raw[j]);
+  }
+  static __device__ __forceinline__ void store(T *row, int c, int group, int dim, float v[4], bool accumulate) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j * group < dim) {
+        T *p = row + c + j * group;
+        *p = from_f32<T>(accumulate ? to_f32(*p) + v[j] : v[j]);
+      }
+  }
+};
+
+// zeros over whole rows that lie side by side: 16 bytes a store
+template <class T> __device__ __forceinline__ void fill_zero(T *p, int64_t n, int t, int group) {
+  const int64_t lead = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T));
+  const int64_t vecs = (n - lead) / (16 / (int64_t)sizeof(T)), done = lead + vecs * (16 / (int64_t)sizeof(T));
+  for (int64_t i = t; i < lead; i += group) p[i] = from_f32<T>(0.f);
+  for (int64_t i = t; i < vecs; i += group) __stcs(reinterpret_cast<uint4 *>(p + lead) + i, make_uint4(0, 0, 0, 0));
+  for (int64_t i = done + t; i < n; i += group) p[i] = from_f32<T>(0.f);
+}
+
+constexpr int HALO = 64;
+
+template <class TI, class TO, int COLS>
+__global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__restrict__ dout, TO *__restrict__ dtable) {
+  constexpr int BATCH = COLS == 8 ? 16 / sizeof(TI) : 8;        // rows in flight a thread
+  extern __shared__ int32_t s_tok[];              // keys, then places in dout, HALO more on both sides
+  __shared__ int64_t s_at[2];
   const int64_t n = count_of(a.n_ids, a.max_ids);
-  const int32_t v = blockIdx.x;
-  const int64_t lo = lower_bound(a.keys, n, v), hi = lower_bound(a.keys, n, v + 1);
-  for (int64_t c = threadIdx.x; c < a.dim; c += 256) {
-    float s = 0;
-    for (int64_t i = lo; i < hi; ++i) s += to_f32(dout[a.pos[i] * a.dout_stride + c]);
-    TO *p = dtable + v * a.dtable_stride + c;
-    s *= a.scale;
-    *p = from_f32<TO>(a.accumulate ? to_f32(*p) + s : s);
+  const int block_items = a.items * a.workers;
+  const int64_t d0 = (int64_t)blockIdx.x * block_items;
+  // tokens of the block's places; padding stands behind every row
+  if (threadIdx.x < 64) {
+    const int64_t at = tokens_before(a.keys, n, d0 + (threadIdx.x >> 5) * block_items);
+    if ((threadIdx.x & 31) == 0) s_at[threadIdx.x >> 5] = at;
+  }
+  __syncthreads();
+  const int64_t i0 = s_at[0];
+  const int n_tok = (int)(s_at[1] - i0);
+  int32_t *s_key = s_tok + HALO, *s_pos = s_key + block_items + HALO;
+  for (int i = (int)threadIdx.x - HALO; i < n_tok + HALO; i += blockDim.x) {
+    const bool there = i0 + i >= 0 && i0 + i < n;
+    s_key[i] = there ? a.keys[i0 + i] : i < 0 ? -1 : INT32_MAX;
+    if (there && i >= 0) s_pos[i] = a.pos[i0 + i];
+  }
+  __syncthreads();
+  const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
+  const int dim = (int)a.dim, n_vocab = (int)a.n_vocab;
+  const int c = (int)blockIdx.y * a.cols + t * (COLS == 8 ? 8 : 1);
+  if (sub >= a.workers) return;
+  const bool mine = c < dim;                    // threads past the columns still fill
+  // the first of [lo, hi) whose key is at least k
+  auto first_of = [&](int lo, int hi, int k) {
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_key[mid] < k) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+  };
+  // The cut at the block's place p: the tokens of the block before it, and the
+  // rows.  One inside a row of at most a.whole tokens moves behind that row.
+  auto cut_at = [&](int p, int &i, int &r) {
+    int lo = 0, hi = min(p, n_tok);
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (i0 + mid + s_key[mid] < d0 + p) lo = mid + 1; else hi = mid;
+    }
+    i = lo;
+    r = (int)min(a.n_vocab, d0 + p - i0 - lo);
+    if (s_key[lo - 1] == r && r < n_vocab) {
+      const int begin = first_of(lo - a.whole, lo, r), end = first_of(lo, lo + a.whole, r + 1);
+      if (end - begin <= a.whole && s_key[begin - 1] < r) {       // else it is longer
+        i = end;
+        ++r;
+      }
+    }
+  };
+  int i, end, r, r_end;
+  cut_at(sub * a.items, i, r);
+  cut_at((sub + 1) * a.items, end, r_end);
+  while (end > i && s_key[end - 1] >= n_vocab) --end;
+  const int w = (int)blockIdx.x * a.workers + sub;
+  bool head = s_key[i - 1] == r && r < n_vocab, any = false;
+  const bool side_by_side = !a.accumulate && gridDim.y == 1 && a.dtable_stride == a.dim;
+  float acc[COLS];
+#pragma unroll
+  for (int j = 0; j < COLS; ++j) acc[j] = 0;
+  auto keep = [&](float *to) {                    // a piece of a cut row
+    float *p = to + (int64_t)w * a.carry_stride + c;
+    if (COLS == 8) {
+      if (mine) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(acc[4 % COLS], acc[5 % COLS], acc[6 % COLS], acc[7 % COLS]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j * a.group < dim) p[j * a.group] = acc[j];
+    }
+  };
+  auto finish_to = [&](int k) {               // rows r .. k-1 end here
+    if (head) {
+      keep(a.heads);
+      if (t == 0 && blockIdx.y == 0) a.cut[atomicAdd(a.cut_count, 1)] = make_int2(w, r);
+    } else if (any) {
+      float v[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) v[j] = acc[j] * a.scale;
+      if (mine) Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride, c, a.group, dim, v, a.accumulate);
+    }
+    if (head || any) ++r;
+    head = any = false;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) acc[j] = 0;
+    if (side_by_side) {
+      if (r < k) fill_zero(dtable + (int64_t)r * a.dim, (int64_t)(k - r) * a.dim, t, a.group);
+    } else if (!a.accumulate && mine) {
+      for (; r < k; ++r) {
+        float v[COLS] = {};
+        Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride, c, a.group, dim, v, false);
+      }
+    }
+    r = k;
+  };
+  for (; i < end; i += BATCH) {
+    Cols<TI, COLS> v[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+      if (mine && i + b < end) v[b].load(dout + (int64_t)s_pos[i + b] * a.dout_stride, c, a.group, dim);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+      if (i + b < end) {
+        const int32_t k = s_key[i + b];
+        if (r < k) finish_to(k);
+        float f[COLS];
+        v[b].f32(f);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) acc[j] += f[j];
+        any = true;
+      }
+  }
+  if (r < r_end) finish_to(r_end);
+  if (any) {
+    keep(a.tails);
+    if (!head && t == 0 && blockIdx.y == 0) a.row_first[r] = w;
+  }
+}
+
+// the rows that were cut: the tails of the workers before, eight runs of them
+// summed side by side, and the last worker's head; a block 128 columns of a row
+template <class TO>
+__global__ void __launch_bounds__(256) k_grad_join(GradArgs a, TO *__restrict__ dtable) {
+  __shared__ float4 part[8][32];
+  const int count = *a.cut_count, chunks = (int)((a.dim + 127) / 128);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t job = blockIdx.x; job < (int64_t)count * chunks; job += gridDim.x) {
+    const int2 at = a.cut[job / chunks];
+    const int64_t w = at.x, r = at.y, c = (job % chunks) * 128 + lane * 4, first = a.row_first[r];
+    const int64_t each = (w - first + 7) / 8, lo = min(w, first + warp * each), hi = min(w, lo + each);
+    float4 s = make_float4(0, 0, 0, 0);
+    if (c < a.dim) {
+#pragma unroll 8
+      for (int64_t k = lo; k < hi; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(a.tails + k * a.carry_stride + c);
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+      }
+    }
+    __syncthreads();
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < a.dim) {
+      for (int k = 1; k < 8; ++k) {
+        const float4 x = part[k][lane];
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+      }
+      const float4 h = *reinterpret_cast<const float4 *>(a.heads + w * a.carry_stride + c);
+      const float v[4] = {(s.x + h.x) * a.scale, (s.y + h.y) * a.scale, (s.z + h.z) * a.scale, (s.w + h.w) * a.scale};
+      TO *p = dtable + r * a.dtable_stride + c;
+      for (int j = 0; j < 4; ++j)
+        if (c + j < a.dim) p[j] = from_f32<TO>(a.accumulate ? to_f32(p[j]) + v[j] : v[j]);
+    }
   }
 }
 
 // ------------------------------------------------------------ host side
 bool grad_sizes_ok(int64_t max_ids, int64_t n_vocab, int64_t dim) {
-  return max_ids >= 0 && max_ids <= TT_MAX_IDS && vocab_ok(n_vocab) && dim >= 1 && dim <= INT32_MAX;
+  return max_ids >= 0 && max_ids <= TT_MAX_IDS && vocab_ok(n_vocab) && dim >= 1 && dim <= MAX_DIM;
 }
 
 struct GradPlan {
   int tiles = 0, bits[2] = {0, 0};
-  int64_t keys[2], pos[2], hist, total, bytes;   // offsets into the workspace
+  int col_tiles[2], cols[2], group[2], workers[2];       // [1]: eight columns a thread, [0]: four
+  int items[2];
+  int64_t blocks[2];
+  int64_t keys[2], pos[2], hist, total, row_first, cut_count, cut, heads, tails, carry_stride, bytes;   // offsets into the workspace
 };
 
-GradPlan grad_plan(int64_t max_ids, int64_t n_vocab) {
+constexpr int BLOCK_ITEMS = 4096;                 // at most, in shared memory
+
+GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
   GradPlan p;
   int bits = 1;
   while ((n_vocab >> bits) != 0) ++bits;          // keys are 0 .. n_vocab
   p.bits[0] = (bits + 1) / 2;
   p.bits[1] = bits - p.bits[0];
   p.tiles = (int)((max_ids + SORT_TILE - 1) / SORT_TILE);
+  int64_t pieces = 0;
+  for (int v = 0; v < 2; ++v) {
+    const int per = v ? 8 : 4;
+    const int64_t threads = (dim + per - 1) / per;
+    p.col_tiles[v] = (int)((threads + 255) / 256);
+    const int need = (int)((threads + p.col_tiles[v] - 1) / p.col_tiles[v]);
+    if (need > 128) {
+      p.group[v] = (need + 31) / 32 * 32;
+      p.workers[v] = 1;
+    } else {
+      p.group[v] = 1;
+      while (p.group[v] < need) p.group[v] *= 2;
+      p.workers[v] = 256 / p.group[v];
+    }
+    p.cols[v] = p.group[v] * per;
+    p.col_tiles[v] = (int)((dim + p.cols[v] - 1) / p.cols[v]);
+    // about four times the threads the GPU holds, but few enough pieces
+    const int64_t places = n_vocab + max_ids;
+    int64_t workers = (4LL * 152 * 2048) / ((int64_t)p.group[v] * p.col_tiles[v]);
+    workers = std::max<int64_t>(1, std::min(workers, std::max<int64_t>(8192, (1 << 21) / dim)));
+    p.items[v] = (int)std::min<int64_t>(BLOCK_ITEMS / p.workers[v], std::max<int64_t>(8, (places + workers - 1) / workers));
+    p.blocks[v] = (places + (int64_t)p.items[v] * p.workers[v] - 1) / ((int64_t)p.items[v] * p.workers[v]);
+    pieces = std::max(pieces, p.blocks[v] * p.workers[v]);
+  }
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t o = at;
@@ -294,6 +548,15 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab) {
   }
   p.hist = take(4 * ((int64_t)p.tiles << p.bits[0]));
   p.total = take(4 * MAX_BINS);
+  p.carry_stride = (dim + 3) / 4 * 4;
+  p.row_first = p.cut_count = p.cut = p.heads = p.tails = 0;
+  if (max_ids > 0) {
+    p.row_first = take(4 * n_vocab);
+    p.cut_count = take(4);
+    p.cut = take(8 * pieces);
+    p.heads = take(4 * pieces * p.carry_stride);
+    p.tails = take(4 * pieces * p.carry_stride);
+  }
   p.bytes = at;
   return p;
 }
@@ -304,7 +567,7 @@ extern "C" tt_status tt_embed(const int32_t *d_ids, int64_t max_ids, const int64
                               int32_t table_type, int64_t n_vocab, int64_t dim, int64_t table_stride, float scale,
                               void *d_out, int32_t out_type, int64_t out_stride, int32_t *d_status,
                               tt_stream_t stream) {
-  if (!type_ok(table_type) || !type_ok(out_type) || !vocab_ok(n_vocab) || dim < 1 || dim > INT32_MAX || max_ids < 0 ||
+  if (!type_ok(table_type) || !type_ok(out_type) || !vocab_ok(n_vocab) || dim < 1 || dim > MAX_DIM || max_ids < 0 ||
       table_stride < dim || out_stride < dim || !optional_ok(d_n_ids, 8) || !optional_ok(d_status, 4))
     return TT_ERR_INVALID_ARG;
   if (max_ids > TT_MAX_IDS) return TT_ERR_CAPACITY;
@@ -332,7 +595,7 @@ extern "C" tt_status tt_embed(const int32_t *d_ids, int64_t max_ids, const int64
 }
 
 extern "C" int64_t tt_embed_grad_workspace(int64_t max_ids, int64_t n_vocab, int64_t dim) {
-  return grad_sizes_ok(max_ids, n_vocab, dim) ? grad_plan(max_ids, n_vocab).bytes : -1;
+  return grad_sizes_ok(max_ids, n_vocab, dim) ? grad_plan(max_ids, n_vocab, dim).bytes : -1;
 }
 
 extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const int64_t *d_n_ids, const void *d_dout,
@@ -345,7 +608,7 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   if (max_ids > TT_MAX_IDS) return TT_ERR_CAPACITY;
   if (!grad_sizes_ok(max_ids, n_vocab, dim)) return TT_ERR_INVALID_ARG;
   if (max_ids > 0 && (!array_ok(d_ids, 4) || !array_ok(d_dout, type_size(dout_type)))) return TT_ERR_INVALID_ARG;
-  const GradPlan p = grad_plan(max_ids, n_vocab);
+  const GradPlan p = grad_plan(max_ids, n_vocab, dim);
   if (!array_ok(d_workspace, 16)) return TT_ERR_INVALID_ARG;
   if (workspace_bytes < p.bytes) return TT_ERR_CAPACITY;
   char *ws = (char *)d_workspace;
@@ -353,7 +616,7 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   int32_t *pos[2] = {(int32_t *)(ws + p.pos[0]), (int32_t *)(ws + p.pos[1])};
   if (max_ids > 0) {
     SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, 0, 1 << p.bits[0], p.tiles, (uint32_t *)(ws + p.hist),
-               (uint32_t *)(ws + p.total), d_status};
+               (uint32_t *)(ws + p.total), d_status, (int32_t *)(ws + p.cut_count)};
     const auto shared = [](int bins) { return (size_t)bins * 4 + (size_t)bins * 2 * (SORT_THREADS / 32); };
     {
       cudaFuncSetAttribute(k_sort_place<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared(MAX_BINS));
@@ -368,12 +631,22 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
     k_sort_scan<<<s.bins, 256, 0, stream>>>(s);
     k_sort_place<false><<<p.tiles, SORT_THREADS, shared(s.bins), stream>>>(s, keys[0], pos[0], keys[1], pos[1]);
   }
-  const GradArgs a{d_n_ids, max_ids, n_vocab, dim, dout_stride, dtable_stride, scale, accumulate != 0, keys[1], pos[1]};
+  const int v = rows_vector(d_dout, dout_stride, dim) && rows_vector(d_dtable, dtable_stride, dim);
+  const GradArgs a{d_n_ids, max_ids, n_vocab, dim, dout_stride, dtable_stride, scale, accumulate != 0, keys[1], pos[1],
+                   p.items[v], p.workers[v], p.group[v], p.cols[v], p.carry_stride,
+                   (float *)(ws + p.heads), (float *)(ws + p.tails), std::min(p.items[v], HALO - 1),
+                   (int32_t *)(ws + p.row_first), (int32_t *)(ws + p.cut_count), (int2 *)(ws + p.cut)};
   with_type(dout_type, [&](auto ti) {
     with_type(dtable_type, [&](auto to) {
       using TI = decltype(ti);
       using TO = decltype(to);
-      k_grad_rows<TI, TO><<<(unsigned)n_vocab, 256, 0, stream>>>(a, (const TI *)d_dout, (TO *)d_dtable);
+      const dim3 grid((unsigned)p.blocks[v], (unsigned)p.col_tiles[v]);
+      const unsigned threads = (unsigned)(p.group[v] * p.workers[v]);
+      const size_t shared = 4 * (4 * HALO + 2 * (size_t)p.items[v] * p.workers[v]);
+      auto sum = v ? k_grad_sum<TI, TO, 8> : k_grad_sum<TI, TO, 4>;
+      sum<<<grid, threads, shared, stream>>>(a, (const TI *)d_dout, (TO *)d_dtable);
+      if (max_ids > 0)
+        k_grad_join<TO><<<(unsigned)std::min<int64_t>(152 * 8, p.blocks[v] * p.workers[v]), 256, 0, stream>>>(a, (TO *)d_dtable);
     });
   });
   return launched("tt_embed_grad");

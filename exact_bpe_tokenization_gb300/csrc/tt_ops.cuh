@@ -13,6 +13,7 @@ namespace tt {
 namespace ops {
 
 constexpr int64_t MAX_VOCAB = 1 << 20;
+constexpr int64_t MAX_DIM = 1 << 24;
 constexpr float INF = __builtin_huge_valf();
 
 // ------------------------------------------------------------ elements
@@ -24,25 +25,35 @@ template <> __device__ __forceinline__ float from_f32<float>(float x) { return x
 template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// eight elements at a 16-byte aligned address, read through the cache for
-// data that no kernel in flight writes
-__device__ __forceinline__ void load8(const float *p, float v[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <class T2, class T> __device__ __forceinline__ void load8_16(const T *p, float v[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// eight elements as they lie in memory, and as floats
+template <class T> struct Raw8 { uint4 w[sizeof(T) / 2]; };
+template <class T> __device__ __forceinline__ void load_raw(const T *p, Raw8<T> &r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const T *h = reinterpret_cast<const T *>(&w[i]);
-    v[2 * i] = to_f32(h[0]);
-    v[2 * i + 1] = to_f32(h[1]);
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+}
+__device__ __forceinline__ void two_f32(uint32_t w, float *v, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  v[0] = f.x;
+  v[1] = f.y;
+}
+__device__ __forceinline__ void two_f32(uint32_t w, float *v, __nv_bfloat16) {
+  v[0] = __uint_as_float(w << 16);
+  v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+template <class T> __device__ __forceinline__ void raw_f32(const Raw8<T> &r, float v[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) two_f32(w[i], v + 2 * i, T{});
+}
+__device__ __forceinline__ void raw_f32(const Raw8<float> &r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.w[i].x);
+    v[4 * i + 1] = __uint_as_float(r.w[i].y);
+    v[4 * i + 2] = __uint_as_float(r.w[i].z);
+    v[4 * i + 3] = __uint_as_float(r.w[i].w);
   }
 }
-__device__ __forceinline__ void load8(const __half *p, float v[8]) { load8_16<__half2>(p, v); }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float v[8]) { load8_16<__nv_bfloat162>(p, v); }
 
 // eight elements to a 16-byte aligned address, marked as not to be read soon
 __device__ __forceinline__ void store8(float *p, const float v[8]) {

@@ -337,7 +337,7 @@ tt_status tt_pretokenize_batch(tt_tokenizer *h,
  *     statistics are in 32 bits or more, and results are rounded from there
  *     to their type (to nearest even).
  *   - IDs are int32.  A negative ID is padding: it stands for no token.
- *     n_vocab is 1 .. 2^20, as in tt_create.
+ *     n_vocab is 1 .. 2^20, as in tt_create; dim is 1 .. 2^24.
  *   - d_status (device, int32, may be NULL): a kernel that meets a value this
  *     header does not allow writes its tt_status there if the word is
  *     TT_OK (0); it is never cleared.  Such an ID, target or sampling row is
