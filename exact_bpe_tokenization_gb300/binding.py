@@ -269,59 +269,82 @@ def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temp
 
 # ---- the same on torch CUDA tensors: outputs and scratch allocated where they
 # are not given, shapes and types checked.  The kernels run on `stream` (the
-# current one if None); what is allocated here is handed to that stream.
+# current one if None); what is allocated here is handed to that stream.  Small
+# calls cost a few microseconds of device time, so these call the library
+# without a layer in between.
 
-_DTYPES = {"torch.float32": TT_F32, "torch.float16": TT_F16, "torch.bfloat16": TT_BF16}
+_codes = {}          # torch dtype -> tt_dtype; filled with the first tensor
+
+
+def _torch():
+    import torch
+    if not _codes:
+        _codes.update({torch.float32: TT_F32, torch.float16: TT_F16, torch.bfloat16: TT_BF16})
+    return torch
 
 
 def _matrix(x, what, rows=None, cols=None):
-    """(dtype code, row stride) of a 2-D CUDA tensor with unit column stride."""
-    code = _DTYPES.get(str(x.dtype))
+    """(dtype code, rows, columns, row stride) of a 2-D CUDA tensor with unit
+    column stride."""
+    code = _codes.get(x.dtype)
     if code is None:
-        raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
-    n, d = x.shape if x.dim() == 2 else (None, None)
-    if n is None or not x.is_cuda or (rows is not None and n != rows) or (cols is not None and d != cols):
-        raise ValueError("%s: a CUDA tensor [%s, %s] wanted, got %s on %s" % (what, rows or "n", cols or "n",
-                                                                            list(x.shape), x.device))
-    if d > 1 and x.stride(1) != 1:
+        _torch()
+        code = _codes.get(x.dtype)
+        if code is None:
+            raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
+    shape = x.shape
+    if len(shape) != 2 or not x.is_cuda or (rows is not None and shape[0] != rows) or \
+            (cols is not None and shape[1] != cols):
+        raise ValueError("%s: a CUDA tensor [%s, %s] wanted, got %s on %s" % (
+            what, "n" if rows is None else rows, "n" if cols is None else cols, list(shape), x.device))
+    n, d = shape
+    s0, s1 = x.stride()
+    if s1 != 1 and d > 1:
         raise ValueError("%s: columns must be contiguous" % what)
-    return code, (x.stride(0) if n > 1 else d)
+    return code, n, d, (s0 if n > 1 else d)
 
 
 def _vector(x, what, dtype, n=None):
-    """A contiguous 1-D CUDA tensor of `dtype`, or None."""
-    if x is not None and (not x.is_cuda or x.dim() != 1 or str(x.dtype) != dtype or not x.is_contiguous() or
-                          (n is not None and x.shape[0] != n)):
+    """The address of a contiguous 1-D CUDA tensor, or None."""
+    if x is None:
+        return None
+    if x.dtype != dtype or not x.is_cuda or x.dim() != 1 or (n is not None and x.shape[0] != n) or \
+            not x.is_contiguous():
         raise ValueError("%s: a contiguous CUDA tensor %s [%s] wanted, got %s %s on %s" % (
             what, dtype, "n" if n is None else n, x.dtype, list(x.shape), x.device))
-    return x
+    return x.data_ptr()
 
 
-def _handed(stream, *tensors):
-    """Tensors allocated on the current stream but used on another."""
-    import torch
-    if stream is not None:
-        raw = _stream(stream)
-        if raw != torch.cuda.current_stream().cuda_stream:
-            s = torch.cuda.ExternalStream(raw)
-            s.wait_stream(torch.cuda.current_stream())     # the block may still be in use there
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
+def _on(torch, stream, device, *tensors):
+    """The stream's address.  Tensors allocated here come from the current
+    stream's pool: another stream waits for it and keeps them."""
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        return current
+    raw = _stream(stream)
+    if raw != current:
+        s = torch.cuda.ExternalStream(raw, device)
+        s.wait_stream(torch.cuda.current_stream(device))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+    return raw
 
 
 def embed(ids, table, scale=1.0, n_ids=None, dtype=None, out=None, status=None, stream=None):
     """scale * table[ids] (zero rows for padding): out [len(ids), dim] of
     `dtype` (the table's if None).  n_ids: a device int64 count."""
-    import torch
-    _vector(ids, "ids", "torch.int32")
-    t, ts = _matrix(table, "table")
-    n, (vocab, dim) = ids.shape[0], table.shape
+    torch = _torch()
+    pi = _vector(ids, "ids", torch.int32)
+    t, vocab, dim, ts = _matrix(table, "table")
+    n = ids.shape[0]
+    mine = None
     if out is None:
-        out = torch.empty((n, dim), dtype=dtype or table.dtype, device=table.device)
-        _handed(stream, out)
-    o, os_ = _matrix(out, "out", n, dim)
-    tt_embed(ids, n, n_ids, table, t, vocab, dim, ts, scale, out, o, os_, status, stream)
+        out = mine = torch.empty((n, dim), dtype=dtype or table.dtype, device=table.device)
+    o, _, _, os_ = _matrix(out, "out", n, dim)
+    _check(lib().tt_embed(pi, n, None if n_ids is None else _vector(n_ids, "n_ids", torch.int64, 1), table.data_ptr(),
+                          t, vocab, dim, ts, scale, out.data_ptr(), o, os_, _vector(status, "status", torch.int32),
+                          _on(torch, stream, table.device, mine)), "tt_embed")
     return out
 
 
@@ -329,85 +352,84 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
                status=None, stream=None):
     """The gradient of embed: [n_vocab, dim] of `dtype` (float32 if None), the
     scaled sums of dout's rows by ID; with accumulate, added to `out`."""
-    import torch
-    _vector(ids, "ids", "torch.int32")
+    torch = _torch()
+    pi = _vector(ids, "ids", torch.int32)
     n = ids.shape[0]
-    d, ds = _matrix(dout, "dout", n)
-    dim = dout.shape[1]
+    d, _, dim, ds = _matrix(dout, "dout", n)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    need = tt_embed_grad_workspace(n, n_vocab, dim)
-    mine = []
+    mine = scratch = None
     if out is None:
-        out = torch.empty((n_vocab, dim), dtype=dtype or torch.float32, device=dout.device)
-        mine.append(out)
+        out = mine = torch.empty((n_vocab, dim), dtype=dtype or torch.float32, device=dout.device)
+    o, _, _, os_ = _matrix(out, "out", n_vocab, dim)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dout.device)
-        mine.append(workspace)
-    if mine:
-        _handed(stream, *mine)
-    o, os_ = _matrix(out, "out", n_vocab, dim)
-    tt_embed_grad(ids, n, n_ids, dout, d, dim, ds, scale, out, o, n_vocab, os_, accumulate, workspace,
-                  workspace.numel() * workspace.element_size(), status, stream)
+        workspace = scratch = torch.empty(max(lib().tt_embed_grad_workspace(n, n_vocab, dim), 16), dtype=torch.uint8,
+                                          device=dout.device)
+    _check(lib().tt_embed_grad(pi, n, None if n_ids is None else _vector(n_ids, "n_ids", torch.int64, 1),
+                               dout.data_ptr(), d, dim, ds, scale, out.data_ptr(), o, n_vocab, os_, bool(accumulate),
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _vector(status, "status", torch.int32),
+                               _on(torch, stream, dout.device, mine, scratch)), "tt_embed_grad")
     return out
 
 
 def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, status=None, stream=None):
     """Next-token loss of each row: (loss, lse), and with want_grad or dlogits
     (which may be logits itself) the logits' gradient as a third."""
-    import torch
-    t, ls = _matrix(logits, "logits")
-    n, vocab = logits.shape
-    _vector(targets, "targets", "torch.int32", n)
-    _vector(row_grads, "row_grads", "torch.float32", n)
-    loss, lse = torch.empty((2, n), dtype=torch.float32, device=logits.device)
+    torch = _torch()
+    t, n, vocab, ls = _matrix(logits, "logits")
+    pt, pg = _vector(targets, "targets", torch.int32, n), _vector(row_grads, "row_grads", torch.float32, n)
+    loss, lse = both = torch.empty((2, n), dtype=torch.float32, device=logits.device)
     mine = None
     if dlogits is None and want_grad:
         dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
-    _handed(stream, loss, mine)
-    d, ds = t, vocab
+    d, ds, pd = t, vocab, None
     if dlogits is not None:
-        d, ds = _matrix(dlogits, "dlogits", n, vocab)
+        d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
+        pd = dlogits.data_ptr()
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
-    tt_token_loss(logits, t, n, vocab, ls, targets, loss, lse, row_grads, dlogits, ds, status, stream)
+    at = both.data_ptr()
+    _check(lib().tt_token_loss(logits.data_ptr(), t, n, vocab, ls, pt, at, at + 4 * n, pg, pd, ds,
+                               _vector(status, "status", torch.int32),
+                               _on(torch, stream, logits.device, both, mine)), "tt_token_loss")
     return (loss, lse) if dlogits is None else (loss, lse, dlogits)
 
 
 def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=None, stream=None):
     """The gradient of token_loss from the lse that it returned."""
-    import torch
-    t, ls = _matrix(logits, "logits")
-    n, vocab = logits.shape
-    _vector(targets, "targets", "torch.int32", n)
-    _vector(lse, "lse", "torch.float32", n)
-    _vector(row_grads, "row_grads", "torch.float32", n)
+    torch = _torch()
+    t, n, vocab, ls = _matrix(logits, "logits")
+    pt, pl = _vector(targets, "targets", torch.int32, n), _vector(lse, "lse", torch.float32, n)
+    pg = _vector(row_grads, "row_grads", torch.float32, n)
+    mine = None
     if dlogits is None:
-        dlogits = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
-        _handed(stream, dlogits)
-    d, ds = _matrix(dlogits, "dlogits", n, vocab)
+        dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
+    d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
-    tt_token_loss_grad(logits, t, n, vocab, ls, targets, lse, row_grads, dlogits, ds, status, stream)
+    _check(lib().tt_token_loss_grad(logits.data_ptr(), t, n, vocab, ls, pt, pl, pg, dlogits.data_ptr(), ds,
+                                    _vector(status, "status", torch.int32),
+                                    _on(torch, stream, logits.device, mine)), "tt_token_loss_grad")
     return dlogits
 
 
 def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, status=None, stream=None):
     """One token ID drawn from each row: (ids int32, logprobs float32).  The
     parameters are device tensors with an entry a row, or None (off)."""
-    import torch
-    t, ls = _matrix(logits, "logits")
-    n, vocab = logits.shape
-    for x, what, kind in ((uniform, "uniform", "torch.float32"), (temperature, "temperature", "torch.float32"),
-                          (top_k, "top_k", "torch.int32"), (top_p, "top_p", "torch.float32"),
-                          (min_p, "min_p", "torch.float32")):
-        _vector(x, what, kind, n)
-    if uniform is None:
+    torch = _torch()
+    t, n, vocab, ls = _matrix(logits, "logits")
+    f = torch.float32
+    pu = _vector(uniform, "uniform", f, n)
+    if pu is None:
         raise ValueError("uniform: a tensor wanted")
     ids = torch.empty(n, dtype=torch.int32, device=logits.device)
-    logprobs = torch.empty(n, dtype=torch.float32, device=logits.device)
-    _handed(stream, ids, logprobs)
-    tt_sample(logits, t, n, vocab, ls, uniform, temperature, top_k, top_p, min_p, ids, logprobs, status, stream)
+    logprobs = torch.empty(n, dtype=f, device=logits.device)
+    _check(lib().tt_sample(logits.data_ptr(), t, n, vocab, ls, pu, _vector(temperature, "temperature", f, n),
+                           _vector(top_k, "top_k", torch.int32, n), _vector(top_p, "top_p", f, n),
+                           _vector(min_p, "min_p", f, n), ids.data_ptr(), logprobs.data_ptr(),
+                           _vector(status, "status", torch.int32), _on(torch, stream, logits.device, ids, logprobs)),
+           "tt_sample")
     return ids, logprobs
 
 

@@ -122,5 +122,97 @@ template <class V, class Op> __device__ V block_all(V v, Op op, V *box) {
   return v;
 }
 
+// ------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// the same variable of another block of the cluster
+template <class V> __device__ __forceinline__ V *of_block(V *p, uint32_t rank) {
+  uint64_t a;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<V *>(a);
+}
+
+// 2^x, results below the normal range as zero
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x - y) * z of two values at once
+__device__ __forceinline__ float2 sub_mul2(float2 x, float y, float z) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};\n\t"
+      "add.rn.f32x2 a, a, b; mul.rn.f32x2 a, a, c; mov.b64 {%0, %1}, a; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(-y), "f"(z));
+  return r;
+}
+
+// A row of elements as a scalar lead up to the first 16-byte boundary, whole
+// 16-byte vectors, and a scalar rest.
+template <class T> struct RowParts {
+  static constexpr int E = 16 / sizeof(T);
+  int lead, vecs, rest;
+  __device__ __forceinline__ RowParts(const T *p, int n) {
+    lead = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int)sizeof(T));
+    vecs = (n - lead) / E;
+    rest = n - lead - vecs * E;
+  }
+  // the scalar element of a thread of the block that has them, or -1
+  __device__ __forceinline__ int scalar(int tid) const {
+    return tid < lead ? tid : tid >= 32 && tid < 32 + rest ? lead + vecs * E + tid - 32 : -1;
+  }
+};
+
+__device__ __forceinline__ void vec_f32(uint4 r, float v[4], float) {
+  v[0] = __uint_as_float(r.x);
+  v[1] = __uint_as_float(r.y);
+  v[2] = __uint_as_float(r.z);
+  v[3] = __uint_as_float(r.w);
+}
+template <class T> __device__ __forceinline__ void vec_f32(uint4 r, float v[8], T) {
+  two_f32(r.x, v, T{});
+  two_f32(r.y, v + 2, T{});
+  two_f32(r.z, v + 4, T{});
+  two_f32(r.w, v + 6, T{});
+}
+__device__ __forceinline__ uint4 f32_vec(const float v[4], float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <class T> __device__ __forceinline__ uint32_t f32_two(float a, float b) {
+  T h[2] = {from_f32<T>(a), from_f32<T>(b)};
+  return *reinterpret_cast<uint32_t *>(h);
+}
+template <class T> __device__ __forceinline__ uint4 f32_vec(const float v[8], T) {
+  return make_uint4(f32_two<T>(v[0], v[1]), f32_two<T>(v[2], v[3]), f32_two<T>(v[4], v[5]), f32_two<T>(v[6], v[7]));
+}
+
+// launch on clusters of `cluster` blocks along x
+template <class... P, class... A>
+inline void launch_cluster(void (*f)(P...), unsigned grid, unsigned threads, size_t shared, unsigned cluster,
+                           cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, f, static_cast<P>(args)...);
+}
+
 }  // namespace ops
 }  // namespace tt
