@@ -449,7 +449,7 @@ tt_status tt_token_loss_grad(const void *d_logits, int32_t type, int64_t n_rows,
  *           tokens whose sum is >= ceil(top_p * S) (at least one).
  * With K the sum of what is kept, the drawn ID is the least one for which the
  * kept weights of IDs up to and including it sum to more than
- * floor(uniform * K) (the products with S and K rounded to 64-bit floats).
+ * floor(uniform * K).
  *
  *   d_logits       device, type [n_rows][n_vocab], rows logits_stride apart;
  *                  -inf and NaN are never drawn; +inf takes all the weight.

@@ -1,6 +1,7 @@
 """Plain 64-bit forms of the operators around token IDs, in numpy, written
 from the formulas of include/toktier.h, and the error bounds the tests use."""
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -71,9 +72,9 @@ def sample(w, u, t=1.0, top_k=0, top_p=1.0, min_p=0.0):
     order = order[: 1 if t == 0 else top_k if top_k > 0 else len(w)]
     order = order[(w[order] > 0) & (w[order] >= float(np.float32(min_p)) * 2.0**40)]
     c = np.cumsum(w[order])
-    least = max(1, math.ceil(float(np.float32(top_p)) * float(c[-1])))
+    least = max(1, math.ceil(Fraction(float(np.float32(top_p))) * int(c[-1])))
     order = np.sort(order[: 1 + int(np.searchsorted(c, least, side="left"))])
     c = np.cumsum(w[order])
-    r = math.floor(float(np.float32(u)) * float(c[-1]))
+    r = math.floor(Fraction(float(np.float32(u))) * int(c[-1]))
     i = int(np.searchsorted(c, r, side="right"))
     return int(order[i]), math.log(int(w[order[i]]) / int(c[-1]))
