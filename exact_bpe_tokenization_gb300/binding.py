@@ -379,7 +379,8 @@ def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, s
     torch = _torch()
     t, n, vocab, ls = _matrix(logits, "logits")
     pt, pg = _vector(targets, "targets", torch.int32, n), _vector(row_grads, "row_grads", torch.float32, n)
-    loss, lse = both = torch.empty((2, n), dtype=torch.float32, device=logits.device)
+    loss = torch.empty(n, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
     mine = None
     if dlogits is None and want_grad:
         dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
@@ -389,10 +390,9 @@ def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, s
         pd = dlogits.data_ptr()
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
-    at = both.data_ptr()
-    _check(lib().tt_token_loss(logits.data_ptr(), t, n, vocab, ls, pt, at, at + 4 * n, pg, pd, ds,
+    _check(lib().tt_token_loss(logits.data_ptr(), t, n, vocab, ls, pt, loss.data_ptr(), lse.data_ptr(), pg, pd, ds,
                                _vector(status, "status", torch.int32),
-                               _on(torch, stream, logits.device, both, mine)), "tt_token_loss")
+                               _on(torch, stream, logits.device, loss, lse, mine)), "tt_token_loss")
     return (loss, lse) if dlogits is None else (loss, lse, dlogits)
 
 

@@ -495,6 +495,8 @@ bool grad_sizes_ok(int64_t max_ids, int64_t n_vocab, int64_t dim) {
   return max_ids >= 0 && max_ids <= TT_MAX_IDS && vocab_ok(n_vocab) && dim >= 1 && dim <= MAX_DIM;
 }
 
+template <bool FIRST> struct Place {};
+
 struct GradPlan {
   int tiles = 0, bits[2] = {0, 0};
   int col_tiles[2], cols[2], group[2], workers[2];       // [1]: eight columns a thread, [0]: four
@@ -618,10 +620,9 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
     SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, 0, 1 << p.bits[0], p.tiles, (uint32_t *)(ws + p.hist),
                (uint32_t *)(ws + p.total), d_status, (int32_t *)(ws + p.cut_count)};
     const auto shared = [](int bins) { return (size_t)bins * 4 + (size_t)bins * 2 * (SORT_THREADS / 32); };
-    {
-      cudaFuncSetAttribute(k_sort_place<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared(MAX_BINS));
-      cudaFuncSetAttribute(k_sort_place<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared(MAX_BINS));
-    }
+    if (allow_shared<Place<true>>(k_sort_place<true>, (int)shared(MAX_BINS)) ||
+        allow_shared<Place<false>>(k_sort_place<false>, (int)shared(MAX_BINS)))
+      return launched("tt_embed_grad");
     k_sort_count<true><<<p.tiles, SORT_THREADS, 0, stream>>>(s, d_ids);
     k_sort_scan<<<s.bins, 256, 0, stream>>>(s);
     k_sort_place<true><<<p.tiles, SORT_THREADS, shared(s.bins), stream>>>(s, d_ids, nullptr, keys[0], pos[0]);

@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
   if (GRAD != 2 && a.cluster > 1) cluster_wait();
 }
 
+template <class T, int GRAD> struct Tag {};
+
 template <class T, int GRAD>
 void run_rows(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
   const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
@@ -183,8 +185,8 @@ void run_rows(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_
   a.held = GRAD == 1 ? (int)std::min<int64_t>(each, HELD / 16) : 0;
   auto k = k_loss<T, GRAD>;
   const size_t shared = (size_t)a.held * 16;
-  if (shared > 32 * 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, HELD);
-  launch_cluster(k, (unsigned)(n_rows * a.cluster), THREADS, shared, a.cluster, stream, a, (const T *)logits, (T *)dlogits);
+  if (GRAD == 1 && allow_shared<Tag<T, GRAD>>(k, HELD)) return;     // (the error is kept)
+  launch_cluster(k, dim3((unsigned)(n_rows * a.cluster)), THREADS, shared, a.cluster, false, stream, a, (const T *)logits, (T *)dlogits);
 }
 
 tt_status run_loss(const void *d_logits, int32_t type, int64_t n_rows, const LossArgs &a, void *d_dlogits,

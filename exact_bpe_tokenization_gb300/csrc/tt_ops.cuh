@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "../../include/toktier.h"
 
 namespace tt {
@@ -91,6 +93,19 @@ inline tt_status launched(const char *what) {
   if (e == cudaSuccess) return TT_OK;
   fprintf(stderr, "toktier: %s failed: %s\n", what, cudaGetErrorString(e));
   return TT_ERR_CUDA;
+}
+
+// Let a kernel use so much dynamic shared memory, once a device (Tag: the
+// kernel's own type); true if that failed.
+template <class Tag, class K> inline bool allow_shared(K kernel, int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return false;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return true;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return false;
 }
 
 // call f(T{}) with the element type of a tt_dtype
@@ -203,21 +218,34 @@ template <class T> __device__ __forceinline__ uint4 f32_vec(const float v[8], T)
   return make_uint4(f32_two<T>(v[0], v[1]), f32_two<T>(v[2], v[3]), f32_two<T>(v[4], v[5]), f32_two<T>(v[6], v[7]));
 }
 
+// A kernel launched with launch_chained may start when the blocks of the one
+// before have all called let_next_start() or ended; what it does before
+// wait_for_last() must not depend on that kernel.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // launch on clusters of `cluster` blocks along x
 template <class... P, class... A>
-inline void launch_cluster(void (*f)(P...), unsigned grid, unsigned threads, size_t shared, unsigned cluster,
+inline void launch_cluster(void (*f)(P...), dim3 grid, unsigned threads, size_t shared, unsigned cluster, bool chained,
                            cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = shared;
   cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2]{};
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (chained) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.attrs = at;
   cudaLaunchKernelEx(&cfg, f, static_cast<P>(args)...);
 }
 

@@ -1,9 +1,8 @@
 // tt_sample.cu - drawing token IDs from rows of logits (include/toktier.h).
 //
 // Every sum is of whole numbers, so it is exact and any split of a row gives
-// the same ID.  A cluster of blocks holds a row in shared memory: it is read
-// once, and the passes over it (the maximum; the weights' sum; for rows that
-// need them, histograms) cost no memory traffic.
+// the same ID.  A cluster of blocks reads a row once and holds it in shared
+// memory (or L2, where it is larger); the passes over it cost instructions.
 //
 // What top-k and top-p keep is a prefix of the tokens in the order of their
 // weights.  Sorting a row for it would cost far more than reading it, and the
@@ -11,10 +10,12 @@
 // first: the row's maxima over 128 groups of threads are known from the first
 // pass, and the tokens at or above the q-th largest of them are at least q and
 // rarely twice as many.  If the prefix ends within the list (its count, or
-// its sum against the row's, says so), one block ranks the list by counting.
-// Else (a top-k above 96, a flat row) the end is found by histograms of the
-// weights' bits over the cluster, 16 bins an octave and then finer, until few
-// enough tokens share a bin to be ranked.
+// its sum against the row's, says so), one block sorts the list.  The other rows
+// (a top-k above 96, flat rows) are left to a second kernel: a histogram of
+// the weights' bits over the cluster, 64 bins an octave, says between which
+// bins the prefix ends, and the few tokens there are sorted; bins that hold too
+// many are divided further.  Two kernels, since the second one's registers,
+// shared memory and cluster size would slow the first down by half.
 #include <algorithm>
 
 #include "tt_ops.cuh"
@@ -27,16 +28,26 @@ typedef unsigned long long u64;
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int HELD = 74 * 1024;                   // bytes of a row a block holds: two blocks an SM
+constexpr int HELD = 96 * 1024;                   // bytes of a row a block holds, two blocks an SM,
+constexpr int HELD_BINS = 180 * 1024;             // and in the second kernel, one an SM
+constexpr int PENDING = -2, CLAIMED = -3;         // in the place of an ID that the second kernel writes
 constexpr int GROUPS = 128;                       // groups of threads a row's maxima are taken over
-constexpr int LIST = 512;                         // tokens one block ranks
+constexpr int LIST = THREADS;                     // tokens one block sorts
 constexpr int LONG_LIST = 1792;                   // tokens worth a list of their own for the later passes
-constexpr int BIN_LIST = 512;                     // tokens of a range that are ranked and not divided further
 constexpr int SHIFT = 17;                         // first histogram: 64 bins an octave
 constexpr int BINS = (40 << (23 - SHIFT)) + 1;    // weights 1 .. 2^40
 constexpr int FINER_BINS = 640;                   // of a range
 constexpr float ONE = 1099511627776.f;            // 2^40, the largest weight
 constexpr uint32_t KEY_ONE = 0x3F800000u;         // the bits of weight 1
+constexpr float LARGEST = 3.402823466e38f;
+constexpr float NEVER = 2.f;                      // above every power
+
+// the larger, or NaN if there is one
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 struct SampleArgs {
   int64_t n_vocab, stride;
@@ -47,18 +58,20 @@ struct SampleArgs {
   float *logprobs;
   int32_t *status;
   int cluster_log2, held;
+  int64_t n_rows;
 };
 
 // rint(e * 2^40) of an e in [0, 1]: whole above 2^23, below it rounded by the
-// addition
+// addition.  Its bits (the key) order weights.
 __device__ __forceinline__ float weight_of(float e) {
   const float x = e * ONE;
   return x >= 8388608.f ? x : (x + 8388608.f) - 8388608.f;
 }
+__device__ __forceinline__ uint32_t key_of(float e) { return __float_as_uint(weight_of(e)); }
 
-// The least e whose weight's bits are at least `key`: passes over a row compare
-// powers, which they have, and not weights, which cost four instructions more.
-// Below 2^23, half a unit under the weight; a tie goes to an even one.
+// The least e whose key is at least `key`: passes over a row compare powers,
+// which they have, and not weights, which cost four instructions more.  Below
+// 2^23, half a unit under the weight; a tie goes to an even one.
 __device__ __forceinline__ float least_power(uint32_t key) {
   const float w = ceilf(__uint_as_float(key));
   if (w > 8388608.f) return w * (1.f / ONE);
@@ -69,39 +82,56 @@ __device__ __forceinline__ float least_power(uint32_t key) {
 // A sum of rint(e * 2^40) without a conversion: adding 96 leaves e rounded to
 // 2^-17 in the low bits, and adding 1.5 * 2^-17 to what that cut off leaves the
 // rest, rounded to 2^-40.  Both counts stay below 2^31 for 256 terms.  Two
-// terms at a time.
+// terms at a time; the added constants' bits come off at the end.
 struct Sum {
-  int hi = 0, lo = 0;
+  uint32_t hi = 0, lo = 0;
   __device__ __forceinline__ void add2(float e0, float e1) {
-    float a0, a1, b0, b1;
+    uint32_t a0, a1, b0, b1;
     asm("{ .reg .b64 e, a, h, b, k; mov.b64 e, {%4, %5}; mov.b64 k, {%6, %6}; add.rn.f32x2 a, e, k;\n\t"
         "mov.b64 k, {%7, %7}; add.rn.f32x2 h, a, k; mov.b64 k, {%8, %8}; fma.rn.f32x2 b, h, k, e;\n\t"
         "mov.b64 k, {%9, %9}; add.rn.f32x2 b, b, k; mov.b64 {%0, %1}, a; mov.b64 {%2, %3}, b; }"
-        : "=f"(a0), "=f"(a1), "=f"(b0), "=f"(b1)
+        : "=r"(a0), "=r"(a1), "=r"(b0), "=r"(b1)
         : "f"(e0), "f"(e1), "f"(96.f), "f"(-96.f), "f"(-1.f), "f"(1.5f / 131072.f));
-    hi += __float_as_int(a0) - 0x42C00000;
-    hi += __float_as_int(a1) - 0x42C00000;
-    lo += __float_as_int(b0) - 0x37400000;
-    lo += __float_as_int(b1) - 0x37400000;
+    hi += a0 + a1;
+    lo += b0 + b1;
   }
-  __device__ __forceinline__ u64 value() const { return ((u64)hi << 23) + (u64)(long long)lo; }
+  template <int TERMS> __device__ __forceinline__ u64 value() const {
+    return ((u64)(hi - TERMS * 0x42C00000u) << 23) + (u64)(long long)(int)(lo - TERMS * 0x37400000u);
+  }
 };
 
 // the same of one term
 __device__ __forceinline__ u64 whole(float e) {
   Sum t;
   t.add2(e, 0.f);
-  return t.value();
+  return t.value<2>();
 }
+
+// A token in a list: its key above its complemented ID, so that larger means
+// earlier; or with the halves exchanged, for the order of IDs.
+__device__ __forceinline__ u64 list_key(uint32_t key, int j) { return (u64)key << 32 | (uint32_t)~j; }
+__device__ __forceinline__ int list_id(u64 k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ u64 key_whole(uint32_t key) { return whole(__uint_as_float(key) * (1.f / ONE)); }
+__device__ __forceinline__ u64 list_whole(u64 k) { return key_whole((uint32_t)(k >> 32)); }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
+// the sum of the lanes before this one
+__device__ __forceinline__ u64 sum_of_lanes_before(u64 v) {
+  const int lane = threadIdx.x & 31;
+  u64 x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
+}
 
-// floor or ceil of f * t, exactly, for an f in [0, 1]: 64-bit floats would
-// round, and are slow here (4 us for one product and its conversions)
+// floor or ceil of f * t, exactly, for an f in [0, 1]
 __device__ __forceinline__ u64 times(float f, u64 t, bool up) {
   if (f == 1.f) return t;
   const uint32_t b = __float_as_uint(f), e = max(b >> 23, 1u);
@@ -119,45 +149,45 @@ __device__ __forceinline__ u64 times(float f, u64 t, bool up) {
   return q + (up && cut ? 1 : 0);
 }
 
-template <int N> struct Most { static constexpr int value = N; };
-
 struct Shared {
   float4 all_max[GROUPS / 4];       // maxima over the row's groups
   float nth_max;
+  uint32_t lowest;                  // complement of an ID
+  int n_kept, n_list;
   u64 seg[WARPS];                   // sums over the warps' parts of the row
   u64 sums[8], list_sums[8];        // of the row's blocks, and of their lists
   int n_lists[8];
-  u64 total, least, draw;           // of a ranked list: the kept sum, top-p's share, the draw's place
-  u64 scan[WARPS], scan2[WARPS];
+  u64 total, least, draw;           // of a sorted list: the kept sum, top-p's share, the draw's place
+  u64 scan[WARPS];
+  u64 list[LIST];
+  u64 sorted[LIST];                 // the blocks' lists
+};
+
+struct SharedBins : Shared {
+  u64 scan2[WARPS];
   uint32_t scan_n[WARPS];
-  int n_list, n_long;
-  int index;                        // a token found in the row (the first block's counts)
+  int n_long;
   int bin[2];                       // the lowest and the highest bin where a prefix may end
   uint32_t bin_before, bin_to;      // tokens above the highest, and down to the lowest
   u64 cut_key, cut_sum;             // where a prefix ends, and its sum
-  u64 list[LIST];                   // bits of the weight << 32 | ~ID: larger first
+  uint32_t part_low[WARPS], part_high[WARPS];
   uint32_t red_n[BINS];             // a histogram over the row: counts
-  ulonglong2 few[BIN_LIST];         // a bin's tokens and their weights
-  uint32_t n_few, part_low[WARPS], part_high[WARPS];
   union {
     uint32_t counts[BINS];          // this block's
     struct {
       u64 red_sum[FINER_BINS];      // and sums
       uint32_t n[3 * FINER_BINS];   // this block's: counts and the sums of the mantissas' low and high bits
     };
-    ulonglong2 ranked[LIST];        // the blocks' lists: tokens and their weights
     u64 long_list[LONG_LIST];       // the block's tokens among which the prefix ends
   };
 };
 
-__device__ __forceinline__ u64 list_key(float w, int j) { return (u64)__float_as_uint(w) << 32 | (uint32_t)~j; }
-__device__ __forceinline__ u64 key_weight(u64 k) { return whole(__uint_as_float((uint32_t)(k >> 32)) * (1.f / ONE)); }
+extern __shared__ uint4 s_row[];              // the held part of the block's vectors
 
-// One row, as a block of its cluster sees it.
+// One row, as a thread of a block of its cluster sees it.
 template <class T> struct Row {
   static constexpr int E = RowParts<T>::E;
   const uint4 *body;
-  uint4 *s_row;
   int n, slab;                      // the block's vectors, and how many a warp takes
   int held, lo, hi;                 // the warp's
   int first;                        // index of the block's vector 0's first element
@@ -165,265 +195,539 @@ template <class T> struct Row {
   bool lone_first;                  // which comes before the vectors, or behind them
   float x_lone;
   float m, c;
-  bool infinite;                    // the maximum is +inf
+  bool odd, infinite;               // a NaN or +inf among the elements; +inf the largest
 
   __device__ __forceinline__ uint4 vec(int v) const { return v < held ? s_row[v] : __ldg(body + v); }
 
-  // 2^((l - M) c); 0 for NaN and -inf
+  // 2^((l - M) c); 0 for NaN and -inf.  With an infinite M, 1 for +inf alone
+  // (M and c are then the largest floats, so that its power is infinite).
+  __device__ __forceinline__ float mended(float e) const { return infinite ? (e == INF ? 1.f : 0.f) : e == e ? e : 0.f; }
   __device__ __forceinline__ void powers(const uint4 &r, float e[E]) const {
     vec_f32(r, e, T{});
-    if (infinite) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) e[i] = e[i] == INF ? 1.f : 0.f;
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
       const float2 z = sub_mul2(make_float2(e[i], e[i + 1]), m, c);
-      e[i] = ex2(fmaxf(z.x, -200.f));
-      e[i + 1] = ex2(fmaxf(z.y, -200.f));
+      e[i] = ex2(z.x);
+      e[i + 1] = ex2(z.y);
+    }
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) e[i] = mended(e[i]);
     }
   }
-  __device__ __forceinline__ float power(float l) const {
-    if (infinite) return l == INF ? 1.f : 0.f;
-    return ex2(fmaxf((l - m) * c, -200.f));
-  }
+  __device__ __forceinline__ float power(float l) const { return mended(ex2((l - m) * c)); }
   __device__ __forceinline__ int index(int v, int i) const { return first + v * E + i; }
+};
 
-  // f(e, index) of the warp's elements, lane by lane
-  template <class F> __device__ __forceinline__ void each(F f) const {
-    for (int v = lo + (threadIdx.x & 31); v < hi; v += 32) {
-      float e[E];
-      powers(vec(v), e);
-#pragma unroll
-      for (int i = 0; i < E; ++i) f(e[i], index(v, i));
-    }
-    if (lone >= 0) f(power(x_lone), lone);
+// What a pass does with powers in [from, to).
+enum Act { NOTHING, PUSH, PUSH_LONG, COUNT_BINS, SUM_BINS, LOWEST_ID, COUNT };
+// Which weights it adds: all (those below 1 are 0), or from `sum_from` on.
+enum Sums { NONE, ALL, FROM };
+
+struct Pass {
+  float sum_from;                   // adds the weights of powers from here on
+  float from, to;
+  uint32_t base;                    // of the bins' keys
+  int shift, bins;
+};
+
+template <int ACT, class S> __device__ __forceinline__ void act_on(S &s, const Pass &p, float e, int j, u64 &sum) {
+  if constexpr (ACT == COUNT_BINS) {
+    const uint32_t b = (key_of(e) - p.base) >> p.shift;       // (keys below the base come out above the bins)
+    if (e >= p.from && b < (uint32_t)p.bins) atomicAdd(&s.counts[b], 1u);
+    return;
   }
-
-  // the sum of the weights that keep(e, index) keeps, of this thread's elements
-  template <class F> __device__ __forceinline__ u64 sum_if(F keep) const {
-    u64 sum = 0;
-    for (int v = lo + (threadIdx.x & 31); v < hi; v += 32) {
-      float e[E];
-      powers(vec(v), e);
-      Sum t;
-#pragma unroll
-      for (int i = 0; i < E; i += 2)
-        t.add2(keep(e[i], index(v, i)) ? e[i] : 0.f, keep(e[i + 1], index(v, i + 1)) ? e[i + 1] : 0.f);
-      sum += t.value();
-    }
-    if (lone >= 0) {
-      const float e = power(x_lone);
-      if (keep(e, lone)) sum += whole(e);
-    }
-    return sum;
+  if (!(e >= p.from && e < p.to)) return;
+  if constexpr (ACT == PUSH) {
+    if (*(volatile int *)&s.n_list > LIST) return;            // too many already
+    const int n = atomicAdd(&s.n_list, 1);
+    if (n < LIST) s.list[n] = list_key(key_of(e), j);
+  } else if constexpr (ACT == PUSH_LONG) {
+    s.long_list[atomicAdd(&s.n_long, 1)] = list_key(key_of(e), j);
+  } else if constexpr (ACT == SUM_BINS) {
+    const uint32_t key = key_of(e), b = (key - p.base) >> p.shift, low = key & ((1u << p.shift) - 1);
+    atomicAdd(&s.n[b], 1u);
+    atomicAdd(&s.n[FINER_BINS + b], low & 1023u);
+    atomicAdd(&s.n[2 * FINER_BINS + b], low >> 10);
+  } else if constexpr (ACT == LOWEST_ID) {
+    sum = max(sum, (u64)(uint32_t)~j);
+  } else if constexpr (ACT == COUNT) {
+    ++sum;
   }
+}
 
-  // The first of the warp's elements, by index, at which the running sum of
-  // val(e, index) passes r (it does); its value in `own`.
-  template <class F> __device__ int find(F val, u64 r, u64 &own) const {
-    const int lane = threadIdx.x & 31;
-    u64 before = 0;
-    auto lone_step = [&](int &found) {
-      const u64 mine = lone >= 0 ? val(power(x_lone), lone) : 0;
-      return step(mine, before, r, found, own);
-    };
-    int found = -1;
-    const bool any_lone = __any_sync(~0u, lone >= 0), at_first = __any_sync(~0u, lone >= 0 && lone_first);
-    if (any_lone && at_first && lone_step(found)) {
-      own = __shfl_sync(~0u, own, found);
-      return __shfl_sync(~0u, lone, found);
-    }
-    for (int v0 = lo; v0 < hi; v0 += 32) {
-      const int v = v0 + lane;
-      u64 val8[E], mine = 0;
-      if (v < hi) {
-        float e[E];
-        powers(vec(v), e);
+// One pass over the warp's part of the row: this thread's sum (with COUNT a
+// count, with LOWEST_ID the complement of the lowest ID).
+template <int ACT, int SUM, class T, class S> __device__ __forceinline__ u64 pass(const Row<T> &x, S &s, const Pass p) {
+  constexpr int E = Row<T>::E;
+  u64 sum = 0;
+  int v = x.lo + (threadIdx.x & 31);
+  uint4 next = v < x.hi ? x.vec(v) : make_uint4(0, 0, 0, 0);  // (a vector ahead: it may come from L2)
+  for (; v < x.hi; v += 32) {
+    float e[E];
+    const uint4 now = next;
+    if (v + 32 < x.hi) next = x.vec(v + 32);
+    x.powers(now, e);
+    float top = e[0];
+    if (ACT != NOTHING || SUM == FROM) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) mine += val8[i] = val(e[i], index(v, i));
-      }
-      // the warp's sum in parts of 22 bits, each in one instruction
-      const u64 sum = (u64)__reduce_add_sync(~0u, (uint32_t)mine & 0x3FFFFFu) +
-                      ((u64)__reduce_add_sync(~0u, (uint32_t)(mine >> 22)) << 22);
-      if (before + sum <= r) {
-        before += sum;
+      for (int i = 1; i < E; ++i) top = fmaxf(top, e[i]);
+    }
+    if constexpr (ACT == COUNT_BINS) {
+      float least = e[0];
+#pragma unroll
+      for (int i = 1; i < E; ++i) least = fminf(least, e[i]);
+      if (least == top) {                                     // rows of one value would meet at one counter
+        const uint32_t b = (key_of(top) - p.base) >> p.shift;
+        if (top >= p.from && b < (uint32_t)p.bins) atomicAdd(&s.counts[b], (uint32_t)E);
         continue;
       }
-      // the lane whose vector passes r walks through it
-      const u64 start0 = start_of(mine, before);
-      step(mine, before, r, found, own);
-      int at = 0;
-      u64 w = 0, start = start0;
-      if (lane == found) {
-        bool past = false;
+    }
+    if (SUM == ALL || (SUM == FROM && top >= p.sum_from)) {
+      Sum t;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          start += val8[i];
-          if (!past && start > r) {
-            past = true;
-            at = index(v, i);
-            w = val8[i];
-          }
-        }
+      for (int i = 0; i < E; i += 2) {
+        if (SUM == ALL) t.add2(e[i], e[i + 1]);
+        else t.add2(e[i] >= p.sum_from ? e[i] : 0.f, e[i + 1] >= p.sum_from ? e[i + 1] : 0.f);
       }
-      own = __shfl_sync(~0u, w, found);
-      return __shfl_sync(~0u, at, found);
+      sum += t.template value<E>();
     }
-    if (any_lone && !at_first && lone_step(found)) {
-      own = __shfl_sync(~0u, own, found);
-      return __shfl_sync(~0u, lone, found);
-    }
-    return -1;
-  }
-  // sum of the lanes before this one, from `base`
-  static __device__ __forceinline__ u64 start_of(u64 mine, u64 base) {
-    u64 x = mine;
+    if (ACT != NOTHING && top >= p.from) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(~0u, x, o);
-      if ((threadIdx.x & 31) >= o) x += y;
+      for (int i = 0; i < E; ++i) act_on<ACT>(s, p, e[i], x.index(v, i), sum);
     }
-    return base + x - mine;
   }
-  // whether the running sum passes r at a lane; else it is carried on
-  static __device__ __forceinline__ bool step(u64 mine, u64 &before, u64 r, int &found, u64 &own) {
-    const u64 start = start_of(mine, before);
-    const uint32_t past = __ballot_sync(~0u, start + mine > r);
-    own = mine;
-    found = __ffs(past) - 1;
-    before = __shfl_sync(~0u, start + mine, 31);
-    return past != 0;
+  if (x.lone >= 0) {
+    const float e = x.power(x.x_lone);
+    if (SUM != NONE && e >= p.sum_from) sum += whole(e);
+    if (ACT != NOTHING) act_on<ACT>(s, p, e, x.lone, sum);
+  }
+  return sum;
+}
+
+// What is kept: powers from `above` on, and of those from `from` on the ones
+// not behind `end` in the list order.  With `count`, each of [from, above) is 1.
+struct Keep {
+  float from, above;
+  u64 end;
+  bool count;
+  __device__ __forceinline__ u64 value(float e, int j) const {
+    if (count) return e >= from && e < above;
+    return e >= above || (e >= from && list_key(key_of(e), j) >= end) ? whole(e) : 0;
   }
 };
 
-template <class T>
-__global__ void __launch_bounds__(THREADS, 2) k_sample(SampleArgs a, const T *__restrict__ logits) {
-  constexpr int E = RowParts<T>::E, U = 4;
-  extern __shared__ uint4 s_row[];
-  __shared__ Shared s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = 1 << a.cluster_log2, rank = C > 1 ? (int)cluster_rank() : 0;
-  const int64_t row = blockIdx.x >> a.cluster_log2;
-  const int V = (int)a.n_vocab;
-  auto sync_row = [&]() {
-    if (C > 1) cluster_sync(); else __syncthreads();
+// The first of the warp's elements, by index, at which the running sum of the
+// kept values passes r (it does); its value in `own`.
+template <class T> __device__ __forceinline__ int find(const Row<T> x, const Keep keep, u64 r, u64 &own) {
+  constexpr int E = Row<T>::E;
+  const int lane = threadIdx.x & 31;
+  const bool any_lone = __any_sync(~0u, x.lone >= 0), at_first = __any_sync(~0u, x.lone >= 0 && x.lone_first);
+  u64 before = 0;
+  // step -1: single elements ahead of the vectors; the last step: those behind
+  const int steps = (x.hi - x.lo + 31) / 32;
+  for (int i0 = any_lone && at_first ? -1 : 0; i0 < steps + (any_lone && !at_first ? 1 : 0); ++i0) {
+    const bool lones = i0 < 0 || i0 == steps;
+    const int v = x.lo + i0 * 32 + lane;
+    u64 val[E], mine = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) val[i] = 0;
+    if (lones) {
+      if (x.lone >= 0) mine = val[0] = keep.value(x.power(x.x_lone), x.lone);
+    } else if (v < x.hi) {
+      float e[E];
+      x.powers(x.vec(v), e);
+#pragma unroll
+      for (int i = 0; i < E; ++i) mine += val[i] = keep.value(e[i], x.index(v, i));
+    }
+    // the warp's sum in parts of 22 bits, each in one instruction
+    const u64 sum = (u64)__reduce_add_sync(~0u, (uint32_t)mine & 0x3FFFFFu) +
+                    ((u64)__reduce_add_sync(~0u, (uint32_t)(mine >> 22)) << 22);
+    if (before + sum <= r) {
+      before += sum;
+      continue;
+    }
+    // the lane whose elements pass r walks through them
+    u64 start = before + sum_of_lanes_before(mine);
+    const bool here = start <= r && r < start + mine;
+    int at = -1;
+    own = 0;
+    if (here) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        start += val[i];
+        if (at < 0 && start > r) {
+          at = lones ? x.lone : x.index(v, i);
+          own = val[i];
+        }
+      }
+    }
+    const int lane_of = __ffs(__ballot_sync(~0u, here)) - 1;
+    own = __shfl_sync(~0u, own, lane_of);
+    return __shfl_sync(~0u, at, lane_of);
+  }
+  return -1;
+}
+
+// The sum over the threads before this one.
+__device__ __forceinline__ u64 sum_before(Shared &s, u64 own) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 before = sum_of_lanes_before(own);
+  __syncthreads();
+  if (lane == 31) s.scan[warp] = before + own;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += s.scan[w];
+  return before;
+}
+
+// A falling sort of one value a thread; n of them, all different, are not 0 and
+// the first n threads'.  Up to half a block by counting what is above each, with
+// 2 to 8 threads a value; else a bitonic sort.
+__device__ __noinline__ u64 sort(Shared &s, u64 key, int n) {
+  const int tid = threadIdx.x;
+  if (n <= THREADS / 2) {
+    __syncthreads();
+    if (tid < n) s.sorted[tid] = key;
+    __syncthreads();
+    int log2 = 1;
+    while (log2 < 3 && (n << (log2 + 1)) <= THREADS) ++log2;
+    const int per = 1 << log2, i = tid >> log2;
+    const u64 own = i < n ? s.sorted[i] : 0;
+    int above = 0;
+    for (int o = tid & (per - 1); o < n; o += per) above += s.sorted[o] > own;
+    for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
+    __syncthreads();
+    if (i < n && (tid & (per - 1)) == 0) s.sorted[above] = own;
+    __syncthreads();
+    return tid < n ? s.sorted[tid] : 0;
+  }
+  for (int size = 2; size < 2 * n; size <<= 1)
+    for (int step = size >> 1; step; step >>= 1) {
+      u64 other;
+      if (step >= 32) {
+        __syncthreads();
+        s.sorted[tid] = key;
+        __syncthreads();
+        other = s.sorted[tid ^ step];
+      } else {
+        other = __shfl_xor_sync(~0u, key, step);
+      }
+      const bool larger = ((tid & step) == 0) == ((tid & size) == 0);
+      key = (key > other) == larger ? key : other;
+    }
+  return key;
+}
+
+// Where a prefix of `want` tokens, or with a sum of `want`, ends in the
+// histogram over the row, from the heaviest bin down.
+//   BY_COUNT  the bin where the count reaches it
+//   BY_SUM    the bin where the sum does
+//   BETWEEN   the bins between which the sum does, from counts alone: a bin's
+//             sum is its count times weights it bounds, added from above, or
+//             from below and taken from the row's sum
+enum Locate { BY_COUNT, BY_SUM, BETWEEN };
+
+__device__ __noinline__ void locate(SharedBins &s, Locate how, int bins, u64 want, uint32_t before_n, u64 above, u64 row_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (bins + THREADS - 1) / THREADS;
+  const int b0 = bins - 1 - tid * per, b1 = max(-1, b0 - per);      // this thread's, falling
+  auto sums = [&](int b, u64 &least, u64 &most) {
+    if (how == BY_COUNT) {
+      least = most = s.red_n[b];
+    } else if (how == BY_SUM) {
+      least = most = s.red_sum[b];
+    } else {
+      // a bin holds whole weights: from its base on, below the next one's
+      const uint32_t key = KEY_ONE + ((uint32_t)b << SHIFT);
+      const u64 low = key_whole(key), next = b == BINS - 1 ? low : max(low, key_whole(key + (1u << SHIFT)));
+      least = s.red_n[b] * low;
+      most = s.red_n[b] * next;
+    }
   };
-  auto at = [&](auto *p, int r) { return C > 1 ? of_block(p, r) : p; };
-  auto arrive = [&]() { if (C > 1) cluster_arrive(); };   // blocks stay until all have read from them
-  auto leave = [&]() { if (C > 1) cluster_wait(); };
+  uint32_t n = 0;
+  u64 low = 0, high = 0;
+  for (int b = b0; b > b1; --b) {
+    u64 l, h;
+    sums(b, l, h);
+    n += s.red_n[b];
+    low += l;
+    high += h;
+  }
+  uint32_t pn = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(~0u, pn, o);
+    if (lane >= o) pn += y;
+  }
+  u64 pl = sum_of_lanes_before(low), ph = sum_of_lanes_before(high);
+  __syncthreads();
+  if (lane == 31) {
+    s.scan_n[warp] = pn;
+    s.scan[warp] = pl + low;
+    s.scan2[warp] = ph + high;
+  }
+  __syncthreads();
+  pn = before_n + pn - n;
+  u64 all_l = 0, all_h = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) pn += s.scan_n[w], pl += s.scan[w], ph += s.scan2[w];
+    all_l += s.scan[w];
+    all_h += s.scan2[w];
+  }
+  if (how == BY_COUNT) pl = ph = pn;
+  if (how == BY_SUM) pl += above, ph += above;
+  const long long t = (long long)want;
+  // a sum is at least what is known from above, or the row's less what may be below; at most ...
+  auto at_least = [&](u64 l, u64 h) { return how == BETWEEN ? max((long long)l, (long long)(row_sum + h - all_h)) : (long long)l; };
+  auto at_most = [&](u64 l, u64 h) { return how == BETWEEN ? min((long long)h, (long long)(row_sum + l - all_l)) : (long long)h; };
+  for (int b = b0; b > b1; --b) {
+    u64 l, h;
+    sums(b, l, h);
+    if (at_most(pl, ph) < t && at_most(pl + l, ph + h) >= t) {
+      s.bin[1] = b;
+      s.bin_before = pn;
+    }
+    if (at_least(pl, ph) < t && at_least(pl + l, ph + h) >= t) {
+      s.bin[0] = b;
+      s.bin_to = pn + s.red_n[b];
+    }
+    pn += s.red_n[b];
+    pl += l;
+    ph += h;
+  }
+  __syncthreads();
+}
 
-  arrive();
-  const float u = a.uniform[row], temp = a.temperature ? a.temperature[row] : 1.f;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-
-  // ---- the row into shared memory, and the groups' maxima.  A warp takes
-  // consecutive vectors, so that warps and blocks lie in the order of the IDs.
+// A block of a row's cluster: what both kernels do first, and how blocks tell
+// each other sums.
+template <class T, class S> struct Block {
+  S &s;
+  const SampleArgs &a;
+  const int tid, lane, warp, C, rank;
   Row<T> x;
-  {
+  float u, temp, top_p, min_p;
+  int k;                            // 1 .. V
+  uint32_t least_key;               // min-p; and weight 0 is never drawn
+  float least_e, row_max;
+  u64 before_block;
+
+  __device__ __forceinline__ Block(S &s, const SampleArgs &a)
+      : s(s), a(a), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), C(1 << a.cluster_log2),
+        rank(a.cluster_log2 ? (int)cluster_rank() : 0) {}
+  __device__ __forceinline__ void arrive() const { if (C > 1) cluster_arrive(); }
+  __device__ __forceinline__ void leave() const { if (C > 1) cluster_wait(); }
+  __device__ __forceinline__ void sync_row() const {
+    if (C > 1) cluster_sync(); else __syncthreads();
+  }
+  template <class P> __device__ __forceinline__ P *at(P *p, int r) const { return C > 1 ? of_block(p, r) : p; }
+
+  // the row's parameters; whether they are what the header allows
+  __device__ __forceinline__ bool parameters(int64_t row) {
+    u = a.uniform[row];
+    temp = a.temperature ? a.temperature[row] : 1.f;
+    top_p = a.top_p ? a.top_p[row] : 1.f;
+    min_p = a.min_p ? a.min_p[row] : 0.f;
+    const int V = (int)a.n_vocab, top_k = a.top_k ? a.top_k[row] : 0;
+    k = temp == 0 ? 1 : top_k > 0 ? min(top_k, V) : V;
+    least_key = __float_as_uint(fmaxf(min_p * ONE, 1.f));
+    least_e = least_power(least_key);
+    return u >= 0 && u < 1 && temp >= 0 && temp < INF && top_p >= 0 && top_p <= 1 && min_p >= 0 && min_p <= 1;
+  }
+
+  // The row into shared memory, and its maxima over groups of threads.  A warp
+  // takes consecutive vectors, so that warps and blocks lie in the order of the
+  // IDs.  What blocks tell each other is written to all of them ahead of a
+  // barrier, so that nothing has to be fetched behind it.  Between begun() and
+  // sync_row(): the blocks have begun, and the last row's words are read.
+  template <class B> __device__ __forceinline__ void load(const T *__restrict__ logits, int64_t row, B begun) {
+    constexpr int E = RowParts<T>::E, U = 4;
+    const int V = (int)a.n_vocab;
     const T *l = logits + row * a.stride;
     const RowParts<T> part(l, V);
     const int each = (part.vecs + C - 1) >> a.cluster_log2, first = min(part.vecs, rank * each);
-    const int n = min(part.vecs - first, each), slab = (n + WARPS - 1) / WARPS;
+    x.n = min(part.vecs - first, each);
+    x.slab = (x.n + WARPS - 1) / WARPS;
     x.body = reinterpret_cast<const uint4 *>(l + part.lead) + first;
-    x.s_row = s_row;
     x.held = a.held;
-    x.n = n;
-    x.slab = slab;
     x.first = part.lead + first * E;
-    x.lo = min(n, warp * slab);
-    x.hi = min(n, x.lo + slab);
+    x.lo = min(x.n, warp * x.slab);
+    x.hi = min(x.n, x.lo + x.slab);
     x.lone_first = rank == 0 && warp == 0 && lane < part.lead;
     x.lone = x.lone_first ? lane : rank == C - 1 && warp == WARPS - 1 && lane < part.rest ? V - part.rest + lane : -1;
-    // (a thread has at most one: with both in one warp, C and WARPS would be 1)
     x.x_lone = x.lone >= 0 ? to_f32(l[x.lone]) : -INF;
-  }
-  float m = fmaxf(x.x_lone, -INF);
-  for (int v0 = x.lo + lane; v0 < x.hi; v0 += 32 * U) {
-    uint4 r[U];
+    float m = fmaxf(x.x_lone, -INF);
+    bool nan = x.x_lone != x.x_lone;
+    for (int v0 = x.lo + lane; v0 < x.hi; v0 += 32 * U) {
+      uint4 r[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (v0 + 32 * i < x.hi) r[i] = __ldg(x.body + v0 + 32 * i);
+      for (int i = 0; i < U; ++i)
+        if (v0 + 32 * i < x.hi) r[i] = __ldg(x.body + v0 + 32 * i);
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (v0 + 32 * i < x.hi) {
-        if (v0 + 32 * i < x.held) s_row[v0 + 32 * i] = r[i];
-        float v[E];
-        vec_f32(r[i], v, T{});
+      for (int i = 0; i < U; ++i)
+        if (v0 + 32 * i < x.hi) {
+          if (v0 + 32 * i < x.held) s_row[v0 + 32 * i] = r[i];
+          float v[E];
+          vec_f32(r[i], v, T{});
+          float top = v[0];
 #pragma unroll
-        for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
-      }
-  }
-  const int group_lanes = 4 * C;
-  for (int o = 1; o < group_lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  // What blocks tell each other is written to all of them ahead of a barrier,
-  // so that nothing has to be fetched behind it.
-  leave();                                                    // all blocks have begun
-  {
+          for (int j = 1; j < E; ++j) top = max_nan(top, v[j]);
+          if (top != top) {                       // a NaN: the others' maximum
+            nan = true;
+#pragma unroll
+            for (int j = 0; j < E; ++j) m = fmaxf(m, v[j]);
+          } else {
+            m = fmaxf(m, top);
+          }
+        }
+    }
+    const int group_lanes = 4 * C;
+    for (int o = 1; o < group_lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    begun();
     const float y = __shfl_sync(~0u, m, lane < 8 ? (lane >> a.cluster_log2) * group_lanes : 0);
     if (lane < 8)
       reinterpret_cast<float *>(at(s.all_max, lane & (C - 1)))[((rank * WARPS + warp) << (3 - a.cluster_log2)) +
                                                                (lane >> a.cluster_log2)] = y;
-  }
-  if (tid == 0) s.n_list = 0;
-  if (C < 8 && tid >= C && tid < 8) s.sums[tid] = s.list_sums[tid] = s.n_lists[tid] = 0;
-  sync_row();
-  static_assert(GROUPS == 128, "a float4 a lane");
-  const float4 four = s.all_max[lane];
-  m = warp_all(fmaxf(fmaxf(four.x, four.y), fmaxf(four.z, four.w)), OpMax());
-  const bool valid = u >= 0 && u < 1 && temp >= 0 && temp < INF && top_p >= 0 && top_p <= 1 && min_p >= 0 && min_p <= 1;
-  if (!valid || m == -INF) {
-    if (rank == 0 && tid == 0) {
-      a.ids[row] = -1;
-      if (a.logprobs) a.logprobs[row] = -INF;
-      if (!valid) op_status(a.status, TT_ERR_INVALID_ARG);
+    if (tid == 0) {
+      s.n_list = 0;
+      s.lowest = 0;
     }
-    return;
+    if (C < 8 && tid >= C && tid < 8) s.sums[tid] = s.list_sums[tid] = s.n_lists[tid] = 0;
+    sync_row();
+    static_assert(GROUPS == 128, "a float4 a lane");
+    const float4 four = s.all_max[lane];
+    m = warp_all(fmaxf(fmaxf(four.x, four.y), fmaxf(four.z, four.w)), OpMax());
+    row_max = m;
+    x.infinite = m == INF;
+    x.odd = nan || x.infinite;
+    x.m = fminf(m, LARGEST);
+    x.c = x.infinite ? LARGEST : fminf(1.44269504f / temp, LARGEST);
   }
-  x.m = m;
-  x.c = fminf(1.44269504f / temp, 3.402823466e38f);
-  x.infinite = m == INF;
-  const int k = temp == 0 ? 1 : top_k > 0 ? min(top_k, V) : V;
-  const float least_w = fmaxf(min_p * ONE, 1.f);              // min-p, and weight 0 is never drawn
-  const uint32_t least_key = __float_as_uint(least_w);
-  const float least_e = least_power(least_key);
-  auto write = [&](int id, u64 w, u64 total) {
+
+  __device__ __forceinline__ u64 share(u64 t) const { return max(times(top_p, t, true), 1ull); }
+  __device__ __forceinline__ u64 place(u64 t) const { return times(u, t, false); }
+  __device__ __forceinline__ void write(int64_t row, int id, u64 w, u64 total) const {
     a.ids[row] = id;
     if (a.logprobs) {
       // the smaller of the share and its complement, whole until then
       const u64 rest = total - w;
       a.logprobs[row] = rest < w ? log1pf(-__fdiv_rn((float)rest, (float)total)) : logf(__fdiv_rn((float)w, (float)total));
     }
+  }
+  __device__ __forceinline__ void block_totals() const {      // s.seg summed, for all blocks; by warp 0
+    if (warp == 0) {
+      const u64 t = warp_sum(lane < WARPS ? s.seg[lane] : 0);
+      if (lane < C) at(s.sums, lane)[rank] = t;
+    }
+  }
+  __device__ __forceinline__ void push_sums(u64 t) const {    // a sum over the row, known behind the next barrier
+    t = warp_sum(t);
+    if (lane == 0) s.seg[warp] = t;
+    __syncthreads();
+    block_totals();
+  }
+  // the row's sum, in every thread, and that of the blocks before this one
+  __device__ __forceinline__ u64 row_total() {
+    u64 t = before_block = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const u64 y = s.sums[r];
+      t += y;
+      before_block += r < rank ? y : 0;
+    }
+    return t;
+  }
+  // the blocks' lists, one token a thread in the first
+  __device__ __forceinline__ u64 gather(int &n) const {
+    u64 key = 0;
+    n = 0;
+    for (int r = 0; r < C; ++r) {
+      const int more = s.n_lists[r];
+      if (tid >= n && tid < n + more) key = at(s.list, r)[tid - n];
+      n += more;
+    }
+    return key;
+  }
+  // The draw among what is kept, whose sums by the warps' parts are in s.seg:
+  // that warp's vectors are divided among all warps, then a warp finds the
+  // element.  Called by the block that holds the drawn place r of the block.
+  __device__ __forceinline__ void draw(int64_t row, const Keep &keep, u64 r, u64 total) {
+    constexpr int E = RowParts<T>::E;
+    int part = 0;
+    while (r >= s.seg[part]) r -= s.seg[part++];
+    Row<T> y = x;
+    const int lo = min(x.n, part * x.slab), hi = min(x.n, lo + x.slab), each = (hi - lo + WARPS - 1) / WARPS;
+    y.lo = min(hi, lo + warp * each);
+    y.hi = min(hi, y.lo + each);
+    if (part != (x.lone_first ? 0 : WARPS - 1)) y.lone = -1;  // single elements stay with the first and the last
+    u64 sum = 0;
+    for (int v = y.lo + lane; v < y.hi; v += 32) {
+      float e[E];
+      y.powers(y.vec(v), e);
+#pragma unroll
+      for (int i = 0; i < E; ++i) sum += keep.value(e[i], y.index(v, i));
+    }
+    if (y.lone >= 0) sum += keep.value(y.power(y.x_lone), y.lone);
+    sum = warp_sum(sum);
+    __syncthreads();
+    if (lane == 0) s.seg[warp] = sum;
+    __syncthreads();
+    u64 before = 0;
+    for (int w = 0; w < warp; ++w) before += s.seg[w];
+    if (before <= r && r < before + sum) {
+      u64 own;
+      const int j = find(y, keep, r - before, own);
+      if (lane == 0) write(row, j, own, total);
+    }
+  }
+};
+
+template <class T>
+__global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const T *__restrict__ logits) {
+  __shared__ Shared s;
+  Block<T, Shared> b(s, a);
+  const int tid = b.tid, lane = b.lane, warp = b.warp, C = b.C, rank = b.rank, V = (int)a.n_vocab;
+  const int64_t row = blockIdx.x >> a.cluster_log2;
+  auto none = [&](int id) {                                   // for the second kernel, or nothing to draw
+    if (rank == 0 && tid == 0) {
+      a.ids[row] = id;
+      if (a.logprobs) a.logprobs[row] = -INF;
+    }
   };
+  let_next_start();
+  b.arrive();
+  const bool valid = b.parameters(row);
+  const int k = b.k;
+  const float top_p = b.top_p;
+  if (valid && k < V && k > GROUPS * 3 / 4) {                 // more than a list holds
+    none(PENDING);
+    b.leave();
+    return;
+  }
+  b.load(logits, row, [&]() { b.leave(); });
+  if (!valid || b.row_max == -INF) {
+    none(-1);
+    if (!valid && rank == 0 && tid == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+    return;
+  }
 
   // ---- the lowest ID of the largest weight
   if (k == 1) {
-    int best = INT32_MAX;
-    x.each([&](float e, int j) {
-      if (weight_of(e) == ONE) best = min(best, j);
-    });
-    best = __reduce_min_sync(~0u, best);
-    if (lane == 0) s.scan_n[warp] = best;
+    const u64 mine = pass<LOWEST_ID, NONE>(b.x, s, Pass{NEVER, least_power(__float_as_uint(ONE)), NEVER, 0, 0, 0});
+    const uint32_t warps = __reduce_max_sync(~0u, (uint32_t)mine);
+    if (lane == 0) atomicMax(&s.lowest, warps);
     __syncthreads();
-    if (warp == 0) {
-      best = __reduce_min_sync(~0u, lane < WARPS ? (int)s.scan_n[lane] : INT32_MAX);
-      if (lane == 0) at(s.n_lists, 0)[rank] = best;
-    }
-    sync_row();
+    if (tid == 0) b.at(s.n_lists, 0)[rank] = (int)s.lowest;
+    b.sync_row();
     if (rank == 0 && warp == 0) {
-      best = __reduce_min_sync(~0u, lane < C ? s.n_lists[lane] : INT32_MAX);
-      if (lane == 0) write(best, 1, 1);
+      const uint32_t rows = __reduce_max_sync(~0u, lane < C ? (uint32_t)s.n_lists[lane] : 0u);
+      if (lane == 0) b.write(row, (int)~rows, 1, 1);
     }
     return;
   }
 
-  // ---- sums, and the list of the heaviest tokens
+  // ---- the row's sum, and the list of its heaviest tokens
   const bool all = k == V && top_p == 1.f;                    // nothing but min-p cuts
-  const bool many = k < V && k > GROUPS * 3 / 4;              // more than the first list holds
-  float list_w = least_w;                                     // the list holds all weights from here on
-  if (!all && !many) {
+  uint32_t list_from = b.least_key;                           // the list holds all keys from here on
+  if (!all) {
     const int q = min(k, GROUPS * 3 / 4);
     // four threads count what is above a group's maximum, and what equals it
     const float own = reinterpret_cast<const float *>(s.all_max)[tid >> 2];
@@ -440,111 +744,25 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(SampleArgs a, const T *__
     from += __shfl_xor_sync(~0u, from, 2);
     if (above < q && q <= from) s.nth_max = own;              // the same value whoever writes it
     __syncthreads();
-    list_w = fmaxf(list_w, weight_of(x.power(s.nth_max)));
+    list_from = max(list_from, key_of(b.x.power(s.nth_max)));
   }
-  auto push = [&](float w, int j) {
-    const int n = atomicAdd(&s.n_list, 1);
-    if (n < LIST) s.list[n] = list_key(w, j);
-  };
-  auto block_totals = [&]() {                                 // s.seg summed, for all blocks; by warp 0
-    if (warp == 0) {
-      const u64 t = warp_sum(lane < WARPS ? s.seg[lane] : 0);
-      if (lane < C) at(s.sums, lane)[rank] = t;
+  const Pass p{b.least_e, all ? NEVER : least_power(list_from), INF, 0, 0, 0};
+  b.push_sums(b.least_key == KEY_ONE ? pass<PUSH, ALL>(b.x, s, p) : pass<PUSH, FROM>(b.x, s, p));
+  if (warp == 1 && !all) {
+    u64 l = 0;
+    const int n = s.n_list;
+    for (int i = lane; i < min(n, LIST); i += 32) l += list_whole(s.list[i]);
+    l = warp_sum(l);
+    if (lane < C) {
+      b.at(s.list_sums, lane)[rank] = l;
+      b.at(s.n_lists, lane)[rank] = n;
     }
-  };
-  auto push_sums = [&](u64 t) {                               // a sum over the row, known behind the next barrier
-    t = warp_sum(t);
-    if (lane == 0) s.seg[warp] = t;
-    __syncthreads();
-    block_totals();
-  };
-  if (!many) {
-    u64 sum = 0;
-    const float near_e = all ? 2.f : least_power(__float_as_uint(list_w));
-    if (min_p == 0.f) {
-      for (int v = x.lo + lane; v < x.hi; v += 32) {
-        float e[E];
-        x.powers(x.vec(v), e);
-        Sum t;
-        float top = e[0];
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          t.add2(e[i], e[i + 1]);
-          top = fmaxf(top, fmaxf(e[i], e[i + 1]));
-        }
-        sum += t.value();
-        if (top >= near_e) {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (e[i] >= near_e) push(weight_of(e[i]), x.index(v, i));
-        }
-      }
-      if (x.lone >= 0) {
-        const float e = x.power(x.x_lone);
-        sum += whole(e);
-        if (e >= near_e) push(weight_of(e), x.lone);
-      }
-    } else {
-      sum = x.sum_if([&](float e, int j) {
-        if (e >= near_e) push(weight_of(e), j);
-        return e >= least_e;
-      });
-    }
-    push_sums(sum);
-    if (warp == 1 && !all) {
-      u64 l = 0;
-      const int n = s.n_list;
-      for (int i = lane; i < min(n, LIST); i += 32) l += key_weight(s.list[i]);
-      l = warp_sum(l);
-      if (lane < C) {
-        at(s.list_sums, lane)[rank] = l;
-        at(s.n_lists, lane)[rank] = n;
-      }
-    }
-    sync_row();
   }
-
-  // ---- what the row's sums say
-  auto share = [&](u64 t) { return max(times(top_p, t, true), 1ull); };
-  auto place = [&](u64 t) { return times(u, t, false); };
-  // of the row's blocks, in every thread: their sum, and that of the ones before this
-  auto row_total = [&](u64 &before) {
-    u64 t = before = 0;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const u64 y = s.sums[r];
-      t += y;
-      before += r < rank ? y : 0;
-    }
-    return t;
-  };
-  u64 before_block = 0, total = many ? 0 : row_total(before_block);
-
-  // ---- the draw among all elements: the block, the warp, the element
-  auto draw_row = [&](auto keep) {
-    const u64 r = place(total);
-    u64 before = before_block;
-    if (r < before || r >= before + s.sums[rank]) return;
-    int part = 0;
-    while (r >= before + s.seg[part]) before += s.seg[part++];
-    // that warp's vectors, divided among all warps
-    const int lo = min(x.n, part * x.slab), hi = min(x.n, lo + x.slab), each = (hi - lo + WARPS - 1) / WARPS;
-    x.lo = min(hi, lo + warp * each);
-    x.hi = min(hi, x.lo + each);
-    if (part != (x.lone_first ? 0 : WARPS - 1)) x.lone = -1;  // single elements stay with the first and the last
-    const u64 sum = warp_sum(x.sum_if(keep));
-    __syncthreads();
-    if (lane == 0) s.seg[warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before += s.seg[w];
-    if (before <= r && r < before + sum) {
-      u64 own;
-      const int j = x.find([&](float e, int i) { return keep(e, i) ? whole(e) : 0ull; }, r - before, own);
-      if (lane == 0) write(j, own, total);
-    }
-  };
+  b.sync_row();
+  const u64 total = b.row_total();
   if (all) {
-    draw_row([&](float e, int) { return e >= least_e; });
+    const u64 r = b.place(total) - b.before_block;
+    if (r < s.sums[rank]) b.draw(row, Keep{b.least_e, b.least_e, 0, false}, r, total);
     return;
   }
   u64 list_sum = 0;
@@ -555,481 +773,354 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(SampleArgs a, const T *__
     n_list += s.n_lists[r];
   }
 
-  // the blocks' lists side by side in the first, a warp a block; the others have gone on
-  auto gather = [&](ulonglong2 *into) {
-    int to = 0;
-    for (int r = 0; r < C; ++r) {
-      const int n = s.n_lists[r];
-      if (warp == r)
-        for (int i = lane; i < n; i += 32) {
-          const u64 key = at(s.list, r)[i];
-          into[to + i] = make_ulonglong2(key, key_weight(key));
-        }
-      to += n;
-    }
-    return to;
-  };
-
-  // ---- the prefix ends within the list: one block ranks it
-  const bool all_listed = list_w == least_w;                  // the list is all there is
-  if (!many && n_list <= LIST && (all_listed || (k < V ? k <= n_list : share(total) <= list_sum))) {
-    if (rank != 0) {
-      arrive();
-      leave();
-      return;
-    }
-    const int n = gather(s.ranked), kept_n = min(k, n);
-    arrive();
-    __syncthreads();
-    // the rank of each token and the sum before it; 1, 2, 4 or 8 threads a token
-    int per_log2 = 0;
-    while (per_log2 < 3 && (n << (per_log2 + 1)) <= THREADS) ++per_log2;
-    const int per = 1 << per_log2, i = tid >> per_log2, part = tid & (per - 1);
-    const ulonglong2 own = i < n ? s.ranked[i] : make_ulonglong2(0, 0);
-    int before_n = 0;
-    u64 before = 0;
-    for (int o = part; o < n; o += per) {
-      const ulonglong2 y = s.ranked[o];
-      if (y.x > own.x) {
-        ++before_n;
-        before += y.y;
-      }
-    }
-    for (int o = 1; o < per; o <<= 1) {
-      before_n += __shfl_xor_sync(~0u, before_n, o);
-      before += __shfl_xor_sync(~0u, before, o);
-    }
-    const bool one = part == 0 && i < n;
-    if (k < V) {                                              // top-k's sum, then what top-p leaves of it
-      if (one && before_n == kept_n - 1) s.least = top_p < 1.f ? share(before + own.y) : before + own.y;
-      __syncthreads();
-    }
-    const u64 least = top_p < 1.f ? (k < V ? s.least : share(total)) : ~0ull;
-    const bool keep = before_n < kept_n && before < least;
-    if (one && keep) {
-      s.list[before_n] = own.x;                               // in their order
-      if (before_n == kept_n - 1 || before + own.y >= least) {
-        s.index = before_n + 1;
-        s.total = before + own.y;
-        s.draw = place(before + own.y);
-      }
-    }
-    __syncthreads();
-    const int n_kept = s.index;
-    u64 low = 0;                                              // kept weights of lower IDs
-    if (i < n && keep)
-      for (int o = part; o < n_kept; o += per) {
-        const u64 y = s.list[o];
-        if ((uint32_t)y > (uint32_t)own.x) low += key_weight(y);
-      }
-    for (int o = 1; o < per; o <<= 1) low += __shfl_xor_sync(~0u, low, o);
-    if (one && keep && low <= s.draw && s.draw < low + own.y) write((int)~(uint32_t)own.x, own.y, s.total);
-    leave();
+  // ---- if the prefix ends within the list, one block sorts it
+  const bool all_listed = list_from == b.least_key;           // the list is all there is
+  const bool ends = n_list <= LIST && (all_listed || (k < V ? k <= n_list : b.share(total) <= list_sum));
+  if (!ends) none(PENDING);
+  if (!ends || rank != 0) {
+    b.arrive();
+    b.leave();
     return;
   }
-
-  // ---- the prefix's end by histograms of the weights' bits
-  auto key_of = [&](float e) { return __float_as_uint(weight_of(e)); };
-  auto key_whole = [&](uint32_t key) { return key_weight((u64)key << 32); };
-  uint32_t hist_base = 0;
-  int hist_shift = -1;
-  // counts of the keys from `base` on, in bins of 2^shift
-  auto count_bins = [&](uint32_t base, int shift, int bins) {
-    hist_base = base;
-    hist_shift = shift;
-    for (int b = tid; b < bins; b += THREADS) s.counts[b] = 0;
+  int n;
+  u64 key = b.gather(n);
+  b.arrive();
+  const int kept_n = min(k, n);
+  key = sort(s, key, n);
+  u64 w = list_whole(key), before = sum_before(s, w);
+  if (k < V) {                                                // top-k's sum, then what top-p leaves of it
+    if (tid == kept_n - 1) s.least = top_p < 1.f ? b.share(before + w) : before + w;
     __syncthreads();
-    x.each([&](float e, int) {
-      const uint32_t b = (key_of(e) - base) >> shift;         // (keys below the base come out above the bins)
-      if (e >= least_e && b < (uint32_t)bins) atomicAdd(&s.counts[b], 1u);
-    });
-    sync_row();
+  }
+  const u64 least = top_p < 1.f ? (k < V ? s.least : b.share(total)) : ~0ull;
+  const bool keep = tid < kept_n && before < least;
+  if (keep && (tid == kept_n - 1 || before + w >= least)) {
+    s.n_kept = tid + 1;
+    s.total = before + w;
+    s.draw = b.place(before + w);
+  }
+  __syncthreads();
+  key = sort(s, keep ? key << 32 | key >> 32 : 0, s.n_kept);  // by ID
+  w = key_whole((uint32_t)key);
+  before = sum_before(s, w);
+  if (before <= s.draw && s.draw < before + w) b.write(row, (int)~(uint32_t)(key >> 32), w, s.total);
+  b.leave();
+}
+
+// One row that the list could not do: all blocks of the cluster.
+template <class T>
+__device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const SampleArgs &a, int64_t row) {
+  constexpr int E = RowParts<T>::E;
+  SharedBins &s = b.s;
+  const int tid = b.tid, lane = b.lane, warp = b.warp, C = b.C, rank = b.rank, V = (int)a.n_vocab, k = b.k;
+  const float top_p = b.top_p;
+  u64 end_key = 0, total = 0;                                 // keeps everything
+  bool listed = false;                                        // s.long_list holds what may be kept
+  bool parts_known = false;                                   // s.seg has the sums of what lies above s.list
+  // ---- the prefix's end by histograms of the weights' bits
+  int hist = 0;                                             // 1: s.red_n holds the first histogram
+  auto add_bins = [&](int bins, bool sums, uint32_t base, int shift) {
     // each block adds up its share of the bins over the row
     const int share_bins = (bins + C - 1) >> a.cluster_log2;
-    for (int i = tid; i < share_bins; i += THREADS) {
-      const int b = rank * share_bins + i;
-      if (b < bins) {
-        uint32_t n = 0;
+    for (int i = rank * share_bins + tid; i < min(bins, (rank + 1) * share_bins); i += THREADS) {
+      u64 n = 0, low = 0;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < C) n += at(s.counts, r)[b];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < C) at(s.red_n, r)[b] = n;
-      }
-    }
-    sync_row();
-  };
-  // The same with the bins' sums (a mantissa's low and high bits counted
-  // apart), and the sum of what lies above the bins.
-  auto sum_bins = [&](uint32_t base, int shift, int bins) {
-    hist_shift = -1;
-    for (int b = tid; b < 3 * FINER_BINS; b += THREADS) s.n[b] = 0;
-    __syncthreads();
-    const float from_e = fmaxf(least_e, least_power(base)), above_e = fmaxf(least_e, least_power(base + ((uint32_t)bins << shift)));
-    const u64 above = x.sum_if([&](float e, int) {
-      if (e >= from_e && e < above_e) {
-        const uint32_t key = key_of(e), b = (key - base) >> shift, low = key & ((1u << shift) - 1);
-        atomicAdd(&s.n[b], 1u);
-        atomicAdd(&s.n[FINER_BINS + b], low & 1023u);
-        atomicAdd(&s.n[2 * FINER_BINS + b], low >> 10);
-      }
-      return e >= above_e;
-    });
-    push_sums(above);
-    sync_row();
-    const int share_bins = (bins + C - 1) >> a.cluster_log2;
-    for (int i = tid; i < share_bins; i += THREADS) {
-      const int b = rank * share_bins + i;
-      if (b < bins) {
-        u64 n = 0, low = 0;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < C) {
-            n += at(s.n, r)[b];
-            low += at(s.n, r)[FINER_BINS + b] + ((u64)at(s.n, r)[2 * FINER_BINS + b] << 10);
-          }
-        // weights are mantissa << (exponent - 23); whole, so nothing is lost
-        const uint32_t key = base + ((uint32_t)b << shift);
-        const int ex = (int)(key >> 23) - 150;
-        const u64 mant = n * ((key & 0x7FFFFFu) | 0x800000u) + low, w = ex >= 0 ? mant << ex : mant >> -ex;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < C) {
-            at(s.red_n, r)[b] = (uint32_t)n;
-            at(s.red_sum, r)[b] = w;
-          }
-      }
-    }
-    sync_row();
-  };
-  // From the heaviest bin down, f(bin, count, count before, sum, sum before) of
-  // this thread's bins; what goes into the sums, val(bin, which) for two sums.
-  auto scan_bins = [&](auto most, int bins, auto val, auto f) {
-    constexpr int PER = (decltype(most)::value + THREADS - 1) / THREADS;
-    uint32_t n[PER], own_n = 0;
-    u64 w[PER][2], own_w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = bins - 1 - (tid * PER + i);
-      n[i] = b >= 0 ? s.red_n[b] : 0;
-      own_n += n[i];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) own_w[c] += w[i][c] = b >= 0 ? val(b, c) : 0;
-    }
-    uint32_t pn = own_n;
-    u64 pw[2] = {own_w[0], own_w[1]};
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t yn = __shfl_up_sync(~0u, pn, o);
-      const u64 y0 = __shfl_up_sync(~0u, pw[0], o), y1 = __shfl_up_sync(~0u, pw[1], o);
-      if (lane >= o) pn += yn, pw[0] += y0, pw[1] += y1;
-    }
-    __syncthreads();
-    if (lane == 31) s.scan_n[warp] = pn, s.scan[warp] = pw[0], s.scan2[warp] = pw[1];
-    __syncthreads();
-    pn -= own_n;
-    pw[0] -= own_w[0];
-    pw[1] -= own_w[1];
-    u64 all_w[2] = {0, 0};
-    for (int i = 0; i < WARPS; ++i) {
-      if (i < warp) pn += s.scan_n[i], pw[0] += s.scan[i], pw[1] += s.scan2[i];
-      all_w[0] += s.scan[i];
-      all_w[1] += s.scan2[i];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = bins - 1 - (tid * PER + i);
-      if (b >= 0) f(b, n[i], pn, w[i], pw, all_w);
-      pn += n[i];
-      pw[0] += w[i][0];
-      pw[1] += w[i][1];
-    }
-    __syncthreads();
-  };
-  // In the first histogram, the bin where the count reaches `want`; or the bins
-  // between which the sum does: a bin's sum is its count times weights it
-  // bounds, added from above, or from below and taken from the row's sum.
-  u64 row_sum = total;
-  auto first_bins = [&](bool by_n, u64 want) {
-    if (hist_base != KEY_ONE || hist_shift != SHIFT) count_bins(KEY_ONE, SHIFT, BINS);
-    if (by_n) {
-      scan_bins(Most<BINS>{}, BINS, [](int, int) { return 0ull; }, [&](int b, uint32_t n, uint32_t pn, const u64 *, const u64 *, const u64 *) {
-        if (pn < want && pn + n >= want) {
-          s.bin[0] = s.bin[1] = b;
-          s.bin_before = pn;
-          s.bin_to = pn + n;
+      for (int r = 0; r < 8; ++r)
+        if (r < C) {
+          n += sums ? b.at(s.n, r)[i] : b.at(s.counts, r)[i];
+          if (sums) low += b.at(s.n, r)[FINER_BINS + i] + ((u64)b.at(s.n, r)[2 * FINER_BINS + i] << 10);
         }
-      });
-    } else {
-      scan_bins(
-          Most<BINS>{}, BINS,
-          [&](int b, int c) {
-            // a bin holds weights of whole numbers: from its base on, below the next one's
-            const uint32_t key = KEY_ONE + ((uint32_t)b << SHIFT);
-            const u64 low = key_whole(key), next = key_whole(key + (1u << SHIFT));
-            return s.red_n[b] * (c == 0 ? low : b == BINS - 1 ? low : max(low, next));
-          },
-          [&](int b, uint32_t n, uint32_t pn, const u64 *w, const u64 *pw, const u64 *all_w) {
-            auto least_sum = [&](u64 l, u64 h) { return max((long long)l, (long long)(row_sum + h - all_w[1])); };
-            auto most_sum = [&](u64 l, u64 h) { return min((long long)h, (long long)(row_sum + l - all_w[0])); };
-            const long long t = (long long)want;
-            if (most_sum(pw[0], pw[1]) < t && most_sum(pw[0] + w[0], pw[1] + w[1]) >= t) {
-              s.bin[1] = b;
-              s.bin_before = pn;
-            }
-            if (least_sum(pw[0], pw[1]) < t && least_sum(pw[0] + w[0], pw[1] + w[1]) >= t) {
-              s.bin[0] = b;
-              s.bin_to = pn + n;
-            }
-          });
+      // weights are mantissa << (exponent - 23); whole, so nothing is lost
+      const uint32_t key = base + ((uint32_t)i << shift);
+      const int ex = (int)(key >> 23) - 150;
+      const u64 mant = n * ((key & 0x7FFFFFu) | 0x800000u) + low, w = ex >= 0 ? mant << ex : mant >> -ex;
+      for (int r = 0; r < C; ++r) {
+        b.at(s.red_n, r)[i] = (uint32_t)n;
+        if (sums) b.at(s.red_sum, r)[i] = w;
+      }
     }
+    b.sync_row();
   };
-
-  // A row's heaviest tokens, from a key on, as lists of the blocks' own: the
-  // later passes go over these where they are few.
-  bool listed = false;
-  auto make_list = [&](uint32_t least_in) {
+  auto count_bins = [&](uint32_t base, int shift, int bins) {
+    for (int i = tid; i < bins; i += THREADS) s.counts[i] = 0;
+    __syncthreads();
+    pass<COUNT_BINS, NONE>(b.x, s, Pass{NEVER, b.least_e, INF, base, shift, bins});
+    b.sync_row();
+    add_bins(bins, false, base, shift);
+  };
+  auto first_bins = [&](Locate how, u64 want, u64 row_sum) {
+    if (!hist) count_bins(KEY_ONE, SHIFT, BINS);
+    hist = 1;
+    locate(s, how, BINS, want, 0, 0, row_sum);
+  };
+  // a list of its own for what the prefix ends in, where that is short
+  auto list_if_few = [&]() {
+    if (s.bin_to > LONG_LIST) return;
+    const uint32_t from = max(b.least_key, KEY_ONE + ((uint32_t)s.bin[0] << SHIFT));
     if (tid == 0) s.n_long = 0;
     __syncthreads();
-    const float from_e = least_power(least_in);
-    x.each([&](float e, int j) {
-      if (e >= from_e) s.long_list[atomicAdd(&s.n_long, 1)] = list_key(weight_of(e), j);
-    });
+    pass<PUSH_LONG, NONE>(b.x, s, Pass{NEVER, least_power(from), INF, 0, 0, 0});
     __syncthreads();
     listed = true;
   };
-  // the sum of the weights that f(power, ID) keeps, of this thread's share of the block
-  auto sum_keys = [&](auto f) {
-    if (!listed) return x.sum_if(f);
-    u64 sum = 0;
-    for (int i = tid; i < s.n_long; i += THREADS) {
-      const u64 key = s.long_list[i];
-      const float e = __uint_as_float((uint32_t)(key >> 32)) * (1.f / ONE);
-      if (f(e, (int)~(uint32_t)key)) sum += whole(e);
-    }
-    return sum;
-  };
-
-  // the last token (as a list key) of the shortest prefix with `want` tokens
-  // (by_n) or a sum of `want`, and the prefix's sum; behind first_bins
-  bool parts_known = false;                                   // s.seg has the sums of what lies above s.list
-  auto prefix_end = [&](bool by_n, u64 want, u64 &end_key, u64 &prefix_sum) {
+  // The last token (as a list key) of the shortest prefix with `want` tokens
+  // (by_n) or a sum of `want`, and the prefix's sum; behind first_bins.
+  auto prefix_end = [&](bool by_n, u64 want) {
     parts_known = false;
-    uint32_t base = KEY_ONE, before_n = 0;
-    int shift = SHIFT;
-    uint32_t end = base + ((uint32_t)(s.bin[1] + 1) << shift);
-    base += (uint32_t)s.bin[0] << shift;
-    uint32_t n_range = s.bin_to - s.bin_before;
-    if (by_n) before_n = s.bin_before;
+    uint32_t base = KEY_ONE + ((uint32_t)s.bin[0] << SHIFT), end = KEY_ONE + ((uint32_t)(s.bin[1] + 1) << SHIFT);
+    uint32_t before_n = s.bin_before, n_range = s.bin_to - s.bin_before;
     for (;;) {
+      const float from_e = fmaxf(b.least_e, least_power(base)), above_e = fmaxf(b.least_e, least_power(end));
       __syncthreads();
-      if (n_range <= BIN_LIST) {
-        // the tokens that are left, ranked in the first block
+      if (n_range <= LIST) {
+        // the tokens that are left, sorted in the first block
         if (tid == 0) s.n_list = 0;
         __syncthreads();
-        const float from_e = fmaxf(least_e, least_power(base)), above_e = fmaxf(least_e, least_power(end));
-        const u64 above = sum_keys([&](float e, int j) {
-          if (e >= from_e && e < above_e) push(weight_of(e), j);
-          return e >= above_e;
-        });
-        push_sums(above);
-        if (tid == 0) at(s.n_lists, 0)[rank] = s.n_list;
-        sync_row();
-        if (rank == 0) {
-          const int n = gather(s.few), two = n <= THREADS / 2, i = tid >> two;
-          u64 unused;
-          const u64 before_sum = row_total(unused);
-          __syncthreads();
-          const ulonglong2 own = i < n ? s.few[i] : make_ulonglong2(0, 0);
-          u64 rank_n = 0, sum_to = 0;
-          for (int o = tid & two; o < n; o += 1 + two) {
-            const ulonglong2 y = s.few[o];
-            if (y.x >= own.x) {
-              ++rank_n;
-              sum_to += y.y;
-            }
+        u64 above = 0;
+        if (listed) {
+          for (int i = tid; i < s.n_long; i += THREADS) {
+            const u64 key = s.long_list[i];
+            const float e = __uint_as_float((uint32_t)(key >> 32)) * (1.f / ONE);
+            if (e >= above_e) above += whole(e);
+            else if (e >= from_e) s.list[atomicAdd(&s.n_list, 1)] = key;
           }
-          if (two) {
-            rank_n += __shfl_xor_sync(~0u, rank_n, 1);
-            sum_to += __shfl_xor_sync(~0u, sum_to, 1);
-          }
-          rank_n += before_n;
-          sum_to += before_sum;
-          if ((tid & two) == 0 && i < n && (by_n ? rank_n == want : sum_to >= want && sum_to - own.y < want)) {
-            for (int r = 0; r < C; ++r) {
-              *at(&s.cut_key, r) = own.x;
-              *at(&s.cut_sum, r) = sum_to;
-            }
-          }
+        } else {
+          above = pass<PUSH, FROM>(b.x, s, Pass{above_e, from_e, above_e, 0, 0, 0});
         }
-        sync_row();
+        b.push_sums(above);
+        if (tid == 0) b.at(s.n_lists, 0)[rank] = s.n_list;
+        b.sync_row();
+        if (rank == 0) {
+          int n;
+          u64 key = b.gather(n);
+          key = sort(s, key, n);
+          const u64 w = list_whole(key), before = sum_before(s, w) + b.row_total();
+          if (tid < n && (by_n ? before_n + tid + 1 == want : before < want && before + w >= want))
+            for (int r = 0; r < C; ++r) {
+              *b.at(&s.cut_key, r) = key;
+              *b.at(&s.cut_sum, r) = before + w;
+            }
+        }
+        b.sync_row();
         end_key = s.cut_key;
-        prefix_sum = s.cut_sum;
+        total = s.cut_sum;
         parts_known = true;
         return;
       }
       if (end - base == 1) {
         // tokens of one weight: the prefix ends at one of them by its place
         const u64 w = key_whole(base);
-        const float own_e = least_power(base), above_e = least_power(base + 1);
-        push_sums(x.sum_if([&](float e, int) { return e >= above_e; }));
-        sync_row();
-        u64 before;
-        const u64 above = row_total(before), some = by_n ? want - before_n : (want - above + w - 1) / w;
-        prefix_sum = above + some * w;
-        u64 c = 0;
-        x.each([&](float e, int) { c += e >= own_e && e < above_e; });
-        sync_row();                                           // (the sums are read)
-        push_sums(c);
-        sync_row();
-        row_total(before);
+        b.push_sums(pass<NOTHING, FROM>(b.x, s, Pass{above_e, NEVER, NEVER, 0, 0, 0}));
+        b.sync_row();
+        const u64 above = b.row_total(), some = by_n ? want - before_n : (want - above + w - 1) / w;
+        total = above + some * w;
+        b.sync_row();                                         // (the sums are read)
+        b.push_sums(pass<COUNT, NONE>(b.x, s, Pass{NEVER, from_e, above_e, 0, 0, 0}));
+        b.sync_row();
+        b.row_total();
+        u64 before = b.before_block;
         if (before < some && some <= before + s.sums[rank]) {
           for (int i = 0; i < warp; ++i) before += s.seg[i];
           if (before < some && some <= before + s.seg[warp]) {
             u64 own;
-            const int j = x.find([&](float e, int) { return e >= own_e && e < above_e ? 1ull : 0ull; }, some - 1 - before, own);
-            if (lane < C) *at(&s.cut_key, lane) = list_key(__uint_as_float(base), j);
+            const int j = find(b.x, Keep{from_e, above_e, 0, true}, some - 1 - before, own);
+            if (lane < C) *b.at(&s.cut_key, lane) = list_key(base, j);
           }
         }
-        sync_row();
+        b.sync_row();
         end_key = s.cut_key;
         return;
       }
       // finer bins of what is left, as many as fit; none spans an octave
-      listed = false;                                         // (they lie over the list)
-      for (shift = 0; (end - (base >> shift << shift) + (1u << shift) - 1) >> shift > FINER_BINS;) ++shift;
+      listed = false;                                       // (they lie over the list)
+      hist = 0;
+      int shift = 0;
+      while ((end - (base >> shift << shift) + (1u << shift) - 1) >> shift > FINER_BINS) ++shift;
       base = base >> shift << shift;
       const int bins = (int)((end - base + (1u << shift) - 1) >> shift);
       if (by_n) {
         count_bins(base, shift, bins);
-        const uint32_t from = before_n;
-        scan_bins(Most<FINER_BINS>{}, bins, [](int, int) { return 0ull; }, [&](int b, uint32_t n, uint32_t pn, const u64 *, const u64 *, const u64 *) {
-          pn += from;
-          if (pn < want && pn + n >= want) {
-            s.bin[0] = b;
-            s.bin_before = pn;
-          }
-        });
+        locate(s, BY_COUNT, bins, want, before_n, 0, 0);
         before_n = s.bin_before;
       } else {
-        sum_bins(base, shift, bins);
-        u64 unused;
-        const u64 above = row_total(unused);
-        scan_bins(Most<FINER_BINS>{}, bins, [&](int b, int c) { return c == 0 ? s.red_sum[b] : 0; },
-                  [&](int b, uint32_t, uint32_t, const u64 *w, const u64 *pw, const u64 *) {
-                    if (above + pw[0] < want && above + pw[0] + w[0] >= want) s.bin[0] = b;
-                  });
+        for (int i = tid; i < 3 * FINER_BINS; i += THREADS) s.n[i] = 0;
+        __syncthreads();
+        const float bins_e = fmaxf(b.least_e, least_power(base + ((uint32_t)bins << shift)));
+        b.push_sums(pass<SUM_BINS, FROM>(b.x, s, Pass{bins_e, fmaxf(b.least_e, least_power(base)), bins_e, base, shift, bins}));
+        b.sync_row();
+        add_bins(bins, true, base, shift);
+        locate(s, BY_SUM, bins, want, 0, b.row_total(), 0);
       }
       n_range = s.red_n[s.bin[0]];
       base += (uint32_t)s.bin[0] << shift;
       end = base + (1u << shift);
     }
   };
-  u64 end_key = 0;                                            // keeps everything
-  auto list_if_few = [&]() {
-    const uint32_t n = s.bin_to, from = KEY_ONE + ((uint32_t)s.bin[0] << SHIFT);
-    if (n <= LONG_LIST) make_list(max(least_key, from));
-  };
-  if (k < V) {
+  u64 row_sum = 0;
+  if (k == V) {
+    b.push_sums(pass<NOTHING, FROM>(b.x, s, Pass{b.least_e, NEVER, NEVER, 0, 0, 0}));
+    b.sync_row();
+    row_sum = total = b.row_total();
+    b.sync_row();
+  } else {
     // fewer than k tokens may be left by min-p
     count_bins(KEY_ONE, SHIFT, BINS);
+    hist = 1;
     uint32_t n = 0;
-    for (int b = tid; b < BINS; b += THREADS) n += s.red_n[b];
+    for (int i = tid; i < BINS; i += THREADS) n += s.red_n[i];
     n = block_all(n, OpSum(), s.scan_n);
     const bool cuts = n > (uint32_t)k;
-    if (many && (!cuts || top_p < 1.f)) {
-      push_sums(x.sum_if([&](float e, int) { return e >= least_e; }));
-      sync_row();
-      row_sum = total = row_total(before_block);
-      sync_row();
+    if (!cuts || top_p < 1.f) {
+      b.push_sums(pass<NOTHING, FROM>(b.x, s, Pass{b.least_e, NEVER, NEVER, 0, 0, 0}));
+      b.sync_row();
+      row_sum = total = b.row_total();
+      b.sync_row();
     }
     if (cuts) {
-      first_bins(true, k);
+      first_bins(BY_COUNT, k, 0);
       list_if_few();
-      prefix_end(true, k, end_key, total);
+      prefix_end(true, k);
     }
   }
   if (top_p < 1.f) {
-    const u64 least = share(total);
+    const u64 least = b.share(total);
     if (least < total) {
-      first_bins(false, least);
+      first_bins(BETWEEN, least, row_sum);
       if (end_key == 0) list_if_few();
-      prefix_end(false, least, end_key, total);
+      prefix_end(false, least);
     }
   }
-  // what is kept, by the warps' parts of the row
-  const uint32_t end_w = max(least_key, (uint32_t)(end_key >> 32));
-  const float from_e = least_power(end_w), above_e = least_power(end_w + 1);
-  auto keep = [&](float e, int j) { return e >= above_e || (e >= from_e && list_key(weight_of(e), j) >= end_key); };
+
+  // ---- the draw: what is kept by the warps' parts of the row, then the
+  // block, the part and the element that holds the drawn place
+  const uint32_t end_w = max(b.least_key, (uint32_t)(end_key >> 32));
+  const Keep keep{least_power(end_w), least_power(end_w + 1), end_key, false};
   auto part_of = [&](u64 key) {
-    const int j = (int)~(uint32_t)key, v = (j - x.first) / E;
-    return j < x.first ? 0 : v >= x.n ? WARPS - 1 : v / x.slab;
+    const int j = list_id(key), v = (j - b.x.first) / E;
+    return j < b.x.first ? 0 : v >= b.x.n ? WARPS - 1 : v / b.x.slab;
   };
+  {
+    if (listed) {
+      if (tid < WARPS) s.part_low[tid] = s.part_high[tid] = 0;
+      __syncthreads();
+      for (int i = tid; i < s.n_long; i += THREADS) {
+        const u64 key = s.long_list[i];
+        if (key >= end_key) {                                 // 2^21 * LONG_LIST is below 2^32
+          const u64 w = list_whole(key);
+          const int part = part_of(key);
+          atomicAdd(&s.part_low[part], (uint32_t)w & 0x1FFFFFu);
+          atomicAdd(&s.part_high[part], (uint32_t)(w >> 21));
+        }
+      }
+      __syncthreads();
+      if (tid < WARPS) s.seg[tid] = s.part_low[tid] + ((u64)s.part_high[tid] << 21);
+      __syncthreads();
+      b.block_totals();
+    } else if (parts_known) {
+      // the sums of what lies above the sorted tokens, and those
+      for (int i = tid; i < s.n_list; i += THREADS) {
+        const u64 key = s.list[i];
+        if (key >= end_key) atomicAdd(&s.seg[part_of(key)], list_whole(key));
+      }
+      __syncthreads();
+      b.block_totals();
+    } else {
+      u64 sum = pass<NOTHING, FROM>(b.x, s, Pass{keep.above, NEVER, NEVER, 0, 0, 0});
+      // those of the last weight, in the list's order
+      if (keep.from < keep.above) {
+        for (int v = b.x.lo + lane; v < b.x.hi; v += 32) {
+          float e[E];
+          b.x.powers(b.x.vec(v), e);
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (e[i] < keep.above) sum += keep.value(e[i], b.x.index(v, i));
+        }
+        if (b.x.lone >= 0 && b.x.power(b.x.x_lone) < keep.above) sum += keep.value(b.x.power(b.x.x_lone), b.x.lone);
+      }
+      b.push_sums(sum);
+    }
+    b.sync_row();
+    total = b.row_total();
+  }
+  const u64 r = b.place(total) - b.before_block;
+  if (r >= s.sums[rank]) return;
   if (listed) {
-    if (tid < WARPS) s.part_low[tid] = s.part_high[tid] = 0;
-    if (tid == 0) s.n_few = 0;
+    int part = 0;
+    u64 at_r = r;
+    while (at_r >= s.seg[part]) at_r -= s.seg[part++];
+    if (tid == 0) s.n_list = 0;
     __syncthreads();
     for (int i = tid; i < s.n_long; i += THREADS) {
       const u64 key = s.long_list[i];
-      if (key >= end_key) {                                   // 2^21 * LONG_LIST is below 2^32
-        const u64 w = key_weight(key);
-        const int part = part_of(key);
-        atomicAdd(&s.part_low[part], (uint32_t)w & 0x1FFFFFu);
-        atomicAdd(&s.part_high[part], (uint32_t)(w >> 21));
+      if (key >= end_key && part_of(key) == part) {
+        const int n = atomicAdd(&s.n_list, 1);
+        if (n < LIST) s.list[n] = key << 32 | key >> 32;
       }
     }
     __syncthreads();
-    if (tid < WARPS) s.seg[tid] = s.part_low[tid] + ((u64)s.part_high[tid] << 21);
-    __syncthreads();
-    block_totals();
-  } else if (parts_known) {
-    // the sums of what lies above the ranked tokens, and those
-    for (int i = tid; i < s.n_list; i += THREADS) {
-      const u64 key = s.list[i];
-      if (key >= end_key) atomicAdd(&s.seg[part_of(key)], key_weight(key));
-    }
-    __syncthreads();
-    block_totals();
-  } else {
-    push_sums(x.sum_if(keep));
-  }
-  sync_row();
-  total = row_total(before_block);
-  if (!listed) {
-    draw_row(keep);
-    return;
-  }
-  // the part of the row that holds the drawn token, and its listed tokens by ID
-  const u64 r = place(total);
-  if (r < before_block || r >= before_block + s.sums[rank]) return;
-  int part = 0;
-  while (r >= before_block + s.seg[part]) before_block += s.seg[part++];
-  for (int i = tid; i < s.n_long; i += THREADS) {
-    const u64 key = s.long_list[i];
-    if (key >= end_key && part_of(key) == part) {
-      const uint32_t n = atomicAdd(&s.n_few, 1u);
-      if (n < BIN_LIST) s.few[n] = make_ulonglong2(key, key_weight(key));
+    const int n = s.n_list;
+    if (n <= LIST) {
+      const u64 key = sort(s, tid < n ? s.list[tid] : 0, n), w = key_whole((uint32_t)key);
+      const u64 before = sum_before(s, w);
+      if (before <= at_r && at_r < before + w) b.write(row, (int)~(uint32_t)(key >> 32), w, total);
+      return;
     }
   }
-  __syncthreads();
-  const int n_few = s.n_few;
-  if (n_few <= THREADS / 2) {
-    const int i = tid >> 1;
-    const ulonglong2 own = i < n_few ? s.few[i] : make_ulonglong2(0, 0);
-    u64 low = 0;
-    for (int o = tid & 1; o < n_few; o += 2) {
-      const ulonglong2 y = s.few[o];
-      if ((uint32_t)y.x > (uint32_t)own.x) low += y.y;
+  b.draw(row, keep, r, total);
+}
+
+// The rows that the first kernel left.  A cluster claims one at a time, so that
+// they spread over the clusters wherever they lie; each begins to look at a
+// place of its own and goes round once.
+template <class T>
+__global__ void __launch_bounds__(THREADS, 1) k_sample_bins(const SampleArgs a, const T *__restrict__ logits) {
+  __shared__ SharedBins s;
+  __shared__ int64_t s_row_of_cluster;
+  Block<T, SharedBins> b(s, a);
+  const int64_t clusters = gridDim.x >> a.cluster_log2, cluster = blockIdx.x >> a.cluster_log2;
+  const int64_t begin = a.n_rows * cluster / clusters;
+  int64_t looked = 0;                                         // rows from `begin` on that are claimed or done
+  wait_for_last();
+  b.sync_row();                                               // all blocks have begun
+  for (;;) {
+    if (b.rank == 0 && b.warp == 0) {
+      int64_t row = -1;
+      while (row < 0 && looked < a.n_rows) {
+        // 256 rows at a time, eight a lane
+        int mine = 8;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const int64_t n = looked + i * 32 + b.lane, r = begin + n - (begin + n >= a.n_rows ? a.n_rows : 0);
+          if (n < a.n_rows && *(volatile int32_t *)(a.ids + r) == PENDING) mine = i;
+        }
+        const int first = __reduce_min_sync(~0u, mine * 32 + b.lane);
+        if (first >= 256) {
+          looked += 256;
+          continue;
+        }
+        looked += first + 1;
+        const int64_t n = looked - 1, r = begin + n - (begin + n >= a.n_rows ? a.n_rows : 0);
+        int32_t old = 0;
+        if (b.lane == 0) old = atomicCAS(a.ids + r, PENDING, CLAIMED);
+        if (__shfl_sync(~0u, old, 0) == PENDING) row = r;
+      }
+      if (b.lane < b.C) *b.at(&s_row_of_cluster, b.lane) = row;
     }
-    low += __shfl_xor_sync(~0u, low, 1) + before_block;
-    if ((tid & 1) == 0 && i < n_few && low <= r && r < low + own.y) write((int)~(uint32_t)own.x, own.y, total);
-  } else if (warp == part) {
-    u64 own;
-    const int j = x.find([&](float e, int i) { return keep(e, i) ? whole(e) : 0ull; }, r - before_block, own);
-    if (lane == 0) write(j, own, total);
+    b.sync_row();                                             // the row is known, and all are done with the last one
+    const int64_t row = s_row_of_cluster;
+    if (row < 0) return;
+    b.parameters(row);
+    b.load(logits, row, [] {});
+    if (b.row_max == -INF) {                                  // nothing to draw
+      if (b.rank == 0 && b.tid == 0) a.ids[row] = -1;
+    } else {
+      sample_by_bins<T>(b, a, row);
+    }
   }
 }
+
+template <class T> struct Lists {};
+template <class T> struct Bins {};
 
 }  // namespace
 
@@ -1045,7 +1136,7 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
   if (n_rows == 0) return TT_OK;
   if (!array_ok(d_logits, type_size(type)) || !array_ok(d_uniform, 4) || !array_ok(d_out_ids, 4)) return TT_ERR_INVALID_ARG;
   SampleArgs a{n_vocab, logits_stride, d_uniform, d_temperature, d_top_k, d_top_p, d_min_p,
-               d_out_ids, d_out_logprobs, d_status, 0, 0};
+               d_out_ids, d_out_logprobs, d_status, 0, 0, n_rows};
   // Blocks a row: as many as run at once for all rows (clusters of 8, 4 and 2
   // fit 32, 72 and 152 times, two blocks an SM), of at least 8,192 elements
   const int64_t at_once[4] = {INT64_MAX, 152, 72, 32};
@@ -1053,11 +1144,18 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
   with_type(type, [&](auto t) {
     using T = decltype(t);
     const int64_t vecs = (n_vocab * (int64_t)sizeof(T) + 15) / 16;
-    a.held = (int)std::min<int64_t>((vecs + (1 << a.cluster_log2) - 1) >> a.cluster_log2, HELD / 16);
-    const size_t shared = (size_t)a.held * 16;
-    auto k = k_sample<T>;
-    if (shared + sizeof(Shared) > 48 * 1024) cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, HELD);
-    launch_cluster(k, (unsigned)(n_rows << a.cluster_log2), THREADS, shared, 1u << a.cluster_log2, stream, a, (const T *)d_logits);
+    auto launch = [&](auto tag, auto k, int64_t clusters, int most, bool chained) {
+      a.held = (int)std::min<int64_t>((vecs + (1 << a.cluster_log2) - 1) >> a.cluster_log2, most / 16);
+      if (allow_shared<decltype(tag)>(k, most)) return;       // (the error is kept)
+      launch_cluster(k, dim3((unsigned)(clusters << a.cluster_log2)), THREADS, (size_t)a.held * 16, 1u << a.cluster_log2, chained,
+                     stream, a, (const T *)d_logits);
+    };
+    launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
+    if (d_top_k || d_top_p) {
+      // one block an SM, and a few rows a cluster if all are left
+      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 18 ? 3 : n_rows <= 72 ? 2 : n_rows <= 288 ? 1 : 0;
+      launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
+    }
   });
   return launched("tt_sample");
 }
