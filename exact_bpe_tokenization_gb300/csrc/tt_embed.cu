@@ -82,20 +82,27 @@ __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__rest
 
 // ============================================================ tt_embed_grad
 // Tokens sorted by ID with their order kept (two passes of a radix sort), then
-// each row's terms summed in that order.
+// each row's terms summed in that order.  The kernels are chained: each starts
+// while the one before ends.
+//
+// A pass needs, for each tile of tokens and digit, how many tokens of the digit
+// stand before the tile.  The first pass's counts are a kernel of their own;
+// the second's are added up by the first pass as it places tokens in tiles.
+// With up to SUM_TILES tiles each block adds the earlier tiles' counts itself
+// (they come from L2); with more, a kernel scans them.
 constexpr int SORT_THREADS = 512;
-constexpr int SORT_KEYS = 8;                             // keys a thread
-constexpr int SORT_TILE = SORT_THREADS * SORT_KEYS;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_BINS = 1 << 11;
+constexpr int SUM_TILES = 32;
 
 struct SortArgs {
   const int64_t *n_ids;
   int64_t max_ids;
   int32_t n_vocab;
-  int shift, bins;          // this pass's digit: (key >> shift) & (bins - 1)
+  int bits[2];              // of the two digits, low first
   int tiles;
-  uint32_t *hist;           // [bins][tiles]
-  uint32_t *total;          // [bins]
+  uint32_t *hist[2];        // [tiles][bins]: counts, or scanned
+  uint32_t *total[2];       // [bins], where scanned
   int32_t *status;
   int32_t *cut_count;       // cleared for the sums
 };
@@ -109,78 +116,123 @@ __device__ __forceinline__ uint32_t key_of(int32_t id, int32_t n_vocab) {
   return (uint32_t)id < (uint32_t)n_vocab ? (uint32_t)id : (uint32_t)n_vocab;
 }
 
-// keys: of the IDs in the first pass, sorted by the low digit in the second
-template <bool FIRST>
-__global__ void __launch_bounds__(SORT_THREADS) k_sort_count(SortArgs a, const int32_t *__restrict__ keys) {
+// the first digit's counts; and the second's cleared
+template <int KEYS>
+__global__ void __launch_bounds__(SORT_THREADS) k_sort_count(SortArgs a, const int32_t *__restrict__ ids) {
   __shared__ uint32_t count[MAX_BINS];
-  const int64_t n = count_of(a.n_ids, a.max_ids), base = (int64_t)blockIdx.x * SORT_TILE;
-  for (int i = threadIdx.x; i < a.bins; i += SORT_THREADS) count[i] = 0;
-  if (FIRST && blockIdx.x == 0 && threadIdx.x == 0) *a.cut_count = 0;
+  let_next_start();
+  const int64_t n = count_of(a.n_ids, a.max_ids), base = (int64_t)blockIdx.x * (SORT_THREADS * KEYS);
+  const int bins = 1 << a.bits[0];
+  int32_t id[KEYS];
+#pragma unroll
+  for (int k = 0; k < KEYS; ++k) {
+    const int64_t i = base + k * SORT_THREADS + threadIdx.x;
+    id[k] = i < n ? ids[i] : -1;
+  }
+  for (int i = threadIdx.x; i < bins; i += SORT_THREADS) count[i] = 0;
+  for (int i = threadIdx.x; i < 1 << a.bits[1]; i += SORT_THREADS) a.hist[1][((int64_t)blockIdx.x << a.bits[1]) + i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.cut_count[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < SORT_KEYS; ++k) {
+  for (int k = 0; k < KEYS; ++k) {
     const int64_t i = base + k * SORT_THREADS + threadIdx.x;
     if (i < n) {
-      const int32_t id = keys[i];
-      if (FIRST && id >= a.n_vocab) op_status(a.status, TT_ERR_INVALID_ARG);
-      const uint32_t key = FIRST ? key_of(id, a.n_vocab) : (uint32_t)id;
-      atomicAdd(&count[(key >> a.shift) & (a.bins - 1)], 1u);
+      if (id[k] >= a.n_vocab) op_status(a.status, TT_ERR_INVALID_ARG);
+      atomicAdd(&count[key_of(id[k], a.n_vocab) & (bins - 1)], 1u);
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.bins; i += SORT_THREADS) a.hist[(int64_t)i * a.tiles + blockIdx.x] = count[i];
+  for (int i = threadIdx.x; i < bins; i += SORT_THREADS) a.hist[0][((int64_t)blockIdx.x << a.bits[0]) + i] = count[i];
 }
 
-// one block a digit: exclusive scan of its counts over the tiles
-__global__ void __launch_bounds__(256) k_sort_scan(SortArgs a) {
-  __shared__ uint32_t box[8];
-  uint32_t *h = a.hist + (int64_t)blockIdx.x * a.tiles;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t before = 0;
-  for (int base = 0; base < a.tiles; base += 256) {
-    const int i = base + threadIdx.x;
-    const uint32_t own = i < a.tiles ? h[i] : 0;
-    uint32_t x = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) box[warp] = x;
-    __syncthreads();
-    uint32_t add = 0, all = 0;
-    for (int w = 0; w < 8; ++w) {
-      add += w < warp ? box[w] : 0;
-      all += box[w];
-    }
-    if (i < a.tiles) h[i] = before + add + x - own;
-    before += all;
-    __syncthreads();
+// counts -> how many in earlier tiles; a block 32 digits, its warps parts of the tiles
+__global__ void __launch_bounds__(1024) k_sort_scan(SortArgs a, int pass) {
+  __shared__ uint32_t part[32][33];
+  wait_for_last();
+  let_next_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.x * 32 + lane, bins = 1 << a.bits[pass];
+  const int each = (a.tiles + 31) / 32, lo = min(a.tiles, warp * each), hi = min(a.tiles, lo + each);
+  uint32_t *h = a.hist[pass] + d;
+  uint32_t sum = 0;
+  if (d < bins)
+#pragma unroll 8
+    for (int t = lo; t < hi; ++t) sum += h[(int64_t)t << a.bits[pass]];
+  part[warp][lane] = sum;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (int w = 0; w < 32; ++w) {
+    before += w < warp ? part[w][lane] : 0;
+    all += part[w][lane];
   }
-  if (threadIdx.x == 0) a.total[blockIdx.x] = before;
+  if (d < bins) {
+#pragma unroll 4
+    for (int t = lo; t < hi; ++t) {
+      const uint32_t c = h[(int64_t)t << a.bits[pass]];
+      h[(int64_t)t << a.bits[pass]] = before;
+      before += c;
+    }
+    if (warp == 0) a.total[pass][d] = all;
+  }
 }
 
-template <bool FIRST>
+template <int PASS, int KEYS>
 __global__ void __launch_bounds__(SORT_THREADS)
 k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__restrict__ pos, int32_t *__restrict__ keys_out,
              int32_t *__restrict__ pos_out) {
-  constexpr int WARPS = SORT_THREADS / 32;
-  extern __shared__ uint32_t sm[];                         // base[bins], then uint16 seen[WARPS][bins]
-  __shared__ uint32_t box[WARPS];
+  extern __shared__ uint32_t sm[];                         // base[bins], then uint16 seen[SORT_WARPS][bins]
+  __shared__ uint32_t box[SORT_WARPS];
+  const int bins = 1 << a.bits[PASS], shift = PASS ? a.bits[0] : 0;
   uint32_t *base = sm;
-  uint16_t *seen = reinterpret_cast<uint16_t *>(sm + a.bins);
-  const int64_t n = count_of(a.n_ids, a.max_ids), tile = (int64_t)blockIdx.x * SORT_TILE;
+  uint16_t *seen = reinterpret_cast<uint16_t *>(sm + bins);
+  const int64_t tile = (int64_t)blockIdx.x * (SORT_THREADS * KEYS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (tile >= n) return;
-  for (int i = threadIdx.x; i < a.bins * WARPS / 2; i += SORT_THREADS) reinterpret_cast<uint32_t *>(seen)[i] = 0;
-  // where each digit begins: exclusive scan of the totals, four a thread
-  uint32_t t[4], x = 0;
+  for (int i = threadIdx.x; i < bins * SORT_WARPS / 2; i += SORT_THREADS) reinterpret_cast<uint32_t *>(seen)[i] = 0;
+  if (PASS || a.tiles > SUM_TILES) wait_for_last();
+  const int64_t n = count_of(a.n_ids, a.max_ids);
+  // a warp's keys are KEYS consecutive groups of 32
+  const int64_t first = tile + warp * (32 * KEYS) + lane;
+  uint32_t key[KEYS];
+  int32_t at[KEYS];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int d = threadIdx.x * 4 + k;
-    t[k] = d < a.bins ? a.total[d] : 0;
-    x += t[k];
+  for (int k = 0; k < KEYS; ++k) {
+    const int64_t i = first + k * 32;
+    key[k] = i < n ? (PASS ? (uint32_t)keys[i] : key_of(keys[i], a.n_vocab)) : 0;
+    at[k] = PASS ? (i < n ? pos[i] : 0) : (int32_t)i;
   }
+  if (!PASS && a.tiles <= SUM_TILES) wait_for_last();
+  let_next_start();
+  // four digits a thread: their tokens in earlier tiles and in all
+  uint32_t t[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0}, x = 0;
+  const int d0 = threadIdx.x * 4;
+  if (d0 < bins) {
+    if (a.tiles <= SUM_TILES) {
+      if (bins >= 4) {
+        const uint4 *h = reinterpret_cast<const uint4 *>(a.hist[PASS] + d0);
+#pragma unroll 8
+        for (int i = 0; i < a.tiles; ++i) {
+          const uint4 c = h[(int64_t)i << (a.bits[PASS] - 2)];
+          t[0] += c.x, t[1] += c.y, t[2] += c.z, t[3] += c.w;
+          if (i < (int)blockIdx.x) before[0] += c.x, before[1] += c.y, before[2] += c.z, before[3] += c.w;
+        }
+      } else {
+        for (int i = 0; i < a.tiles; ++i)
+          for (int k = 0; k < bins; ++k) {
+            const uint32_t c = a.hist[PASS][i * bins + k];
+            t[k & 3] += c;
+            before[k & 3] += i < (int)blockIdx.x ? c : 0;
+          }
+      }
+    } else {
+      for (int k = 0; k < 4; ++k)
+        if (d0 + k < bins) {
+          t[k] = a.total[PASS][d0 + k];
+          before[k] = a.hist[PASS][((int64_t)blockIdx.x << a.bits[PASS]) + d0 + k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x += t[k];
+  }
+  // where each digit begins: exclusive scan of the totals
   const uint32_t own = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -193,47 +245,43 @@ k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__rest
   for (int w = 0; w < warp; ++w) x += box[w];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int d = threadIdx.x * 4 + k;
-    if (d < a.bins) base[d] = x + a.hist[(int64_t)d * a.tiles + blockIdx.x];
+    if (d0 + k < bins) base[d0 + k] = x + before[k];
     x += t[k];
   }
-  // rank of each key among its warp's keys of the same digit; a warp's keys
-  // are SORT_KEYS consecutive groups of 32
-  uint32_t key[SORT_KEYS], rank[SORT_KEYS];
+  // rank of each key among its warp's keys of the same digit
+  uint32_t rank[KEYS];
 #pragma unroll
-  for (int k = 0; k < SORT_KEYS; ++k) {
-    const int64_t i = tile + warp * (32 * SORT_KEYS) + k * 32 + lane;
-    const bool there = i < n;
-    key[k] = there ? (FIRST ? key_of(keys[i], a.n_vocab) : (uint32_t)keys[i]) : 0;
-    const uint32_t d = there ? (key[k] >> a.shift) & (a.bins - 1) : 0xFFFFu;
+  for (int k = 0; k < KEYS; ++k) {
+    const bool there = first + k * 32 < n;
+    const uint32_t d = there ? (key[k] >> shift) & (bins - 1) : 0xFFFFu;
     const uint32_t same = __match_any_sync(~0u, d);
     const int lead = __ffs(same) - 1;
     uint32_t s = 0;
     if (there && lane == lead) {
-      s = seen[warp * a.bins + d];
-      seen[warp * a.bins + d] = (uint16_t)(s + __popc(same));
+      s = seen[warp * bins + d];
+      seen[warp * bins + d] = (uint16_t)(s + __popc(same));
     }
     rank[k] = __shfl_sync(~0u, s, lead) + __popc(same & ((1u << lane) - 1));
     __syncwarp();
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < a.bins; d += SORT_THREADS) {
-    uint32_t before = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      const uint32_t c = seen[w * a.bins + d];
-      seen[w * a.bins + d] = (uint16_t)before;
-      before += c;
+  for (int d = threadIdx.x; d < bins; d += SORT_THREADS) {
+    uint32_t sum = 0;
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const uint32_t c = seen[w * bins + d];
+      seen[w * bins + d] = (uint16_t)sum;
+      sum += c;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < SORT_KEYS; ++k) {
-    const int64_t i = tile + warp * (32 * SORT_KEYS) + k * 32 + lane;
-    if (i < n) {
-      const uint32_t d = (key[k] >> a.shift) & (a.bins - 1);
-      const uint32_t to = base[d] + seen[warp * a.bins + d] + rank[k];
+  for (int k = 0; k < KEYS; ++k) {
+    if (first + k * 32 < n) {
+      const uint32_t d = (key[k] >> shift) & (bins - 1);
+      const uint32_t to = base[d] + seen[warp * bins + d] + rank[k];
       keys_out[to] = (int32_t)key[k];
-      pos_out[to] = FIRST ? (int32_t)i : pos[i];
+      pos_out[to] = at[k];
+      if (!PASS) atomicAdd(&a.hist[1][((int64_t)(to / (SORT_THREADS * KEYS)) << a.bits[1]) + (key[k] >> a.bits[0])], 1u);
     }
   }
 }
@@ -260,6 +308,7 @@ struct GradArgs {
   int32_t *row_first;            // [n_vocab]: the worker where a cut row begins
   int32_t *cut_count;
   int2 *cut;                     // the worker where a cut row ends, and the row
+  int64_t pieces;                // room in `cut`
 };
 
 // how many of 0 .. n-1, from the first on, satisfy `pred` (a prefix does): a
@@ -328,12 +377,15 @@ template <class T> __device__ __forceinline__ void fill_zero(T *p, int64_t n, in
 }
 
 constexpr int HALO = 64;
+constexpr int LONG_ROW = 6;                       // pieces, at least, of a row that a block joins
 
 template <class TI, class TO, int COLS>
 __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__restrict__ dout, TO *__restrict__ dtable) {
   constexpr int BATCH = COLS == 8 ? 16 / sizeof(TI) : 8;        // rows in flight a thread
   extern __shared__ int32_t s_tok[];              // keys, then places in dout, HALO more on both sides
   __shared__ int64_t s_at[2];
+  wait_for_last();
+  let_next_start();
   const int64_t n = count_of(a.n_ids, a.max_ids);
   const int block_items = a.items * a.workers;
   const int64_t d0 = (int64_t)blockIdx.x * block_items;
@@ -409,7 +461,12 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   auto finish_to = [&](int k) {               // rows r .. k-1 end here
     if (head) {
       keep(a.heads);
-      if (t == 0 && blockIdx.y == 0) a.cut[atomicAdd(a.cut_count, 1)] = make_int2(w, r);
+      if (t == 0 && blockIdx.y == 0) {
+        // rows of many pieces are listed from the other end
+        const int64_t far = i0 + i - (int64_t)LONG_ROW * a.items;
+        if (far >= 0 && a.keys[far] == r) a.cut[a.pieces - 1 - atomicAdd(a.cut_count + 1, 1)] = make_int2(w, r);
+        else a.cut[atomicAdd(a.cut_count, 1)] = make_int2(w, r);
+      }
     } else if (any) {
       float v[COLS];
 #pragma unroll
@@ -454,39 +511,58 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   }
 }
 
-// the rows that were cut: the tails of the workers before, eight runs of them
-// summed side by side, and the last worker's head; a block 128 columns of a row
+// The rows that were cut: the tails of the workers before, then the last
+// worker's head, 128 columns at a time.  A warp takes rows of few pieces; a
+// block those of many, in 32 runs side by side.
 template <class TO>
-__global__ void __launch_bounds__(256) k_grad_join(GradArgs a, TO *__restrict__ dtable) {
-  __shared__ float4 part[8][32];
-  const int count = *a.cut_count, chunks = (int)((a.dim + 127) / 128);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t job = blockIdx.x; job < (int64_t)count * chunks; job += gridDim.x) {
-    const int2 at = a.cut[job / chunks];
-    const int64_t w = at.x, r = at.y, c = (job % chunks) * 128 + lane * 4, first = a.row_first[r];
-    const int64_t each = (w - first + 7) / 8, lo = min(w, first + warp * each), hi = min(w, lo + each);
-    float4 s = make_float4(0, 0, 0, 0);
-    if (c < a.dim) {
+__device__ __forceinline__ float4 join_pieces(const GradArgs &a, int64_t c, int64_t lo, int64_t hi) {
+  float4 s = make_float4(0, 0, 0, 0);
+  if (c < a.dim) {
 #pragma unroll 8
-      for (int64_t k = lo; k < hi; ++k) {
-        const float4 x = *reinterpret_cast<const float4 *>(a.tails + k * a.carry_stride + c);
-        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-      }
+    for (int64_t k = lo; k < hi; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(a.tails + k * a.carry_stride + c);
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
     }
+  }
+  return s;
+}
+template <class TO>
+__device__ __forceinline__ void join_store(const GradArgs &a, TO *dtable, int2 at, int64_t c, float4 s) {
+  if (c >= a.dim) return;
+  const float4 h = *reinterpret_cast<const float4 *>(a.heads + at.x * a.carry_stride + c);
+  const float v[4] = {(s.x + h.x) * a.scale, (s.y + h.y) * a.scale, (s.z + h.z) * a.scale, (s.w + h.w) * a.scale};
+  TO *p = dtable + at.y * a.dtable_stride + c;
+  for (int j = 0; j < 4; ++j)
+    if (c + j < a.dim) p[j] = from_f32<TO>(a.accumulate ? to_f32(p[j]) + v[j] : v[j]);
+}
+
+template <class TO>
+__global__ void __launch_bounds__(1024) k_grad_join(GradArgs a, TO *__restrict__ dtable) {
+  __shared__ float4 part[32][32];
+  wait_for_last();
+  const int few = a.cut_count[0], many = a.cut_count[1], chunks = (int)((a.dim + 127) / 128);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t job = blockIdx.x; job < (int64_t)many * chunks; job += gridDim.x) {
+    const int2 at = a.cut[a.pieces - 1 - job / chunks];
+    const int64_t w = at.x, c = (job % chunks) * 128 + lane * 4, first = a.row_first[at.y];
+    const int64_t each = (w - first + 31) / 32, lo = min(w, first + warp * each);
+    float4 s = join_pieces<TO>(a, c, lo, min(w, lo + each));
     __syncthreads();
     part[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < a.dim) {
-      for (int k = 1; k < 8; ++k) {
+    if (warp == 0) {
+#pragma unroll 8
+      for (int k = 1; k < 32; ++k) {
         const float4 x = part[k][lane];
         s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
       }
-      const float4 h = *reinterpret_cast<const float4 *>(a.heads + w * a.carry_stride + c);
-      const float v[4] = {(s.x + h.x) * a.scale, (s.y + h.y) * a.scale, (s.z + h.z) * a.scale, (s.w + h.w) * a.scale};
-      TO *p = dtable + r * a.dtable_stride + c;
-      for (int j = 0; j < 4; ++j)
-        if (c + j < a.dim) p[j] = from_f32<TO>(a.accumulate ? to_f32(p[j]) + v[j] : v[j]);
+      join_store(a, dtable, at, c, s);
     }
+  }
+  for (int64_t job = (int64_t)(gridDim.x - 1 - blockIdx.x) * 32 + warp; job < (int64_t)few * chunks; job += (int64_t)gridDim.x * 32) {
+    const int2 at = a.cut[job / chunks];
+    const int64_t c = (job % chunks) * 128 + lane * 4;
+    join_store(a, dtable, at, c, join_pieces<TO>(a, c, a.row_first[at.y], at.x));
   }
 }
 
@@ -495,15 +571,17 @@ bool grad_sizes_ok(int64_t max_ids, int64_t n_vocab, int64_t dim) {
   return max_ids >= 0 && max_ids <= TT_MAX_IDS && vocab_ok(n_vocab) && dim >= 1 && dim <= MAX_DIM;
 }
 
-template <bool FIRST> struct Place {};
+template <int PASS, int KEYS> struct Place {};
+template <int N> struct Per { static constexpr int value = N; };
 
 struct GradPlan {
-  int tiles = 0, bits[2] = {0, 0};
+  int tiles = 0, per_thread = 0, bits[2] = {0, 0};       // tokens a thread in the sort: fewer make short calls shorter
   int col_tiles[2], cols[2], group[2], workers[2];       // [1]: eight columns a thread, [0]: four
   int items[2];
   int64_t blocks[2];
-  int64_t keys[2], pos[2], hist, total, row_first, cut_count, cut, heads, tails, carry_stride, bytes;   // offsets into the workspace
+  int64_t keys[2], pos[2], hist[2], total[2], pieces, row_first, cut_count, cut, heads, tails, carry_stride, bytes;   // offsets into the workspace
 };
+
 
 constexpr int BLOCK_ITEMS = 4096;                 // at most, in shared memory
 
@@ -513,7 +591,8 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
   while ((n_vocab >> bits) != 0) ++bits;          // keys are 0 .. n_vocab
   p.bits[0] = (bits + 1) / 2;
   p.bits[1] = bits - p.bits[0];
-  p.tiles = (int)((max_ids + SORT_TILE - 1) / SORT_TILE);
+  p.per_thread = max_ids <= 32768 ? 2 : max_ids <= 1 << 20 ? 4 : 8;
+  p.tiles = (int)((max_ids + SORT_THREADS * p.per_thread - 1) / (SORT_THREADS * p.per_thread));
   int64_t pieces = 0;
   for (int v = 0; v < 2; ++v) {
     const int per = v ? 8 : 4;
@@ -534,7 +613,7 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
     const int64_t places = n_vocab + max_ids;
     int64_t workers = (4LL * 152 * 2048) / ((int64_t)p.group[v] * p.col_tiles[v]);
     workers = std::max<int64_t>(1, std::min(workers, std::max<int64_t>(8192, (1 << 21) / dim)));
-    p.items[v] = (int)std::min<int64_t>(BLOCK_ITEMS / p.workers[v], std::max<int64_t>(8, (places + workers - 1) / workers));
+    p.items[v] = (int)std::min<int64_t>(BLOCK_ITEMS / p.workers[v], std::max<int64_t>(16, (places + workers - 1) / workers));
     p.blocks[v] = (places + (int64_t)p.items[v] * p.workers[v] - 1) / ((int64_t)p.items[v] * p.workers[v]);
     pieces = std::max(pieces, p.blocks[v] * p.workers[v]);
   }
@@ -548,13 +627,16 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
     p.keys[i] = take(4 * max_ids);
     p.pos[i] = take(4 * max_ids);
   }
-  p.hist = take(4 * ((int64_t)p.tiles << p.bits[0]));
-  p.total = take(4 * MAX_BINS);
+  for (int i = 0; i < 2; ++i) {
+    p.hist[i] = take(4 * ((int64_t)p.tiles << p.bits[i]));
+    p.total[i] = take(4 * MAX_BINS);
+  }
+  p.pieces = pieces;
   p.carry_stride = (dim + 3) / 4 * 4;
   p.row_first = p.cut_count = p.cut = p.heads = p.tails = 0;
   if (max_ids > 0) {
     p.row_first = take(4 * n_vocab);
-    p.cut_count = take(4);
+    p.cut_count = take(8);
     p.cut = take(8 * pieces);
     p.heads = take(4 * pieces * p.carry_stride);
     p.tails = take(4 * pieces * p.carry_stride);
@@ -617,26 +699,32 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   int32_t *keys[2] = {(int32_t *)(ws + p.keys[0]), (int32_t *)(ws + p.keys[1])};
   int32_t *pos[2] = {(int32_t *)(ws + p.pos[0]), (int32_t *)(ws + p.pos[1])};
   if (max_ids > 0) {
-    SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, 0, 1 << p.bits[0], p.tiles, (uint32_t *)(ws + p.hist),
-               (uint32_t *)(ws + p.total), d_status, (int32_t *)(ws + p.cut_count)};
-    const auto shared = [](int bins) { return (size_t)bins * 4 + (size_t)bins * 2 * (SORT_THREADS / 32); };
-    if (allow_shared<Place<true>>(k_sort_place<true>, (int)shared(MAX_BINS)) ||
-        allow_shared<Place<false>>(k_sort_place<false>, (int)shared(MAX_BINS)))
-      return launched("tt_embed_grad");
-    k_sort_count<true><<<p.tiles, SORT_THREADS, 0, stream>>>(s, d_ids);
-    k_sort_scan<<<s.bins, 256, 0, stream>>>(s);
-    k_sort_place<true><<<p.tiles, SORT_THREADS, shared(s.bins), stream>>>(s, d_ids, nullptr, keys[0], pos[0]);
-    s.shift = p.bits[0];
-    s.bins = 1 << p.bits[1];
-    k_sort_count<false><<<p.tiles, SORT_THREADS, 0, stream>>>(s, keys[0]);
-    k_sort_scan<<<s.bins, 256, 0, stream>>>(s);
-    k_sort_place<false><<<p.tiles, SORT_THREADS, shared(s.bins), stream>>>(s, keys[0], pos[0], keys[1], pos[1]);
+    const SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, {p.bits[0], p.bits[1]}, p.tiles,
+                     {(uint32_t *)(ws + p.hist[0]), (uint32_t *)(ws + p.hist[1])},
+                     {(uint32_t *)(ws + p.total[0]), (uint32_t *)(ws + p.total[1])}, d_status, (int32_t *)(ws + p.cut_count)};
+    auto run = [&](auto per) {
+      constexpr int KEYS = decltype(per)::value;
+      const auto shared = [](int bits) { return ((size_t)4 << bits) + ((size_t)2 * SORT_WARPS << bits); };
+      if (allow_shared<Place<0, KEYS>>(k_sort_place<0, KEYS>, (int)shared(11)) ||
+          allow_shared<Place<1, KEYS>>(k_sort_place<1, KEYS>, (int)shared(11)))
+        return;                                               // (the error is kept)
+      k_sort_count<KEYS><<<p.tiles, SORT_THREADS, 0, stream>>>(s, d_ids);
+      for (int pass = 0; pass < 2; ++pass) {
+        if (p.tiles > SUM_TILES)
+          launch_cluster(k_sort_scan, dim3(((1u << p.bits[pass]) + 31) / 32), 1024, 0, 1, true, stream, s, pass);
+        launch_cluster(pass ? k_sort_place<1, KEYS> : k_sort_place<0, KEYS>, dim3(p.tiles), SORT_THREADS, shared(p.bits[pass]), 1, true,
+                       stream, s, pass ? (const int32_t *)keys[0] : d_ids, (const int32_t *)pos[0], keys[pass], pos[pass]);
+      }
+    };
+    if (p.per_thread == 2) run(Per<2>{});
+    else if (p.per_thread == 4) run(Per<4>{});
+    else run(Per<8>{});
   }
   const int v = rows_vector(d_dout, dout_stride, dim) && rows_vector(d_dtable, dtable_stride, dim);
   const GradArgs a{d_n_ids, max_ids, n_vocab, dim, dout_stride, dtable_stride, scale, accumulate != 0, keys[1], pos[1],
                    p.items[v], p.workers[v], p.group[v], p.cols[v], p.carry_stride,
                    (float *)(ws + p.heads), (float *)(ws + p.tails), std::min(p.items[v], HALO - 1),
-                   (int32_t *)(ws + p.row_first), (int32_t *)(ws + p.cut_count), (int2 *)(ws + p.cut)};
+                   (int32_t *)(ws + p.row_first), (int32_t *)(ws + p.cut_count), (int2 *)(ws + p.cut), p.pieces};
   with_type(dout_type, [&](auto ti) {
     with_type(dtable_type, [&](auto to) {
       using TI = decltype(ti);
@@ -645,9 +733,10 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
       const unsigned threads = (unsigned)(p.group[v] * p.workers[v]);
       const size_t shared = 4 * (4 * HALO + 2 * (size_t)p.items[v] * p.workers[v]);
       auto sum = v ? k_grad_sum<TI, TO, 8> : k_grad_sum<TI, TO, 4>;
-      sum<<<grid, threads, shared, stream>>>(a, (const TI *)d_dout, (TO *)d_dtable);
+      launch_cluster(sum, grid, threads, shared, 1, max_ids > 0, stream, a, (const TI *)d_dout, (TO *)d_dtable);
       if (max_ids > 0)
-        k_grad_join<TO><<<(unsigned)std::min<int64_t>(152 * 8, p.blocks[v] * p.workers[v]), 256, 0, stream>>>(a, (TO *)d_dtable);
+        launch_cluster(k_grad_join<TO>, dim3((unsigned)std::min<int64_t>(152 * 2, p.blocks[v] * p.workers[v])), 1024, 0, 1, true, stream, a,
+                       (TO *)d_dtable);
     });
   });
   return launched("tt_embed_grad");

@@ -61,6 +61,11 @@ struct Running {
 };
 
 // GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
+constexpr int UC = 2, AHEAD = 6;                // vectors a group of copies, groups ahead
+
+// a thread's first vector behind the held ones
+__device__ __forceinline__ int first_of(int tid, int held) { return tid + (held - tid + THREADS - 1) / THREADS * THREADS; }
+
 template <class T, int GRAD>
 __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits, T *dlogits) {
   constexpr int E = RowParts<T>::E, U = 4;
@@ -87,7 +92,30 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
     // read by one thread, before any block can write to the row
     const float lt = there && rank == 0 && tid == 0 ? to_f32(l[t]) : 0.f;
     Running run;
-    for (int v0 = tid; v0 < n; v0 += U * THREADS) {
+    if (GRAD) {
+      // what is held comes by copies that run ahead; a thread reads its own
+      const int n_held = min(n, a.held);
+      auto fetch = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+          if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+        copy_group();
+      };
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d) fetch(tid + d * UC * THREADS);
+      for (int v0 = tid; v0 < n_held; v0 += UC * THREADS) {
+        copy_wait<AHEAD - 1>();
+        fetch(v0 + AHEAD * UC * THREADS);
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+          if (v0 + u * THREADS < n_held) {
+            float v[E];
+            vec_f32(s_row[v0 + u * THREADS], v, T{});
+            run.add(v);
+          }
+      }
+    }
+    for (int v0 = GRAD ? first_of(tid, a.held) : tid; v0 < n; v0 += U * THREADS) {
       uint4 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -95,7 +123,6 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * THREADS < n) {
-          if (GRAD && v0 + u * THREADS < a.held) s_row[v0 + u * THREADS] = r[u];
           float v[E];
           vec_f32(r[u], v, T{});
           run.add(v);

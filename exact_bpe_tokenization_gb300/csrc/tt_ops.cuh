@@ -163,6 +163,14 @@ template <class V> __device__ __forceinline__ V *of_block(V *p, uint32_t rank) {
   return reinterpret_cast<V *>(a);
 }
 
+// 16 bytes from global to shared memory behind the thread's back; groups of
+// copies end in order
+__device__ __forceinline__ void copy_async(uint4 *to, const uint4 *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // 2^x, results below the normal range as zero
 __device__ __forceinline__ float ex2(float x) {
   float y;
