@@ -36,23 +36,31 @@ struct LossArgs {
 // the finite floats, so that a difference is NaN only where a logit is: +inf
 // adds +inf to the sum, -inf nothing.
 struct Running {
-  float m = LOWEST, s = 0;
-  template <int E> __device__ __forceinline__ void add(const float (&v)[E]) {
-    float vm = v[0];
-#pragma unroll
-    for (int i = 1; i < E; ++i) vm = fmaxf(vm, v[i]);
-    if (vm > m) {
-      vm = fminf(vm, -LOWEST);
-      s *= ex2((m - vm) * LOG2E);
-      m = vm;
-    }
+  float m = LOWEST;
+  float2 s2 = make_float2(0, 0);                 // the sum in two halves
+  float s;                                       // and whole, from total() on
+  template <class T> __device__ __forceinline__ void add(uint4 r, T) {
+    constexpr int E = 16 / sizeof(T);
+    const float vm = vec_max(r, T{});
+    if (vm > m) raise(vm);
+    float v[E];
+    vec_f32(r, v, T{});
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
       const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
-      s += ex2(y.x);
-      s += ex2(y.y);
+      s2 = add2(s2, make_float2(ex2(y.x), ex2(y.y)));
     }
   }
+  __device__ __forceinline__ void add(float x) {
+    if (x > m) raise(x);
+    s2.x += ex2((x - m) * LOG2E);
+  }
+  __device__ __forceinline__ void raise(float vm) {
+    vm = fminf(vm, -LOWEST);
+    s2 = mul2(s2, ex2((m - vm) * LOG2E));
+    m = vm;
+  }
+  __device__ __forceinline__ void total() { s = s2.x + s2.y; }
   __device__ __forceinline__ void join(float om, float os) {
     const float nm = fmaxf(m, om);
     s = s * ex2((m - nm) * LOG2E) + os * ex2((om - nm) * LOG2E);
@@ -61,24 +69,47 @@ struct Running {
 };
 
 // GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
-constexpr int UC = 2, AHEAD = 6;                // vectors a group of copies, groups ahead
+constexpr int U = 4;                             // vectors a thread takes at a time
+constexpr int UC = 2, AHEAD = 6;                 // vectors a group of copies, groups ahead
 
-// a thread's first vector behind the held ones
-__device__ __forceinline__ int first_of(int tid, int held) { return tid + (held - tid + THREADS - 1) / THREADS * THREADS; }
+// f(vector, whether all of the group's are there) for groups of `per` vectors
+// a thread between lo and hi: the tests of whole groups are left out.
+template <bool WHOLE> struct Whole { static constexpr bool value = WHOLE; };
+template <class F> __device__ __forceinline__ void groups(int lo, int hi, int per, F f) {
+  for (; lo + per * THREADS <= hi; lo += per * THREADS) f(lo + (int)threadIdx.x, Whole<true>{});
+  if (lo < hi) f(lo + (int)threadIdx.x, Whole<false>{});
+}
 
 template <class T, int GRAD>
 __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits, T *dlogits) {
-  constexpr int E = RowParts<T>::E, U = 4;
+  constexpr int E = RowParts<T>::E;
   extern __shared__ uint4 s_row[];
-  __shared__ float2 s_warp[WARPS], s_block;
+  __shared__ float2 s_warp[WARPS], s_blocks[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+  if (GRAD != 2 && a.cluster > 1) cluster_arrive();
   const int64_t row = blockIdx.x / a.cluster;
   const T *l = logits + row * a.logits_stride;
   const RowParts<T> part(l, (int)a.n_vocab);
   const int each = (part.vecs + a.cluster - 1) / a.cluster, first = min(part.vecs, rank * each);
-  const int n = min(part.vecs - first, each);
+  const int n = min(part.vecs - first, each), n_held = GRAD == 1 ? min(n, a.held) : 0;
   const uint4 *body = reinterpret_cast<const uint4 *>(l + part.lead) + first;
+  // what is held comes by copies that run ahead; a thread reads its own
+  auto fetch = [&](int v0) {
+    if (v0 - tid + UC * THREADS <= n_held) {
+#pragma unroll
+      for (int u = 0; u < UC; ++u) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+    } else {
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+        if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+    }
+    copy_group();
+  };
+  if (GRAD == 1) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(tid + d * UC * THREADS);
+  }
   const int lone = rank == 0 ? part.scalar(tid) : -1;
   const float x = lone >= 0 ? to_f32(l[lone]) : -INF;
   const int32_t t = a.targets[row];
@@ -92,61 +123,40 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
     // read by one thread, before any block can write to the row
     const float lt = there && rank == 0 && tid == 0 ? to_f32(l[t]) : 0.f;
     Running run;
-    if (GRAD) {
-      // what is held comes by copies that run ahead; a thread reads its own
-      const int n_held = min(n, a.held);
-      auto fetch = [&](int v0) {
-#pragma unroll
-        for (int u = 0; u < UC; ++u)
-          if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
-        copy_group();
-      };
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d) fetch(tid + d * UC * THREADS);
-      for (int v0 = tid; v0 < n_held; v0 += UC * THREADS) {
+    if (GRAD == 1)
+      groups(0, n_held, UC, [&](int v0, auto whole) {
         copy_wait<AHEAD - 1>();
         fetch(v0 + AHEAD * UC * THREADS);
 #pragma unroll
         for (int u = 0; u < UC; ++u)
-          if (v0 + u * THREADS < n_held) {
-            float v[E];
-            vec_f32(s_row[v0 + u * THREADS], v, T{});
-            run.add(v);
-          }
-      }
-    }
-    for (int v0 = GRAD ? first_of(tid, a.held) : tid; v0 < n; v0 += U * THREADS) {
+          if (whole.value || v0 + u * THREADS < n_held) run.add(s_row[v0 + u * THREADS], T{});
+      });
+    groups(n_held, n, U, [&](int v0, auto whole) {
       uint4 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
+        if (whole.value || v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + u * THREADS < n) {
-          float v[E];
-          vec_f32(r[u], v, T{});
-          run.add(v);
-        }
-    }
-    if (lone >= 0) {
-      const float v[2] = {x, -INF};
-      run.add(v);
-    }
+        if (whole.value || v0 + u * THREADS < n) run.add(r[u], T{});
+    });
+    if (lone >= 0) run.add(x);
+    run.total();
 #pragma unroll
     for (int o = 16; o; o >>= 1) run.join(__shfl_xor_sync(~0u, run.m, o), __shfl_xor_sync(~0u, run.s, o));
     if (lane == 0) s_warp[warp] = make_float2(run.m, run.s);
     __syncthreads();
-    run = Running();
+    run.m = LOWEST;
+    run.s = 0;
     for (int w = 0; w < WARPS; ++w) run.join(s_warp[w].x, s_warp[w].y);
     if (a.cluster > 1) {
-      if (tid == 0) s_block = make_float2(run.m, run.s);
+      // written to all blocks ahead of the barrier, so that nothing has to be fetched behind it
+      cluster_wait();                            // all blocks have begun
+      if (tid < a.cluster) *of_block(&s_blocks[rank], tid) = make_float2(run.m, run.s);
       cluster_sync();
-      run = Running();
-      for (int b = 0; b < a.cluster; ++b) {
-        const float2 o = *of_block(&s_block, b);
-        run.join(o.x, o.y);
-      }
-      cluster_arrive();                          // blocks stay until all have read
+      run.m = LOWEST;
+      run.s = 0;
+      for (int b = 0; b < a.cluster; ++b) run.join(s_blocks[b].x, s_blocks[b].y);
     }
     lse = run.m + logf(run.s);
     if (rank == 0 && tid == 0) {
@@ -159,45 +169,51 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
     const bool none = !there || lse == -INF;
     const float g = none ? 0.f : a.row_grads ? a.row_grads[row] : 1.f;
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(l)) & 15) == 0;
-    // the target among this block's vectors: its vector, and its place there
-    const int at = t - part.lead - first * E, tv = there && at >= 0 ? at / E : -1;
-    for (int v0 = tid; v0 < n; v0 += U * THREADS) {
+    T *out = d + part.lead + (int64_t)first * E;
+    // the thread that has the target among its vectors writes it once more behind them
+    const int at = t - part.lead - first * E;
+    const bool held = at / E < n_held, mine = there && at >= 0 && at / E < n && (at / E - (held ? 0 : n_held)) % THREADS == tid;
+    const float xt = mine ? to_f32(l[t]) : 0.f;
+    auto write = [&](uint4 r, int vi) {
+      float v[E];
+      vec_f32(r, v, T{});
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        float2 y = sub_mul2(make_float2(v[i], v[i + 1]), lse, LOG2E);
+        y.x = ex2(y.x);
+        y.y = ex2(y.y);
+        y = mul2(y, g);
+        v[i] = y.x;
+        v[i + 1] = y.y;
+      }
+      if (none)
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = 0;
+      T *to = out + (int64_t)vi * E;
+      if (same) {
+        __stcs(reinterpret_cast<uint4 *>(to), f32_vec(v, T{}));
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) to[i] = from_f32<T>(v[i]);
+      }
+    };
+    groups(0, n_held, U, [&](int v0, auto whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n_held) write(s_row[v0 + u * THREADS], v0 + u * THREADS);
+    });
+    groups(n_held, n, U, [&](int v0, auto whole) {
       uint4 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (v0 + u * THREADS < n)
-          r[u] = GRAD == 1 && v0 + u * THREADS < a.held ? s_row[v0 + u * THREADS] : __ldcs(body + v0 + u * THREADS);
+        if (whole.value || v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int vi = v0 + u * THREADS;
-        if (vi < n) {
-          float v[E];
-          vec_f32(r[u], v, T{});
-#pragma unroll
-          for (int i = 0; i < E; i += 2) {
-            const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), lse, LOG2E);
-            v[i] = ex2(y.x);
-            v[i + 1] = ex2(y.y);
-          }
-          if (vi == tv) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] -= i == at % E ? 1.f : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[i] = none ? 0.f : v[i] * g;
-          T *to = d + part.lead + (int64_t)(first + vi) * E;
-          if (same) {
-            __stcs(reinterpret_cast<uint4 *>(to), f32_vec(v, T{}));
-          } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) to[i] = from_f32<T>(v[i]);
-          }
-        }
-      }
-    }
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n) write(r[u], v0 + u * THREADS);
+    });
+    if (mine) d[t] = from_f32<T>(none ? 0.f : (ex2((xt - lse) * LOG2E) - 1.f) * g);
     if (lone >= 0) d[lone] = from_f32<T>(none ? 0.f : (ex2((x - lse) * LOG2E) - (lone == t ? 1.f : 0.f)) * g);
   }
-  if (GRAD != 2 && a.cluster > 1) cluster_wait();
 }
 
 template <class T, int GRAD> struct Tag {};

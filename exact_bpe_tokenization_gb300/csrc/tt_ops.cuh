@@ -62,16 +62,6 @@ __device__ __forceinline__ void store8(float *p, const float v[8]) {
   __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
   __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
-template <class T> __device__ __forceinline__ void store8(T *p, const float v[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    T h[2] = {from_f32<T>(v[2 * i]), from_f32<T>(v[2 * i + 1])};
-    w[i] = *reinterpret_cast<uint32_t *>(h);
-  }
-  __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
-}
-
 __device__ __forceinline__ void op_status(int32_t *st, int code) {
   if (st) atomicCAS(st, TT_OK, code);
 }
@@ -187,6 +177,37 @@ __device__ __forceinline__ float2 sub_mul2(float2 x, float y, float z) {
   return r;
 }
 
+// two sums, or products with the same factor, at once
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float z) {
+  float2 r;
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(z));
+  return r;
+}
+
+// the largest of a 16-byte vector's elements that are not NaN (NaN if all are)
+__device__ __forceinline__ float vec_max(uint4 r, float) {
+  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+template <class T2> __device__ __forceinline__ T2 as_two(uint32_t w) { return *reinterpret_cast<T2 *>(&w); }
+__device__ __forceinline__ float vec_max(uint4 r, __half) {
+  const __half2 m = __hmax2(__hmax2(as_two<__half2>(r.x), as_two<__half2>(r.y)), __hmax2(as_two<__half2>(r.z), as_two<__half2>(r.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float vec_max(uint4 r, __nv_bfloat16) {
+  const __nv_bfloat162 m = __hmax2(__hmax2(as_two<__nv_bfloat162>(r.x), as_two<__nv_bfloat162>(r.y)),
+                                   __hmax2(as_two<__nv_bfloat162>(r.z), as_two<__nv_bfloat162>(r.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 // A row of elements as a scalar lead up to the first 16-byte boundary, whole
 // 16-byte vectors, and a scalar rest.
 template <class T> struct RowParts {
@@ -218,12 +239,21 @@ template <class T> __device__ __forceinline__ void vec_f32(uint4 r, float v[8], 
 __device__ __forceinline__ uint4 f32_vec(const float v[4], float) {
   return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
-template <class T> __device__ __forceinline__ uint32_t f32_two(float a, float b) {
-  T h[2] = {from_f32<T>(a), from_f32<T>(b)};
-  return *reinterpret_cast<uint32_t *>(h);
+template <class T> __device__ __forceinline__ uint32_t f32_two(float a, float b);
+template <> __device__ __forceinline__ uint32_t f32_two<__half>(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t f32_two<__nv_bfloat16>(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
 }
 template <class T> __device__ __forceinline__ uint4 f32_vec(const float v[8], T) {
   return make_uint4(f32_two<T>(v[0], v[1]), f32_two<T>(v[2], v[3]), f32_two<T>(v[4], v[5]), f32_two<T>(v[6], v[7]));
+}
+
+template <class T> __device__ __forceinline__ void store8(T *p, const float v[8]) {
+  __stcs(reinterpret_cast<uint4 *>(p), f32_vec(v, T{}));
 }
 
 // A kernel launched with launch_chained may start when the blocks of the one
