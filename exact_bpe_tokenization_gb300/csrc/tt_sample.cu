@@ -32,6 +32,7 @@ constexpr int HELD = 96 * 1024;                   // bytes of a row a block hold
 constexpr int HELD_BINS = 180 * 1024;             // and in the second kernel, one an SM
 constexpr int PENDING = -2, CLAIMED = -3;         // in the place of an ID that the second kernel writes
 constexpr int GROUPS = 128;                       // groups of threads a row's maxima are taken over
+constexpr int MOST_LISTED = GROUPS * 3 / 4;       // the largest top-k that a list is made for
 constexpr int LIST = THREADS;                     // tokens one block sorts
 constexpr int LONG_LIST = 1792;                   // tokens worth a list of their own for the later passes
 constexpr int SHIFT = 17;                         // first histogram: 64 bins an octave
@@ -612,6 +613,12 @@ template <class T, class S> struct Block {
       a.logprobs[row] = rest < w ? log1pf(-__fdiv_rn((float)rest, (float)total)) : logf(__fdiv_rn((float)w, (float)total));
     }
   }
+  __device__ __forceinline__ void none(int64_t row, int id) const {       // for the second kernel, or nothing to draw
+    if (rank == 0 && tid == 0) {
+      a.ids[row] = id;
+      if (a.logprobs) a.logprobs[row] = -INF;
+    }
+  }
   __device__ __forceinline__ void block_totals() const {      // s.seg summed, for all blocks; by warp 0
     if (warp == 0) {
       const u64 t = warp_sum(lane < WARPS ? s.seg[lane] : 0);
@@ -680,34 +687,12 @@ template <class T, class S> struct Block {
   }
 };
 
-template <class T>
-__global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const T *__restrict__ logits) {
-  __shared__ Shared s;
-  Block<T, Shared> b(s, a);
-  const int tid = b.tid, lane = b.lane, warp = b.warp, C = b.C, rank = b.rank, V = (int)a.n_vocab;
-  const int64_t row = blockIdx.x >> a.cluster_log2;
-  auto none = [&](int id) {                                   // for the second kernel, or nothing to draw
-    if (rank == 0 && tid == 0) {
-      a.ids[row] = id;
-      if (a.logprobs) a.logprobs[row] = -INF;
-    }
-  };
-  let_next_start();
-  b.arrive();
-  const bool valid = b.parameters(row);
-  const int k = b.k;
+// One row by its heaviest tokens: whether that did.  Where it did not, all
+// blocks return together.
+template <class T, class S> __device__ __forceinline__ bool sample_by_list(Block<T, S> &b, const SampleArgs &a, int64_t row) {
+  S &s = b.s;
+  const int tid = b.tid, lane = b.lane, warp = b.warp, C = b.C, rank = b.rank, V = (int)a.n_vocab, k = b.k;
   const float top_p = b.top_p;
-  if (valid && k < V && k > GROUPS * 3 / 4) {                 // more than a list holds
-    none(PENDING);
-    b.leave();
-    return;
-  }
-  b.load(logits, row, [&]() { b.leave(); });
-  if (!valid || b.row_max == -INF) {
-    none(-1);
-    if (!valid && rank == 0 && tid == 0) op_status(a.status, TT_ERR_INVALID_ARG);
-    return;
-  }
 
   // ---- the lowest ID of the largest weight
   if (k == 1) {
@@ -721,14 +706,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const
       const uint32_t rows = __reduce_max_sync(~0u, lane < C ? (uint32_t)s.n_lists[lane] : 0u);
       if (lane == 0) b.write(row, (int)~rows, 1, 1);
     }
-    return;
+    return true;
   }
 
   // ---- the row's sum, and the list of its heaviest tokens
   const bool all = k == V && top_p == 1.f;                    // nothing but min-p cuts
   uint32_t list_from = b.least_key;                           // the list holds all keys from here on
   if (!all) {
-    const int q = min(k, GROUPS * 3 / 4);
+    const int q = min(k, MOST_LISTED);
     // four threads count what is above a group's maximum, and what equals it
     const float own = reinterpret_cast<const float *>(s.all_max)[tid >> 2];
     int above = 0, from = 0;
@@ -763,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const
   if (all) {
     const u64 r = b.place(total) - b.before_block;
     if (r < s.sums[rank]) b.draw(row, Keep{b.least_e, b.least_e, 0, false}, r, total);
-    return;
+    return true;
   }
   u64 list_sum = 0;
   int n_list = 0;
@@ -775,12 +760,11 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const
 
   // ---- if the prefix ends within the list, one block sorts it
   const bool all_listed = list_from == b.least_key;           // the list is all there is
-  const bool ends = n_list <= LIST && (all_listed || (k < V ? k <= n_list : b.share(total) <= list_sum));
-  if (!ends) none(PENDING);
-  if (!ends || rank != 0) {
+  if (n_list > LIST || !(all_listed || (k < V ? k <= n_list : b.share(total) <= list_sum))) return false;
+  if (rank != 0) {
     b.arrive();
     b.leave();
-    return;
+    return true;
   }
   int n;
   u64 key = b.gather(n);
@@ -805,6 +789,29 @@ __global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const
   before = sum_before(s, w);
   if (before <= s.draw && s.draw < before + w) b.write(row, (int)~(uint32_t)(key >> 32), w, s.total);
   b.leave();
+  return true;
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS, 2) k_sample(const SampleArgs a, const T *__restrict__ logits) {
+  __shared__ Shared s;
+  Block<T, Shared> b(s, a);
+  const int64_t row = blockIdx.x >> a.cluster_log2;
+  let_next_start();
+  b.arrive();
+  const bool valid = b.parameters(row);
+  if (valid && b.k < (int)a.n_vocab && b.k > MOST_LISTED) {   // more than a list holds
+    b.none(row, PENDING);
+    b.leave();
+    return;
+  }
+  b.load(logits, row, [&]() { b.leave(); });
+  if (!valid || b.row_max == -INF) {
+    b.none(row, -1);
+    if (!valid && b.rank == 0 && b.tid == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+    return;
+  }
+  if (!sample_by_list(b, a, row)) b.none(row, PENDING);
 }
 
 // One row that the list could not do: all blocks of the cluster.
@@ -1069,6 +1076,27 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
   b.draw(row, keep, r, total);
 }
 
+// Few rows: both in one launch, a cluster a row.
+template <class T>
+__global__ void __launch_bounds__(THREADS, 1) k_sample_few(const SampleArgs a, const T *__restrict__ logits) {
+  __shared__ SharedBins s;
+  Block<T, SharedBins> b(s, a);
+  const int64_t row = blockIdx.x >> a.cluster_log2;
+  b.arrive();
+  const bool valid = b.parameters(row);
+  b.load(logits, row, [&]() { b.leave(); });
+  if (!valid || b.row_max == -INF) {
+    b.none(row, -1);
+    if (!valid && b.rank == 0 && b.tid == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+    return;
+  }
+  if (!(b.k < (int)a.n_vocab && b.k > MOST_LISTED)) {
+    if (sample_by_list(b, a, row)) return;
+    b.sync_row();                                             // (the sums are read)
+  }
+  sample_by_bins<T>(b, a, row);
+}
+
 // The rows that the first kernel left.  A cluster claims one at a time, so that
 // they spread over the clusters wherever they lie; each begins to look at a
 // place of its own and goes round once.
@@ -1121,6 +1149,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_sample_bins(const SampleArgs a, 
 
 template <class T> struct Lists {};
 template <class T> struct Bins {};
+template <class T> struct Few {};
 
 }  // namespace
 
@@ -1150,10 +1179,14 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
       launch_cluster(k, dim3((unsigned)(clusters << a.cluster_log2)), THREADS, (size_t)a.held * 16, 1u << a.cluster_log2, chained,
                      stream, a, (const T *)d_logits);
     };
+    if ((d_top_k || d_top_p) && n_rows <= 16) {
+      launch(Few<T>{}, k_sample_few<T>, n_rows, HELD_BINS, false);
+      return;
+    }
     launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
     if (d_top_k || d_top_p) {
       // one block an SM, and a few rows a cluster if all are left
-      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 18 ? 3 : n_rows <= 72 ? 2 : n_rows <= 288 ? 1 : 0;
+      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 2 : n_rows <= 288 ? 1 : 0;
       launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
     }
   });
