@@ -1185,8 +1185,8 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
     }
     launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
     if (d_top_k || d_top_p) {
-      // one block an SM, and a few rows a cluster if all are left
-      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 2 : n_rows <= 288 ? 1 : 0;
+      // one block an SM; as a rule a quarter of the rows is left
+      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 3 : n_rows <= 288 ? 1 : 0;
       launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
     }
   });
