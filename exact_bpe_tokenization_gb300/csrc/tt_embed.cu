@@ -132,7 +132,35 @@ struct SortArgs {
   uint32_t *total[2];       // [bins], where scanned
   int32_t *status;
   int32_t *cut_count;       // cleared for the sums
+  // a table that is cleared meanwhile, in three parts: its rows, in 16-bit
+  // words, and how many of them a block takes
+  uint16_t *clear;
+  int64_t clear_rows, clear_words, clear_stride, clear_each;
+  unsigned clear_blocks;    // of each part
 };
+
+// zeros, 16 bytes a store; thread t of `group`
+__device__ __forceinline__ void fill_zero(uint16_t *p, int64_t n, int t, int group) {
+  const int64_t lead = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 2);
+  const int64_t vecs = (n - lead) / 8, done = lead + vecs * 8;
+  if (t < lead) p[t] = 0;
+  uint4 *q = reinterpret_cast<uint4 *>(p + lead);
+  for (int64_t i = t; i < vecs; i += group) __stcs(q + i, make_uint4(0, 0, 0, 0));
+  for (int64_t i = done + t; i < n; i += group) p[i] = 0;
+  for (int64_t i = group + t; i < lead; i += group) p[i] = 0;
+}
+
+__device__ __forceinline__ void clear_part(const SortArgs &a, int part) {
+  const int64_t r = ((int64_t)part * a.clear_blocks + blockIdx.x - a.tiles) * a.clear_each;
+  const int64_t rows = min(a.clear_each, a.clear_rows - r);
+  uint16_t *p = a.clear + r * a.clear_stride;
+  if (rows <= 0) return;
+  if (a.clear_stride == a.clear_words) {
+    fill_zero(p, rows * a.clear_words, threadIdx.x, SORT_THREADS);
+  } else {
+    for (int64_t i = threadIdx.x >> 5; i < rows; i += SORT_WARPS) fill_zero(p + i * a.clear_stride, a.clear_words, threadIdx.x & 31, 32);
+  }
+}
 
 __device__ __forceinline__ int64_t count_of(const int64_t *n_ids, int64_t max_ids) {
   return n_ids ? max((int64_t)0, min(*n_ids, max_ids)) : max_ids;
@@ -148,6 +176,7 @@ template <int KEYS>
 __global__ void __launch_bounds__(SORT_THREADS) k_sort_count(SortArgs a, const int32_t *__restrict__ ids) {
   __shared__ uint32_t count[MAX_BINS];
   let_next_start();
+  if ((int)blockIdx.x >= a.tiles) return clear_part(a, 0);
   const int64_t n = count_of(a.n_ids, a.max_ids), base = (int64_t)blockIdx.x * (SORT_THREADS * KEYS);
   const int bins = 1 << a.bits[0];
   int32_t id[KEYS];
@@ -208,6 +237,10 @@ k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__rest
              int32_t *__restrict__ pos_out) {
   extern __shared__ uint32_t sm[];                         // base[bins], then uint16 seen[SORT_WARPS][bins]
   __shared__ uint32_t box[SORT_WARPS];
+  if ((int)blockIdx.x >= a.tiles) {
+    let_next_start();
+    return clear_part(a, 1 + PASS);
+  }
   const int bins = 1 << a.bits[PASS], shift = PASS ? a.bits[0] : 0;
   uint32_t *base = sm;
   uint16_t *seen = reinterpret_cast<uint16_t *>(sm + bins);
@@ -321,11 +354,15 @@ k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__rest
 // the tokens are spread: absent rows, rows of one token and rows of a tenth of
 // all tokens.  A row that ends where it began is written at once; one that is
 // cut leaves its pieces in the workspace, and k_grad_join adds them in order.
+// Where rows without tokens cost nothing (they keep what they hold, or are many
+// and the sort's kernels clear them beside their own work), tokens alone are
+// the items.
 struct GradArgs {
   const int64_t *n_ids;
   int64_t max_ids, n_vocab, dim, dout_stride, dtable_stride;
   float scale;
   int accumulate;
+  int tokens_only;               // rows are no items
   const int32_t *keys, *pos;     // sorted
   int items, workers;            // items a worker, workers a block
   int group, cols;               // threads a worker, columns of its tile
@@ -394,15 +431,6 @@ template <class T> struct Cols<T, 4> {
   }
 };
 
-// zeros over whole rows that lie side by side: 16 bytes a store
-template <class T> __device__ __forceinline__ void fill_zero(T *p, int64_t n, int t, int group) {
-  const int64_t lead = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T));
-  const int64_t vecs = (n - lead) / (16 / (int64_t)sizeof(T)), done = lead + vecs * (16 / (int64_t)sizeof(T));
-  for (int64_t i = t; i < lead; i += group) p[i] = from_f32<T>(0.f);
-  for (int64_t i = t; i < vecs; i += group) __stcs(reinterpret_cast<uint4 *>(p + lead) + i, make_uint4(0, 0, 0, 0));
-  for (int64_t i = done + t; i < n; i += group) p[i] = from_f32<T>(0.f);
-}
-
 constexpr int HALO = 64;
 constexpr int LONG_ROW = 6;                       // pieces, at least, of a row that a block joins
 
@@ -417,13 +445,17 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   const int block_items = a.items * a.workers;
   const int64_t d0 = (int64_t)blockIdx.x * block_items;
   // tokens of the block's places; padding stands behind every row
-  if (threadIdx.x < 64) {
-    const int64_t at = tokens_before(a.keys, n, d0 + (threadIdx.x >> 5) * block_items);
-    if ((threadIdx.x & 31) == 0) s_at[threadIdx.x >> 5] = at;
+  int64_t i0 = min(n, d0), i1 = min(n, d0 + block_items);
+  if (!a.tokens_only) {
+    if (threadIdx.x < 64) {
+      const int64_t at = tokens_before(a.keys, n, d0 + (threadIdx.x >> 5) * block_items);
+      if ((threadIdx.x & 31) == 0) s_at[threadIdx.x >> 5] = at;
+    }
+    __syncthreads();
+    i0 = s_at[0];
+    i1 = s_at[1];
   }
-  __syncthreads();
-  const int64_t i0 = s_at[0];
-  const int n_tok = (int)(s_at[1] - i0);
+  const int n_tok = (int)(i1 - i0);
   int32_t *s_key = s_tok + HALO, *s_pos = s_key + block_items + HALO;
   for (int i = (int)threadIdx.x - HALO; i < n_tok + HALO; i += blockDim.x) {
     const bool there = i0 + i >= 0 && i0 + i < n;
@@ -447,18 +479,19 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   // The cut at the block's place p: the tokens of the block before it, and the
   // rows.  One inside a row of at most a.whole tokens moves behind that row.
   auto cut_at = [&](int p, int &i, int &r) {
-    int lo = 0, hi = min(p, n_tok);
+    int lo = p == block_items ? n_tok : 0, hi = min(p, n_tok);
+    if (a.tokens_only) lo = hi;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (i0 + mid + s_key[mid] < d0 + p) lo = mid + 1; else hi = mid;
     }
     i = lo;
-    r = (int)min(a.n_vocab, d0 + p - i0 - lo);
+    r = a.tokens_only ? min(n_vocab, s_key[lo]) : (int)min(a.n_vocab, d0 + p - i0 - lo);
     if (s_key[lo - 1] == r && r < n_vocab) {
       const int begin = first_of(lo - a.whole, lo, r), end = first_of(lo, lo + a.whole, r + 1);
       if (end - begin <= a.whole && s_key[begin - 1] < r) {       // else it is longer
         i = end;
-        ++r;
+        r = a.tokens_only ? min(n_vocab, s_key[end]) : r + 1;
       }
     }
   };
@@ -468,7 +501,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   while (end > i && s_key[end - 1] >= n_vocab) --end;
   const int w = (int)blockIdx.x * a.workers + sub;
   bool head = s_key[i - 1] == r && r < n_vocab, any = false;
-  const bool side_by_side = !a.accumulate && gridDim.y == 1 && a.dtable_stride == a.dim;
+  const bool side_by_side = !a.tokens_only && gridDim.y == 1 && a.dtable_stride == a.dim;
   float acc[COLS];
 #pragma unroll
   for (int j = 0; j < COLS; ++j) acc[j] = 0;
@@ -505,8 +538,9 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
 #pragma unroll
     for (int j = 0; j < COLS; ++j) acc[j] = 0;
     if (side_by_side) {
-      if (r < k) fill_zero(dtable + (int64_t)r * a.dim, (int64_t)(k - r) * a.dim, t, a.group);
-    } else if (!a.accumulate && mine) {
+      constexpr int WORDS = sizeof(TO) / 2;
+      if (r < k) fill_zero(reinterpret_cast<uint16_t *>(dtable + (int64_t)r * a.dim), (int64_t)(k - r) * a.dim * WORDS, t, a.group);
+    } else if (!a.tokens_only && mine) {
       for (; r < k; ++r) {
         float v[COLS] = {};
         Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride, c, a.group, dim, v, false);
@@ -604,8 +638,8 @@ template <int N> struct Per { static constexpr int value = N; };
 struct GradPlan {
   int tiles = 0, per_thread = 0, bits[2] = {0, 0};       // tokens a thread in the sort: fewer make short calls shorter
   int col_tiles[2], cols[2], group[2], workers[2];       // [1]: eight columns a thread, [0]: four
-  int items[2];
-  int64_t blocks[2];
+  int items[2][2];                                       // [..][1]: tokens only
+  int64_t blocks[2][2];
   int64_t keys[2], pos[2], hist[2], total[2], pieces, row_first, cut_count, cut, heads, tails, carry_stride, bytes;   // offsets into the workspace
 };
 
@@ -636,13 +670,19 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
     }
     p.cols[v] = p.group[v] * per;
     p.col_tiles[v] = (int)((dim + p.cols[v] - 1) / p.cols[v]);
-    // about four times the threads the GPU holds, but few enough pieces
-    const int64_t places = n_vocab + max_ids;
-    int64_t workers = (4LL * 152 * 2048) / ((int64_t)p.group[v] * p.col_tiles[v]);
-    workers = std::max<int64_t>(1, std::min(workers, std::max<int64_t>(8192, (1 << 21) / dim)));
-    p.items[v] = (int)std::min<int64_t>(BLOCK_ITEMS / p.workers[v], std::max<int64_t>(16, (places + workers - 1) / workers));
-    p.blocks[v] = (places + (int64_t)p.items[v] * p.workers[v] - 1) / ((int64_t)p.items[v] * p.workers[v]);
-    pieces = std::max(pieces, p.blocks[v] * p.workers[v]);
+    // Four rounds of the blocks that run at once, or fewer for short calls, but
+    // whole rounds: one block more costs a round.  Few enough pieces.
+    const int64_t at_once = std::max<int64_t>(1, 152 * (1024 / (p.group[v] * p.workers[v])) / p.col_tiles[v]);
+    for (int tokens_only = 0; tokens_only < 2; ++tokens_only) {
+      const int64_t places = tokens_only ? std::max<int64_t>(max_ids, 1) : n_vocab + max_ids;
+      const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(4, places / (16 * p.workers[v] * at_once)));
+      const int64_t blocks = std::min(rounds * at_once, std::max<int64_t>(1, std::max<int64_t>(8192, (1 << 21) / dim) / p.workers[v]));
+      int64_t items = (places + blocks * p.workers[v] - 1) / (blocks * p.workers[v]);
+      items = std::min<int64_t>(BLOCK_ITEMS / p.workers[v], std::max<int64_t>(16, items));
+      p.items[v][tokens_only] = (int)items;
+      p.blocks[v][tokens_only] = (places + items * p.workers[v] - 1) / (items * p.workers[v]);
+      pieces = std::max(pieces, p.blocks[v][tokens_only] * p.workers[v]);
+    }
   }
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -726,24 +766,38 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   const GradPlan p = grad_plan(max_ids, n_vocab, dim);
   if (!array_ok(d_workspace, 16)) return TT_ERR_INVALID_ARG;
   if (workspace_bytes < p.bytes) return TT_ERR_CAPACITY;
+  if (max_ids == 0 && accumulate) return TT_OK;
   char *ws = (char *)d_workspace;
+  // Rows that are mostly absent are cleared by blocks beside the sort's (8191 x
+  // 641 bf16 into 200,256 rows: 70 us, and 77 us where the sums write them);
+  // with more tokens, rows written twice would cost more than that saves.
+  const bool clear = !accumulate && max_ids > 0 && max_ids <= n_vocab / 4;
+  const int tokens_only = accumulate || clear;
   int32_t *keys[2] = {(int32_t *)(ws + p.keys[0]), (int32_t *)(ws + p.keys[1])};
   int32_t *pos[2] = {(int32_t *)(ws + p.pos[0]), (int32_t *)(ws + p.pos[1])};
   if (max_ids > 0) {
-    const SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, {p.bits[0], p.bits[1]}, p.tiles,
+    SortArgs s{d_n_ids, max_ids, (int32_t)n_vocab, {p.bits[0], p.bits[1]}, p.tiles,
                      {(uint32_t *)(ws + p.hist[0]), (uint32_t *)(ws + p.hist[1])},
-                     {(uint32_t *)(ws + p.total[0]), (uint32_t *)(ws + p.total[1])}, d_status, (int32_t *)(ws + p.cut_count)};
+                     {(uint32_t *)(ws + p.total[0]), (uint32_t *)(ws + p.total[1])}, d_status, (int32_t *)(ws + p.cut_count),
+               (uint16_t *)d_dtable, n_vocab, 0, 0, 0, 0};
+    if (clear) {
+      const int64_t words = (int64_t)type_size(dtable_type) / 2;
+      s.clear_words = dim * words;
+      s.clear_stride = dtable_stride * words;
+      s.clear_each = std::max<int64_t>(1, 65536 / s.clear_words);
+      s.clear_blocks = (unsigned)((n_vocab + 3 * s.clear_each - 1) / (3 * s.clear_each));
+    }
     auto run = [&](auto per) {
       constexpr int KEYS = decltype(per)::value;
       const auto shared = [](int bits) { return ((size_t)4 << bits) + ((size_t)2 * SORT_WARPS << bits); };
       if (allow_shared<Place<0, KEYS>>(k_sort_place<0, KEYS>, (int)shared(11)) ||
           allow_shared<Place<1, KEYS>>(k_sort_place<1, KEYS>, (int)shared(11)))
         return;                                               // (the error is kept)
-      k_sort_count<KEYS><<<p.tiles, SORT_THREADS, 0, stream>>>(s, d_ids);
+      k_sort_count<KEYS><<<p.tiles + s.clear_blocks, SORT_THREADS, 0, stream>>>(s, d_ids);
       for (int pass = 0; pass < 2; ++pass) {
         if (p.tiles > SUM_TILES)
           launch_cluster(k_sort_scan, dim3(((1u << p.bits[pass]) + 31) / 32), 1024, 0, 1, true, stream, s, pass);
-        launch_cluster(pass ? k_sort_place<1, KEYS> : k_sort_place<0, KEYS>, dim3(p.tiles), SORT_THREADS, shared(p.bits[pass]), 1, true,
+        launch_cluster(pass ? k_sort_place<1, KEYS> : k_sort_place<0, KEYS>, dim3(p.tiles + s.clear_blocks), SORT_THREADS, shared(p.bits[pass]), 1, true,
                        stream, s, pass ? (const int32_t *)keys[0] : d_ids, (const int32_t *)pos[0], keys[pass], pos[pass]);
       }
     };
@@ -752,21 +806,21 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
     else run(Per<8>{});
   }
   const int v = rows_vector(d_dout, dout_stride, dim) && rows_vector(d_dtable, dtable_stride, dim);
-  const GradArgs a{d_n_ids, max_ids, n_vocab, dim, dout_stride, dtable_stride, scale, accumulate != 0, keys[1], pos[1],
-                   p.items[v], p.workers[v], p.group[v], p.cols[v], p.carry_stride,
-                   (float *)(ws + p.heads), (float *)(ws + p.tails), std::min(p.items[v], HALO - 1),
+  const GradArgs a{d_n_ids, max_ids, n_vocab, dim, dout_stride, dtable_stride, scale, accumulate != 0, tokens_only, keys[1], pos[1],
+                   p.items[v][tokens_only], p.workers[v], p.group[v], p.cols[v], p.carry_stride,
+                   (float *)(ws + p.heads), (float *)(ws + p.tails), std::min(std::max(p.items[v][tokens_only], 16), HALO - 1),
                    (int32_t *)(ws + p.row_first), (int32_t *)(ws + p.cut_count), (int2 *)(ws + p.cut), p.pieces};
   with_type(dout_type, [&](auto ti) {
     with_type(dtable_type, [&](auto to) {
       using TI = decltype(ti);
       using TO = decltype(to);
-      const dim3 grid((unsigned)p.blocks[v], (unsigned)p.col_tiles[v]);
+      const dim3 grid((unsigned)p.blocks[v][tokens_only], (unsigned)p.col_tiles[v]);
       const unsigned threads = (unsigned)(p.group[v] * p.workers[v]);
-      const size_t shared = 4 * (4 * HALO + 2 * (size_t)p.items[v] * p.workers[v]);
+      const size_t shared = 4 * (4 * HALO + 2 * (size_t)p.items[v][tokens_only] * p.workers[v]);
       auto sum = v ? k_grad_sum<TI, TO, 8> : k_grad_sum<TI, TO, 4>;
       launch_cluster(sum, grid, threads, shared, 1, max_ids > 0, stream, a, (const TI *)d_dout, (TO *)d_dtable);
       if (max_ids > 0)
-        launch_cluster(k_grad_join<TO>, dim3((unsigned)std::min<int64_t>(152 * 2, p.blocks[v] * p.workers[v])), 1024, 0, 1, true, stream, a,
+        launch_cluster(k_grad_join<TO>, dim3((unsigned)std::min<int64_t>(152 * 2, p.blocks[v][tokens_only] * p.workers[v])), 1024, 0, 1, true, stream, a,
                        (TO *)d_dtable);
     });
   });

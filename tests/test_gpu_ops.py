@@ -616,3 +616,86 @@ def test_from_the_tokenizer(tt):
     # equal terms: the sum of c copies, each addition rounded
     assert bool(((g - count[:, None] * table).abs() <= plain.EPS * count[:, None]**2 * table.abs()).all())
     tok.close()
+
+
+def test_example(tt, capsys):
+    """The example trains (its loss falls well below the uniform one) and what it
+    draws are IDs of its vocabulary."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "bigram.py")
+    spec = importlib.util.spec_from_file_location("bigram", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, drawn = m.main(["--steps", "30", "--tokens", "8"])
+    assert losses[-1] < losses[0] - 0.5
+    assert drawn.shape == (2, 8) and drawn.min() >= 0 and drawn.max() < 1256
+
+
+# ------------------------------------------------------------ where the kernels' ways part
+
+@pytest.mark.parametrize("n,vocab", [(17, 20011), (73, 20011), (100, 40001), (153, 20011), (300, 17001), (400, 1003), (33, 200255)])
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+def test_sample_batches(tt, n, vocab, name):
+    """Batches of every cluster size, their rows a mix of listed ones and ones
+    that need histograms."""
+    rng = np.random.default_rng(n)
+    x = rows_of(n, vocab, name, gen(n), scale=2.0)
+    u = np.minimum(rng.random(n).astype(np.float32), np.float32(1) - np.float32(2.0**-24))
+    check_sample(tt, x, u, params(n, rng), range(0, n, max(1, n // 40)))
+
+
+@pytest.mark.parametrize("vocab", [3000, 50000, 200001])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_sample_flat_rows(tt, vocab, rows):
+    """Prefixes that end among thousands of nearly equal weights, at shares
+    from a single token to all but one."""
+    rng = np.random.default_rng(vocab)
+    x = rows_of(rows, vocab, "float32", gen(vocab), scale=0.01)
+    x[1] *= 100
+    x[2] = torch.round(x[2] * 200)
+    p = dict(top_p=np.float32([0.5, 0.999999, 0.9, 1e-6] * 10)[:rows],
+             top_k=np.int32([0, 0, 0, vocab - 1, 2000, vocab // 2, 97, 512, 1793, 0] * 4)[:rows],
+             min_p=np.float32([0.0, 0.0, 1e-3, 0.0, 0.98] * 8)[:rows],
+             temperature=np.float32([1.0, 0.5, 1.0, 2.0] * 10)[:rows])
+    for k in range(3):
+        u = np.minimum(rng.random(rows).astype(np.float32), np.float32(1) - np.float32(2.0**-24))
+        check_sample(tt, x, u, p)
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(100, 5000, 641), (3000, 20000, 72), (2000, 8000, 9), (40000, 200000, 16)])
+@pytest.mark.parametrize("to", ["float32", "bfloat16"])
+@pytest.mark.parametrize("stride", [0, 5, 8])
+def test_embed_grad_few_tokens(tt, n, vocab, dim, to, stride):
+    """Tables of mostly absent rows: cleared, not added to; gaps left alone."""
+    rng = np.random.default_rng(n)
+    ids = np.minimum(rng.zipf(1.3, n) * 7 % vocab, vocab - 1).astype(np.int32)
+    ids[rng.random(n) < 0.1] = -1
+    dout = rows_of(n, dim, "float32", gen(n))
+    out = rows_of(vocab, dim, to, gen(2), dim + stride)
+    tt.embed_grad(torch.from_numpy(ids).cuda(), dout, vocab, out=out)
+    want = np.zeros((vocab, dim))
+    size = np.zeros((vocab, dim))
+    there = ids >= 0
+    np.add.at(want, ids[there], host(dout)[there])
+    np.add.at(size, ids[there], np.abs(host(dout)[there]))
+    count = np.bincount(ids[there], minlength=vocab)[:, None]
+    tol = plain.EPS * 1.01 * (count + 3) * size + plain.UNIT[to] * 1.01 * np.abs(want)
+    assert np.all(np.abs(host(out) - want) <= tol)
+    if stride:
+        gaps = torch.as_strided(out, (vocab - 1, stride), (dim + stride, 1), out.storage_offset() + dim)
+        assert bool(torch.isnan(gaps).all())
+
+
+def test_loss_and_lookup_of_many_rows(tt):
+    """More rows than run at once, of sizes that leave blocks partly filled."""
+    x = rows_of(5000, 777, "bfloat16", gen(1))
+    targets = torch.randint(-1, 777, (5000,), generator=gen(2), device="cuda", dtype=torch.int32)
+    loss, lse, d = tt.token_loss(x, targets, want_grad=True)
+    want, want_lse, want_d = plain.token_loss(host(x), targets.cpu().numpy(), np.ones(5000))
+    tol = plain.lse_bound(host(x), want_lse)
+    assert np.all(np.abs(host(loss) - want) <= tol + plain.EPS * np.abs(want)) and np.all(np.abs(host(lse) - want_lse) <= tol)
+    assert np.all(np.abs(host(d) - want_d) <= plain.UNIT["bfloat16"] * 1.01 * np.abs(want_d) + tol[:, None] + 20 * plain.EPS)
+    ids = torch.randint(0, 300, (100001,), generator=gen(3), device="cuda", dtype=torch.int32)
+    table = rows_of(300, 264, "float16", gen(4))
+    assert torch.equal(tt.embed(ids, table), table[ids.long()])
