@@ -281,6 +281,7 @@ template <int ACT, int SUM, class T, class S> __device__ __forceinline__ u64 pas
       if (least == top) {                                     // rows of one value would meet at one counter
         const uint32_t b = (key_of(top) - p.base) >> p.shift;
         if (top >= p.from && b < (uint32_t)p.bins) atomicAdd(&s.counts[b], (uint32_t)E);
+        if (SUM != NONE && top >= p.sum_from) sum += E * whole(top);
         continue;
       }
     }
@@ -848,15 +849,16 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     }
     b.sync_row();
   };
-  auto count_bins = [&](uint32_t base, int shift, int bins) {
+  auto count_bins = [&](uint32_t base, int shift, int bins, bool sum) {
     for (int i = tid; i < bins; i += THREADS) s.counts[i] = 0;
     __syncthreads();
-    pass<COUNT_BINS, NONE>(b.x, s, Pass{NEVER, b.least_e, INF, base, shift, bins});
+    if (sum) b.push_sums(pass<COUNT_BINS, FROM>(b.x, s, Pass{b.least_e, b.least_e, INF, base, shift, bins}));
+    else pass<COUNT_BINS, NONE>(b.x, s, Pass{NEVER, b.least_e, INF, base, shift, bins});
     b.sync_row();
     add_bins(bins, false, base, shift);
   };
   auto first_bins = [&](Locate how, u64 want, u64 row_sum) {
-    if (!hist) count_bins(KEY_ONE, SHIFT, BINS);
+    if (!hist) count_bins(KEY_ONE, SHIFT, BINS, false);
     hist = 1;
     locate(s, how, BINS, want, 0, 0, row_sum);
   };
@@ -946,7 +948,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
       base = base >> shift << shift;
       const int bins = (int)((end - base + (1u << shift) - 1) >> shift);
       if (by_n) {
-        count_bins(base, shift, bins);
+        count_bins(base, shift, bins, false);
         locate(s, BY_COUNT, bins, want, before_n, 0, 0);
         before_n = s.bin_before;
       } else {
@@ -963,27 +965,16 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
       end = base + (1u << shift);
     }
   };
-  u64 row_sum = 0;
-  if (k == V) {
-    b.push_sums(pass<NOTHING, FROM>(b.x, s, Pass{b.least_e, NEVER, NEVER, 0, 0, 0}));
-    b.sync_row();
-    row_sum = total = b.row_total();
-    b.sync_row();
-  } else {
+  // the first histogram, and the row's sum where it is wanted
+  count_bins(KEY_ONE, SHIFT, BINS, top_p < 1.f);
+  hist = 1;
+  const u64 row_sum = total = b.row_total();
+  if (k < V) {
     // fewer than k tokens may be left by min-p
-    count_bins(KEY_ONE, SHIFT, BINS);
-    hist = 1;
     uint32_t n = 0;
     for (int i = tid; i < BINS; i += THREADS) n += s.red_n[i];
     n = block_all(n, OpSum(), s.scan_n);
-    const bool cuts = n > (uint32_t)k;
-    if (!cuts || top_p < 1.f) {
-      b.push_sums(pass<NOTHING, FROM>(b.x, s, Pass{b.least_e, NEVER, NEVER, 0, 0, 0}));
-      b.sync_row();
-      row_sum = total = b.row_total();
-      b.sync_row();
-    }
-    if (cuts) {
+    if (n > (uint32_t)k) {
       first_bins(BY_COUNT, k, 0);
       list_if_few();
       prefix_end(true, k);
