@@ -273,13 +273,15 @@ def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temp
 # calls cost a few microseconds of device time, so these call the library
 # without a layer in between.
 
-_codes = {}          # torch dtype -> tt_dtype; filled with the first tensor
+_codes = {}          # torch dtype -> tt_dtype; filled with the first use of torch
+_torch = None        # the module, which this one does not need for anything else
 
 
-def _torch():
+def _load_torch():
+    global _torch
     import torch
-    if not _codes:
-        _codes.update({torch.float32: TT_F32, torch.float16: TT_F16, torch.bfloat16: TT_BF16})
+    _codes.update({torch.float32: TT_F32, torch.float16: TT_F16, torch.bfloat16: TT_BF16})
+    _torch = torch
     return torch
 
 
@@ -288,10 +290,7 @@ def _matrix(x, what, rows=None, cols=None):
     column stride."""
     code = _codes.get(x.dtype)
     if code is None:
-        _torch()
-        code = _codes.get(x.dtype)
-        if code is None:
-            raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
+        raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
     shape = x.shape
     if len(shape) != 2 or not x.is_cuda or (rows is not None and shape[0] != rows) or \
             (cols is not None and shape[1] != cols):
@@ -304,10 +303,12 @@ def _matrix(x, what, rows=None, cols=None):
     return code, n, d, (s0 if n > 1 else d)
 
 
-def _vector(x, what, dtype, n=None):
-    """The address of a contiguous 1-D CUDA tensor, or None."""
+def _vector(x, what, dtype, n=None, optional=False):
+    """The address of a contiguous 1-D CUDA tensor (or None where it is optional)."""
     if x is None:
-        return None
+        if optional:
+            return None
+        raise ValueError("%s: a tensor wanted" % what)
     if x.dtype != dtype or not x.is_cuda or x.dim() != 1 or (n is not None and x.shape[0] != n) or \
             not x.is_contiguous():
         raise ValueError("%s: a contiguous CUDA tensor %s [%s] wanted, got %s %s on %s" % (
@@ -315,36 +316,49 @@ def _vector(x, what, dtype, n=None):
     return x.data_ptr()
 
 
+def _new(torch, rows, cols, dtype, device, what):
+    """An output of its own: the tensor and its dtype code."""
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, dtype))
+    return torch.empty((rows, cols), dtype=dtype, device=device), code
+
+
 def _on(torch, stream, device, *tensors):
     """The stream's address.  Tensors allocated here come from the current
     stream's pool: another stream waits for it and keeps them."""
+    if torch._C._cuda_getDevice() != device.index:
+        raise ValueError("the tensors are on %s, which is not the current device" % device)
     current = torch._C._cuda_getCurrentRawStream(device.index)
     if stream is None:
         return current
     raw = _stream(stream)
-    if raw != current:
+    mine = [t for t in tensors if t is not None]
+    if raw != current and mine:
         s = torch.cuda.ExternalStream(raw, device)
         s.wait_stream(torch.cuda.current_stream(device))
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+        for t in mine:
+            t.record_stream(s)
     return raw
 
 
 def embed(ids, table, scale=1.0, n_ids=None, dtype=None, out=None, status=None, stream=None):
     """scale * table[ids] (zero rows for padding): out [len(ids), dim] of
     `dtype` (the table's if None).  n_ids: a device int64 count."""
-    torch = _torch()
+    torch = _torch or _load_torch()
     pi = _vector(ids, "ids", torch.int32)
     t, vocab, dim, ts = _matrix(table, "table")
     n = ids.shape[0]
+    device = table.device
     mine = None
     if out is None:
-        out = mine = torch.empty((n, dim), dtype=dtype or table.dtype, device=table.device)
-    o, _, _, os_ = _matrix(out, "out", n, dim)
-    _check(lib().tt_embed(pi, n, None if n_ids is None else _vector(n_ids, "n_ids", torch.int64, 1), table.data_ptr(),
-                          t, vocab, dim, ts, scale, out.data_ptr(), o, os_, _vector(status, "status", torch.int32),
-                          _on(torch, stream, table.device, mine)), "tt_embed")
+        out, o = _new(torch, n, dim, dtype or table.dtype, device, "dtype")
+        mine, os_ = out, dim
+    else:
+        o, _, _, os_ = _matrix(out, "out", n, dim)
+    _check(lib().tt_embed(pi, n, _vector(n_ids, "n_ids", torch.int64, 1, True), table.data_ptr(), t, vocab, dim, ts, scale,
+                          out.data_ptr(), o, os_, _vector(status, "status", torch.int32, 1, True),
+                          _on(torch, stream, device, mine)), "tt_embed")
     return out
 
 
@@ -352,7 +366,7 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
                status=None, stream=None):
     """The gradient of embed: [n_vocab, dim] of `dtype` (float32 if None), the
     scaled sums of dout's rows by ID; with accumulate, added to `out`."""
-    torch = _torch()
+    torch = _torch or _load_torch()
     pi = _vector(ids, "ids", torch.int32)
     n = ids.shape[0]
     d, _, dim, ds = _matrix(dout, "dout", n)
@@ -360,15 +374,17 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
         raise ValueError("accumulate needs out")
     mine = scratch = None
     if out is None:
-        out = mine = torch.empty((n_vocab, dim), dtype=dtype or torch.float32, device=dout.device)
-    o, _, _, os_ = _matrix(out, "out", n_vocab, dim)
+        out, o = _new(torch, n_vocab, dim, dtype or torch.float32, dout.device, "dtype")
+        mine, os_ = out, dim
+    else:
+        o, _, _, os_ = _matrix(out, "out", n_vocab, dim)
     if workspace is None:
         workspace = scratch = torch.empty(max(lib().tt_embed_grad_workspace(n, n_vocab, dim), 16), dtype=torch.uint8,
                                           device=dout.device)
-    _check(lib().tt_embed_grad(pi, n, None if n_ids is None else _vector(n_ids, "n_ids", torch.int64, 1),
+    _check(lib().tt_embed_grad(pi, n, _vector(n_ids, "n_ids", torch.int64, 1, True),
                                dout.data_ptr(), d, dim, ds, scale, out.data_ptr(), o, n_vocab, os_, bool(accumulate),
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _vector(status, "status", torch.int32),
+                               _vector(status, "status", torch.int32, 1, True),
                                _on(torch, stream, dout.device, mine, scratch)), "tt_embed_grad")
     return out
 
@@ -376,9 +392,9 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
 def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, status=None, stream=None):
     """Next-token loss of each row: (loss, lse), and with want_grad or dlogits
     (which may be logits itself) the logits' gradient as a third."""
-    torch = _torch()
+    torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
-    pt, pg = _vector(targets, "targets", torch.int32, n), _vector(row_grads, "row_grads", torch.float32, n)
+    pt, pg = _vector(targets, "targets", torch.int32, n), _vector(row_grads, "row_grads", torch.float32, n, True)
     loss = torch.empty(n, dtype=torch.float32, device=logits.device)
     lse = torch.empty(n, dtype=torch.float32, device=logits.device)
     mine = None
@@ -386,22 +402,23 @@ def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, s
         dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
     d, ds, pd = t, vocab, None
     if dlogits is not None:
-        d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
+        if mine is None:
+            d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
         pd = dlogits.data_ptr()
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
     _check(lib().tt_token_loss(logits.data_ptr(), t, n, vocab, ls, pt, loss.data_ptr(), lse.data_ptr(), pg, pd, ds,
-                               _vector(status, "status", torch.int32),
+                               _vector(status, "status", torch.int32, 1, True),
                                _on(torch, stream, logits.device, loss, lse, mine)), "tt_token_loss")
     return (loss, lse) if dlogits is None else (loss, lse, dlogits)
 
 
 def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=None, stream=None):
     """The gradient of token_loss from the lse that it returned."""
-    torch = _torch()
+    torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
     pt, pl = _vector(targets, "targets", torch.int32, n), _vector(lse, "lse", torch.float32, n)
-    pg = _vector(row_grads, "row_grads", torch.float32, n)
+    pg = _vector(row_grads, "row_grads", torch.float32, n, True)
     mine = None
     if dlogits is None:
         dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
@@ -409,7 +426,7 @@ def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=N
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
     _check(lib().tt_token_loss_grad(logits.data_ptr(), t, n, vocab, ls, pt, pl, pg, dlogits.data_ptr(), ds,
-                                    _vector(status, "status", torch.int32),
+                                    _vector(status, "status", torch.int32, 1, True),
                                     _on(torch, stream, logits.device, mine)), "tt_token_loss_grad")
     return dlogits
 
@@ -417,18 +434,16 @@ def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=N
 def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, status=None, stream=None):
     """One token ID drawn from each row: (ids int32, logprobs float32).  The
     parameters are device tensors with an entry a row, or None (off)."""
-    torch = _torch()
+    torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
     f = torch.float32
     pu = _vector(uniform, "uniform", f, n)
-    if pu is None:
-        raise ValueError("uniform: a tensor wanted")
     ids = torch.empty(n, dtype=torch.int32, device=logits.device)
     logprobs = torch.empty(n, dtype=f, device=logits.device)
-    _check(lib().tt_sample(logits.data_ptr(), t, n, vocab, ls, pu, _vector(temperature, "temperature", f, n),
-                           _vector(top_k, "top_k", torch.int32, n), _vector(top_p, "top_p", f, n),
-                           _vector(min_p, "min_p", f, n), ids.data_ptr(), logprobs.data_ptr(),
-                           _vector(status, "status", torch.int32), _on(torch, stream, logits.device, ids, logprobs)),
+    _check(lib().tt_sample(logits.data_ptr(), t, n, vocab, ls, pu, _vector(temperature, "temperature", f, n, True),
+                           _vector(top_k, "top_k", torch.int32, n, True), _vector(top_p, "top_p", f, n, True),
+                           _vector(min_p, "min_p", f, n, True), ids.data_ptr(), logprobs.data_ptr(),
+                           _vector(status, "status", torch.int32, 1, True), _on(torch, stream, logits.device, ids, logprobs)),
            "tt_sample")
     return ids, logprobs
 

@@ -29,12 +29,14 @@ typedef unsigned long long u64;
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int HELD = 96 * 1024;                   // bytes of a row a block holds, two blocks an SM,
-constexpr int HELD_BINS = 180 * 1024;             // and in the second kernel, one an SM
+constexpr int HELD_BINS = 160 * 1024;             // and in the second kernel, one an SM
 constexpr int PENDING = -2, CLAIMED = -3;         // in the place of an ID that the second kernel writes
 constexpr int GROUPS = 128;                       // groups of threads a row's maxima are taken over
 constexpr int MOST_LISTED = GROUPS * 3 / 4;       // the largest top-k that a list is made for
 constexpr int LIST = THREADS;                     // tokens one block sorts
 constexpr int LONG_LIST = 1792;                   // tokens worth a list of their own for the later passes
+constexpr int RANGE = 1024;                       // tokens of a range that are ranked and not divided further, by
+constexpr int RANGE_FEW = 512;                    // clusters of 4 or 8 blocks, and by fewer
 constexpr int SHIFT = 17;                         // first histogram: 64 bins an octave
 constexpr int BINS = (40 << (23 - SHIFT)) + 1;    // weights 1 .. 2^40
 constexpr int FINER_BINS = 640;                   // of a range
@@ -165,6 +167,8 @@ struct Shared {
 };
 
 struct SharedBins : Shared {
+  u64 range[RANGE];                 // the block's tokens of a range
+  ulonglong2 all_range[RANGE];      // the row's, and their weights
   u64 scan2[WARPS];
   uint32_t scan_n[WARPS];
   int n_long;
@@ -221,7 +225,7 @@ template <class T> struct Row {
 };
 
 // What a pass does with powers in [from, to).
-enum Act { NOTHING, PUSH, PUSH_LONG, COUNT_BINS, SUM_BINS, LOWEST_ID, COUNT };
+enum Act { NOTHING, PUSH, PUSH_RANGE, PUSH_LONG, COUNT_BINS, SUM_BINS, LOWEST_ID, COUNT };
 // Which weights it adds: all (those below 1 are 0), or from `sum_from` on.
 enum Sums { NONE, ALL, FROM };
 
@@ -243,6 +247,8 @@ template <int ACT, class S> __device__ __forceinline__ void act_on(S &s, const P
     if (*(volatile int *)&s.n_list > LIST) return;            // too many already
     const int n = atomicAdd(&s.n_list, 1);
     if (n < LIST) s.list[n] = list_key(key_of(e), j);
+  } else if constexpr (ACT == PUSH_RANGE) {
+    s.range[atomicAdd(&s.n_list, 1)] = list_key(key_of(e), j);
   } else if constexpr (ACT == PUSH_LONG) {
     s.long_list[atomicAdd(&s.n_long, 1)] = list_key(key_of(e), j);
   } else if constexpr (ACT == SUM_BINS) {
@@ -432,24 +438,32 @@ enum Locate { BY_COUNT, BY_SUM, BETWEEN };
 __device__ __noinline__ void locate(SharedBins &s, Locate how, int bins, u64 want, uint32_t before_n, u64 above, u64 row_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (bins + THREADS - 1) / THREADS;
   const int b0 = bins - 1 - tid * per, b1 = max(-1, b0 - per);      // this thread's, falling
-  auto sums = [&](int b, u64 &least, u64 &most) {
+  // a bin's sum is at least and at most ...: it holds whole weights, from its
+  // base on and below the next one's, which `next` hands down
+  auto base_of = [&](int b) {
+    const uint32_t key = KEY_ONE + ((uint32_t)b << SHIFT);
+    const int ex = (int)(key >> 23) - 150;
+    const u64 mant = (key & 0x7FFFFFu) | 0x800000u;
+    return ex >= 0 ? mant << ex : mant >> -ex;
+  };
+  auto sums = [&](int b, u64 &next, u64 &least, u64 &most) {
     if (how == BY_COUNT) {
       least = most = s.red_n[b];
     } else if (how == BY_SUM) {
       least = most = s.red_sum[b];
     } else {
-      // a bin holds whole weights: from its base on, below the next one's
-      const uint32_t key = KEY_ONE + ((uint32_t)b << SHIFT);
-      const u64 low = key_whole(key), next = b == BINS - 1 ? low : max(low, key_whole(key + (1u << SHIFT)));
+      const u64 low = base_of(b);
       least = s.red_n[b] * low;
-      most = s.red_n[b] * next;
+      most = s.red_n[b] * (b == BINS - 1 ? low : next);
+      next = low;
     }
   };
+  u64 next = how == BETWEEN ? base_of(b0 + 1) : 0;
   uint32_t n = 0;
   u64 low = 0, high = 0;
   for (int b = b0; b > b1; --b) {
     u64 l, h;
-    sums(b, l, h);
+    sums(b, next, l, h);
     n += s.red_n[b];
     low += l;
     high += h;
@@ -481,9 +495,10 @@ __device__ __noinline__ void locate(SharedBins &s, Locate how, int bins, u64 wan
   // a sum is at least what is known from above, or the row's less what may be below; at most ...
   auto at_least = [&](u64 l, u64 h) { return how == BETWEEN ? max((long long)l, (long long)(row_sum + h - all_h)) : (long long)l; };
   auto at_most = [&](u64 l, u64 h) { return how == BETWEEN ? min((long long)h, (long long)(row_sum + l - all_l)) : (long long)h; };
+  if (how == BETWEEN) next = base_of(b0 + 1);
   for (int b = b0; b > b1; --b) {
     u64 l, h;
-    sums(b, l, h);
+    sums(b, next, l, h);
     if (at_most(pl, ph) < t && at_most(pl + l, ph + h) >= t) {
       s.bin[1] = b;
       s.bin_before = pn;
@@ -643,16 +658,19 @@ template <class T, class S> struct Block {
     }
     return t;
   }
-  // the blocks' lists, one token a thread in the first
-  __device__ __forceinline__ u64 gather(int &n) const {
-    u64 key = 0;
-    n = 0;
-    for (int r = 0; r < C; ++r) {
-      const int more = s.n_lists[r];
-      if (tid >= n && tid < n + more) key = at(s.list, r)[tid - n];
-      n += more;
-    }
-    return key;
+  // token i of the blocks' lists one behind another; 0 behind the last
+  __device__ __forceinline__ u64 listed(u64 *list, int i) const {
+    int r = 0;
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (r == k && r < C - 1 && i >= s.n_lists[k]) i -= s.n_lists[k], r = k + 1;
+    return i < s.n_lists[r] ? at(list, r)[i] : 0;
+  }
+  __device__ __forceinline__ int all_listed() const {
+    int n = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) n += r < C ? s.n_lists[r] : 0;
+    return n;
   }
   // The draw among what is kept, whose sums by the warps' parts are in s.seg:
   // that warp's vectors are divided among all warps, then a warp finds the
@@ -767,8 +785,8 @@ template <class T, class S> __device__ __forceinline__ bool sample_by_list(Block
     b.leave();
     return true;
   }
-  int n;
-  u64 key = b.gather(n);
+  const int n = n_list;
+  u64 key = b.listed(s.list, tid);
   b.arrive();
   const int kept_n = min(k, n);
   key = sort(s, key, n);
@@ -824,7 +842,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
   const float top_p = b.top_p;
   u64 end_key = 0, total = 0;                                 // keeps everything
   bool listed = false;                                        // s.long_list holds what may be kept
-  bool parts_known = false;                                   // s.seg has the sums of what lies above s.list
+  bool parts_known = false;                                   // s.seg has the sums of what lies above s.range
   // ---- the prefix's end by histograms of the weights' bits
   int hist = 0;                                             // 1: s.red_n holds the first histogram
   auto add_bins = [&](int bins, bool sums, uint32_t base, int shift) {
@@ -881,8 +899,9 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     for (;;) {
       const float from_e = fmaxf(b.least_e, least_power(base)), above_e = fmaxf(b.least_e, least_power(end));
       __syncthreads();
-      if (n_range <= LIST) {
-        // the tokens that are left, sorted in the first block
+      if (n_range <= (C >= 4 ? RANGE : RANGE_FEW)) {
+        // The tokens that are left, in every block; each ranks its share: what
+        // is before a token, and their sum, by as many threads as there are.
         if (tid == 0) s.n_list = 0;
         __syncthreads();
         u64 above = 0;
@@ -891,23 +910,48 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
             const u64 key = s.long_list[i];
             const float e = __uint_as_float((uint32_t)(key >> 32)) * (1.f / ONE);
             if (e >= above_e) above += whole(e);
-            else if (e >= from_e) s.list[atomicAdd(&s.n_list, 1)] = key;
+            else if (e >= from_e) s.range[atomicAdd(&s.n_list, 1)] = key;
           }
         } else {
-          above = pass<PUSH, FROM>(b.x, s, Pass{above_e, from_e, above_e, 0, 0, 0});
+          above = pass<PUSH_RANGE, FROM>(b.x, s, Pass{above_e, from_e, above_e, 0, 0, 0});
         }
         b.push_sums(above);
-        if (tid == 0) b.at(s.n_lists, 0)[rank] = s.n_list;
+        if (tid < C) b.at(s.n_lists, tid)[rank] = s.n_list;
         b.sync_row();
-        if (rank == 0) {
-          int n;
-          u64 key = b.gather(n);
-          key = sort(s, key, n);
-          const u64 w = list_whole(key), before = sum_before(s, w) + b.row_total();
-          if (tid < n && (by_n ? before_n + tid + 1 == want : before < want && before + w >= want))
+        const u64 sum_above = b.row_total();
+        const int n = b.all_listed();
+        for (int i = tid; i < n; i += THREADS) {
+          const u64 key = b.listed(s.range, i);
+          s.all_range[i] = make_ulonglong2(key, list_whole(key));
+        }
+        __syncthreads();
+        const int each = (n + C - 1) >> a.cluster_log2;
+        int log2 = 0;
+        while (log2 < 5 && (each << (log2 + 1)) <= THREADS) ++log2;
+        const int per = 1 << log2;
+        for (int i0 = 0; i0 < each; i0 += THREADS >> log2) {
+          const int i = rank * each + i0 + (tid >> log2);
+          const bool there = i0 + (tid >> log2) < each && i < n;
+          const ulonglong2 own = there ? s.all_range[i] : make_ulonglong2(0, 0);
+          uint32_t rank_n = 0;                                // it among them
+          u64 sum_to = 0;
+          for (int o = tid & (per - 1); o < n; o += per) {
+            const ulonglong2 y = s.all_range[o];
+            if (y.x >= own.x) {
+              ++rank_n;
+              sum_to += y.y;
+            }
+          }
+          for (int o = 1; o < per; o <<= 1) {
+            rank_n += __shfl_xor_sync(~0u, rank_n, o);
+            sum_to += __shfl_xor_sync(~0u, sum_to, o);
+          }
+          rank_n += before_n;
+          sum_to += sum_above;
+          if (there && (tid & (per - 1)) == 0 && (by_n ? rank_n == want : sum_to >= want && sum_to - own.y < want))
             for (int r = 0; r < C; ++r) {
-              *b.at(&s.cut_key, r) = key;
-              *b.at(&s.cut_sum, r) = before + w;
+              *b.at(&s.cut_key, r) = own.x;
+              *b.at(&s.cut_sum, r) = sum_to;
             }
         }
         b.sync_row();
@@ -1017,7 +1061,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     } else if (parts_known) {
       // the sums of what lies above the sorted tokens, and those
       for (int i = tid; i < s.n_list; i += THREADS) {
-        const u64 key = s.list[i];
+        const u64 key = s.range[i];
         if (key >= end_key) atomicAdd(&s.seg[part_of(key)], list_whole(key));
       }
       __syncthreads();

@@ -147,3 +147,8 @@ def test_binding_refuses_tensors_that_do_not_fit():
             call()
     with pytest.raises(ValueError):
         tt._matrix(torch.zeros(4, 8, dtype=torch.float64), "x")
+    for call in (lambda: tt.embed(None, m), lambda: tt.token_loss(m, None), lambda: tt.sample(m, None)):
+        with pytest.raises(ValueError):      # what is not optional
+            call()
+    with pytest.raises(ValueError):
+        tt.embed_grad(ids, m, 8, accumulate=True)
