@@ -92,19 +92,35 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
   }
 }
 
-// rows that are not whole 16-byte groups: a warp a row, an element a lane
+// Rows that are not whole 16-byte groups: a warp a row, its lanes side by side,
+// eight loads ahead of the stores.  (Loads of one element an instruction keep it
+// at about half of the copy rate.)
 template <class TI, class TO>
 __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__restrict__ table, TO *__restrict__ out) {
+  constexpr int R = 8;
   const int64_t n = a.n_ids ? max((int64_t)0, min(*a.n_ids, a.max_ids)) : a.max_ids;
-  const int lane = threadIdx.x & 31;
-  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < n; row += (int64_t)gridDim.x * 8) {
-    const int32_t id = __ldg(a.ids + row);
-    const bool there = (uint32_t)id < (uint32_t)a.n_vocab;
-    if (!there && id >= 0 && lane == 0 && blockIdx.y == 0) op_status(a.status, TT_ERR_INVALID_ARG);
-    const TI *src = table + (there ? id : 0) * a.table_stride;
-    TO *dst = out + row * a.out_stride;
-    for (int64_t c = lane; c < a.dim; c += 32) dst[c] = from_f32<TO>(there ? to_f32(src[c]) * a.scale : 0.f);
+  const int lane = threadIdx.x & 31, dim = (int)a.dim;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= n) return;
+  const int32_t id = __ldg(a.ids + row);
+  const bool there = (uint32_t)id < (uint32_t)a.n_vocab;
+  if (!there && id >= 0 && lane == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+  const TI *src = table + (there ? id : 0) * a.table_stride;
+  TO *dst = out + row * a.out_stride;
+  int c = lane;
+  for (; c - lane + 32 * R <= dim; c += 32 * R) {
+    float v[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) v[j] = there ? to_f32(__ldg(src + c + j * 32)) * a.scale : 0.f;
+#pragma unroll
+    for (int j = 0; j < R; ++j) dst[c + j * 32] = from_f32<TO>(v[j]);
   }
+  float v[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) v[j] = there && c + j * 32 < dim ? to_f32(__ldg(src + c + j * 32)) * a.scale : 0.f;
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (c + j * 32 < dim) dst[c + j * 32] = from_f32<TO>(v[j]);
 }
 
 // ============================================================ tt_embed_grad
@@ -394,40 +410,37 @@ __device__ __forceinline__ int64_t tokens_before(const int32_t *keys, int64_t n,
   return warp_search(n, [&](int64_t i) { return i + keys[i] < place; });
 }
 
-// how a thread's columns lie: eight side by side, or four `group` apart
+// how a thread's columns lie: eight side by side, or four 32 apart (a warp's 128)
 template <class T, int COLS> struct Cols;
 template <class T> struct Cols<T, 8> {
   Raw8<T> raw;
-  __device__ __forceinline__ void load(const T *row, int c, int, int) { load_raw(row + c, raw); }
+  __device__ __forceinline__ void load(const T *row, int) { load_raw(row, raw); }
   __device__ __forceinline__ void f32(float v[8]) const { raw_f32(raw, v); }
-  static __device__ __forceinline__ void store(T *row, int c, int, int, float v[8], bool accumulate) {
+  static __device__ __forceinline__ void store(T *row, int, float v[8], bool accumulate) {
     if (accumulate) {
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = to_f32(row[c + j]);
+      for (int j = 0; j < 8; ++j) o[j] = to_f32(row[j]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += o[j];
     }
-    store8(row + c, v);
+    store8(row, v);
   }
 };
-template <class T> struct Cols<T, 4> {
+template <class T> struct Cols<T, 4> {              // `left`: columns from the thread's first on
   T raw[4];
-  __device__ __forceinline__ void load(const T *row, int c, int group, int dim) {
+  __device__ __forceinline__ void load(const T *row, int left) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw[j] = c + j * group < dim ? row[c + j * group] : from_f32<T>(0.f);
+    for (int j = 0; j < 4; ++j) raw[j] = j * 32 < left ? row[j * 32] : from_f32<T>(0.f);
   }
   __device__ __forceinline__ void f32(float v[4]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = to_f32(raw[j]);
   }
-  static __device__ __forceinline__ void store(T *row, int c, int group, int dim, float v[4], bool accumulate) {
+  static __device__ __forceinline__ void store(T *row, int left, float v[4], bool accumulate) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (c + j * group < dim) {
-        T *p = row + c + j * group;
-        *p = from_f32<T>(accumulate ? to_f32(*p) + v[j] : v[j]);
-      }
+      if (j * 32 < left) row[j * 32] = from_f32<T>(accumulate ? to_f32(row[j * 32]) + v[j] : v[j]);
   }
 };
 
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
   __syncthreads();
   const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
   const int dim = (int)a.dim, n_vocab = (int)a.n_vocab;
-  const int c = (int)blockIdx.y * a.cols + t * (COLS == 8 ? 8 : 1);
+  const int c = (int)blockIdx.y * a.cols + (COLS == 8 ? t * 8 : t / 32 * 128 + t % 32);
   if (sub >= a.workers) return;
   const bool mine = c < dim;                    // threads past the columns still fill
   // the first of [lo, hi) whose key is at least k
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (c + j * a.group < dim) p[j * a.group] = acc[j];
+        if (c + j * 32 < dim) p[j * 32] = acc[j];
     }
   };
   auto finish_to = [&](int k) {               // rows r .. k-1 end here
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
       float v[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) v[j] = acc[j] * a.scale;
-      if (mine) Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride, c, a.group, dim, v, a.accumulate);
+      if (mine) Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride + c, dim - c, v, a.accumulate);
     }
     if (head || any) ++r;
     head = any = false;
@@ -543,7 +556,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
     } else if (!a.tokens_only && mine) {
       for (; r < k; ++r) {
         float v[COLS] = {};
-        Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride, c, a.group, dim, v, false);
+        Cols<TO, COLS>::store(dtable + (int64_t)r * a.dtable_stride + c, dim - c, v, false);
       }
     }
     r = k;
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
     Cols<TI, COLS> v[BATCH];
 #pragma unroll
     for (int b = 0; b < BATCH; ++b)
-      if (mine && i + b < end) v[b].load(dout + (int64_t)s_pos[i + b] * a.dout_stride, c, a.group, dim);
+      if (mine && i + b < end) v[b].load(dout + (int64_t)s_pos[i + b] * a.dout_stride + c, dim - c);
 #pragma unroll
     for (int b = 0; b < BATCH; ++b)
       if (i + b < end) {
@@ -659,7 +672,8 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
     const int per = v ? 8 : 4;
     const int64_t threads = (dim + per - 1) / per;
     p.col_tiles[v] = (int)((threads + 255) / 256);
-    const int need = (int)((threads + p.col_tiles[v] - 1) / p.col_tiles[v]);
+    int need = (int)((threads + p.col_tiles[v] - 1) / p.col_tiles[v]);
+    if (!v) need = std::max(need, (int)std::min<int64_t>(dim, 32));      // its columns are 32 apart
     if (need > 128) {
       p.group[v] = (need + 31) / 32 * 32;
       p.workers[v] = 1;
