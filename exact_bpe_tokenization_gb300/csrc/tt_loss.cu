@@ -17,8 +17,6 @@ using namespace tt::ops;
 
 namespace {
 
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
 constexpr int HELD = 104 * 1024;                 // bytes of a row a block holds: two blocks an SM
 constexpr float LOG2E = 1.44269504f;
 constexpr float LOWEST = -3.402823466e38f;
@@ -70,19 +68,19 @@ struct Running {
 
 // GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
 constexpr int U = 4;                             // vectors a thread takes at a time
-constexpr int UC = 2, AHEAD = 6;                 // vectors a group of copies, groups ahead
+constexpr int UC = 4, AHEAD = 4;                 // vectors a group of copies, groups ahead
 
 // f(vector, whether all of the group's are there) for groups of `per` vectors
 // a thread between lo and hi: the tests of whole groups are left out.
 template <bool WHOLE> struct Whole { static constexpr bool value = WHOLE; };
-template <class F> __device__ __forceinline__ void groups(int lo, int hi, int per, F f) {
+template <int THREADS, class F> __device__ __forceinline__ void groups(int lo, int hi, int per, F f) {
   for (; lo + per * THREADS <= hi; lo += per * THREADS) f(lo + (int)threadIdx.x, Whole<true>{});
   if (lo < hi) f(lo + (int)threadIdx.x, Whole<false>{});
 }
 
-template <class T, int GRAD>
-__global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits, T *dlogits) {
-  constexpr int E = RowParts<T>::E;
+template <class T, int GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, const T *logits, T *dlogits) {
+  constexpr int E = RowParts<T>::E, WARPS = THREADS / 32;
   extern __shared__ uint4 s_row[];
   __shared__ float2 s_warp[WARPS], s_blocks[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -124,14 +122,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
     const float lt = there && rank == 0 && tid == 0 ? to_f32(l[t]) : 0.f;
     Running run;
     if (GRAD == 1)
-      groups(0, n_held, UC, [&](int v0, auto whole) {
+      groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
         copy_wait<AHEAD - 1>();
         fetch(v0 + AHEAD * UC * THREADS);
 #pragma unroll
         for (int u = 0; u < UC; ++u)
           if (whole.value || v0 + u * THREADS < n_held) run.add(s_row[v0 + u * THREADS], T{});
       });
-    groups(n_held, n, U, [&](int v0, auto whole) {
+    groups<THREADS>(n_held, n, U, [&](int v0, auto whole) {
       uint4 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -197,12 +195,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
         for (int i = 0; i < E; ++i) to[i] = from_f32<T>(v[i]);
       }
     };
-    groups(0, n_held, U, [&](int v0, auto whole) {
+    groups<THREADS>(0, n_held, U, [&](int v0, auto whole) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (whole.value || v0 + u * THREADS < n_held) write(s_row[v0 + u * THREADS], v0 + u * THREADS);
     });
-    groups(n_held, n, U, [&](int v0, auto whole) {
+    groups<THREADS>(n_held, n, U, [&](int v0, auto whole) {
       uint4 r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -216,20 +214,39 @@ __global__ void __launch_bounds__(THREADS, 2) k_loss(LossArgs a, const T *logits
   }
 }
 
-template <class T, int GRAD> struct Tag {};
+template <class T, int GRAD, int THREADS> struct Tag {};
 
-template <class T, int GRAD>
-void run_rows(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
+template <class T, int GRAD, int THREADS>
+void run_rows_by(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
   const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
   a.cluster = (int)std::min<int64_t>(8, (bytes + HELD - 1) / HELD);
   // few rows: spread each over more blocks, down to 16 KB a block
   while (a.cluster <= 4 && n_rows * a.cluster * 2 <= 2 * 152 && bytes >= a.cluster * 2 * 16384) a.cluster *= 2;
   const int64_t each = ((bytes + 15) / 16 + a.cluster - 1) / a.cluster;
   a.held = GRAD == 1 ? (int)std::min<int64_t>(each, HELD / 16) : 0;
-  auto k = k_loss<T, GRAD>;
+  auto k = k_loss<T, GRAD, THREADS>;
   const size_t shared = (size_t)a.held * 16;
-  if (GRAD == 1 && allow_shared<Tag<T, GRAD>>(k, HELD)) return;     // (the error is kept)
+  if (GRAD == 1 && allow_shared<Tag<T, GRAD, THREADS>>(k, HELD)) return;     // (the error is kept)
   launch_cluster(k, dim3((unsigned)(n_rows * a.cluster)), THREADS, shared, a.cluster, false, stream, a, (const T *)logits, (T *)dlogits);
+}
+
+// A short row is little work behind a block's start, its barrier and its end, so
+// that small blocks, of which more share an SM, are faster.  Rows and gradients
+// in bfloat16, us for 32, 128, 256, 512 threads:
+//   32768 x   257     23    79   161   378
+//   32768 x  1024     33    85   166   387
+//   32768 x  4096     88   119   193   406
+//   32768 x  8192    182   165   236   451
+//    4096 x 16384     70    47    48    78
+//    4096 x 24000    120    70    62    88
+//    4096 x 50257    426   174   139   139
+//    4096 x 100256   855   359   291   290
+// (32-bit rows, and fewer of them, divide at about the same bytes.)
+template <class T, int GRAD> void run_rows(const LossArgs &a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
+  const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
+  if (bytes <= 4096) run_rows_by<T, GRAD, 32>(a, n_rows, logits, dlogits, stream);
+  else if (bytes <= 32768) run_rows_by<T, GRAD, 128>(a, n_rows, logits, dlogits, stream);
+  else run_rows_by<T, GRAD, 256>(a, n_rows, logits, dlogits, stream);
 }
 
 tt_status run_loss(const void *d_logits, int32_t type, int64_t n_rows, const LossArgs &a, void *d_dlogits,

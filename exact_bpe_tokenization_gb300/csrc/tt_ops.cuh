@@ -218,9 +218,10 @@ template <class T> struct RowParts {
     vecs = (n - lead) / E;
     rest = n - lead - vecs * E;
   }
-  // the scalar element of a thread of the block that has them, or -1
+  // the scalar element of a thread of the block's first warp (at most seven lie
+  // ahead of the vectors and seven behind them), or -1
   __device__ __forceinline__ int scalar(int tid) const {
-    return tid < lead ? tid : tid >= 32 && tid < 32 + rest ? lead + vecs * E + tid - 32 : -1;
+    return tid < lead ? tid : tid >= 16 && tid < 16 + rest ? lead + vecs * E + tid - 16 : -1;
   }
 };
 

@@ -699,3 +699,34 @@ def test_loss_and_lookup_of_many_rows(tt):
     ids = torch.randint(0, 300, (100001,), generator=gen(3), device="cuda", dtype=torch.int32)
     table = rows_of(300, 264, "float16", gen(4))
     assert torch.equal(tt.embed(ids, table), table[ids.long()])
+
+
+@pytest.mark.parametrize("name,vocab", [(name, edge // size + more) for name, size in (("float32", 4), ("bfloat16", 2))
+                                        for edge in (4096, 32768) for more in (-1, 0, 1)] + [("float16", 16385), ("float32", 33)])
+@pytest.mark.parametrize("shift", [0, 3])
+def test_token_loss_at_the_sizes_that_choose_the_threads(tt, name, vocab, shift):
+    rng = np.random.default_rng(vocab)
+    x = rows_of(9, vocab, name, gen(vocab), vocab + 2, shift)
+    targets = rng.integers(0, vocab, 9).astype(np.int32)
+    targets[:3] = 0, vocab - 1, -1
+    out = check_loss(tt, x, targets, None, name)
+    t = torch.from_numpy(targets).cuda()
+    alone = tt.token_loss(x, t)
+    assert torch.equal(alone[0], out[0]) and torch.equal(alone[1], out[1])
+    assert torch.equal(tt.token_loss_grad(x, t, out[1]), out[2])
+    tt.token_loss(x, t, dlogits=x)
+    assert torch.equal(x, out[2])
+
+
+@pytest.mark.parametrize("dim", [9, 31, 33, 129, 1025])
+@pytest.mark.parametrize("name", DTYPES)
+def test_embed_grad_of_odd_widths(tt, dim, name):
+    ids = torch.randint(-1, 40, (900,), generator=gen(dim), device="cuda", dtype=torch.int32)
+    dout = rows_of(900, dim, name, gen(dim), dim + 1, 1)
+    got = tt.embed_grad(ids, dout, 40)
+    k = ids.cpu().numpy()
+    rows, want, size = host(dout), np.zeros((40, dim)), np.zeros((40, dim))
+    np.add.at(want, k[k >= 0], rows[k >= 0])
+    np.add.at(size, k[k >= 0], np.abs(rows[k >= 0]))
+    count = np.bincount(k[k >= 0], minlength=40)[:, None]
+    assert np.all(np.abs(host(got) - want) <= plain.EPS * 1.01 * (count + 3) * size)
