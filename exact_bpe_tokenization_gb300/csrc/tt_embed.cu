@@ -410,12 +410,33 @@ __device__ __forceinline__ int64_t tokens_before(const int32_t *keys, int64_t n,
   return warp_search(n, [&](int64_t i) { return i + keys[i] < place; });
 }
 
-// how a thread's columns lie: eight side by side, or four 32 apart (a warp's 128)
+// A thread's columns: eight side by side, or four 32 apart (a warp's 128).  How
+// its parts of AHEAD rows are kept in flight: what ends a row is much code, and a
+// batch in registers has a copy of it for each of its rows, which soon cost more
+// instruction fetches than the sums; parts that wait in shared memory, where
+// nobody else reads, go through one copy.  us for 100,256 rows of (columns,
+// tokens, type of dout; a batch, copied to shared memory, a batch put there):
+//   256  200,000 bfloat16   86   72   77     1024 60,000 bfloat16 106   87   97
+//   256  200,000 float      84  102   89     1024 60,000 float    140  160  142
+//   641  200,000 bfloat16  262    -  163      641 200,000 float   293  193  176
+enum Ahead { IN_REGISTERS, COPIED, STAGED };
+constexpr int SUM_THREADS = 256;                  // at most
 template <class T, int COLS> struct Cols;
 template <class T> struct Cols<T, 8> {
-  Raw8<T> raw;
-  __device__ __forceinline__ void load(const T *row, int) { load_raw(row, raw); }
-  __device__ __forceinline__ void f32(float v[8]) const { raw_f32(raw, v); }
+  typedef uint4 Part;
+  static constexpr Ahead HOW = sizeof(T) == 4 ? IN_REGISTERS : COPIED;
+  static constexpr int AHEAD = 16 / sizeof(T), PARTS = sizeof(T) / 2;
+  // (`left`: columns from the thread's first on)
+  static __device__ __forceinline__ void load(Part raw[PARTS], const T *row, int) {
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) raw[j] = __ldg(reinterpret_cast<const uint4 *>(row) + j);
+  }
+  static __device__ __forceinline__ void f32(const Part raw[PARTS], float v[8]) {
+    Raw8<T> r;
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) r.w[j] = raw[j];
+    raw_f32(r, v);
+  }
   static __device__ __forceinline__ void store(T *row, int, float v[8], bool accumulate) {
     if (accumulate) {
       float o[8];
@@ -427,13 +448,15 @@ template <class T> struct Cols<T, 8> {
     store8(row, v);
   }
 };
-template <class T> struct Cols<T, 4> {              // `left`: columns from the thread's first on
-  T raw[4];
-  __device__ __forceinline__ void load(const T *row, int left) {
+template <class T> struct Cols<T, 4> {
+  typedef T Part;
+  static constexpr Ahead HOW = STAGED;
+  static constexpr int AHEAD = 8, PARTS = 4;
+  static __device__ __forceinline__ void load(Part raw[4], const T *row, int left) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) raw[j] = j * 32 < left ? row[j * 32] : from_f32<T>(0.f);
   }
-  __device__ __forceinline__ void f32(float v[4]) const {
+  static __device__ __forceinline__ void f32(const Part raw[4], float v[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = to_f32(raw[j]);
   }
@@ -443,14 +466,19 @@ template <class T> struct Cols<T, 4> {              // `left`: columns from the 
       if (j * 32 < left) row[j * 32] = from_f32<T>(accumulate ? to_f32(row[j * 32]) + v[j] : v[j]);
   }
 };
+template <class In> constexpr int slot_bytes() {  // a block's
+  return In::HOW == IN_REGISTERS ? 0 : In::AHEAD * In::PARTS * (int)sizeof(typename In::Part) * SUM_THREADS;
+}
 
 constexpr int HALO = 64;
 constexpr int LONG_ROW = 6;                       // pieces, at least, of a row that a block joins
 
 template <class TI, class TO, int COLS>
-__global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__restrict__ dout, TO *__restrict__ dtable) {
-  constexpr int BATCH = COLS == 8 ? 16 / sizeof(TI) : 8;        // rows in flight a thread
-  extern __shared__ int32_t s_tok[];              // keys, then places in dout, HALO more on both sides
+__global__ void __launch_bounds__(SUM_THREADS, 4) k_grad_sum(GradArgs a, const TI *__restrict__ dout, TO *__restrict__ dtable) {
+  typedef Cols<TI, COLS> In;
+  // the threads' parts ahead; then keys, and places in dout, HALO more on both sides
+  extern __shared__ uint4 s_ahead[];
+  int32_t *const s_tok = reinterpret_cast<int32_t *>(s_ahead) + slot_bytes<In>() / 4;
   __shared__ int64_t s_at[2];
   wait_for_last();
   let_next_start();
@@ -561,22 +589,63 @@ __global__ void __launch_bounds__(256, 4) k_grad_sum(GradArgs a, const TI *__res
     }
     r = k;
   };
-  for (; i < end; i += BATCH) {
-    Cols<TI, COLS> v[BATCH];
+  auto *const slots = reinterpret_cast<typename In::Part *>(s_ahead) + threadIdx.x;
+  auto from = [&](int at) { return dout + (int64_t)s_pos[at] * a.dout_stride + c; };
+  auto add = [&](int32_t k, const typename In::Part raw[In::PARTS]) {
+    if (r < k) finish_to(k);
+    float f[COLS];
+    In::f32(raw, f);
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b)
-      if (mine && i + b < end) v[b].load(dout + (int64_t)s_pos[i + b] * a.dout_stride + c, dim - c);
+    for (int j = 0; j < COLS; ++j) acc[j] += f[j];
+    any = true;
+  };
+  auto add_slot = [&](int slot) {
+    typename In::Part raw[In::PARTS];
 #pragma unroll
-    for (int b = 0; b < BATCH; ++b)
-      if (i + b < end) {
-        const int32_t k = s_key[i + b];
-        if (r < k) finish_to(k);
-        float f[COLS];
-        v[b].f32(f);
+    for (int j = 0; j < In::PARTS; ++j) raw[j] = slots[(slot * In::PARTS + j) * SUM_THREADS];
+    add(s_key[i], raw);
+  };
+  if constexpr (In::HOW == IN_REGISTERS) {
+    for (; i < end; i += In::AHEAD) {
+      typename In::Part raw[In::AHEAD][In::PARTS];
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) acc[j] += f[j];
-        any = true;
+      for (int b = 0; b < In::AHEAD; ++b)
+        if (mine && i + b < end) In::load(raw[b], from(i + b), dim - c);
+#pragma unroll
+      for (int b = 0; b < In::AHEAD; ++b)
+        if (i + b < end) add(s_key[i + b], raw[b]);
+    }
+  } else if constexpr (In::HOW == COPIED) {
+    auto fetch = [&](int at, int slot) {
+      if (mine && at < end) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(from(at));
+#pragma unroll
+        for (int j = 0; j < In::PARTS; ++j) copy_async(slots + (slot * In::PARTS + j) * SUM_THREADS, row + j);
       }
+      copy_group();
+    };
+#pragma unroll
+    for (int b = 0; b < In::AHEAD - 1; ++b) fetch(i + b, b);
+#pragma unroll 1
+    for (int slot = 0; i < end; ++i) {
+      copy_wait<In::AHEAD - 2>();
+      fetch(i + In::AHEAD - 1, slot ? slot - 1 : In::AHEAD - 1);        // into what was added last
+      add_slot(slot);
+      slot = slot + 1 < In::AHEAD ? slot + 1 : 0;
+    }
+    copy_wait<0>();
+  } else {
+    while (i < end) {
+      typename In::Part raw[In::AHEAD][In::PARTS];
+#pragma unroll
+      for (int b = 0; b < In::AHEAD; ++b) In::load(raw[b], from(min(i + b, end - 1)), dim - c);
+#pragma unroll
+      for (int b = 0; b < In::AHEAD; ++b)
+#pragma unroll
+        for (int j = 0; j < In::PARTS; ++j) slots[(b * In::PARTS + j) * SUM_THREADS] = raw[b][j];
+#pragma unroll 1
+      for (int b = 0; b < In::AHEAD && i < end; ++b, ++i) add_slot(b);
+    }
   }
   if (r < r_end) finish_to(r_end);
   if (any) {
@@ -646,6 +715,7 @@ bool grad_sizes_ok(int64_t max_ids, int64_t n_vocab, int64_t dim) {
 }
 
 template <int PASS, int KEYS> struct Place {};
+template <class TI, class TO, int COLS> struct Sum {};
 template <int N> struct Per { static constexpr int value = N; };
 
 struct GradPlan {
@@ -830,9 +900,15 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
       using TO = decltype(to);
       const dim3 grid((unsigned)p.blocks[v][tokens_only], (unsigned)p.col_tiles[v]);
       const unsigned threads = (unsigned)(p.group[v] * p.workers[v]);
-      const size_t shared = 4 * (4 * HALO + 2 * (size_t)p.items[v][tokens_only] * p.workers[v]);
-      auto sum = v ? k_grad_sum<TI, TO, 8> : k_grad_sum<TI, TO, 4>;
-      launch_cluster(sum, grid, threads, shared, 1, max_ids > 0, stream, a, (const TI *)d_dout, (TO *)d_dtable);
+      auto run = [&](auto cols) {
+        constexpr int COLS = decltype(cols)::value;
+        auto sum = k_grad_sum<TI, TO, COLS>;
+        const auto shared = [](int64_t items) { return slot_bytes<Cols<TI, COLS>>() + 4 * (4 * HALO + 2 * (size_t)items); };
+        if (allow_shared<Sum<TI, TO, COLS>>(sum, (int)shared(BLOCK_ITEMS))) return;        // (the error is kept)
+        launch_cluster(sum, grid, threads, shared(p.items[v][tokens_only] * p.workers[v]), 1, max_ids > 0, stream, a,
+                       (const TI *)d_dout, (TO *)d_dtable);
+      };
+      if (v) run(Per<8>{}); else run(Per<4>{});
       if (max_ids > 0)
         launch_cluster(k_grad_join<TO>, dim3((unsigned)std::min<int64_t>(152 * 2, p.blocks[v][tokens_only] * p.workers[v])), 1024, 0, 1, true, stream, a,
                        (TO *)d_dtable);
