@@ -1111,7 +1111,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
   b.draw(row, keep, r, total);
 }
 
-// Few rows: both in one launch, a cluster a row.
+// Rows that run at once: both in one launch, a cluster a row.
 template <class T>
 __global__ void __launch_bounds__(THREADS, 1) k_sample_few(const SampleArgs a, const T *__restrict__ logits) {
   __shared__ SharedBins s;
@@ -1201,10 +1201,15 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
   if (!array_ok(d_logits, type_size(type)) || !array_ok(d_uniform, 4) || !array_ok(d_out_ids, 4)) return TT_ERR_INVALID_ARG;
   SampleArgs a{n_vocab, logits_stride, d_uniform, d_temperature, d_top_k, d_top_p, d_min_p,
                d_out_ids, d_out_logprobs, d_status, 0, 0, n_rows};
-  // Blocks a row: as many as run at once for all rows (clusters of 8, 4 and 2
-  // fit 32, 72 and 152 times, two blocks an SM), of at least 8,192 elements
-  const int64_t at_once[4] = {INT64_MAX, 152, 72, 32};
-  while (a.cluster_log2 < 3 && (n_vocab >> (a.cluster_log2 + 1)) >= 8192 && n_rows <= at_once[a.cluster_log2 + 1]) ++a.cluster_log2;
+  // Blocks a row: as many as run at once for all rows, of at least 8,192
+  // elements.  Clusters of 8, 4, 2 and 1 blocks fit 15, 36, 76 and 152 times at
+  // one block an SM, and 32, 72, 152 and 304 times at two.
+  auto spread = [&](const int64_t at_once[4]) {
+    int log2 = 0;
+    while (log2 < 3 && (n_vocab >> (log2 + 1)) >= 8192 && n_rows <= at_once[log2 + 1]) ++log2;
+    return log2;
+  };
+  static const int64_t one_an_sm[4] = {152, 76, 36, 15}, two_an_sm[4] = {304, 152, 72, 32};
   with_type(type, [&](auto t) {
     using T = decltype(t);
     const int64_t vecs = (n_vocab * (int64_t)sizeof(T) + 15) / 16;
@@ -1214,16 +1219,37 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
       launch_cluster(k, dim3((unsigned)(clusters << a.cluster_log2)), THREADS, (size_t)a.held * 16, 1u << a.cluster_log2, chained,
                      stream, a, (const T *)d_logits);
     };
-    if ((d_top_k || d_top_p) && n_rows <= 16) {
+    if (!d_top_k && !d_top_p) {                               // a list, or no cut, always does
+      a.cluster_log2 = spread(two_an_sm);
+      launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
+      return;
+    }
+    // Rows that run at once, and whose parts are held to four fifths at least,
+    // in one launch.  us for it and for two kernels, rows of bfloat16, with a
+    // top-k of 50 and top-p, a top-k of 1000 and top-p, and a mixture of all:
+    //     8 x 100256    10   12     28   30     28   40
+    //    32 x 100256    11   16     31   72     31   42
+    //    76 x 100256    14   15     39   63     49   58
+    //   152 x 100256    19   21     53   98     75   64
+    //    76 x  32768    11   12      -    -     29   42
+    //   152 x   4352     8   10      -    -     25   37
+    // With less held it loses: 76 x 200255 floats 25 and 26, 94 and 103 us, 37 of
+    // them 25 and 23, 95 and 55.  So do rows that come in turn: 200 x 100256 take
+    // 36 and 28, 76 and 72 us.
+    a.cluster_log2 = spread(one_an_sm);
+    if (n_rows <= one_an_sm[0] && (vecs >> a.cluster_log2) * 16 <= HELD_BINS / 4 * 5) {
       launch(Few<T>{}, k_sample_few<T>, n_rows, HELD_BINS, false);
       return;
     }
+    a.cluster_log2 = spread(two_an_sm);
     launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
-    if (d_top_k || d_top_p) {
-      // one block an SM; as a rule a quarter of the rows is left
-      a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 3 : n_rows <= 288 ? 1 : 0;
-      launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
-    }
+    // One block an SM; as a rule a quarter of the rows is left.  us of the
+    // mixture for 8, 4, 2 and 1 blocks a row:
+    //    37 x 200255 float      55   70   95  147
+    //   256 x 100256 bfloat16  120   89   76   96
+    //   512 x 100256 bfloat16  186  133  120  115
+    a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 3 : n_rows <= 288 ? 1 : 0;
+    launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
   });
   return launched("tt_sample");
 }

@@ -730,3 +730,25 @@ def test_embed_grad_of_odd_widths(tt, dim, name):
     np.add.at(size, k[k >= 0], np.abs(rows[k >= 0]))
     count = np.bincount(k[k >= 0], minlength=40)[:, None]
     assert np.all(np.abs(host(got) - want) <= plain.EPS * 1.01 * (count + 3) * size)
+
+
+@pytest.mark.parametrize("n,vocab,name", [(152, 9001, "bfloat16"), (153, 9001, "float16"), (200, 3001, "float32"),
+                                          (37, 131072, "float32"), (64, 200255, "float32"), (15, 100256, "float32"),
+                                          (36, 100256, "bfloat16"), (76, 60001, "bfloat16")])
+def test_sample_on_both_sides_of_the_rules(tt, n, vocab, name):
+    """Peaked, flat, tied and masked rows, cut in every way, in the sizes that
+    decide how a row is divided and by which kernel it is drawn."""
+    rng = np.random.default_rng(n + vocab)
+    x = rows_of(n, vocab, name, gen(n), scale=3.0)
+    x[1::7] *= 0.1                                            # flat
+    x[2::7] = (x[2::7] * 0.5).round()                         # ties
+    x[3::7, vocab // 3:] = -math.inf
+    x[4::7, ::2] = math.nan
+    x[min(5, n - 1)] = -math.inf
+    x[min(6, n - 1), vocab // 2] = math.inf
+    p = dict(temperature=rng.choice([0.0, 0.7, 1.0, 1.5], n).astype(np.float32),
+             top_k=rng.choice([0, 0, 1, 40, 97, 700, vocab // 2], n).astype(np.int32),
+             top_p=rng.choice([1.0, 0.9, 0.4], n).astype(np.float32),
+             min_p=rng.choice([0.0, 0.0, 0.02], n).astype(np.float32))
+    pick = range(n) if n * vocab <= 2_000_000 else sorted(rng.choice(n, 24, replace=False).tolist() + [1, 2, 3, 4, 5, 6])
+    check_sample(tt, x, rng.random(n).astype(np.float32), p, pick)
