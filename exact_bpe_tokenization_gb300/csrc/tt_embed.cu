@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
 }
 
 // Rows that are not whole 16-byte groups: a warp a row, its lanes side by side,
-// eight loads ahead of the stores.  (Loads of one element an instruction keep it
-// at about half of the copy rate.)
+// eight loads ahead of the stores: 200,000 rows of 641 floats take 160 us (6.4
+// TB/s), of 641 bfloat16, at 64 bytes a warp's load, 106 us (4.8 TB/s).
 template <class TI, class TO>
 __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__restrict__ table, TO *__restrict__ out) {
   constexpr int R = 8;
@@ -132,11 +132,18 @@ __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__rest
 // stand before the tile.  The first pass's counts are a kernel of their own;
 // the second's are added up by the first pass as it places tokens in tiles.
 // With up to SUM_TILES tiles each block adds the earlier tiles' counts itself
-// (they come from L2); with more, a kernel scans them.
+// (they come from L2); with more, a kernel scans them.  Whole calls, 64 columns
+// into 100,256 rows, the one and the other: 8 tiles 23.4 and 25.8 us, 20 tiles
+// 26.4 and 26.2, 30 tiles 31.9 and 29.9.
+//
+// The sums are bound by memory, the sort by the latency of its kernels: 304,824
+// tokens of 2048 bfloat16 into 100,256 float rows take 375 us (2.07 GB, 83% of
+// the measured copy bandwidth), 335 of them the sums; 16,400 tokens of 1024
+// floats into 4,352 rows take 37 us, of which the bytes need 13.
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_BINS = 1 << 11;
-constexpr int SUM_TILES = 32;
+constexpr int SUM_TILES = 20;
 
 struct SortArgs {
   const int64_t *n_ids;
@@ -735,7 +742,10 @@ GradPlan grad_plan(int64_t max_ids, int64_t n_vocab, int64_t dim) {
   while ((n_vocab >> bits) != 0) ++bits;          // keys are 0 .. n_vocab
   p.bits[0] = (bits + 1) / 2;
   p.bits[1] = bits - p.bits[0];
-  p.per_thread = max_ids <= 32768 ? 2 : max_ids <= 1 << 20 ? 4 : 8;
+  // tokens a thread of the sort: 2, 4 and 8 take 23, 27 and 34 us for 8,191 tokens
+  // (of 64 columns), 37, 40 and 46 for 130,000, 43, 41 and 48 for 200,000, 194,
+  // 182 and 178 for 2,000,000
+  p.per_thread = max_ids <= 1 << 17 ? 2 : max_ids <= 1 << 20 ? 4 : 8;
   p.tiles = (int)((max_ids + SORT_THREADS * p.per_thread - 1) / (SORT_THREADS * p.per_thread));
   int64_t pieces = 0;
   for (int v = 0; v < 2; ++v) {
@@ -853,7 +863,8 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   if (max_ids == 0 && accumulate) return TT_OK;
   char *ws = (char *)d_workspace;
   // Rows that are mostly absent are cleared by blocks beside the sort's (8191 x
-  // 641 bf16 into 200,256 rows: 70 us, and 77 us where the sums write them);
+  // 641 bf16 into 200,256 rows, when this was chosen: 70 us, and 77 us where the
+  // sums write them; 61 us now);
   // with more tokens, rows written twice would cost more than that saves.
   const bool clear = !accumulate && max_ids > 0 && max_ids <= n_vocab / 4;
   const int tokens_only = accumulate || clear;

@@ -9,6 +9,13 @@
 // shared memory, and turned into gradients from there: a cluster of blocks
 // holds a row (two blocks an SM, so that one reads or writes while the other
 // computes).  What does not fit (rows above 832 KB) is read again, from L2.
+//
+// With gradients 4096 x 100256 bfloat16 take 289 us (1.64 GB, 85% of the measured
+// copy bandwidth) and 1023 x 200255 floats 297 us (82%).  A block reads, waits
+// for its cluster, and writes; its neighbour on the SM fills the wait, and not
+// all of it.  Rows of that size need clusters of 8, which leave a few SMs of
+// each group of them idle, but hold the row: with 4 blocks a row, half of it
+// comes from L2 a second time, and 323 us became 370.
 #include <algorithm>
 
 #include "tt_ops.cuh"
@@ -220,7 +227,9 @@ template <class T, int GRAD, int THREADS>
 void run_rows_by(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
   const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
   a.cluster = (int)std::min<int64_t>(8, (bytes + HELD - 1) / HELD);
-  // few rows: spread each over more blocks, down to 16 KB a block
+  // few rows: spread each over more blocks, down to 16 KB a block (1 x 100256
+  // bfloat16 7.8 us to 4.9, 16 rows 8.1 to 5.9, 64 rows 8.2 both ways; four blocks
+  // an SM instead of two make those 9.0)
   while (a.cluster <= 4 && n_rows * a.cluster * 2 <= 2 * 152 && bytes >= a.cluster * 2 * 16384) a.cluster *= 2;
   const int64_t each = ((bytes + 15) / 16 + a.cluster - 1) / a.cluster;
   a.held = GRAD == 1 ? (int)std::min<int64_t>(each, HELD / 16) : 0;

@@ -10,12 +10,21 @@
 // first: the row's maxima over 128 groups of threads are known from the first
 // pass, and the tokens at or above the q-th largest of them are at least q and
 // rarely twice as many.  If the prefix ends within the list (its count, or
-// its sum against the row's, says so), one block sorts the list.  The other rows
-// (a top-k above 96, flat rows) are left to a second kernel: a histogram of
-// the weights' bits over the cluster, 64 bins an octave, says between which
-// bins the prefix ends, and the few tokens there are sorted; bins that hold too
-// many are divided further.  Two kernels, since the second one's registers,
-// shared memory and cluster size would slow the first down by half.
+// its sum against the row's, says so), one block sorts the list.  For the other
+// rows (a top-k above 96, flat rows) a histogram of the weights' bits over the
+// cluster, 64 bins an octave, says between which bins the prefix ends, and the
+// few tokens there are sorted; bins that hold too many are divided further.
+// Where all rows run at once, a kernel does both; of more rows, a second kernel
+// does those that the first one left, since the registers, shared memory and
+// cluster size of the histograms would slow the lists down by half.
+//
+// 256 x 100256 bfloat16, whose bytes need 7.7 us, take 23 us with a temperature
+// alone (a pass that reads and one that sums, over one or two rows an SM) and 31
+// with a top-k of 50 and top-p.  A mixture, of which a quarter goes to the
+// histograms, takes 83: their kernel's 45 us are, for a row, 3 of reading, 10 of
+// the first histogram (an atomic in shared memory for each token of the row,
+// which twice the warps do not speed up), 4 to find the bins, and 20 for the
+// finer ones and the last tokens, passes and cluster barriers in turn.
 #include <algorithm>
 
 #include "tt_ops.cuh"

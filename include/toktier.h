@@ -460,7 +460,8 @@ tt_status tt_token_loss_grad(const void *d_logits, int32_t type, int64_t n_rows,
  *   d_top_k        device, int32 [n_rows]; <= 0 or >= n_vocab: off.  NULL: off.
  *   d_top_p        device, float [n_rows], each in [0, 1]; 1: off.  NULL: off.
  *   d_min_p        device, float [n_rows], each in [0, 1]; 0: off.  NULL: off.
- *   d_out_ids      device, int32 [n_rows].
+ *   d_out_ids      device, int32 [n_rows]; holds working values (negative) until
+ *                  the call's work on the stream is done.
  *   d_out_logprobs device, float [n_rows], or NULL: log(w[id] / K), the
  *                  logarithm of the probability with which it was drawn.
  * A row with nothing to draw (all -inf or NaN) gives ID -1 and logprob -inf.
