@@ -177,7 +177,7 @@ struct Shared {
 
 struct SharedBins : Shared {
   u64 range[RANGE];                 // the block's tokens of a range
-  ulonglong2 all_range[RANGE];      // the row's, and their weights
+  u64 all_range[RANGE], sorted_range[RANGE];      // the row's
   u64 scan2[WARPS];
   uint32_t scan_n[WARPS];
   int n_long;
@@ -443,47 +443,46 @@ __device__ __noinline__ u64 sort(Shared &s, u64 key, int n) {
 //             sum is its count times weights it bounds, added from above, or
 //             from below and taken from the row's sum
 enum Locate { BY_COUNT, BY_SUM, BETWEEN };
+template <Locate L> struct How { static constexpr Locate value = L; };
 
-__device__ __noinline__ void locate(SharedBins &s, Locate how, int bins, u64 want, uint32_t before_n, u64 above, u64 row_sum) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (bins + THREADS - 1) / THREADS;
-  const int b0 = bins - 1 - tid * per, b1 = max(-1, b0 - per);      // this thread's, falling
+template <Locate HOW, int PER>                    // PER bins a thread
+__device__ __noinline__ void locate(SharedBins &s, int bins, u64 want, uint32_t before_n, u64 above, u64 row_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b0 = bins - 1 - tid * PER;                        // this thread's first, falling
   // a bin's sum is at least and at most ...: it holds whole weights, from its
-  // base on and below the next one's, which `next` hands down
+  // base on and below the next one's
   auto base_of = [&](int b) {
     const uint32_t key = KEY_ONE + ((uint32_t)b << SHIFT);
     const int ex = (int)(key >> 23) - 150;
     const u64 mant = (key & 0x7FFFFFu) | 0x800000u;
     return ex >= 0 ? mant << ex : mant >> -ex;
   };
-  auto sums = [&](int b, u64 &next, u64 &least, u64 &most) {
-    if (how == BY_COUNT) {
-      least = most = s.red_n[b];
-    } else if (how == BY_SUM) {
-      least = most = s.red_sum[b];
+  uint32_t n[PER], mine = 0;
+  u64 least[PER], most[PER], low = 0, high = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = b0 - i;
+    n[i] = b >= 0 ? s.red_n[b] : 0;
+    if (HOW == BY_COUNT) {
+      least[i] = n[i];
+    } else if (HOW == BY_SUM) {
+      least[i] = b >= 0 ? s.red_sum[b] : 0;
     } else {
-      const u64 low = base_of(b);
-      least = s.red_n[b] * low;
-      most = s.red_n[b] * (b == BINS - 1 ? low : next);
-      next = low;
+      least[i] = n[i] * base_of(b);
+      most[i] = b == BINS - 1 ? least[i] : n[i] * base_of(b + 1);
     }
-  };
-  u64 next = how == BETWEEN ? base_of(b0 + 1) : 0;
-  uint32_t n = 0;
-  u64 low = 0, high = 0;
-  for (int b = b0; b > b1; --b) {
-    u64 l, h;
-    sums(b, next, l, h);
-    n += s.red_n[b];
-    low += l;
-    high += h;
+    if (HOW != BETWEEN) most[i] = least[i];
+    mine += n[i];
+    low += least[i];
+    high += most[i];
   }
-  uint32_t pn = n;
+  uint32_t pn = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(~0u, pn, o);
     if (lane >= o) pn += y;
   }
-  u64 pl = sum_of_lanes_before(low), ph = sum_of_lanes_before(high);
+  u64 pl = sum_of_lanes_before(low), ph = HOW == BETWEEN ? sum_of_lanes_before(high) : pl;
   __syncthreads();
   if (lane == 31) {
     s.scan_n[warp] = pn;
@@ -491,34 +490,36 @@ __device__ __noinline__ void locate(SharedBins &s, Locate how, int bins, u64 wan
     s.scan2[warp] = ph + high;
   }
   __syncthreads();
-  pn = before_n + pn - n;
+  pn = before_n + pn - mine;
   u64 all_l = 0, all_h = 0;
+#pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) pn += s.scan_n[w], pl += s.scan[w], ph += s.scan2[w];
-    all_l += s.scan[w];
-    all_h += s.scan2[w];
+    if (HOW == BETWEEN) all_l += s.scan[w], all_h += s.scan2[w];
   }
-  if (how == BY_COUNT) pl = ph = pn;
-  if (how == BY_SUM) pl += above, ph += above;
+  if (HOW == BY_COUNT) pl = ph = pn;
+  if (HOW == BY_SUM) pl += above, ph += above;
   const long long t = (long long)want;
   // a sum is at least what is known from above, or the row's less what may be below; at most ...
-  auto at_least = [&](u64 l, u64 h) { return how == BETWEEN ? max((long long)l, (long long)(row_sum + h - all_h)) : (long long)l; };
-  auto at_most = [&](u64 l, u64 h) { return how == BETWEEN ? min((long long)h, (long long)(row_sum + l - all_l)) : (long long)h; };
-  if (how == BETWEEN) next = base_of(b0 + 1);
-  for (int b = b0; b > b1; --b) {
-    u64 l, h;
-    sums(b, next, l, h);
-    if (at_most(pl, ph) < t && at_most(pl + l, ph + h) >= t) {
-      s.bin[1] = b;
-      s.bin_before = pn;
+  auto at_least = [&](u64 l, u64 h) { return HOW == BETWEEN ? max((long long)l, (long long)(row_sum + h - all_h)) : (long long)l; };
+  auto at_most = [&](u64 l, u64 h) { return HOW == BETWEEN ? min((long long)h, (long long)(row_sum + l - all_l)) : (long long)h; };
+  // it ends in one thread's bins
+  if ((at_most(pl, ph) < t && at_most(pl + low, ph + high) >= t) || (at_least(pl, ph) < t && at_least(pl + low, ph + high) >= t)) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const u64 l = least[i], h = most[i];
+      if (at_most(pl, ph) < t && at_most(pl + l, ph + h) >= t) {
+        s.bin[1] = b0 - i;
+        s.bin_before = pn;
+      }
+      if (at_least(pl, ph) < t && at_least(pl + l, ph + h) >= t) {
+        s.bin[0] = b0 - i;
+        s.bin_to = pn + n[i];
+      }
+      pn += n[i];
+      pl += l;
+      ph += h;
     }
-    if (at_least(pl, ph) < t && at_least(pl + l, ph + h) >= t) {
-      s.bin[0] = b;
-      s.bin_to = pn + s.red_n[b];
-    }
-    pn += s.red_n[b];
-    pl += l;
-    ph += h;
   }
   __syncthreads();
 }
@@ -884,10 +885,11 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     b.sync_row();
     add_bins(bins, false, base, shift);
   };
-  auto first_bins = [&](Locate how, u64 want, u64 row_sum) {
+  constexpr int PER = (BINS + THREADS - 1) / THREADS, PER_FINER = (FINER_BINS + THREADS - 1) / THREADS;
+  auto first_bins = [&](auto how, u64 want, u64 row_sum) {
     if (!hist) count_bins(KEY_ONE, SHIFT, BINS, false);
     hist = 1;
-    locate(s, how, BINS, want, 0, 0, row_sum);
+    locate<decltype(how)::value, PER>(s, BINS, want, 0, 0, row_sum);
   };
   // a list of its own for what the prefix ends in, where that is short
   auto list_if_few = [&]() {
@@ -909,8 +911,8 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
       const float from_e = fmaxf(b.least_e, least_power(base)), above_e = fmaxf(b.least_e, least_power(end));
       __syncthreads();
       if (n_range <= (C >= 4 ? RANGE : RANGE_FEW)) {
-        // The tokens that are left, in every block; each ranks its share: what
-        // is before a token, and their sum, by as many threads as there are.
+        // The tokens that are left, in every block; each finds the places of its
+        // share, by as many threads as there are, for all of them.
         if (tid == 0) s.n_list = 0;
         __syncthreads();
         u64 above = 0;
@@ -929,10 +931,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
         b.sync_row();
         const u64 sum_above = b.row_total();
         const int n = b.all_listed();
-        for (int i = tid; i < n; i += THREADS) {
-          const u64 key = b.listed(s.range, i);
-          s.all_range[i] = make_ulonglong2(key, list_whole(key));
-        }
+        for (int i = tid; i < n; i += THREADS) s.all_range[i] = b.listed(s.range, i);
         __syncthreads();
         const int each = (n + C - 1) >> a.cluster_log2;
         int log2 = 0;
@@ -941,29 +940,32 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
         for (int i0 = 0; i0 < each; i0 += THREADS >> log2) {
           const int i = rank * each + i0 + (tid >> log2);
           const bool there = i0 + (tid >> log2) < each && i < n;
-          const ulonglong2 own = there ? s.all_range[i] : make_ulonglong2(0, 0);
-          uint32_t rank_n = 0;                                // it among them
-          u64 sum_to = 0;
-          for (int o = tid & (per - 1); o < n; o += per) {
-            const ulonglong2 y = s.all_range[o];
-            if (y.x >= own.x) {
-              ++rank_n;
-              sum_to += y.y;
-            }
-          }
-          for (int o = 1; o < per; o <<= 1) {
-            rank_n += __shfl_xor_sync(~0u, rank_n, o);
-            sum_to += __shfl_xor_sync(~0u, sum_to, o);
-          }
-          rank_n += before_n;
-          sum_to += sum_above;
-          if (there && (tid & (per - 1)) == 0 && (by_n ? rank_n == want : sum_to >= want && sum_to - own.y < want))
-            for (int r = 0; r < C; ++r) {
-              *b.at(&s.cut_key, r) = own.x;
-              *b.at(&s.cut_sum, r) = sum_to;
-            }
+          const u64 own = there ? s.all_range[i] : 0;
+          int above = 0;
+#pragma unroll 4
+          for (int o = tid & (per - 1); o < n; o += per) above += s.all_range[o] > own;
+          for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
+          if (there && (tid & (per - 1)) == 0)
+            for (int r = 0; r < C; ++r) b.at(s.sorted_range, r)[above] = own;
         }
         b.sync_row();
+        static_assert(RANGE == 2 * THREADS, "two tokens a thread");
+        u64 key[2], w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          key[i] = 2 * tid + i < n ? s.sorted_range[2 * tid + i] : 0;
+          w[i] = list_whole(key[i]);
+        }
+        u64 sum_to = sum_above + sum_before(s, w[0] + w[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sum_to += w[i];
+          if (2 * tid + i < n && (by_n ? before_n + 2 * tid + i + 1 == want : sum_to >= want && sum_to - w[i] < want)) {
+            s.cut_key = key[i];
+            s.cut_sum = sum_to;
+          }
+        }
+        __syncthreads();
         end_key = s.cut_key;
         total = s.cut_sum;
         parts_known = true;
@@ -1002,7 +1004,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
       const int bins = (int)((end - base + (1u << shift) - 1) >> shift);
       if (by_n) {
         count_bins(base, shift, bins, false);
-        locate(s, BY_COUNT, bins, want, before_n, 0, 0);
+        locate<BY_COUNT, PER_FINER>(s, bins, want, before_n, 0, 0);
         before_n = s.bin_before;
       } else {
         for (int i = tid; i < 3 * FINER_BINS; i += THREADS) s.n[i] = 0;
@@ -1011,7 +1013,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
         b.push_sums(pass<SUM_BINS, FROM>(b.x, s, Pass{bins_e, fmaxf(b.least_e, least_power(base)), bins_e, base, shift, bins}));
         b.sync_row();
         add_bins(bins, true, base, shift);
-        locate(s, BY_SUM, bins, want, 0, b.row_total(), 0);
+        locate<BY_SUM, PER_FINER>(s, bins, want, 0, b.row_total(), 0);
       }
       n_range = s.red_n[s.bin[0]];
       base += (uint32_t)s.bin[0] << shift;
@@ -1028,7 +1030,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     for (int i = tid; i < BINS; i += THREADS) n += s.red_n[i];
     n = block_all(n, OpSum(), s.scan_n);
     if (n > (uint32_t)k) {
-      first_bins(BY_COUNT, k, 0);
+      first_bins(How<BY_COUNT>{}, k, 0);
       list_if_few();
       prefix_end(true, k);
     }
@@ -1036,7 +1038,7 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
   if (top_p < 1.f) {
     const u64 least = b.share(total);
     if (least < total) {
-      first_bins(BETWEEN, least, row_sum);
+      first_bins(How<BETWEEN>{}, least, row_sum);
       if (end_key == 0) list_if_few();
       prefix_end(false, least);
     }
