@@ -21,7 +21,7 @@
 // 256 x 100256 bfloat16, whose bytes need 7.7 us, take 23 us with a temperature
 // alone (a pass that reads and one that sums, over one or two rows an SM) and 31
 // with a top-k of 50 and top-p.  A mixture, of which a quarter goes to the
-// histograms, takes 83: their kernel's 45 us are, for a row, 3 of reading, 10 of
+// histograms, takes 82: their kernel's 45 us are, for a row, 3 of reading, 10 of
 // the first histogram (an atomic in shared memory for each token of the row,
 // which twice the warps do not speed up), 4 to find the bins, and 20 for the
 // finer ones and the last tokens, passes and cluster barriers in turn.

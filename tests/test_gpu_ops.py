@@ -752,3 +752,23 @@ def test_sample_on_both_sides_of_the_rules(tt, n, vocab, name):
              min_p=rng.choice([0.0, 0.0, 0.02], n).astype(np.float32))
     pick = range(n) if n * vocab <= 2_000_000 else sorted(rng.choice(n, 24, replace=False).tolist() + [1, 2, 3, 4, 5, 6])
     check_sample(tt, x, rng.random(n).astype(np.float32), p, pick)
+
+
+@pytest.mark.parametrize("vocab", [7, 5000, 100256])
+@pytest.mark.parametrize("name", DTYPES)
+def test_sample_at_the_ends_of_the_parameters(tt, vocab, name):
+    """The least and the largest values the header allows, denormal ones among
+    them: temperatures whose reciprocal overflows or is denormal, shares and
+    random numbers below the least weight."""
+    tiny, least = np.float32(1e-45), np.float32(2.0**-126)
+    under_one = np.float32(1) - np.float32(2.0**-24)
+    rng = np.random.default_rng(vocab)
+    n = 24
+    x = rows_of(n, vocab, name, gen(vocab + 5), scale=2.0)
+    pick = lambda *v: rng.choice(np.array(v, np.float32), n)  # noqa: E731
+    for _ in range(3):
+        check_sample(tt, x, pick(0, tiny, least, 2.0**-41, under_one),
+                     dict(temperature=pick(0, tiny, least, 3e38, np.finfo(np.float32).max, 1),
+                          top_k=rng.choice([0, -(1 << 31), 1, vocab - 1, vocab, (1 << 31) - 1], n).astype(np.int32),
+                          top_p=pick(0, tiny, least, 2.0**-41, under_one, 1),
+                          min_p=pick(0, tiny, 2.0**-41, 2.0**-40, 1.5 * 2.0**-40, under_one, 1)))
