@@ -50,8 +50,10 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
     if (row >= n) return;
     const int32_t id = __ldg(a.ids + row);
     TO *to = out + row * a.out_stride + unit * 8;
+    const bool there = (uint32_t)id < (uint32_t)a.n_vocab;
+    const float scale = there ? a.scale : 0.f;    // an infinite one leaves padding zero, too
     Raw8<TI> v[R];
-    if ((uint32_t)id < (uint32_t)a.n_vocab) {
+    if (there) {
       const TI *from = table + id * a.table_stride + unit * 8;
 #pragma unroll
       for (int j = 0; j < R; ++j)
@@ -63,19 +65,22 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
     }
 #pragma unroll
     for (int j = 0; j < R; ++j)
-      if (whole || unit + j * 32 < units) store_scaled(to + j * 256, v[j], a.scale);
+      if (whole || unit + j * 32 < units) store_scaled(to + j * 256, v[j], scale);
   } else {
     const int rows_per_warp = 32 >> a.lanes_log2, unit = lane & ((1 << a.lanes_log2) - 1);
     const int64_t rows_per_block = 8 * rows_per_warp * R;
     for (int64_t row0 = blockIdx.x * rows_per_block + warp * rows_per_warp * R + (lane >> a.lanes_log2); row0 < n;
          row0 += gridDim.x * rows_per_block) {
       Raw8<TI> v[R];
+      float scale[R];
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const int64_t row = row0 + j * rows_per_warp;
         if (row < n && unit < units) {
           const int32_t id = __ldg(a.ids + row);
-          if ((uint32_t)id < (uint32_t)a.n_vocab) {
+          const bool there = (uint32_t)id < (uint32_t)a.n_vocab;
+          scale[j] = there ? a.scale : 0.f;
+          if (there) {
             load_raw(table + id * a.table_stride + unit * 8, v[j]);
           } else {
             v[j] = Raw8<TI>{};
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a, const TI *__restrict
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const int64_t row = row0 + j * rows_per_warp;
-        if (row < n && unit < units) store_scaled(out + row * a.out_stride + unit * 8, v[j], a.scale);
+        if (row < n && unit < units) store_scaled(out + row * a.out_stride + unit * 8, v[j], scale[j]);
       }
     }
   }
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__rest
 // The sums are bound by memory, the sort by the latency of its kernels: 304,824
 // tokens of 2048 bfloat16 into 100,256 float rows take 375 us (2.07 GB, 83% of
 // the measured copy bandwidth), 335 of them the sums; 16,400 tokens of 1024
-// floats into 4,352 rows take 37 us, of which the bytes need 13.
+// floats into 4,352 rows take 42 us, of which the bytes need 13.
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_BINS = 1 << 11;

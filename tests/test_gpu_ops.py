@@ -772,3 +772,23 @@ def test_sample_at_the_ends_of_the_parameters(tt, vocab, name):
                           top_k=rng.choice([0, -(1 << 31), 1, vocab - 1, vocab, (1 << 31) - 1], n).astype(np.int32),
                           top_p=pick(0, tiny, least, 2.0**-41, under_one, 1),
                           min_p=pick(0, tiny, 2.0**-41, 2.0**-40, 1.5 * 2.0**-40, under_one, 1)))
+
+
+@pytest.mark.parametrize("dim", [7, 24, 1024])
+@pytest.mark.parametrize("scale", [-2.0, math.inf, math.nan])
+@pytest.mark.parametrize("name", DTYPES)
+def test_padding_is_zero_whatever_the_scale(tt, dim, scale, name):
+    """Rows of padding, and table rows of IDs that do not occur, are +0: their
+    zeros are not multiplied."""
+    table = rows_of(50, dim, name, gen(dim))
+    ids = torch.tensor([3, -1, 49, -7, 0, 50, 3], dtype=torch.int32, device="cuda")
+    out = tt.embed(ids, table, scale)
+    zero = torch.tensor([1, 3, 5], device="cuda")
+    assert not out[zero].any() and not torch.signbit(out[zero]).any()
+    want = (table[[3, 49, 0, 3]].double() * scale).to(out.dtype)
+    assert torch.equal(out[[0, 2, 4, 6]].isnan(), want.isnan()) and torch.equal(out[[0, 2, 4, 6]].nan_to_num(1), want.nan_to_num(1))
+    for n in (7, 2000):                                     # rows mostly absent, and mostly there
+        some = (torch.arange(n, device="cuda") % 40).int()
+        d = tt.embed_grad(some, rows_of(n, dim, name, gen(n)), 50, scale)
+        absent = d[min(n, 40):]
+        assert not absent.any() and not torch.signbit(absent).any()
