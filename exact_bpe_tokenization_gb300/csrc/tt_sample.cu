@@ -877,13 +877,17 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     }
     b.sync_row();
   };
+  // (with `sum`, the row's sum: read between the two barriers, since a block that
+  // is ahead tells new ones behind the second)
   auto count_bins = [&](uint32_t base, int shift, int bins, bool sum) {
     for (int i = tid; i < bins; i += THREADS) s.counts[i] = 0;
     __syncthreads();
     if (sum) b.push_sums(pass<COUNT_BINS, FROM>(b.x, s, Pass{b.least_e, b.least_e, INF, base, shift, bins}));
     else pass<COUNT_BINS, NONE>(b.x, s, Pass{NEVER, b.least_e, INF, base, shift, bins});
     b.sync_row();
+    const u64 all = sum ? b.row_total() : 0;
     add_bins(bins, false, base, shift);
+    return all;
   };
   constexpr int PER = (BINS + THREADS - 1) / THREADS, PER_FINER = (FINER_BINS + THREADS - 1) / THREADS;
   auto first_bins = [&](auto how, u64 want, u64 row_sum) {
@@ -1012,8 +1016,9 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
         const float bins_e = fmaxf(b.least_e, least_power(base + ((uint32_t)bins << shift)));
         b.push_sums(pass<SUM_BINS, FROM>(b.x, s, Pass{bins_e, fmaxf(b.least_e, least_power(base)), bins_e, base, shift, bins}));
         b.sync_row();
+        const u64 above = b.row_total();                    // (before the barrier in add_bins, as in count_bins)
         add_bins(bins, true, base, shift);
-        locate<BY_SUM, PER_FINER>(s, bins, want, 0, b.row_total(), 0);
+        locate<BY_SUM, PER_FINER>(s, bins, want, 0, above, 0);
       }
       n_range = s.red_n[s.bin[0]];
       base += (uint32_t)s.bin[0] << shift;
@@ -1021,9 +1026,8 @@ __device__ __forceinline__ void sample_by_bins(Block<T, SharedBins> &b, const Sa
     }
   };
   // the first histogram, and the row's sum where it is wanted
-  count_bins(KEY_ONE, SHIFT, BINS, top_p < 1.f);
+  const u64 row_sum = total = count_bins(KEY_ONE, SHIFT, BINS, top_p < 1.f);
   hist = 1;
-  const u64 row_sum = total = b.row_total();
   if (k < V) {
     // fewer than k tokens may be left by min-p
     uint32_t n = 0;
