@@ -259,10 +259,14 @@ __global__ void __launch_bounds__(1024) k_sort_scan(SortArgs a, int pass) {
   }
 }
 
+// The second pass reads what the kernel before writes while this one may be there
+// already: keys and pos are plain pointers, read behind wait_for_last(), since
+// const and __restrict__ would allow loads that take memory as constant from the
+// kernel's start on.  ids, the caller's, are.
 template <int PASS, int KEYS>
 __global__ void __launch_bounds__(SORT_THREADS)
-k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__restrict__ pos, int32_t *__restrict__ keys_out,
-             int32_t *__restrict__ pos_out) {
+k_sort_place(SortArgs a, const int32_t *__restrict__ ids, const int32_t *keys, const int32_t *pos, int32_t *keys_out,
+             int32_t *pos_out) {
   extern __shared__ uint32_t sm[];                         // base[bins], then uint16 seen[SORT_WARPS][bins]
   __shared__ uint32_t box[SORT_WARPS];
   if ((int)blockIdx.x >= a.tiles) {
@@ -284,7 +288,7 @@ k_sort_place(SortArgs a, const int32_t *__restrict__ keys, const int32_t *__rest
 #pragma unroll
   for (int k = 0; k < KEYS; ++k) {
     const int64_t i = first + k * 32;
-    key[k] = i < n ? (PASS ? (uint32_t)keys[i] : key_of(keys[i], a.n_vocab)) : 0;
+    key[k] = i < n ? (PASS ? (uint32_t)keys[i] : key_of(ids[i], a.n_vocab)) : 0;
     at[k] = PASS ? (i < n ? pos[i] : 0) : (int32_t)i;
   }
   if (!PASS && a.tiles <= SUM_TILES) wait_for_last();
@@ -898,7 +902,7 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
         if (p.tiles > SUM_TILES)
           launch_cluster(k_sort_scan, dim3(((1u << p.bits[pass]) + 31) / 32), 1024, 0, 1, true, stream, s, pass);
         launch_cluster(pass ? k_sort_place<1, KEYS> : k_sort_place<0, KEYS>, dim3(p.tiles + s.clear_blocks), SORT_THREADS, shared(p.bits[pass]), 1, true,
-                       stream, s, pass ? (const int32_t *)keys[0] : d_ids, (const int32_t *)pos[0], keys[pass], pos[pass]);
+                       stream, s, d_ids, keys[0], pos[0], keys[pass], pos[pass]);
       }
     };
     if (p.per_thread == 2) run(Per<2>{});

@@ -155,3 +155,17 @@ def test_a_rows_sums_are_read_before_new_ones_are_told():
     assert len(re.findall(r"row_total\(", body)) >= 4 and "prefix_end" in body
     assert walk(body) == []
     assert walk(body_of(text, r"bool sample_by_list\(")) == []
+
+
+def test_chained_kernels_take_only_the_callers_inputs_as_constant():
+    """A kernel that is there before the one ahead of it ends may declare
+    constant (const __restrict__) only what no kernel of the call writes."""
+    inputs = {"ids", "table", "dout", "logits"}             # parameters that the calls' own inputs are given to
+    chained = {}
+    for name in ("tt_embed.cu", "tt_loss.cu", "tt_sample.cu"):
+        text = source(name)
+        for m in re.finditer(r"__global__[^;{]*?(k_\w+)\(([^{;]*)\)\s*\{", text):
+            if "wait_for_last()" in body_of(text, re.escape(m[0][:-1])):
+                chained[m[1]] = set(re.findall(r"const \w+ \*__restrict__ (\w+)", m[2]))
+    assert {"k_sort_place", "k_sort_scan", "k_grad_sum", "k_grad_join", "k_sample_bins"} <= set(chained)
+    assert not {k: v - inputs for k, v in chained.items() if v - inputs}
