@@ -1,0 +1,118 @@
+"""The operators around token IDs where a result is easily lost unnoticed:
+gradients of whole numbers, whose sums are exact whatever their order, on every
+way through the sort and the sums."""
+
+import numpy as np
+import pytest
+
+from test_gpu_ops import DTYPES, dtype, gen, rows_of, status_word, tt  # noqa: F401 (tt: the fixture)
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ------------------------------------------------------------ embed_grad, exactly
+
+def whole_rows(n, d, name, seed, stride=None, shift=0):
+    """[n, d] whole numbers of -8 .. 8, all different sums."""
+    x = rows_of(n, d, name, gen(seed), stride, shift)
+    for a in range(0, n, 65536):
+        m = min(65536, n - a)
+        x[a:a + m] = torch.randint(-8, 9, (m, d), generator=gen(seed + a), device="cuda").to(dtype(name))
+    return x
+
+
+def ids_of(kind, n, vocab, rng):
+    if kind == "zipf":
+        ids = np.minimum(rng.zipf(1.2, n) - 1, vocab - 1)
+    elif kind == "one":
+        ids = np.full(n, min(3, vocab - 1))
+    elif kind == "last":
+        ids = np.full(n, vocab - 1)
+    elif kind == "two":
+        ids = np.where(np.arange(n) < n // 3, vocab - 1, 0)
+    elif kind == "runs":         # rows of 62 .. 65 tokens, whose places drift against every cut
+        ids = np.repeat(np.arange(vocab), np.resize([62, 63, 64, 65, 63, 64, 62], vocab))
+        ids = np.concatenate([ids[:n], rng.integers(0, vocab, max(0, n - len(ids)))])
+        rng.shuffle(ids)
+    else:                        # "mixed": a row of a third, rows of one, padding and invalid IDs
+        ids = rng.integers(-1, vocab + 1, n)
+        ids[rng.random(n) < 0.3] = vocab // 2
+    return torch.from_numpy(ids.astype(np.int32)).cuda()
+
+
+def whole_sums(ids, dout, vocab):
+    """The sums by ID, in 64 bits, and that 32 hold every partial one."""
+    there = (ids >= 0) & (ids < vocab)
+    at = ids[there].long()
+    want = torch.zeros(vocab, dout.shape[1], dtype=torch.float64, device="cuda")
+    for a in range(0, dout.shape[1], 64):
+        want[:, a:a + 64] = want[:, a:a + 64].index_add(0, at, dout[there, a:a + 64].double())
+    assert 8 * int(torch.bincount(at, minlength=1).max()) < 1 << 24
+    return want
+
+
+def check_whole(tt, ids, dout, vocab, to="float32", **kw):
+    want = whole_sums(ids, dout, vocab)
+    got = tt.embed_grad(ids, dout, vocab, scale=0.5, dtype=dtype(to), **kw)
+    assert torch.equal(got, (want * 0.5).float().to(dtype(to)))
+    return want
+
+
+KINDS = ["zipf", "one", "last", "two", "runs", "mixed"]
+
+
+@pytest.mark.parametrize("n", [1, 31, 4097, 16384, 70001, 131072, 131073, 300000, 1048576, 1048577, 1500000])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [8, 7])
+def test_embed_grad_of_whole_numbers(tt, n, kind, dim):
+    """Two, four and eight tokens a thread of the sort, with the counts before a
+    tile added up and scanned; rows cut over up to all of the workers."""
+    rng = np.random.default_rng(n)
+    vocab = 5000
+    ids, dout = ids_of(kind, n, vocab, rng), whole_rows(n, dim, "float32", n)
+    want = check_whole(tt, ids, dout, vocab)
+    base = torch.arange(vocab * dim, device="cuda").view(vocab, dim) % 1000
+    out = base.float()
+    tt.embed_grad(ids, dout, vocab, scale=0.5, out=out, accumulate=True)
+    assert torch.equal(out, (base + want * 0.5).float())
+
+
+@pytest.mark.parametrize("n", [200000, 600000, 1100000])
+@pytest.mark.parametrize("count", [0, 1, 130000, 199999])
+def test_embed_grad_of_fewer_tokens_than_the_bound(tt, n, count):
+    rng = np.random.default_rng(n + count)
+    ids, dout = ids_of("mixed", n, 3000, rng), whole_rows(n, 8, "bfloat16", n)
+    got = tt.embed_grad(ids, dout, 3000, n_ids=torch.tensor([count], device="cuda"), status=(st := status_word()))
+    assert torch.equal(got, whole_sums(ids[:count], dout[:count], 3000).float())
+    assert st.item() == (tt.TT_ERR_INVALID_ARG if bool((ids[:count] >= 3000).any()) else 0)
+
+
+@pytest.mark.parametrize("n,dim,name", [(200000, 2048, "bfloat16"), (110000, 2048, "float32"), (250000, 1024, "float16"),
+                                        (150000, 1025, "bfloat16"), (90000, 1537, "float32"), (400000, 520, "bfloat16")])
+@pytest.mark.parametrize("kind,vocab", [("runs", 300), ("runs", 2500), ("zipf", 4000), ("mixed", 700), ("one", 5)])
+def test_embed_grad_of_long_parts(tt, n, dim, name, kind, vocab):
+    """Widths where a worker's part of the list is long, with rows around the 63
+    tokens up to which a row is not cut."""
+    rng = np.random.default_rng(n + vocab)
+    ids, dout = ids_of(kind, n, vocab, rng), whole_rows(n, dim, name, n)
+    want = check_whole(tt, ids, dout, vocab)
+    out = torch.ones(vocab, dim, device="cuda")
+    tt.embed_grad(ids, dout, vocab, scale=0.5, out=out, accumulate=True)
+    assert torch.equal(out, (1 + want * 0.5).float())
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(200000, 1 << 20, 8), (200000, 1 << 20, 9), (50000, 200256, 641), (250000, 1000003, 96)])
+@pytest.mark.parametrize("kind", ["zipf", "runs", "mixed", "two"])
+@pytest.mark.parametrize("to", ["float32", "bfloat16"])
+def test_embed_grad_of_whole_numbers_into_mostly_absent_rows(tt, n, vocab, dim, kind, to):
+    rng = np.random.default_rng(n + dim)
+    check_whole(tt, ids_of(kind, n, vocab, rng), whole_rows(n, dim, "bfloat16", n), vocab, to)
+
+
+@pytest.mark.parametrize("ti", DTYPES)
+@pytest.mark.parametrize("to", DTYPES)
+@pytest.mark.parametrize("dim,stride,shift", [(264, 264, 0), (264, 267, 0), (257, 300, 3)])
+def test_embed_grad_of_whole_numbers_by_type(tt, ti, to, dim, stride, shift):
+    rng = np.random.default_rng(dim)
+    check_whole(tt, ids_of("mixed", 20000, 1000, rng), whole_rows(20000, dim, ti, dim, stride, shift), 1000, to)
