@@ -548,11 +548,13 @@ template <class T, class S> struct Block {
   template <class P> __device__ __forceinline__ P *at(P *p, int r) const { return C > 1 ? of_block(p, r) : p; }
 
   // the row's parameters; whether they are what the header allows
+  // (adding 0 takes a zero's sign off and changes nothing else: a negative one
+  // would turn 1 / T around, and times() reads a factor's bits)
   __device__ __forceinline__ bool parameters(int64_t row) {
-    u = a.uniform[row];
-    temp = a.temperature ? a.temperature[row] : 1.f;
-    top_p = a.top_p ? a.top_p[row] : 1.f;
-    min_p = a.min_p ? a.min_p[row] : 0.f;
+    u = a.uniform[row] + 0.f;
+    temp = a.temperature ? a.temperature[row] + 0.f : 1.f;
+    top_p = a.top_p ? a.top_p[row] + 0.f : 1.f;
+    min_p = a.min_p ? a.min_p[row] + 0.f : 0.f;
     const int V = (int)a.n_vocab, top_k = a.top_k ? a.top_k[row] : 0;
     k = temp == 0 ? 1 : top_k > 0 ? min(top_k, V) : V;
     least_key = __float_as_uint(fmaxf(min_p * ONE, 1.f));

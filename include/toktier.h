@@ -466,7 +466,7 @@ tt_status tt_token_loss_grad(const void *d_logits, int32_t type, int64_t n_rows,
  *                  logarithm of the probability with which it was drawn.
  * A row with nothing to draw (all -inf or NaN) gives ID -1 and logprob -inf.
  * A row with a parameter outside these ranges gives the same and sets
- * TT_ERR_INVALID_ARG in d_status.
+ * TT_ERR_INVALID_ARG in d_status.  A zero may have either sign.
  */
 tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
                     const float *d_uniform, const float *d_temperature, const int32_t *d_top_k,

@@ -1,11 +1,12 @@
 """The operators around token IDs where a result is easily lost unnoticed:
 gradients of whole numbers, whose sums are exact whatever their order, on every
-way through the sort and the sums."""
+way through the sort and the sums; zeros of either sign among the sampling
+parameters."""
 
 import numpy as np
 import pytest
 
-from test_gpu_ops import DTYPES, dtype, gen, rows_of, status_word, tt  # noqa: F401 (tt: the fixture)
+from test_gpu_ops import DTYPES, check_sample, dtype, gen, rows_of, status_word, tt  # noqa: F401 (tt: the fixture)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -116,3 +117,26 @@ def test_embed_grad_of_whole_numbers_into_mostly_absent_rows(tt, n, vocab, dim, 
 def test_embed_grad_of_whole_numbers_by_type(tt, ti, to, dim, stride, shift):
     rng = np.random.default_rng(dim)
     check_whole(tt, ids_of("mixed", 20000, 1000, rng), whole_rows(20000, dim, ti, dim, stride, shift), 1000, to)
+
+
+# ------------------------------------------------------------ zeros of either sign
+
+@pytest.mark.parametrize("vocab", [9, 5000, 100256])
+@pytest.mark.parametrize("n", [6, 200])
+@pytest.mark.parametrize("key", ["temperature", "top_p", "min_p", "uniform"])
+def test_sample_takes_a_negative_zero_as_zero(tt, vocab, n, key):
+    x = rows_of(n, vocab, "float32", gen(vocab), scale=2.0)
+    x[n // 2:] *= 0.01                                        # flat rows, for the histograms
+    rng = np.random.default_rng(n)
+    a = dict(temperature=torch.ones(n, device="cuda"), top_p=torch.full((n,), 0.9, device="cuda"),
+             min_p=torch.zeros(n, device="cuda"), uniform=torch.rand(n, generator=gen(n), device="cuda"),
+             top_k=torch.from_numpy(rng.choice([0, 5, 3000], n).astype(np.int32)).cuda())
+    a[key] = torch.zeros(n, device="cuda")
+    want = tt.sample(x, **a)
+    a[key] = torch.full((n,), -0.0, device="cuda")
+    st = status_word()
+    got = tt.sample(x, status=st, **a)
+    assert st.item() == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    if key == "temperature":
+        assert torch.equal(got[0], x.argmax(1).int())
+    check_sample(tt, x, np.zeros(n, np.float32), {"top_p": np.zeros(n, np.float32)}, range(0, n, 20))
