@@ -1,8 +1,15 @@
 // tt_loss.cu - next-token loss of rows of logits and its gradient
 // (include/toktier.h).
 //
-//   lse = M + log(sum_j exp(l_j - M)),  loss = lse - l_t,
+//   lse = M + log(S),  S = sum_j exp(l_j - M),  loss = (M - l_t) + log(S),
 //   dl_j = g * (exp(l_j - lse) - (j == t))
+//
+// lse is rounded to 32 bits, by up to 2^-24 of itself, which every probability
+// taken from it is off by: 5e-7 at lse = 15.  That is the gradient's error, so that
+// it has the same bits whether it comes with the loss or from lse later, as long
+// as lse stays below FAR; above, log(S) would soon be lost in it (a row of the
+// type's lowest value would get probabilities of 1), and the gradient that comes
+// with the loss is exp(l_j - M) / S instead.  The loss never goes through lse.
 //
 // Bound by memory: each logit has to be read and each gradient written once.
 // The gradient needs lse, which needs the whole row, so a row is read, kept in
@@ -27,6 +34,7 @@ namespace {
 constexpr int HELD = 104 * 1024;                 // bytes of a row a block holds: two blocks an SM
 constexpr float LOG2E = 1.44269504f;
 constexpr float LOWEST = -3.402823466e38f;
+constexpr float FAR = 128.f;                     // |lse| from where a probability would be off by 2^-18
 
 struct LossArgs {
   int64_t n_vocab, logits_stride, dlogits_stride;
@@ -118,12 +126,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, co
   const int lone = rank == 0 ? part.scalar(tid) : -1;
   const float x = lone >= 0 ? to_f32(l[lone]) : -INF;
   const int32_t t = a.targets[row];
+  const float g_row = GRAD && a.row_grads ? a.row_grads[row] : 1.f;        // (here, so that it is there behind the barrier)
   const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
   if (!there && t >= 0 && rank == 0 && tid == 0) op_status(a.status, TT_ERR_INVALID_ARG);
 
-  float lse;
+  float lse, from, inverse = 1.f;                // probabilities are exp(l - from) * inverse
   if (GRAD == 2) {
-    lse = a.lse_in[row];
+    lse = from = a.lse_in[row];
   } else {
     // read by one thread, before any block can write to the row
     const float lt = there && rank == 0 && tid == 0 ? to_f32(l[t]) : 0.f;
@@ -163,16 +172,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, co
       run.s = 0;
       for (int b = 0; b < a.cluster; ++b) run.join(s_blocks[b].x, s_blocks[b].y);
     }
-    lse = run.m + logf(run.s);
+    const float log_s = logf(run.s);
+    lse = from = run.m + log_s;
+    if (fabsf(lse) >= FAR && fabsf(lse) < INF) {
+      from = run.m;
+      inverse = __fdividef(1.f, run.s);         // of 1 .. 2^20
+    }
     if (rank == 0 && tid == 0) {
       if (a.lse_out) a.lse_out[row] = lse;
-      a.loss[row] = !there ? 0.f : lse == -INF ? INF : lse - lt;
+      a.loss[row] = !there ? 0.f : lse == -INF ? INF : (run.m - lt) + log_s;
     }
   }
   if (GRAD) {
     T *d = dlogits + row * a.dlogits_stride;
     const bool none = !there || lse == -INF;
-    const float g = none ? 0.f : a.row_grads ? a.row_grads[row] : 1.f;
+    const float g = none ? 0.f : g_row, g_inverse = g * inverse;
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(l)) & 15) == 0;
     T *out = d + part.lead + (int64_t)first * E;
     // the thread that has the target among its vectors writes it once more behind them
@@ -184,10 +198,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, co
       vec_f32(r, v, T{});
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
-        float2 y = sub_mul2(make_float2(v[i], v[i + 1]), lse, LOG2E);
+        float2 y = sub_mul2(make_float2(v[i], v[i + 1]), from, LOG2E);
         y.x = ex2(y.x);
         y.y = ex2(y.y);
-        y = mul2(y, g);
+        y = mul2(y, g_inverse);
         v[i] = y.x;
         v[i + 1] = y.y;
       }
@@ -216,8 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, co
       for (int u = 0; u < U; ++u)
         if (whole.value || v0 + u * THREADS < n) write(r[u], v0 + u * THREADS);
     });
-    if (mine) d[t] = from_f32<T>(none ? 0.f : (ex2((xt - lse) * LOG2E) - 1.f) * g);
-    if (lone >= 0) d[lone] = from_f32<T>(none ? 0.f : (ex2((x - lse) * LOG2E) - (lone == t ? 1.f : 0.f)) * g);
+    if (mine) d[t] = from_f32<T>(none ? 0.f : (ex2((xt - from) * LOG2E) * inverse - 1.f) * g);
+    if (lone >= 0) d[lone] = from_f32<T>(none ? 0.f : (ex2((x - from) * LOG2E) * inverse - (lone == t ? 1.f : 0.f)) * g);
   }
 }
 

@@ -419,14 +419,21 @@ int64_t tt_embed_grad_workspace(int64_t max_ids, int64_t n_vocab, int64_t dim);
  * +inf in a row makes its lse NaN or +inf, and its loss and gradient what the
  * formulas then give in IEEE arithmetic.  A target >= n_vocab is padding and
  * sets TT_ERR_INVALID_ARG in d_status.
+ * The loss does not go through the 32-bit lse.  The gradient does where |lse| <
+ * 128 (up to 2^-18 of each probability, 2^-21 below 16); beyond, it is taken
+ * from the row's maximum and sum, so that rows far from zero, and rows that
+ * hold nothing but a mask's lowest value, have the softmax's gradient.
  */
 tt_status tt_token_loss(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
                         const int32_t *d_targets, float *d_loss, float *d_lse, const float *d_row_grads,
                         void *d_dlogits, int64_t dlogits_stride, int32_t *d_status, tt_stream_t stream);
 
 /* tt_token_loss_grad - the gradient of tt_token_loss alone, from the lse that
- * it returned (for a gradient that is known only later); arguments and
- * results as there. */
+ * it returned (for a gradient that is known only later); arguments as there.
+ * The results are the same to the bit where |lse| < 128; beyond, lse's rounding
+ * (2^-24 |lse| of each probability) stays in them, and where it swallows the
+ * sum they are no longer the softmax's: such rows want the gradient from
+ * tt_token_loss. */
 tt_status tt_token_loss_grad(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab,
                              int64_t logits_stride, const int32_t *d_targets, const float *d_lse,
                              const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,

@@ -1,12 +1,14 @@
 """The operators around token IDs where a result is easily lost unnoticed:
 gradients of whole numbers, whose sums are exact whatever their order, on every
-way through the sort and the sums; zeros of either sign among the sampling
-parameters."""
+way through the sort and the sums; losses of rows far from zero; zeros of either
+sign among the sampling parameters."""
+import math
 
 import numpy as np
 import pytest
 
-from test_gpu_ops import DTYPES, check_sample, dtype, gen, rows_of, status_word, tt  # noqa: F401 (tt: the fixture)
+import ops_plain as plain
+from test_gpu_ops import DTYPES, check_sample, dtype, gen, host, rows_of, status_word, tt  # noqa: F401 (tt: the fixture)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -117,6 +119,79 @@ def test_embed_grad_of_whole_numbers_into_mostly_absent_rows(tt, n, vocab, dim, 
 def test_embed_grad_of_whole_numbers_by_type(tt, ti, to, dim, stride, shift):
     rng = np.random.default_rng(dim)
     check_whole(tt, ids_of("mixed", 20000, 1000, rng), whole_rows(20000, dim, ti, dim, stride, shift), 1000, to)
+
+
+# ------------------------------------------------------------ losses far from zero
+
+def far_rows(n, vocab, name, offset, shift):
+    """Rows around `offset`, as their type holds them, the third with a few of
+    the lowest values, the fourth with -inf."""
+    x = rows_of(n, vocab, name, gen(vocab), vocab + 3, shift, scale=3.0)
+    x += offset
+    x[2, : vocab // 2] = torch.finfo(dtype(name)).min
+    x[3, vocab // 2:] = -math.inf
+    return x
+
+
+def check_far_loss(tt, x, targets, g, name):
+    """Losses and gradients from the maximum M and the sum S of exp(l - M).
+    A term's exponent has three roundings (the difference, the product, log2 e)
+    and exp an error of 4 units; the running sums and their joins have some 60
+    and the additions that follow one another: S is that far off.  M - l_t, log S
+    (2 units) and their sum are rounded; a probability has S's error, its
+    exponent's, and a few roundings more, p - 1 another one."""
+    loss, lse, d = (host(o) for o in tt.token_loss(x, torch.from_numpy(targets).cuda(), torch.from_numpy(g).cuda(), want_grad=True))
+    xs = host(x)
+    m = xs.max(1, keepdims=True)
+    e = np.exp(xs - m)
+    s = e.sum(1, keepdims=True)
+    p, rows = e / s, np.arange(len(xs))
+    far = np.where(p > 0, np.minimum(np.abs(xs - m), 1e4), 0)
+    of_sum = plain.EPS * (64 + xs.shape[1] / 128 + 3 * (p * far).sum(1))
+    log_s, m = np.log(s)[:, 0], m[:, 0]
+    want = m - xs[rows, targets] + log_s
+    with np.errstate(over="ignore"):
+        want[np.isinf(want.astype(np.float32))] = math.inf    # what rounds to no float
+    fine = np.isfinite(want)
+    assert np.array_equal(loss[~fine], want[~fine])
+    assert np.all(np.abs(loss[fine] - want[fine]) <= of_sum[fine] + 5 * plain.EPS * np.abs(want[fine]))
+    assert np.all(np.abs(lse - (m + log_s)) <= of_sum + plain.EPS * (4 * log_s + 2 * np.abs(m)))
+    want_d = p.copy()
+    want_d[rows, targets] -= 1
+    want_d *= g[:, None].astype(np.float64)
+    tol = np.abs(g)[:, None] * (p * (of_sum[:, None] + plain.EPS * (3 * far + 16)) + 3 * plain.EPS * (p > 0)) + \
+        1.01 * plain.UNIT[name] * np.abs(want_d) + plain.TINY[name]
+    assert np.all(np.abs(d - want_d) <= tol)
+
+
+@pytest.mark.parametrize("name,offset", [("float32", 300.0), ("float32", -1e4), ("float32", 3e6), ("float32", 1e30), ("float16", 1000.0),
+                                         ("float16", -60000.0), ("bfloat16", 500.0), ("bfloat16", -1e5), ("bfloat16", 1e38)])
+@pytest.mark.parametrize("vocab,shift", [(7, 0), (1000, 0), (4099, 3), (30001, 1), (120001, 0), (300000, 3)])
+def test_token_loss_far_from_zero(tt, name, offset, vocab, shift):
+    rng = np.random.default_rng(vocab)
+    x = far_rows(6, vocab, name, offset, shift)
+    targets = rng.integers(0, vocab, 6).astype(np.int32)
+    targets[:2] = 0, vocab - 1
+    g = rng.standard_normal(6).astype(np.float32)
+    check_far_loss(tt, x, targets, g, name)
+    # in place, and the loss alone
+    out = tt.token_loss(x, torch.from_numpy(targets).cuda(), torch.from_numpy(g).cuda(), want_grad=True)
+    alone = tt.token_loss(x, torch.from_numpy(targets).cuda())
+    assert torch.equal(alone[0], out[0]) and torch.equal(alone[1], out[1])
+    tt.token_loss(x, torch.from_numpy(targets).cuda(), torch.from_numpy(g).cuda(), dlogits=x)
+    assert torch.equal(x, out[2])
+
+
+@pytest.mark.parametrize("name", DTYPES)
+@pytest.mark.parametrize("vocab", [3, 1000, 33333, 200255])
+def test_token_loss_of_rows_of_one_value(tt, name, vocab):
+    """Whatever the value, the lowest as a mask that leaves nothing among them:
+    the loss is log V and the probabilities are equal."""
+    info = torch.finfo(dtype(name))
+    values = [0.0, 5.0, info.min, info.max, -300.0, 2.0**14]
+    x = torch.tensor(values, device="cuda").to(dtype(name))[:, None].repeat(1, vocab)
+    targets = np.array([0, 1, 2, vocab - 1, vocab // 2, 1], dtype=np.int32)
+    check_far_loss(tt, x, targets, np.ones(6, np.float32), name)
 
 
 # ------------------------------------------------------------ zeros of either sign
