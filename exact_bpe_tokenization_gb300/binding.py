@@ -268,7 +268,7 @@ def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temp
 
 
 # ---- the same on torch CUDA tensors: outputs and scratch allocated where they
-# are not given, shapes and types checked.  The kernels run on `stream` (the
+# are not given, shapes, types and devices checked.  The kernels run on `stream` (the
 # current one if None); what is allocated here is handed to that stream.  Small
 # calls cost a few microseconds of device time, so these call the library
 # without a layer in between.
@@ -285,17 +285,21 @@ def _load_torch():
     return torch
 
 
-def _matrix(x, what, rows=None, cols=None):
+def _cuda(on):
+    return "CUDA" if on is None else "cuda:%d" % on
+
+
+def _matrix(x, what, rows=None, cols=None, on=None):
     """(dtype code, rows, columns, row stride) of a 2-D CUDA tensor with unit
-    column stride."""
+    column stride, on the device of index `on` if that is given."""
     code = _codes.get(x.dtype)
     if code is None:
         raise ValueError("%s: float32, float16 or bfloat16 wanted, got %s" % (what, x.dtype))
-    shape = x.shape
-    if len(shape) != 2 or not x.is_cuda or (rows is not None and shape[0] != rows) or \
+    shape, at = x.shape, x.get_device()
+    if len(shape) != 2 or at < 0 or (on is not None and at != on) or (rows is not None and shape[0] != rows) or \
             (cols is not None and shape[1] != cols):
-        raise ValueError("%s: a CUDA tensor [%s, %s] wanted, got %s on %s" % (
-            what, "n" if rows is None else rows, "n" if cols is None else cols, list(shape), x.device))
+        raise ValueError("%s: a tensor [%s, %s] on %s wanted, got %s on %s" % (
+            what, "n" if rows is None else rows, "n" if cols is None else cols, _cuda(on), list(shape), x.device))
     n, d = shape
     s0, s1 = x.stride()
     if s1 != 1 and d > 1:
@@ -303,16 +307,17 @@ def _matrix(x, what, rows=None, cols=None):
     return code, n, d, (s0 if n > 1 else d)
 
 
-def _vector(x, what, dtype, n=None, optional=False):
-    """The address of a contiguous 1-D CUDA tensor (or None where it is optional)."""
+def _vector(x, what, on, dtype, n=None, optional=False):
+    """The address of a contiguous 1-D tensor on the device of index `on` (or
+    None where it is optional)."""
     if x is None:
         if optional:
             return None
         raise ValueError("%s: a tensor wanted" % what)
-    if x.dtype != dtype or not x.is_cuda or x.dim() != 1 or (n is not None and x.shape[0] != n) or \
+    if x.dtype != dtype or x.get_device() != on or x.dim() != 1 or (n is not None and x.shape[0] != n) or \
             not x.is_contiguous():
-        raise ValueError("%s: a contiguous CUDA tensor %s [%s] wanted, got %s %s on %s" % (
-            what, dtype, "n" if n is None else n, x.dtype, list(x.shape), x.device))
+        raise ValueError("%s: a contiguous tensor %s [%s] on %s wanted, got %s %s on %s" % (
+            what, dtype, "n" if n is None else n, _cuda(on), x.dtype, list(x.shape), x.device))
     return x.data_ptr()
 
 
@@ -324,19 +329,19 @@ def _new(torch, rows, cols, dtype, device, what):
     return torch.empty((rows, cols), dtype=dtype, device=device), code
 
 
-def _on(torch, stream, device, *tensors):
+def _on(torch, stream, on, *tensors):
     """The stream's address.  Tensors allocated here come from the current
     stream's pool: another stream waits for it and keeps them."""
-    if torch._C._cuda_getDevice() != device.index:
-        raise ValueError("the tensors are on %s, which is not the current device" % device)
-    current = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() != on:
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % on)
+    current = torch._C._cuda_getCurrentRawStream(on)
     if stream is None:
         return current
     raw = _stream(stream)
     mine = [t for t in tensors if t is not None]
     if raw != current and mine:
-        s = torch.cuda.ExternalStream(raw, device)
-        s.wait_stream(torch.cuda.current_stream(device))
+        s = torch.cuda.ExternalStream(raw, on)
+        s.wait_stream(torch.cuda.current_stream(on))
         for t in mine:
             t.record_stream(s)
     return raw
@@ -346,19 +351,19 @@ def embed(ids, table, scale=1.0, n_ids=None, dtype=None, out=None, status=None, 
     """scale * table[ids] (zero rows for padding): out [len(ids), dim] of
     `dtype` (the table's if None).  n_ids: a device int64 count."""
     torch = _torch or _load_torch()
-    pi = _vector(ids, "ids", torch.int32)
     t, vocab, dim, ts = _matrix(table, "table")
+    on = table.get_device()
+    pi = _vector(ids, "ids", on, torch.int32)
     n = ids.shape[0]
-    device = table.device
     mine = None
     if out is None:
-        out, o = _new(torch, n, dim, dtype or table.dtype, device, "dtype")
+        out, o = _new(torch, n, dim, dtype or table.dtype, table.device, "dtype")
         mine, os_ = out, dim
     else:
-        o, _, _, os_ = _matrix(out, "out", n, dim)
-    _check(lib().tt_embed(pi, n, _vector(n_ids, "n_ids", torch.int64, 1, True), table.data_ptr(), t, vocab, dim, ts, scale,
-                          out.data_ptr(), o, os_, _vector(status, "status", torch.int32, 1, True),
-                          _on(torch, stream, device, mine)), "tt_embed")
+        o, _, _, os_ = _matrix(out, "out", n, dim, on)
+    _check(lib().tt_embed(pi, n, _vector(n_ids, "n_ids", on, torch.int64, 1, True), table.data_ptr(), t, vocab, dim, ts,
+                          scale, out.data_ptr(), o, os_, _vector(status, "status", on, torch.int32, 1, True),
+                          _on(torch, stream, on, mine)), "tt_embed")
     return out
 
 
@@ -367,9 +372,9 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
     """The gradient of embed: [n_vocab, dim] of `dtype` (float32 if None), the
     scaled sums of dout's rows by ID; with accumulate, added to `out`."""
     torch = _torch or _load_torch()
-    pi = _vector(ids, "ids", torch.int32)
-    n = ids.shape[0]
-    d, _, dim, ds = _matrix(dout, "dout", n)
+    d, n, dim, ds = _matrix(dout, "dout")
+    on = dout.get_device()
+    pi = _vector(ids, "ids", on, torch.int32, n)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     mine = scratch = None
@@ -377,15 +382,15 @@ def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, 
         out, o = _new(torch, n_vocab, dim, dtype or torch.float32, dout.device, "dtype")
         mine, os_ = out, dim
     else:
-        o, _, _, os_ = _matrix(out, "out", n_vocab, dim)
+        o, _, _, os_ = _matrix(out, "out", n_vocab, dim, on)
     if workspace is None:
         workspace = scratch = torch.empty(max(lib().tt_embed_grad_workspace(n, n_vocab, dim), 16), dtype=torch.uint8,
                                           device=dout.device)
-    _check(lib().tt_embed_grad(pi, n, _vector(n_ids, "n_ids", torch.int64, 1, True),
+    _check(lib().tt_embed_grad(pi, n, _vector(n_ids, "n_ids", on, torch.int64, 1, True),
                                dout.data_ptr(), d, dim, ds, scale, out.data_ptr(), o, n_vocab, os_, bool(accumulate),
                                workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _vector(status, "status", torch.int32, 1, True),
-                               _on(torch, stream, dout.device, mine, scratch)), "tt_embed_grad")
+                               _vector(status, "status", on, torch.int32, 1, True),
+                               _on(torch, stream, on, mine, scratch)), "tt_embed_grad")
     return out
 
 
@@ -394,7 +399,8 @@ def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, s
     (which may be logits itself) the logits' gradient as a third."""
     torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
-    pt, pg = _vector(targets, "targets", torch.int32, n), _vector(row_grads, "row_grads", torch.float32, n, True)
+    on = logits.get_device()
+    pt, pg = _vector(targets, "targets", on, torch.int32, n), _vector(row_grads, "row_grads", on, torch.float32, n, True)
     loss = torch.empty(n, dtype=torch.float32, device=logits.device)
     lse = torch.empty(n, dtype=torch.float32, device=logits.device)
     mine = None
@@ -403,13 +409,13 @@ def token_loss(logits, targets, row_grads=None, want_grad=False, dlogits=None, s
     d, ds, pd = t, vocab, None
     if dlogits is not None:
         if mine is None:
-            d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
+            d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab, on)
         pd = dlogits.data_ptr()
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
     _check(lib().tt_token_loss(logits.data_ptr(), t, n, vocab, ls, pt, loss.data_ptr(), lse.data_ptr(), pg, pd, ds,
-                               _vector(status, "status", torch.int32, 1, True),
-                               _on(torch, stream, logits.device, loss, lse, mine)), "tt_token_loss")
+                               _vector(status, "status", on, torch.int32, 1, True),
+                               _on(torch, stream, on, loss, lse, mine)), "tt_token_loss")
     return (loss, lse) if dlogits is None else (loss, lse, dlogits)
 
 
@@ -417,17 +423,18 @@ def token_loss_grad(logits, targets, lse, row_grads=None, dlogits=None, status=N
     """The gradient of token_loss from the lse that it returned."""
     torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
-    pt, pl = _vector(targets, "targets", torch.int32, n), _vector(lse, "lse", torch.float32, n)
-    pg = _vector(row_grads, "row_grads", torch.float32, n, True)
+    on = logits.get_device()
+    pt, pl = _vector(targets, "targets", on, torch.int32, n), _vector(lse, "lse", on, torch.float32, n)
+    pg = _vector(row_grads, "row_grads", on, torch.float32, n, True)
     mine = None
     if dlogits is None:
         dlogits = mine = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
-    d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab)
+    d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab, on)
     if d != t:
         raise ValueError("dlogits: the type of logits wanted")
     _check(lib().tt_token_loss_grad(logits.data_ptr(), t, n, vocab, ls, pt, pl, pg, dlogits.data_ptr(), ds,
-                                    _vector(status, "status", torch.int32, 1, True),
-                                    _on(torch, stream, logits.device, mine)), "tt_token_loss_grad")
+                                    _vector(status, "status", on, torch.int32, 1, True),
+                                    _on(torch, stream, on, mine)), "tt_token_loss_grad")
     return dlogits
 
 
@@ -436,14 +443,14 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
     parameters are device tensors with an entry a row, or None (off)."""
     torch = _torch or _load_torch()
     t, n, vocab, ls = _matrix(logits, "logits")
-    f = torch.float32
-    pu = _vector(uniform, "uniform", f, n)
+    on, f = logits.get_device(), torch.float32
+    pu = _vector(uniform, "uniform", on, f, n)
     ids = torch.empty(n, dtype=torch.int32, device=logits.device)
     logprobs = torch.empty(n, dtype=f, device=logits.device)
-    _check(lib().tt_sample(logits.data_ptr(), t, n, vocab, ls, pu, _vector(temperature, "temperature", f, n, True),
-                           _vector(top_k, "top_k", torch.int32, n, True), _vector(top_p, "top_p", f, n, True),
-                           _vector(min_p, "min_p", f, n, True), ids.data_ptr(), logprobs.data_ptr(),
-                           _vector(status, "status", torch.int32, 1, True), _on(torch, stream, logits.device, ids, logprobs)),
+    _check(lib().tt_sample(logits.data_ptr(), t, n, vocab, ls, pu, _vector(temperature, "temperature", on, f, n, True),
+                           _vector(top_k, "top_k", on, torch.int32, n, True), _vector(top_p, "top_p", on, f, n, True),
+                           _vector(min_p, "min_p", on, f, n, True), ids.data_ptr(), logprobs.data_ptr(),
+                           _vector(status, "status", on, torch.int32, 1, True), _on(torch, stream, on, ids, logprobs)),
            "tt_sample")
     return ids, logprobs
 
