@@ -370,13 +370,18 @@ def embed(ids, table, scale=1.0, n_ids=None, dtype=None, out=None, status=None, 
 def embed_grad(ids, dout, n_vocab, scale=1.0, n_ids=None, dtype=None, out=None, accumulate=False, workspace=None,
                status=None, stream=None):
     """The gradient of embed: [n_vocab, dim] of `dtype` (float32 if None), the
-    scaled sums of dout's rows by ID; with accumulate, added to `out`."""
+    scaled sums of dout's rows by ID; with accumulate, added to `out`.
+    workspace: a contiguous tensor of any type, of tt_embed_grad_workspace()
+    bytes (allocated if None)."""
     torch = _torch or _load_torch()
     d, n, dim, ds = _matrix(dout, "dout")
     on = dout.get_device()
     pi = _vector(ids, "ids", on, torch.int32, n)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
+    if workspace is not None and (workspace.get_device() != on or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on cuda:%d wanted, got %s with strides %s on %s" % (
+            on, list(workspace.shape), list(workspace.stride()), workspace.device))
     mine = scratch = None
     if out is None:
         out, o = _new(torch, n_vocab, dim, dtype or torch.float32, dout.device, "dtype")

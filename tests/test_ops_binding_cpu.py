@@ -83,7 +83,8 @@ CALLS = {
     "embed": (tt.embed, lambda: dict(ids=ints(4), table=Standin(300, 16), n_ids=ints(1, torch.int64), out=Standin(4, 16),
                                      status=ints(1))),
     "embed_grad": (tt.embed_grad, lambda: dict(ids=ints(4), dout=Standin(4, 16), n_vocab=300, n_ids=ints(1, torch.int64),
-                                               out=Standin(300, 16), status=ints(1))),
+                                               out=Standin(300, 16), workspace=Standin(1024, dtype=torch.uint8),
+                                               status=ints(1))),
     "token_loss": (tt.token_loss, lambda: dict(logits=Standin(4, 300), targets=ints(4), row_grads=Standin(4),
                                                dlogits=Standin(4, 300), status=ints(1))),
     "token_loss_grad": (tt.token_loss_grad, lambda: dict(logits=Standin(4, 300), targets=ints(4), lse=Standin(4),
@@ -122,4 +123,14 @@ def test_the_tensors_device_is_the_current_one(library, call):
             v.on = 1
     with pytest.raises(ValueError, match="current device"):
         f(**a)
+    assert library.calls == 0
+
+
+@pytest.mark.parametrize("workspace", [Standin(1 << 20, dtype=torch.uint8, stride=(0,)), Standin(64, 64, stride=(128, 1)),
+                                       Standin(1024, dtype=torch.uint8, on=-1), torch.empty(1024, dtype=torch.uint8)])
+def test_a_workspace_holds_what_it_says(library, workspace):
+    """More elements than bytes behind them (an expanded tensor), gaps, or host memory."""
+    f, args = CALLS["embed_grad"]
+    with pytest.raises(ValueError, match="workspace"):
+        f(**{**args(), "workspace": workspace})
     assert library.calls == 0
