@@ -269,9 +269,13 @@ def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temp
 
 # ---- the same on torch CUDA tensors: outputs and scratch allocated where they
 # are not given, shapes, types and devices checked.  The kernels run on `stream` (the
-# current one if None); what is allocated here is handed to that stream.  Small
-# calls cost a few microseconds of device time, so these call the library
-# without a layer in between.
+# current one if None); what is allocated here is handed to that stream, and
+# tensors that come from another one are the caller's to order and to keep
+# (record_stream).  Small calls cost a few microseconds of device time, so these
+# call the library without a layer in between.
+#
+# They are forward and backward calls, not autograd functions: tensors that require
+# gradients are taken by their values, and no output has a graph behind it.
 
 _codes = {}          # torch dtype -> tt_dtype; filled with the first use of torch
 _torch = None        # the module, which this one does not need for anything else

@@ -15,7 +15,7 @@ namespace {
 // time, so that four loads are in flight before the first store: of one row
 // (WIDE), whose address is then worked out once, or of several rows.  Blocks take
 // rows in their order and do not loop: 304,824 rows of 4096 bf16 take 423 us
-// (99% of the measured copy bandwidth), and 458 us by 16 blocks an SM that go on
+// (97% of the measured copy bandwidth), and 458 us by 16 blocks an SM that go on
 // to later rows, whose stores are further apart.
 struct EmbedArgs {
   const int32_t *ids;
@@ -142,9 +142,10 @@ __global__ void __launch_bounds__(256) k_embed_any(EmbedArgs a, const TI *__rest
 // 26.4 and 26.2, 30 tiles 31.9 and 29.9.
 //
 // The sums are bound by memory, the sort by the latency of its kernels: 304,824
-// tokens of 2048 bfloat16 into 100,256 float rows take 375 us (2.07 GB, 83% of
-// the measured copy bandwidth), 335 of them the sums; 16,400 tokens of 1024
-// floats into 4,352 rows take 42 us, of which the bytes need 13.
+// tokens of 2048 bfloat16 into 100,256 float rows take 374 us (2.07 GB, 81% of
+// the measured copy bandwidth), some 330 of them the sums, and 367 us added to
+// what the rows hold (1.82 GB, since absent rows are left alone); 16,400 tokens
+// of 1024 floats into 4,352 rows take 42 us, of which the bytes need 13.
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_BINS = 1 << 11;
@@ -435,6 +436,8 @@ __device__ __forceinline__ int64_t tokens_before(const int32_t *keys, int64_t n,
 //   256  200,000 bfloat16   86   72   77     1024 60,000 bfloat16 106   87   97
 //   256  200,000 float      84  102   89     1024 60,000 float    140  160  142
 //   641  200,000 bfloat16  262    -  163      641 200,000 float   293  193  176
+// The float batch in registers is a tight fit: 64 of them, and 16 to 28 bytes
+// spilled, with which these were measured.
 enum Ahead { IN_REGISTERS, COPIED, STAGED };
 constexpr int SUM_THREADS = 256;                  // at most
 template <class T, int COLS> struct Cols;
@@ -871,10 +874,15 @@ extern "C" tt_status tt_embed_grad(const int32_t *d_ids, int64_t max_ids, const 
   if (workspace_bytes < p.bytes) return TT_ERR_CAPACITY;
   if (max_ids == 0 && accumulate) return TT_OK;
   char *ws = (char *)d_workspace;
-  // Rows that are mostly absent are cleared by blocks beside the sort's (8191 x
-  // 641 bf16 into 200,256 rows, when this was chosen: 70 us, and 77 us where the
-  // sums write them; 61 us now);
-  // with more tokens, rows written twice would cost more than that saves.
+  // Rows that are mostly absent are cleared by blocks beside the sort's; with more
+  // tokens, rows written twice cost what that saves.  us cleared there and written
+  // by the sums, for a token count of 1/32, 1/8, 1/4, 1/2 and all of the rows':
+  //    200256 x  641 bfloat16            61  73    79  87    99 101   128 126   181 177
+  //    100256 x 1024 bfloat16 -> float   81  82    82  92    95 101   109 113   138 134
+  //    200256 x 2048 bfloat16           129 153   158 175   185 191   224 224   298 292
+  //   1048576 x  128 bfloat16 -> float  107 120   115 134   131 152   174 179   228 224
+  //    100256 x   64 float               39  34    41  38    46  42    46  46    56  50
+  // (The last, a table of 26 MB, would rather not.)
   const bool clear = !accumulate && max_ids > 0 && max_ids <= n_vocab / 4;
   const int tokens_only = accumulate || clear;
   int32_t *keys[2] = {(int32_t *)(ws + p.keys[0]), (int32_t *)(ws + p.keys[1])};

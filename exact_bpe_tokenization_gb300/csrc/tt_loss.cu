@@ -17,12 +17,18 @@
 // holds a row (two blocks an SM, so that one reads or writes while the other
 // computes).  What does not fit (rows above 832 KB) is read again, from L2.
 //
-// With gradients 4096 x 100256 bfloat16 take 289 us (1.64 GB, 85% of the measured
-// copy bandwidth) and 1023 x 200255 floats 297 us (82%).  A block reads, waits
+// With gradients 4096 x 100256 bfloat16 take 287 us (1.64 GB, 84% of the measured
+// copy bandwidth) and 1023 x 200255 floats 291 us (83%); in place 306 us either,
+// the loss alone 129 and 137, and the gradient from lse 240 us, the time of a copy
+// of as many bytes.  A block reads, waits
 // for its cluster, and writes; its neighbour on the SM fills the wait, and not
 // all of it.  Rows of that size need clusters of 8, which leave a few SMs of
 // each group of them idle, but hold the row: with 4 blocks a row, half of it
-// comes from L2 a second time, and 323 us became 370.
+// comes from L2 a second time, and 323 us became 370 when that was tried.
+//
+// Gradients whose rows lie otherwise against 16 bytes than the logits' are written
+// an element at a time: rows of 100,257 cut from 100,352 bfloat16 take 286 us into
+// gradients of the same stride and 817 into contiguous ones.
 #include <algorithm>
 
 #include "tt_ops.cuh"
@@ -255,7 +261,7 @@ void run_rows_by(LossArgs a, int64_t n_rows, const void *logits, void *dlogits, 
 
 // A short row is little work behind a block's start, its barrier and its end, so
 // that small blocks, of which more share an SM, are faster.  Rows and gradients
-// in bfloat16, us for 32, 128, 256, 512 threads:
+// in bfloat16, us for 32, 128, 256, 512 threads, when this was chosen:
 //   32768 x   257     23    79   161   378
 //   32768 x  1024     33    85   166   387
 //   32768 x  4096     88   119   193   406

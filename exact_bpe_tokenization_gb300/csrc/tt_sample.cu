@@ -18,13 +18,15 @@
 // does those that the first one left, since the registers, shared memory and
 // cluster size of the histograms would slow the lists down by half.
 //
-// 256 x 100256 bfloat16, whose bytes need 7.7 us, take 23 us with a temperature
-// alone (a pass that reads and one that sums, over one or two rows an SM) and 31
-// with a top-k of 50 and top-p.  A mixture, of which a quarter goes to the
-// histograms, takes 82: their kernel's 45 us are, for a row, 3 of reading, 10 of
-// the first histogram (an atomic in shared memory for each token of the row,
-// which twice the warps do not speed up), 4 to find the bins, and 20 for the
-// finer ones and the last tokens, passes and cluster barriers in turn.
+// 256 x 100256 bfloat16, whose bytes need 7.6 us, take 31 us with a temperature
+// alone (a pass that reads and one that sums, over one or two rows an SM), 37
+// with a top-k of 50 and top-p, 147 with a top-k of 1000 and 204 where every row
+// is flat (calls back to back, their inputs not in L2).  A mixture, of which a
+// quarter goes to the histograms, takes 81: 37 for the lists' kernel and 52 for
+// theirs, each alone.  Of a row's time in the latter, parts that were timed are 3 of
+// reading, 10 of the first histogram (an atomic in shared memory for each token of
+// the row, which twice the warps do not speed up), 4 to find the bins, and 20 for
+// the finer ones and the last tokens, passes and cluster barriers in turn.
 #include <algorithm>
 
 #include "tt_ops.cuh"
@@ -1252,7 +1254,9 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
     //   152 x   4352     8   10      -    -     25   37
     // With less held it loses: 76 x 200255 floats 25 and 26, 94 and 103 us, 37 of
     // them 25 and 23, 95 and 55.  So do rows that come in turn: 200 x 100256 take
-    // 36 and 28, 76 and 72 us.
+    // 36 and 28, 76 and 72 us.  Other mixtures, by which row is the slowest: 37 x
+    // 100256 70 and 54 us, 64 of them 56 and 77, 80 of them 89 and 79; 37 to 120 of
+    // 20000 to 50257 IDs 40 to 60 and 50 to 62.
     a.cluster_log2 = spread(one_an_sm);
     if (n_rows <= one_an_sm[0] && (vecs >> a.cluster_log2) * 16 <= HELD_BINS / 4 * 5) {
       launch(Few<T>{}, k_sample_few<T>, n_rows, HELD_BINS, false);
@@ -1260,11 +1264,22 @@ extern "C" tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_row
     }
     a.cluster_log2 = spread(two_an_sm);
     launch(Lists<T>{}, k_sample<T>, n_rows, HELD, false);
-    // One block an SM; as a rule a quarter of the rows is left.  us of the
-    // mixture for 8, 4, 2 and 1 blocks a row:
-    //    37 x 200255 float      55   70   95  147
-    //   256 x 100256 bfloat16  120   89   76   96
-    //   512 x 100256 bfloat16  186  133  120  115
+    // One block an SM; as a rule a quarter of the rows is left.  us of a call on a
+    // mixture, its input not in L2, for 8, 4, 2 and 1 blocks a row:
+    //        100256 bfloat16          200255 float
+    //    37    (in one launch)        67   79  113  164
+    //    64                           74   87  119  171
+    //    80                           91  103  134  185
+    //   120                          117  107  137  186
+    //   153   91   70   83   99      160  147  174  226
+    //   200  117   99   89  107      202  191  191  245
+    //   256  128  101   91  107      222  201  195  251
+    //   300  142  109   93  109      238  214  199  253
+    //   400  180  132  124  117      342  295  304  310
+    //   512  213  144  132  127      424  350  339  378
+    // The rule takes the best of them up to 72 rows and from 200 to 288.  Between, 8
+    // blocks would save up to a third and 4 a sixth; above 288, 2 would save up to a
+    // fifth.  Rows of 20,000 to 50,257 IDs, 153 to 512 of them, are within a tenth.
     a.cluster_log2 = n_vocab < 16384 ? 0 : n_rows <= 72 ? 3 : n_rows <= 288 ? 1 : 0;
     launch(Bins<T>{}, k_sample_bins<T>, std::min<int64_t>(n_rows, 144 >> a.cluster_log2), HELD_BINS, true);
   });
