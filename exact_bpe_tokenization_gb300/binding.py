@@ -22,6 +22,7 @@ TT_FAMILY_CL100K_STYLE, TT_FAMILY_O200K_STYLE, TT_FAMILY_DEEPSEEK_STYLE = 1, 2, 
 TT_NOALLOC_MAX_BYTES, TT_NOALLOC_MAX_REQUESTS = 256 * 1024, 1024
 TT_F32, TT_F16, TT_BF16 = range(3)
 TT_MAX_IDS = 1 << 29
+TT_MAX_TEACHER = 1024
 
 _lib = None
 _lock = threading.Lock()
@@ -71,13 +72,20 @@ def lib():
             L.tt_embed_grad_workspace.restype = i64
             L.tt_token_loss.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, i64, p, p]
             L.tt_token_loss_grad.argtypes = [p, i32, i64, i64, i64, p, p, p, p, i64, p, p]
+            L.tt_linear_loss.argtypes = [p, p, i32] + [i64] * 5 + [p] * 5 + [i64, p, i32, i64, i32, p, i64, p, p]
+            L.tt_linear_loss_grad.argtypes = [p, p, i32] + [i64] * 5 + [p] * 4 + [i64, p, i32, i64, i32, p, i64, p, p]
+            L.tt_linear_loss_workspace.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+            L.tt_linear_loss_workspace.restype = i64
+            L.tt_distill_loss.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, i64, i64, f32] + [p] * 4 + [i64, p, p]
+            L.tt_distill_loss_grad.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, i64, i64, f32] + [p] * 3 + [i64, p, p]
             L.tt_sample.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, p, p, p, p]
             for name in ("tt_create", "tt_encode_batch", "tt_encode_batch_bounded", "tt_encode_batch_spans",
                          "tt_set_added_tokens",
                          "tt_encode_batch_noalloc",
                          "tt_encode_host",
                          "tt_get_status", "tt_pretokenize_batch", "tt_profile_read", "tt_debug_lookback",
-                         "tt_embed", "tt_embed_grad", "tt_token_loss", "tt_token_loss_grad", "tt_sample"):
+                         "tt_embed", "tt_embed_grad", "tt_token_loss", "tt_token_loss_grad", "tt_sample",
+                         "tt_linear_loss", "tt_linear_loss_grad", "tt_distill_loss", "tt_distill_loss_grad"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -265,6 +273,50 @@ def tt_sample(d_logits, dtype, n_rows, n_vocab, logits_stride, d_uniform, d_temp
     _check(lib().tt_sample(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_uniform),
                            _ptr(d_temperature), _ptr(d_top_k), _ptr(d_top_p), _ptr(d_min_p), _ptr(d_out_ids),
                            _ptr(d_out_logprobs), _ptr(d_status), _stream(stream)), "tt_sample")
+
+
+def tt_linear_loss(d_hidden, d_weight, dtype, n_rows, n_vocab, dim, hidden_stride, weight_stride, d_targets, d_loss, d_lse,
+                   d_row_grads, d_dhidden, dhidden_stride, d_dweight, dweight_type, dweight_stride, accumulate,
+                   d_workspace, workspace_bytes, d_status=None, stream=None):
+    _check(lib().tt_linear_loss(_ptr(d_hidden), _ptr(d_weight), dtype, n_rows, n_vocab, dim, hidden_stride,
+                                weight_stride, _ptr(d_targets), _ptr(d_loss), _ptr(d_lse), _ptr(d_row_grads),
+                                _ptr(d_dhidden), dhidden_stride, _ptr(d_dweight), dweight_type, dweight_stride,
+                                int(accumulate), _ptr(d_workspace), workspace_bytes, _ptr(d_status),
+                                _stream(stream)), "tt_linear_loss")
+
+
+def tt_linear_loss_grad(d_hidden, d_weight, dtype, n_rows, n_vocab, dim, hidden_stride, weight_stride, d_targets, d_lse,
+                        d_row_grads, d_dhidden, dhidden_stride, d_dweight, dweight_type, dweight_stride, accumulate,
+                        d_workspace, workspace_bytes, d_status=None, stream=None):
+    _check(lib().tt_linear_loss_grad(_ptr(d_hidden), _ptr(d_weight), dtype, n_rows, n_vocab, dim, hidden_stride,
+                                     weight_stride, _ptr(d_targets), _ptr(d_lse), _ptr(d_row_grads), _ptr(d_dhidden),
+                                     dhidden_stride, _ptr(d_dweight), dweight_type, dweight_stride, int(accumulate),
+                                     _ptr(d_workspace), workspace_bytes, _ptr(d_status), _stream(stream)),
+           "tt_linear_loss_grad")
+
+
+def tt_linear_loss_workspace(n_rows, n_vocab, dim, dtype, aligned_rows, dweight_type, want_grad):
+    """Bytes of scratch, or -1 for sizes that tt_linear_loss rejects."""
+    return lib().tt_linear_loss_workspace(int(n_rows), int(n_vocab), int(dim), dtype, int(aligned_rows), dweight_type,
+                                          int(want_grad))
+
+
+def tt_distill_loss(d_logits, dtype, n_rows, n_vocab, logits_stride, d_teacher_ids, ids_stride, d_teacher_logits,
+                    teacher_type, teacher_stride, k, temperature, d_loss, d_lse, d_row_grads, d_dlogits, dlogits_stride,
+                    d_status=None, stream=None):
+    _check(lib().tt_distill_loss(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_teacher_ids), ids_stride,
+                                 _ptr(d_teacher_logits), teacher_type, teacher_stride, k, temperature, _ptr(d_loss),
+                                 _ptr(d_lse), _ptr(d_row_grads), _ptr(d_dlogits), dlogits_stride, _ptr(d_status),
+                                 _stream(stream)), "tt_distill_loss")
+
+
+def tt_distill_loss_grad(d_logits, dtype, n_rows, n_vocab, logits_stride, d_teacher_ids, ids_stride, d_teacher_logits,
+                         teacher_type, teacher_stride, k, temperature, d_lse, d_row_grads, d_dlogits, dlogits_stride,
+                         d_status=None, stream=None):
+    _check(lib().tt_distill_loss_grad(_ptr(d_logits), dtype, n_rows, n_vocab, logits_stride, _ptr(d_teacher_ids),
+                                      ids_stride, _ptr(d_teacher_logits), teacher_type, teacher_stride, k, temperature,
+                                      _ptr(d_lse), _ptr(d_row_grads), _ptr(d_dlogits), dlogits_stride, _ptr(d_status),
+                                      _stream(stream)), "tt_distill_loss_grad")
 
 
 # ---- the same on torch CUDA tensors: outputs and scratch allocated where they
@@ -462,6 +514,140 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
                            _vector(status, "status", on, torch.int32, 1, True), _on(torch, stream, on, ids, logprobs)),
            "tt_sample")
     return ids, logprobs
+
+
+def _linear(torch, hidden, weight, targets, row_grads, want_grad, dhidden, dweight, accumulate, workspace, status, stream,
+            lse=None):
+    """What linear_loss and linear_loss_grad (with lse) share."""
+    t, n, dim, hs = _matrix(hidden, "hidden")
+    on, dev = hidden.get_device(), hidden.device
+    w, vocab, _, ws = _matrix(weight, "weight", None, dim, on)
+    if w != t:
+        raise ValueError("weight: the type of hidden wanted, got %s" % weight.dtype)
+    pt, pg = _vector(targets, "targets", on, torch.int32, n), _vector(row_grads, "row_grads", on, torch.float32, n, True)
+    grads = lse is not None
+    pl = _vector(lse, "lse", on, torch.float32, n) if grads else None
+    st = _vector(status, "status", on, torch.int32, 1, True)
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs dweight")
+    mine = []
+    if want_grad and dhidden is None:
+        dhidden = torch.empty((n, dim), dtype=hidden.dtype, device=dev)
+        mine.append(dhidden)
+    if want_grad and dweight is None:
+        dweight = torch.empty((vocab, dim), dtype=hidden.dtype, device=dev)
+        mine.append(dweight)
+    ph = pw = None
+    dhs = dws = dim
+    dw = t
+    if dhidden is not None:
+        d, _, _, dhs = _matrix(dhidden, "dhidden", n, dim, on)
+        if d != t:
+            raise ValueError("dhidden: the type of hidden wanted, got %s" % dhidden.dtype)
+        ph = dhidden.data_ptr()
+    if dweight is not None:
+        dw, _, _, dws = _matrix(dweight, "dweight", vocab, dim, on)
+        if dw != t and dw != TT_F32:
+            raise ValueError("dweight: the type of weight or float32 wanted, got %s" % dweight.dtype)
+        pw = dweight.data_ptr()
+    if workspace is not None and (workspace.get_device() != on or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on cuda:%d wanted, got %s with strides %s on %s" % (
+            on, list(workspace.shape), list(workspace.stride()), workspace.device))
+    if not grads:
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+        out = torch.empty(n, dtype=torch.float32, device=dev)
+        mine += [loss, out]
+    if workspace is None:
+        px, pv = hidden.data_ptr(), weight.data_ptr()
+        rows = t != TT_F32 and not (px | pv) & 15 and not (hs | ws) & 7
+        workspace = torch.empty(max(lib().tt_linear_loss_workspace(n, vocab, dim, t, rows, dw, ph is not None or
+                                                                   pw is not None), 256), dtype=torch.uint8, device=dev)
+        mine.append(workspace)
+    space = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), st, _on(torch, stream, on, *mine))
+    if grads:
+        _check(lib().tt_linear_loss_grad(hidden.data_ptr(), weight.data_ptr(), t, n, vocab, dim, hs, ws, pt, pl, pg, ph, dhs, pw,
+                                         dw, dws, bool(accumulate), *space), "tt_linear_loss_grad")
+        return dhidden, dweight
+    _check(lib().tt_linear_loss(hidden.data_ptr(), weight.data_ptr(), t, n, vocab, dim, hs, ws, pt, loss.data_ptr(),
+                                out.data_ptr(), pg, ph, dhs, pw, dw, dws, bool(accumulate), *space), "tt_linear_loss")
+    return (loss, out) if ph is None and pw is None else (loss, out, dhidden, dweight)
+
+
+def linear_loss(hidden, weight, targets, row_grads=None, want_grad=False, dhidden=None, dweight=None, accumulate=False,
+                workspace=None, status=None, stream=None):
+    """Next-token loss of hidden states [n, dim] through a head's weight [vocab, dim],
+    without the logits: (loss, lse), and with want_grad the gradients of hidden and
+    weight as a third and fourth.  dhidden, dweight: where they go; with one of them
+    given and not want_grad, the other is None and is not computed.  dweight may be
+    float32; with accumulate it is added to.  workspace: a contiguous tensor of any type, of
+    tt_linear_loss_workspace() bytes (allocated if None)."""
+    return _linear(_torch or _load_torch(), hidden, weight, targets, row_grads, want_grad, dhidden, dweight, accumulate,
+                   workspace, status, stream)
+
+
+def linear_loss_grad(hidden, weight, targets, lse, row_grads=None, dhidden=None, dweight=None, accumulate=False,
+                     workspace=None, status=None, stream=None):
+    """The gradients of linear_loss from the lse that it returned: (dhidden, dweight),
+    both if neither is given, else the given ones."""
+    torch = _torch or _load_torch()
+    if lse is None:
+        raise ValueError("lse: a tensor wanted")
+    return _linear(torch, hidden, weight, targets, row_grads, dhidden is None and dweight is None, dhidden, dweight,
+                   accumulate, workspace, status, stream, lse)
+
+
+def _distill(torch, logits, teacher_ids, teacher_logits, temperature, row_grads, want_grad, dlogits, status, stream, lse=None):
+    """What distill_loss and distill_loss_grad (with lse) share."""
+    t, n, vocab, ls = _matrix(logits, "logits")
+    on, dev, f = logits.get_device(), logits.device, torch.float32
+    tt, _, k, ts = _matrix(teacher_logits, "teacher_logits", n, None, on)
+    if teacher_ids is None or teacher_ids.dtype != torch.int32 or teacher_ids.dim() != 2 or teacher_ids.get_device() != on or \
+            tuple(teacher_ids.shape) != (n, k) or (teacher_ids.stride()[1] != 1 and k > 1):
+        raise ValueError("teacher_ids: a tensor %s [%d, %d] with contiguous columns on %s wanted" % (torch.int32, n, k, _cuda(on)))
+    ids = teacher_ids.stride()[0] if n > 1 else k
+    pg, st = _vector(row_grads, "row_grads", on, f, n, True), _vector(status, "status", on, torch.int32, 1, True)
+    grads = lse is not None
+    pl = _vector(lse, "lse", on, f, n) if grads else None
+    mine = []
+    if dlogits is None and want_grad:
+        dlogits = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
+        mine.append(dlogits)
+    pd, ds = None, vocab
+    if dlogits is not None:
+        d, _, _, ds = _matrix(dlogits, "dlogits", n, vocab, on)
+        if d != t:
+            raise ValueError("dlogits: the type of logits wanted")
+        pd = dlogits.data_ptr()
+    if not grads:
+        loss = torch.empty(n, dtype=f, device=dev)
+        out = torch.empty(n, dtype=f, device=dev)
+        mine += [loss, out]
+    stream = _on(torch, stream, on, *mine)
+    if grads:
+        _check(lib().tt_distill_loss_grad(logits.data_ptr(), t, n, vocab, ls, teacher_ids.data_ptr(), ids, teacher_logits.data_ptr(),
+                                          tt, ts, k, temperature, pl, pg, pd, ds, st, stream), "tt_distill_loss_grad")
+        return dlogits
+    _check(lib().tt_distill_loss(logits.data_ptr(), t, n, vocab, ls, teacher_ids.data_ptr(), ids, teacher_logits.data_ptr(), tt, ts, k,
+                                 temperature, loss.data_ptr(), out.data_ptr(), pg, pd, ds, st, stream), "tt_distill_loss")
+    return (loss, out) if pd is None else (loss, out, dlogits)
+
+
+def distill_loss(logits, teacher_ids, teacher_logits, temperature=1.0, row_grads=None, want_grad=False, dlogits=None,
+                 status=None, stream=None):
+    """Divergence of each row of logits [n, vocab] from a teacher's top logits
+    (teacher_ids int32 and teacher_logits, both [n, k]): (loss, lse), and with want_grad
+    or dlogits (which may be logits itself) the logits' gradient as a third."""
+    return _distill(_torch or _load_torch(), logits, teacher_ids, teacher_logits, temperature, row_grads, want_grad,
+                    dlogits, status, stream)
+
+
+def distill_loss_grad(logits, teacher_ids, teacher_logits, lse, temperature=1.0, row_grads=None, dlogits=None, status=None,
+                      stream=None):
+    """The gradient of distill_loss from the lse that it returned."""
+    torch = _torch or _load_torch()
+    if lse is None:
+        raise ValueError("lse: a tensor wanted")
+    return _distill(torch, logits, teacher_ids, teacher_logits, temperature, row_grads, True, dlogits, status, stream, lse)
 
 
 class Tokenizer:

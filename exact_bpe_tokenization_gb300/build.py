@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(REPO, "_build", "toktier-" + platform.machine())
 LIB = os.path.join(HERE, "libtoktier.so")
 TRACE_LIB = os.path.join(HERE, "libtoktier_trace.so")
-SOURCES = ["tt_api.cu", "tt_pretok.cu", "tt_bpe.cu", "tt_literals.cu", "tt_embed.cu", "tt_loss.cu", "tt_sample.cu"]
+SOURCES = ["tt_api.cu", "tt_pretok.cu", "tt_bpe.cu", "tt_literals.cu", "tt_embed.cu", "tt_loss.cu", "tt_sample.cu",
+           "tt_linear.cu", "tt_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall"]

@@ -1,0 +1,336 @@
+// tt_distill.cu - distillation from a teacher's top logits: the Kullback-Leibler
+// divergence of each row of logits from them, and its gradient (include/toktier.h).
+//
+//   q = softmax of the row's teacher logits over the temperature T
+//   lse = M / T + log(S),  S = sum_j exp((l_j - M) / T)
+//   loss = sum_k q_k (log q_k - (l_id(k) - M) / T + log(S))
+//   dl_j = g / T (exp((l_j - M) / T) / S - sum of q_k over the k with id(k) = j)
+//
+// Bound by memory, like the next-token loss: a row is read once into the shared
+// memory of a cluster of blocks, summed on the way with a running maximum, and
+// turned into gradients from there.  The teacher's entries (at most 1024) stay beside
+// it: each block has their shares q, and the logits of those that lie in its part of
+// the row.  The gradient of the whole part is written first, without q; behind a
+// barrier of the block the entries' places are written once more.  An ID that occurs
+// more than once belongs to its first entry, which a small hash table in shared memory
+// finds: that entry adds the shares up, in their order.
+#include <algorithm>
+
+#include "tt_rows.cuh"
+
+using namespace tt::ops;
+
+namespace {
+
+constexpr int SPACE = 112 * 1024;                // bytes of shared memory of a block: two blocks an SM
+constexpr int HELD = 104 * 1024;                 // the most of them for a row
+constexpr int U = 4;                             // vectors a thread takes at a time
+constexpr int UC = 4, AHEAD = 4;                 // vectors a group of copies, groups ahead
+
+struct DistillArgs {
+  int64_t n_vocab, logits_stride, dlogits_stride, ids_stride, values_stride;
+  const int32_t *ids;
+  const void *values;
+  int32_t values_type;
+  int k, slots;                                  // entries a row, slots of the hash table (0: no gradient)
+  float inv_t, c;                                // 1 / T and log2(e) / T
+  float *loss, *lse_out;
+  const float *lse_in, *row_grads;
+  int32_t *status;
+  int cluster, held;                             // blocks a row, vectors a block can hold
+};
+
+__device__ __forceinline__ float value_of(const DistillArgs &a, int64_t row, int i) {
+  const int64_t at = row * a.values_stride + i;
+  if (a.values_type == TT_F32) return reinterpret_cast<const float *>(a.values)[at];
+  if (a.values_type == TT_F16) return to_f32(reinterpret_cast<const __half *>(a.values)[at]);
+  return to_f32(reinterpret_cast<const __nv_bfloat16 *>(a.values)[at]);
+}
+
+struct OpMaxNan { __device__ float operator()(float a, float b) const { return a > b || a != a ? a : b; } };
+
+// GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
+template <class T, int GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs a, const T *logits, T *dlogits) {
+  constexpr int E = RowParts<T>::E, WARPS = THREADS / 32;
+  extern __shared__ uint4 s_row[];
+  int32_t *s_id = reinterpret_cast<int32_t *>(s_row + a.held);              // [k] the entries' IDs, -1: none
+  float *s_q = reinterpret_cast<float *>(s_id + a.k), *s_x = s_q + a.k;     // [k] shares and logits
+  int32_t *s_key = reinterpret_cast<int32_t *>(s_x + a.k), *s_first = s_key + a.slots;
+  __shared__ float2 s_warp[WARPS], s_blocks[8];
+  __shared__ float s_box[WARPS];
+  __shared__ int s_twice;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+  if (GRAD != 2 && a.cluster > 1) cluster_arrive();
+  const int64_t row = blockIdx.x / a.cluster;
+  const T *l = logits + row * a.logits_stride;
+  const RowParts<T> part(l, (int)a.n_vocab);
+  const int each = (part.vecs + a.cluster - 1) / a.cluster, first = min(part.vecs, rank * each);
+  const int n = min(part.vecs - first, each), n_held = GRAD == 1 ? min(n, a.held) : 0;
+  const uint4 *body = reinterpret_cast<const uint4 *>(l + part.lead) + first;
+  // what is held comes by copies that run ahead; a thread reads its own
+  auto fetch = [&](int v0) {
+#pragma unroll
+    for (int u = 0; u < UC; ++u)
+      if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+    copy_group();
+  };
+  if (GRAD == 1) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) fetch(tid + d * UC * THREADS);
+  }
+  const int lone = rank == 0 ? part.scalar(tid) : -1;
+  const float x = lone >= 0 ? to_f32(l[lone]) : -INF;
+  const float g_row = GRAD && a.row_grads ? a.row_grads[row] : 1.f;
+
+  // the teacher's entries: the maximum and sum of their softmax, and their logits
+  const int lo = part.lead + first * E, hi = lo + n * E;                    // this block's part of the row
+  auto in_part = [&](int id) { return (id >= lo && id < hi) || (rank == 0 && (id < part.lead || id >= part.lead + part.vecs * E)); };
+  if (tid == 0) s_twice = 0;
+  for (int i = tid; i < a.slots; i += THREADS) {
+    s_key[i] = -1;
+    s_first[i] = 1 << 30;
+  }
+  float top = -INF;
+  for (int i = tid; i < a.k; i += THREADS) {
+    int id = a.ids[row * a.ids_stride + i];
+    if (id >= a.n_vocab) {
+      if (rank == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+      id = -1;
+    }
+    const float v = id >= 0 ? value_of(a, row, i) : -INF;
+    s_id[i] = max(id, -1);
+    s_q[i] = v;
+    // read here, before any block can write to the row
+    s_x[i] = id >= 0 && ((GRAD != 2 && rank == 0) || (GRAD && in_part(id))) ? to_f32(l[id]) : 0.f;
+    top = OpMaxNan{}(top, v);
+  }
+  top = block_all(top, OpMaxNan{}, s_box);
+  float mass = 0;
+  for (int i = tid; i < a.k; i += THREADS) mass += s_id[i] >= 0 ? ex2((s_q[i] - top) * a.c) : 0.f;
+  mass = block_all(mass, OpSum{}, s_box);
+  // nothing that the teacher gives any weight to
+  const bool none = top == -INF;
+  const float log_mass = logf(mass);
+  // slots are claimed by the entries of this block's part
+  if (GRAD) {
+    for (int i = tid; i < a.k; i += THREADS) {
+      const int id = s_id[i];
+      if (id < 0 || !in_part(id)) continue;
+      int at = (int)((uint32_t)id * 2654435761u >> 16) & (a.slots - 1);
+      for (int tries = 0; tries < a.slots; ++tries) {                       // (half of them at most are taken)
+        const int old = atomicCAS(&s_key[at], -1, id);
+        if (old == -1 || old == id) {
+          atomicMin(&s_first[at], i);
+          if (old == id) s_twice = 1;
+          break;
+        }
+        at = (at + 1) & (a.slots - 1);
+      }
+    }
+  }
+
+  float lse, from, inverse = 1.f;                // probabilities are 2^(c (l - from)) * inverse
+  if (GRAD == 2) {
+    lse = a.lse_in[row];
+    from = 0;
+  } else {
+    Running<true> run;
+    run.c = a.c;
+    if (GRAD == 1)
+      groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
+        copy_wait<AHEAD - 1>();
+        fetch(v0 + AHEAD * UC * THREADS);
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+          if (whole.value || v0 + u * THREADS < n_held) run.add(s_row[v0 + u * THREADS], T{});
+      });
+    groups<THREADS>(n_held, n, U, [&](int v0, auto whole) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n) run.add(r[u], T{});
+    });
+    if (lone >= 0) run.add(x);
+    run.total();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) run.join(__shfl_xor_sync(~0u, run.m, o), __shfl_xor_sync(~0u, run.s, o));
+    if (lane == 0) s_warp[warp] = make_float2(run.m, run.s);
+    __syncthreads();
+    run.m = LOWEST;
+    run.s = 0;
+    for (int w = 0; w < WARPS; ++w) run.join(s_warp[w].x, s_warp[w].y);
+    if (a.cluster > 1) {
+      cluster_wait();                            // all blocks have begun
+      if (tid < a.cluster) *of_block(&s_blocks[rank], tid) = make_float2(run.m, run.s);
+      cluster_sync();
+      run.m = LOWEST;
+      run.s = 0;
+      for (int b = 0; b < a.cluster; ++b) run.join(s_blocks[b].x, s_blocks[b].y);
+    }
+    const float log_s = logf(run.s);
+    from = run.m;
+    inverse = __fdividef(1.f, run.s);            // of 1 .. 2^20
+    lse = run.s == 0 ? -INF : run.m * a.inv_t + log_s;
+    if (rank == 0) {
+      float loss = 0;
+      for (int i = tid; i < a.k; i += THREADS) {
+        if (s_id[i] < 0) continue;
+        const float y = (s_q[i] - top) * a.c, q = ex2(y) * __fdividef(1.f, mass);
+        if (q != 0) loss += q * ((s_q[i] - top) * a.inv_t - log_mass - (s_x[i] - run.m) * a.inv_t + log_s);
+      }
+      loss = block_all(loss, OpSum{}, s_box);
+      if (tid == 0) {
+        if (a.lse_out) a.lse_out[row] = lse;
+        a.loss[row] = none ? 0.f : run.s == 0 ? INF : loss;
+      }
+    }
+  }
+  if (GRAD) {
+    T *d = dlogits + row * a.dlogits_stride;
+    const bool zero = none || lse == -INF;
+    const float g = zero ? 0.f : g_row * a.inv_t, shift = GRAD == 2 ? lse * LOG2E : 0.f, factor = g * inverse;
+    // 2^(c (l - from)), or from lse 2^(c l - lse log2(e))
+    auto power = [&](float v) { return GRAD == 2 ? ex2(fmaf(v, a.c, -shift)) : ex2((v - from) * a.c); };
+    const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(l)) & 15) == 0;
+    T *out = d + part.lead + (int64_t)first * E;
+    auto write = [&](uint4 r, int vi) {
+      float v[E];
+      vec_f32(r, v, T{});
+#pragma unroll
+      for (int i = 0; i < E; i += 2) {
+        float2 y;
+        if (GRAD == 2) {
+          y = make_float2(power(v[i]), power(v[i + 1]));
+        } else {
+          y = sub_mul2(make_float2(v[i], v[i + 1]), from, a.c);
+          y = make_float2(ex2(y.x), ex2(y.y));
+        }
+        y = mul2(y, factor);
+        v[i] = y.x;
+        v[i + 1] = y.y;
+      }
+      if (zero)
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = 0;
+      T *to = out + (int64_t)vi * E;
+      if (same) {
+        __stcs(reinterpret_cast<uint4 *>(to), f32_vec(v, T{}));
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) to[i] = from_f32<T>(v[i]);
+      }
+    };
+    groups<THREADS>(0, n_held, U, [&](int v0, auto whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n_held) write(s_row[v0 + u * THREADS], v0 + u * THREADS);
+    });
+    groups<THREADS>(n_held, n, U, [&](int v0, auto whole) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (whole.value || v0 + u * THREADS < n) write(r[u], v0 + u * THREADS);
+    });
+    if (lone >= 0) d[lone] = from_f32<T>(zero ? 0.f : power(x) * factor);
+    if (zero) return;
+    __syncthreads();                             // the part's gradients are written, the slots claimed
+    const bool twice = s_twice;
+    for (int i = tid; i < a.k; i += THREADS) {
+      const int id = s_id[i];
+      if (id < 0 || !in_part(id)) continue;
+      auto share = [&](int e) { return ex2((s_q[e] - top) * a.c) * __fdividef(1.f, mass); };
+      float q = share(i);
+      if (twice) {
+        int at = (int)((uint32_t)id * 2654435761u >> 16) & (a.slots - 1);
+        while (s_key[at] != id) at = (at + 1) & (a.slots - 1);
+        if (s_first[at] != i) continue;
+        for (int e = i + 1; e < a.k; ++e)
+          if (s_id[e] == id) q += share(e);
+      }
+      d[id] = from_f32<T>((power(s_x[i]) * inverse - q) * g);
+    }
+  }
+}
+
+template <class T, int GRAD, int THREADS> struct Tag {};
+
+template <class T, int GRAD, int THREADS>
+void run_rows_by(DistillArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
+  const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
+  a.slots = 0;
+  if (GRAD)
+    for (a.slots = 32; a.slots < 2 * a.k;) a.slots *= 2;
+  const int extra = (a.k * 12 + a.slots * 8 + 15) / 16 * 16, held = std::min(HELD, SPACE - extra) / 16 * 16;
+  a.cluster = (int)std::min<int64_t>(8, (bytes + held - 1) / held);
+  // few rows: spread each over more blocks, down to 16 KB a block, as for the next-token loss
+  while (a.cluster <= 4 && n_rows * a.cluster * 2 <= 2 * 152 && bytes >= a.cluster * 2 * 16384) a.cluster *= 2;
+  const int64_t each = ((bytes + 15) / 16 + a.cluster - 1) / a.cluster;
+  a.held = GRAD == 1 ? (int)std::min<int64_t>(each, held / 16) : 0;
+  auto k = k_distill<T, GRAD, THREADS>;
+  if (allow_shared<Tag<T, GRAD, THREADS>>(k, SPACE)) return;                // (the error is kept)
+  launch_cluster(k, dim3((unsigned)(n_rows * a.cluster)), THREADS, (size_t)a.held * 16 + extra, a.cluster, false, stream, a,
+                 (const T *)logits, (T *)dlogits);
+}
+
+// block sizes by the row's bytes, as for the next-token loss (tt_loss.cu has the table)
+template <class T, int GRAD> void run_rows(const DistillArgs &a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
+  const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
+  if (bytes <= 4096) run_rows_by<T, GRAD, 32>(a, n_rows, logits, dlogits, stream);
+  else if (bytes <= 32768) run_rows_by<T, GRAD, 128>(a, n_rows, logits, dlogits, stream);
+  else run_rows_by<T, GRAD, 256>(a, n_rows, logits, dlogits, stream);
+}
+
+tt_status run_distill(const void *d_logits, int32_t type, int64_t n_rows, int64_t k, float temperature, DistillArgs a, void *d_dlogits,
+                      tt_stream_t stream, const char *what) {
+  if (!type_ok(type) || !type_ok(a.values_type) || n_rows < 0 || !vocab_ok(a.n_vocab) || a.logits_stride < a.n_vocab ||
+      (d_dlogits && a.dlogits_stride < a.n_vocab) || k < 1 || k > TT_MAX_TEACHER || a.ids_stride < k || a.values_stride < k ||
+      !(temperature >= 0x1p-64f && temperature <= 0x1p64f) || !optional_ok(a.status, 4) || !optional_ok(a.row_grads, 4) ||
+      !optional_ok(a.lse_out, 4) || !optional_ok(a.lse_in, 4) || !optional_ok(a.loss, 4) ||
+      !optional_ok(d_dlogits, type_size(type)) || (d_dlogits == d_logits && d_logits && a.dlogits_stride != a.logits_stride))
+    return TT_ERR_INVALID_ARG;
+  if (n_rows > TT_MAX_IDS) return TT_ERR_CAPACITY;
+  if (n_rows == 0) return TT_OK;
+  if (!array_ok(d_logits, type_size(type)) || !array_ok(a.ids, 4) || !array_ok(a.values, type_size(a.values_type))) return TT_ERR_INVALID_ARG;
+  if (!a.lse_in && !a.loss) return TT_ERR_INVALID_ARG;
+  a.k = (int)k;
+  a.inv_t = 1.f / temperature;
+  a.c = (float)(1.4426950408889634 / temperature);
+  with_type(type, [&](auto t) {
+    using T = decltype(t);
+    if (a.lse_in) run_rows<T, 2>(a, n_rows, d_logits, d_dlogits, stream);
+    else if (d_dlogits) run_rows<T, 1>(a, n_rows, d_logits, d_dlogits, stream);
+    else run_rows<T, 0>(a, n_rows, d_logits, nullptr, stream);
+  });
+  return launched(what);
+}
+
+}  // namespace
+
+extern "C" tt_status tt_distill_loss(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
+                                     const int32_t *d_teacher_ids, int64_t ids_stride, const void *d_teacher_logits,
+                                     int32_t teacher_type, int64_t teacher_stride, int64_t k, float temperature, float *d_loss,
+                                     float *d_lse, const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,
+                                     int32_t *d_status, tt_stream_t stream) {
+  const DistillArgs a{n_vocab, logits_stride, dlogits_stride, ids_stride, teacher_stride, d_teacher_ids, d_teacher_logits, teacher_type,
+                      0, 0, 0, 0, d_loss, d_lse, nullptr, d_row_grads, d_status, 1, 0};
+  return run_distill(d_logits, type, n_rows, k, temperature, a, d_dlogits, stream, "tt_distill_loss");
+}
+
+extern "C" tt_status tt_distill_loss_grad(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
+                                          const int32_t *d_teacher_ids, int64_t ids_stride, const void *d_teacher_logits,
+                                          int32_t teacher_type, int64_t teacher_stride, int64_t k, float temperature,
+                                          const float *d_lse, const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,
+                                          int32_t *d_status, tt_stream_t stream) {
+  if (n_rows > 0 && n_rows <= TT_MAX_IDS && (!d_lse || !d_dlogits)) return TT_ERR_INVALID_ARG;
+  const DistillArgs a{n_vocab, logits_stride, dlogits_stride, ids_stride, teacher_stride, d_teacher_ids, d_teacher_logits, teacher_type,
+                      0, 0, 0, 0, nullptr, nullptr, d_lse, d_row_grads, d_status, 1, 0};
+  return run_distill(d_logits, type, n_rows, k, temperature, a, d_dlogits, stream, "tt_distill_loss_grad");
+}

@@ -1,0 +1,338 @@
+// tt_gemm.cuh - matrix products of 16-bit operands on the tensor cores, with an
+// epilogue of the caller's: D = A * B^T in 32 bits, tile by tile.
+//
+// A pair of SMs computes a tile of 256 x 256: each loads half of A's rows and half
+// of B's by TMA (64 of the contraction a stage), one thread of the pair issues the
+// products (tcgen05, cta_group::2), and 128 rows of the result lie in the tensor
+// memory of each.  Two tiles fit there, so that the epilogue's warps read one while
+// the next is computed.  A launch has a pair for every two SMs; tiles are handed out
+// by number.
+//
+// An operand lies in memory either with the contraction along its rows ("K-major")
+// or across them ("MN-major"); both are what a TMA box of 64 elements by 8 rows and
+// more leaves in shared memory with the 128-byte swizzle.  An operand may be a sum
+// of up to three parts (32-bit values split into bfloat16 ones): then the products
+// of the listed pairs of parts are added up.
+#pragma once
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "tt_ops.cuh"
+
+namespace tt {
+namespace gemm {
+
+using namespace tt::ops;
+
+constexpr int TILE = 256, HALF = 128, KB = 64;            // rows and columns of a tile, a block's part, contraction a stage
+constexpr int STAGES = 6, STAGE_BYTES = 2 * HALF * KB * 2;
+constexpr int EPI_WARPS = 8, THREADS = (4 + EPI_WARPS) * 32;
+constexpr int SHARED = STAGES * STAGE_BYTES + 1024;       // and what aligns the stages to 1024 bytes
+constexpr int SMS = 152;
+constexpr uint32_t TRIES = 1u << 22;                      // of a wait, before the call gives up
+
+struct Gemm {
+  int m_tiles, n_tiles, splits;                           // the contraction is cut into `splits` parts
+  int k_blocks;                                           // of 64, the last filled up with zeros
+  int pairs;                                              // of parts, listed in nibbles of pair_a and pair_b
+  uint32_t pair_a, pair_b, idesc;
+  int group;                                              // tile rows that are passed through together
+  int32_t *status;
+};
+
+// ------------------------------------------------------------ device: waits
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t in_block(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok;
+}
+// false: the wait ran out, here or in another role of the block
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *dead) {
+  for (uint32_t i = 0; i < TRIES; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if ((i & 255) == 255 && *dead) return false;
+  }
+  *dead = 1;
+  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *dead) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, dead);
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {   // an address of the cluster
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// ------------------------------------------------------------ device: copies and products
+// a box to this block's shared memory, its bytes told to a barrier of the pair
+__device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::
+                   "r"(to), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+               "l"(b), "r"(idesc), "r"((uint32_t)add)
+               : "memory");
+}
+// the barrier at this address of both blocks, when the products issued so far are done
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t at, float v[32]) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+
+// A shared memory descriptor: the address and two distances in units of 16 bytes,
+// version 1, 128-byte swizzle.  K-major: groups of eight rows (of 128 bytes) lie
+// `stride` apart.  MN-major: eight of the contraction lie `stride` apart, 64 of the
+// rows `lead`.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// how a block's half of an operand (128 rows by 64 of the contraction) is loaded
+// and described: K-major one box of 128 rows, MN-major two boxes of 64 rows
+template <bool MN> struct Operand {
+  static __device__ __forceinline__ void load(uint32_t to, const CUtensorMap *map, int row, int k, int part, uint32_t bar) {
+    if (MN) {
+      load_box(to, map, row, k, part, bar);
+      load_box(to + HALF * KB, map, row + 64, k, part, bar);
+    } else {
+      load_box(to, map, k, row, part, bar);
+    }
+  }
+  // of the 16 of the contraction from 16 * step on
+  static __device__ __forceinline__ uint64_t desc(uint32_t at, int step) {
+    return MN ? smem_desc(at + step * 2048, HALF * KB, 1024) : smem_desc(at + step * 32, 16, 1024);
+  }
+};
+
+// tile number -> its place: `group` tile rows are passed through together, column by
+// column, so that what runs at a time shares operands of both sides
+struct Place { int m, n, split; };
+__device__ __forceinline__ Place place_of(const Gemm &g, int t) {
+  const int per = g.m_tiles * g.n_tiles;
+  Place p;
+  p.split = t / per;
+  t -= p.split * per;
+  const int first = t / (g.group * g.n_tiles) * g.group, rows = min(g.group, g.m_tiles - first);
+  t -= first * g.n_tiles;
+  p.m = first + t % rows;
+  p.n = t / rows;
+  return p;
+}
+__device__ __forceinline__ int2 blocks_of(const Gemm &g, int split) {
+  return make_int2((int)((int64_t)g.k_blocks * split / g.splits), (int)((int64_t)g.k_blocks * (split + 1) / g.splits));
+}
+
+// Epi is called by each thread of the epilogue's warps as epi(row, column, split, half, load):
+// the row of the result that it has, the first of the 128 columns that it reads, and
+// load(c, v), which brings 32 of them from the c-th on and is called by whole warps.
+template <bool A_MN, bool B_MN, class Epi>
+__global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
+    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Gemm g, const Epi epi) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ uint64_t s_bar[2 * STAGES + 4];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const uint32_t stages = (saddr(s_raw) + 1023) & ~1023u;
+  const uint32_t full = saddr(s_bar), empty = full + 8 * STAGES, done = empty + 8 * STAGES, free_ = done + 16;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(done + 8 * i, 1);
+      bar_init(free_ + 8 * i, 2 * EPI_WARPS);
+    }
+    s_dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
+  const int n_tiles = g.m_tiles * g.n_tiles * g.splits, n_pairs = gridDim.x / 2;
+  bool ok = true;
+
+  if (warp == 0 && lane == 0) {
+    // copies: a stage is free when the products that read it are done
+    int stage = 0;
+    uint32_t phase = 1;
+    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs) {
+      const Place p = place_of(g, t);
+      const int2 kb = blocks_of(g, p.split);
+      const int ra = p.m * TILE + rank * HALF, rb = p.n * TILE + rank * HALF;
+      for (int i = 0; ok && i < g.pairs; ++i) {
+        for (int k = kb.x; k < kb.y; ++k) {
+          if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) break;
+          if (rank == 0) bar_expect(full + 8 * stage, 2 * STAGE_BYTES);
+          const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
+          Operand<A_MN>::load(to, &map_a, ra, k * KB, g.pair_a >> (4 * i) & 15, bar);
+          Operand<B_MN>::load(to + STAGE_BYTES / 2, &map_b, rb, k * KB, g.pair_b >> (4 * i) & 15, bar);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int i = 0;
+    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs, ++i) {
+      const Place p = place_of(g, t);
+      const int2 kb = blocks_of(g, p.split);
+      const int count = (kb.y - kb.x) * g.pairs;
+      if (!(ok = bar_wait(free_ + 8 * (i & 1), (i >> 1 & 1) ^ 1, &s_dead))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t d = tmem + (i & 1) * TILE;
+      for (int k = 0; k < count; ++k) {
+        if (!(ok = bar_wait(full + 8 * stage, phase, &s_dead))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = stages + stage * STAGE_BYTES;
+#pragma unroll
+        for (int s = 0; s < KB / 16; ++s)
+          mma(d, Operand<A_MN>::desc(at, s), Operand<B_MN>::desc(at + STAGE_BYTES / 2, s), g.idesc, k || s);
+        commit(empty + 8 * stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) commit(done + 8 * (i & 1));
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    int i = 0;
+    for (int t = blockIdx.x / 2; t < n_tiles; t += n_pairs, ++i) {
+      const Place p = place_of(g, t);
+      ok = bar_wait(done + 8 * (i & 1), i >> 1 & 1, &s_dead);
+      if (!__all_sync(~0u, ok)) {
+        ok = false;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t at = tmem + (i & 1) * TILE + half * HALF + ((uint32_t)(quarter * 32) << 16);
+      epi(p.m * TILE + (int)rank * HALF + quarter * 32 + lane, p.n * TILE + half * HALF, p.split, half,
+          [&](int c, float v[32]) { tmem_load32(at + c, v); });
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(in_block(free_ + 8 * (i & 1), 0));
+    }
+  }
+  if (!ok) {
+    // what is under way (copies, products) ends by itself within this time
+    op_status(g.status, TT_ERR_TIMEOUT);
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  if (warp == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------ host
+// A matrix of up to three parts in 16-bit elements, 16-byte aligned: what a TMA map needs.
+struct Matrix {
+  const void *p;
+  int64_t rows, cols, stride, parts, part_stride;          // in elements
+};
+
+CUresult encode_map(CUtensorMap *map, bool bf16, const Matrix &m, uint32_t box_rows);
+
+inline uint32_t idesc_of(bool bf16, bool a_mn, bool b_mn) {
+  const uint32_t type = bf16 ? 1 : 0;
+  return 1u << 4 | type << 7 | type << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (TILE >> 3) << 17 | (TILE >> 4) << 24;
+}
+
+template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
+
+// D [rows of a][rows of b] = a * b^T over the contraction; with _MN the matrix lies the
+// other way round (its rows are the contraction).  False: an error, which is kept.
+template <bool A_MN, bool B_MN, class Epi>
+inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, int group, const Epi &epi, int32_t *status,
+                     cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  if (encode_map(&ma, bf16, a, A_MN ? KB : HALF) != CUDA_SUCCESS || encode_map(&mb, bf16, b, B_MN ? KB : HALF) != CUDA_SUCCESS) return false;
+  Gemm g;
+  g.m_tiles = (int)(((A_MN ? a.cols : a.rows) + TILE - 1) / TILE);
+  g.n_tiles = (int)(((B_MN ? b.cols : b.rows) + TILE - 1) / TILE);
+  g.k_blocks = (int)(((A_MN ? a.rows : a.cols) + KB - 1) / KB);
+  g.splits = splits;
+  // the products of parts whose orders add up to less than three, the smallest first (the
+  // sums are cut off, not rounded, at each step: small ones lose less); the rest is below 2^-24
+  g.pairs = a.parts == 1 ? 1 : 6;
+  g.pair_a = a.parts == 1 ? 0 : 0x001102;
+  g.pair_b = a.parts == 1 ? 0 : 0x010120;
+  g.idesc = idesc_of(bf16, A_MN, B_MN);
+  g.group = group;
+  g.status = status;
+  auto k = k_gemm<A_MN, B_MN, Epi>;
+  if (allow_shared<GemmTag<A_MN, B_MN, Epi>>(k, SHARED)) return false;
+  const int tiles = g.m_tiles * g.n_tiles * g.splits;
+  k<<<2 * std::min(tiles, SMS / 2), THREADS, SHARED, stream>>>(ma, mb, g, epi);
+  return true;
+}
+
+// Parts to cut a contraction into, so that every pair of SMs has as much to do: the
+// least of the rounds of tiles, each of its blocks and a tile's start and end, and the
+// traffic of the parts (times in blocks of 64, 0.27 us).
+inline int choose_splits(int64_t m, int64_t n, int64_t k, int pairs) {
+  const int64_t tiles = ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE), blocks = (k + KB - 1) / KB;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 32 && s * 4 <= std::max<int64_t>(blocks, 4); ++s) {
+    const int64_t rounds = (tiles * s + SMS / 2 - 1) / (SMS / 2);
+    double cost = (double)rounds * ((double)((blocks + s - 1) / s) * pairs + 4);
+    if (s > 1) cost += 12 + (double)s * m * n * 8 / 6.8e12 / 0.27e-6;
+    if (cost < least * 0.99) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+}  // namespace gemm
+}  // namespace tt

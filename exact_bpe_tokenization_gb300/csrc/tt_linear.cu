@@ -1,0 +1,587 @@
+// tt_linear.cu - next-token loss of hidden states through the head's weight, and
+// its gradients, without the matrix of logits (include/toktier.h).
+//
+//   l = H W^T,  lse_i = M + log(S),  S = sum_j exp(l_ij - M),  loss_i = (M - l_it) + log(S)
+//   G_ij = g_i (exp(l_ij - lse_i) - (j == t_i)),  dH = G W,  dW = G^T H
+//
+// The products run on the tensor cores (tt_gemm.cuh), and what would be the logits
+// never leaves them: the first product's epilogue keeps a maximum and a sum of each
+// row and tile, k_finish joins them, and the second run of the same product turns its
+// tiles into G.  G is in the operands' type, the one place where less than 32 bits
+// stands between the logits and the gradients; a chunk of rows of it (1 GB) is kept at
+// a time.  32-bit operands are split into three bfloat16 parts each, whose products
+// are added in 32 bits: what is left out is below 2^-24.
+#include "tt_gemm.cuh"
+#include "tt_rows.cuh"
+
+using namespace tt::ops;
+using namespace tt::gemm;
+
+namespace tt {
+namespace gemm {
+
+CUresult encode_map(CUtensorMap *map, bool bf16, const Matrix &m, uint32_t box_rows) {
+  static std::atomic<void *> entry{nullptr};
+  void *f = entry.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return CUDA_ERROR_NOT_FOUND;
+    entry.store(f, std::memory_order_release);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)m.stride * 2, (cuuint64_t)m.part_stride * 2};
+  const cuuint32_t box[3] = {KB, box_rows, 1}, steps[3] = {1, 1, 1};
+  return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f)(
+      map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(m.p), dims, strides, box, steps,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+}  // namespace gemm
+}  // namespace tt
+
+namespace {
+
+constexpr int64_t MAX_WIDTH = 1 << 16;
+constexpr int64_t KEPT = 1ll << 30;                        // bytes of G at a time
+constexpr int64_t PARTIALS = 1ll << 28;                    // bytes of maxima and sums at a time
+constexpr int F16_UP = 14;                                 // G in 16 bits: the largest |g| becomes 2^14
+
+// what a row's gradient is made from: G = exp(l - from) * mul - g (j == t); t < 0: none
+struct RowInfo { float from, mul, g; int t; };
+
+// ------------------------------------------------------------ epilogues
+// The maximum and sum of each row and 128 columns, and the target's logit.  The
+// maximum stays within the finite floats, so that a difference is NaN only where a
+// logit is.
+struct StatsEpi {
+  int n_rows, n_cols;
+  int64_t row0;                                            // the chunk's first row
+  const int32_t *targets;
+  float2 *part;                                            // [column halves][n_rows]
+  float *target_logit;                                     // [n_rows]
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
+    const bool mine = row < n_rows;
+    const int t = mine ? targets[row0 + row] : -1;
+    float m = LOWEST;
+    float2 s = make_float2(0, 0);
+    for (int c = 0; c < HALF; c += 32) {
+      float v[32];
+      load(c, v);
+      const int n = n_cols - col - c;                      // columns that are there
+      if (n < 32)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -INF;
+      if ((uint32_t)(t - col - c) < 32u)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i == t - col - c && i < n) target_logit[row] = v[i];
+      float top = v[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+      top = fminf(top, -LOWEST);
+      if (top > m) {
+        s = mul2(s, ex2((m - top) * LOG2E));
+        m = top;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
+        s = add2(s, make_float2(ex2(y.x), ex2(y.y)));
+      }
+    }
+    if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = make_float2(m, s.x + s.y);
+  }
+};
+
+__device__ __forceinline__ float f16_up(const uint32_t *g_max) {
+  // 2^(F16_UP - e) for a largest |g| of [2^(e-1), 2^e): what G is multiplied by
+  const float g = __uint_as_float(*g_max);
+  return g > 0 ? exp2f((float)min(max(F16_UP - 1 - ilogbf(g), -100), 100)) : 1.f;
+}
+
+// G in the operands' type (T: float, three parts).  16-bit floats lack the range for
+// a mean's 1 / n: there G is scaled by a power of two that brings the largest |g| to
+// 2^14, and the gradients' epilogue takes it back.
+template <class T> struct GradEpi {
+  int n_rows, n_cols;
+  const RowInfo *info;
+  const uint32_t *g_max;
+  uint16_t *g;                                             // [parts][n_rows][stride]
+  int64_t stride, part_stride;
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
+    const bool mine = row < n_rows;
+    RowInfo r = {0, 0, 0, -1};
+    if (mine) r = info[row];
+    if (sizeof(T) == 2 && g_max) {
+      const float up = f16_up(g_max);
+      r.mul *= up;
+      r.g *= up;
+    }
+    for (int c = 0; c < HALF; c += 32) {
+      float v[32];
+      load(c, v);
+      if (!mine || col + c >= stride) continue;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float2 y = sub_mul2(make_float2(v[i], v[i + 1]), r.from, LOG2E);
+        y = mul2(make_float2(ex2(y.x), ex2(y.y)), r.mul);
+        v[i] = y.x;
+        v[i + 1] = y.y;
+      }
+      if ((uint32_t)(r.t - col - c) < 32u)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i == r.t - col - c) v[i] -= r.g;
+      if (r.t < 0)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0;
+      uint16_t *to = g + (int64_t)row * stride + col + c;
+      put(to, v);
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t *to, const float v[32]) const {
+    using E = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + i) = f32_vec(v + i, E{});
+    if (sizeof(T) == 4) {
+      float w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + part_stride + i) = f32_vec(w + i, E{});
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = w[i] - __bfloat162float(__float2bfloat16_rn(w[i]));
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + 2 * part_stride + i) = f32_vec(w + i, E{});
+    }
+  }
+};
+
+// Where a gradient goes: dst = sums * scale (+ src), T the type of dst.
+struct Target {
+  int64_t n_rows, n_cols;
+  void *dst;
+  int64_t dst_stride;
+  const void *src;                                         // or NULL
+  int64_t src_stride;
+  int32_t src_type;
+  const uint32_t *g_max;                                   // 16-bit floats: what scaled G, or NULL
+  int vec;                                                 // rows of dst and src lie on 16-byte boundaries
+};
+
+template <class S> __device__ __forceinline__ void add8(const void *src, int64_t at, float v[8], int n, bool vec) {
+  const S *p = reinterpret_cast<const S *>(src) + at;
+  if (vec) {
+    Raw8<S> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(S) / 2); ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    float w[8];
+    raw_f32(r, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i] += to_f32(p[i]);
+  }
+}
+
+template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t row, int64_t col, float v[8], float scale) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
+  T *to = reinterpret_cast<T *>(o.dst) + row * o.dst_stride + col;
+  const int n = (int)min((int64_t)8, o.n_cols - col);
+  const bool vec = o.vec && n == 8;
+  if (o.src) {
+    const int64_t at = row * o.src_stride + col;
+    if (o.src_type == TT_F32) add8<float>(o.src, at, v, n, vec);
+    else if (o.src_type == TT_F16) add8<__half>(o.src, at, v, n, vec);
+    else add8<__nv_bfloat16>(o.src, at, v, n, vec);
+  }
+  if (vec) {
+    store8(to, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) to[i] = from_f32<T>(v[i]);
+  }
+}
+
+template <class T> struct OutEpi {
+  Target o;
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
+    const float scale = o.g_max ? 1.f / f16_up(o.g_max) : 1.f;
+    for (int c = 0; c < HALF; c += 32) {
+      float v[32];
+      load(c, v);
+      if (row < o.n_rows)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (col + c + i < o.n_cols) put8<T>(o, row, col + c + i, v + i, scale);
+    }
+  }
+};
+
+// parts of a contraction's sums, [split][n_rows][stride] floats, stride a multiple of 8
+struct PartEpi {
+  int n_rows, stride;
+  float *part;
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int split, int, Load load) const {
+    for (int c = 0; c < HALF; c += 32) {
+      float v[32];
+      load(c, v);
+      if (row < n_rows)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (col + c + i < stride) {
+            float4 *to = reinterpret_cast<float4 *>(part + ((int64_t)split * n_rows + row) * stride + col + c + i);
+            to[0] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            to[1] = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+          }
+    }
+  }
+};
+
+template <class T> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
+  const int64_t per = stride / 8, total = o.n_rows * per;
+  const float scale = o.g_max ? 1.f / f16_up(o.g_max) : 1.f;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t row = i / per, col = (i - row * per) * 8;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s) {
+      const float4 *p = reinterpret_cast<const float4 *>(part + ((int64_t)s * o.n_rows + row) * stride + col);
+      const float4 a = p[0], b = p[1];
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    if (col < o.n_cols) put8<T>(o, row, col, v, scale);
+  }
+}
+
+// ------------------------------------------------------------ rows
+// Operands as TMA can read them: rows of whole 16-byte groups; floats in three parts.
+template <class T> __global__ void __launch_bounds__(256) k_pack(const T *x, int64_t n, int dim, int64_t x_stride, uint16_t *out, int stride) {
+  using E = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
+  const int per = stride / 8;
+  const int64_t total = n * per;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t row = i / per;
+    const int col = (int)(i - row * per) * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col + j < dim ? to_f32(x[row * x_stride + col + j]) : 0.f;
+    uint16_t *to = out + row * stride + col;
+    *reinterpret_cast<uint4 *>(to) = f32_vec(v, E{});
+    if (sizeof(T) == 4)
+      for (int p = 1; p < 3; ++p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+        *reinterpret_cast<uint4 *>(to + p * n * stride) = f32_vec(v, E{});
+      }
+  }
+}
+
+struct FinishArgs {
+  int n_rows, n_parts, n_vocab;
+  int64_t row0;
+  const float2 *part;
+  const float *target_logit, *row_grads, *lse_in;
+  const int32_t *targets;
+  float *loss, *lse;
+  RowInfo *info;                                           // or NULL
+  uint32_t *g_max;                                         // or NULL
+  int32_t *status;
+};
+
+__device__ __forceinline__ void row_info(const FinishArgs &a, int row, bool there, float from, float inverse, float lse) {
+  const float g = a.row_grads ? a.row_grads[a.row0 + row] : 1.f;
+  const bool none = !there || lse == -INF;
+  a.info[row] = RowInfo{from, g * inverse, g, none ? -1 : a.targets[a.row0 + row]};
+  if (a.g_max && !none && fabsf(g) < INF) atomicMax(a.g_max, __float_as_uint(fabsf(g)));
+}
+
+// R rows a block: the parts of a row are joined by 256 / R threads
+template <int R> __global__ void __launch_bounds__(256) k_finish(FinishArgs a) {
+  constexpr int EACH = 256 / R;
+  __shared__ float2 box[256];
+  const int r = threadIdx.x % R, j = threadIdx.x / R, row = blockIdx.x * R + r;
+  float m = LOWEST, s = 0;
+  auto join = [&](float2 p) {
+    const float nm = fmaxf(m, p.x);
+    s = s * ex2((m - nm) * LOG2E) + p.y * ex2((p.x - nm) * LOG2E);
+    m = nm;
+  };
+  if (row < a.n_rows) {
+    const float2 *p = a.part + row;
+    int i = j;
+    for (; i + 3 * EACH < a.n_parts; i += 4 * EACH) {
+      float2 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = p[(int64_t)(i + u * EACH) * a.n_rows];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) join(q[u]);
+    }
+    for (; i < a.n_parts; i += EACH) join(p[(int64_t)i * a.n_rows]);
+  }
+  box[threadIdx.x] = make_float2(m, s);
+  for (int k = EACH / 2; k; k /= 2) {
+    __syncthreads();
+    if (j < k) {
+      join(box[threadIdx.x + k * R]);
+      box[threadIdx.x] = make_float2(m, s);
+    }
+  }
+  if (j || row >= a.n_rows) return;
+  const float log_s = logf(s), lse = m + log_s;
+  const int32_t t = a.targets[a.row0 + row];
+  const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
+  if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
+  if (a.lse) a.lse[a.row0 + row] = lse;
+  a.loss[a.row0 + row] = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
+  if (a.info) row_info(a, row, there, m, __fdividef(1.f, s), lse);
+}
+
+// the same from an lse that the caller has
+__global__ void __launch_bounds__(256) k_info(FinishArgs a) {
+  const int row = blockIdx.x * 256 + threadIdx.x;
+  if (row >= a.n_rows) return;
+  const float lse = a.lse_in[a.row0 + row];
+  const int32_t t = a.targets[a.row0 + row];
+  const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
+  if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
+  row_info(a, row, there, lse, 1.f, lse);
+}
+
+// ------------------------------------------------------------ host
+inline int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+struct Call {
+  const void *hidden, *weight;
+  int32_t type;
+  int64_t n, vocab, dim, hidden_stride, weight_stride;
+  const int32_t *targets;
+  float *loss, *lse;
+  const float *lse_in, *row_grads;
+  void *dhidden, *dweight;
+  int64_t dhidden_stride;
+  int32_t dweight_type;
+  int64_t dweight_stride;
+  int accumulate;
+  int32_t *status;
+};
+
+// what lies where in the workspace, in bytes, and how the rows are cut into chunks
+struct Plan {
+  int64_t chunk, width, g_stride;                          // rows; columns of packed operands and of G
+  int split_h, split_w;
+  int64_t hidden, weight, part, target_logit, info, word, g, acc, sums, bytes;
+};
+
+Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, bool pack_w, bool dh, bool dw, bool dw_f32) {
+  Plan p{};
+  const int parts = type == TT_F32 ? 3 : 1;
+  const bool grad = dh || dw;
+  n = std::max<int64_t>(n, 1);
+  p.width = up(dim, 8);
+  p.g_stride = up(vocab, 64);
+  const int64_t halves = (vocab + HALF - 1) / HALF;
+  int64_t most = PARTIALS / (halves * 8);
+  if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * parts));
+  most = std::max<int64_t>(most / TILE * TILE, TILE);
+  const int64_t chunks = (n + most - 1) / most;
+  p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
+  const int pairs = parts == 1 ? 1 : 6;
+  p.split_h = choose_splits(p.chunk, dim, vocab, pairs);
+  p.split_w = choose_splits(vocab, dim, p.chunk, pairs);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up(bytes, 256);
+    return here;
+  };
+  p.hidden = take(pack_h ? n * p.width * 2 * parts : 0);
+  p.weight = take(pack_w ? vocab * p.width * 2 * parts : 0);
+  p.part = take(halves * 8 * p.chunk);
+  p.target_logit = take(4 * p.chunk);
+  p.word = take(4);
+  if (grad) {
+    p.info = take(sizeof(RowInfo) * p.chunk);
+    p.g = take(p.g_stride * 2 * parts * p.chunk);
+    p.acc = take(dw && !dw_f32 && p.chunk < n ? vocab * p.width * 4 : 0);
+    int64_t sums = 0;
+    if (dh && p.split_h > 1) sums = std::max(sums, p.split_h * p.chunk * p.width * 4);
+    if (dw && p.split_w > 1) sums = std::max(sums, p.split_w * vocab * p.width * 4);
+    p.sums = take(sums);
+  }
+  p.bytes = std::max<int64_t>(at, 256);
+  return p;
+}
+
+inline bool rows_tma(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+inline bool needs_pack(int32_t type, const void *p, int64_t stride) { return type == TT_F32 || !rows_tma(p, stride); }
+
+void pack(int32_t type, const void *x, int64_t n, int64_t dim, int64_t stride, void *out, int64_t width, cudaStream_t stream) {
+  const unsigned blocks = (unsigned)std::min<int64_t>((n * (width / 8) + 255) / 256, SMS * 16);
+  with_type(type, [&](auto t) {
+    using T = decltype(t);
+    k_pack<T><<<blocks, 256, 0, stream>>>((const T *)x, n, (int)dim, stride, (uint16_t *)out, (int)width);
+  });
+}
+
+template <class T> void join(const float *part, int splits, int64_t stride, const Target &o, cudaStream_t stream) {
+  const unsigned blocks = (unsigned)std::min<int64_t>((o.n_rows * (stride / 8) + 255) / 256, SMS * 16);
+  k_join<T><<<blocks, 256, 0, stream>>>(part, splits, stride, o);
+}
+
+// a gradient: the product a * b^T (their contraction lies across b's rows), to o
+template <bool A_MN>
+bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sums, int64_t width, int32_t type, const Target &o,
+             int32_t *status, cudaStream_t stream) {
+  if (splits > 1) {
+    if (!run_gemm<A_MN, true>(bf16, a, b, splits, 8, PartEpi{(int)o.n_rows, (int)width, sums}, status, stream)) return false;
+    with_type(type, [&](auto t) { join<decltype(t)>(sums, splits, width, o, stream); });
+    return true;
+  }
+  bool ok = true;
+  with_type(type, [&](auto t) { ok = run_gemm<A_MN, true>(bf16, a, b, 1, 8, OutEpi<decltype(t)>{o}, status, stream); });
+  return ok;
+}
+
+inline int vec_of(const void *p, int64_t stride, int32_t type) {
+  return aligned(p, 16) && stride * (int64_t)type_size(type) % 16 == 0;
+}
+
+bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) {
+  const int parts = c.type == TT_F32 ? 3 : 1;
+  const bool bf16 = c.type != TT_F16, grad = c.dhidden || c.dweight;
+  Matrix h{c.hidden, c.n, c.dim, c.hidden_stride, parts, 8}, w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
+  if (needs_pack(c.type, c.hidden, c.hidden_stride)) {
+    pack(c.type, c.hidden, c.n, c.dim, c.hidden_stride, ws + p.hidden, p.width, stream);
+    h = Matrix{ws + p.hidden, c.n, c.dim, p.width, parts, c.n * p.width};
+  }
+  if (needs_pack(c.type, c.weight, c.weight_stride)) {
+    pack(c.type, c.weight, c.vocab, c.dim, c.weight_stride, ws + p.weight, p.width, stream);
+    w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
+  }
+  RowInfo *info = grad ? (RowInfo *)(ws + p.info) : nullptr;
+  uint32_t *word = grad && c.type == TT_F16 ? (uint32_t *)(ws + p.word) : nullptr;
+  const int halves = (int)((c.vocab + HALF - 1) / HALF);
+  for (int64_t row0 = 0; row0 < c.n; row0 += p.chunk) {
+    const int n = (int)std::min(p.chunk, c.n - row0);
+    Matrix hc = h;
+    hc.p = (const uint16_t *)h.p + row0 * h.stride;
+    hc.rows = n;
+    FinishArgs f{n, halves, (int)c.vocab, row0, (float2 *)(ws + p.part), (float *)(ws + p.target_logit), c.row_grads, c.lse_in,
+                 c.targets, c.loss, c.lse, info, word, c.status};
+    if (word && cudaMemsetAsync(word, 0, 4, stream) != cudaSuccess) return false;
+    if (c.lse_in) {
+      k_info<<<(n + 255) / 256, 256, 0, stream>>>(f);
+    } else {
+      const StatsEpi e{n, (int)c.vocab, row0, c.targets, (float2 *)(ws + p.part), (float *)(ws + p.target_logit)};
+      if (!run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream)) return false;
+      if (n >= 4096) k_finish<32><<<(n + 31) / 32, 256, 0, stream>>>(f);
+      else if (n >= 1024) k_finish<8><<<(n + 7) / 8, 256, 0, stream>>>(f);
+      else k_finish<1><<<n, 256, 0, stream>>>(f);
+    }
+    if (!grad) continue;
+    uint16_t *g = (uint16_t *)(ws + p.g);
+    const int64_t g_part = p.chunk * p.g_stride;
+    bool ok = true;
+    with_type(c.type, [&](auto t) {
+      const GradEpi<decltype(t)> e{n, (int)c.vocab, info, word, g, p.g_stride, g_part};
+      ok = run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream);
+    });
+    if (!ok) return false;
+    const Matrix gm{g, n, c.vocab, p.g_stride, parts, g_part};
+    float *sums = (float *)(ws + p.sums);
+    if (c.dhidden) {
+      Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * type_size(c.type), c.dhidden_stride, nullptr, 0, TT_F32, word,
+               vec_of(c.dhidden, c.dhidden_stride, c.type)};
+      if (!product<false>(bf16, gm, w, p.split_h, sums, p.width, c.type, o, c.status, stream)) return false;
+    }
+    if (c.dweight) {
+      // the sums of several chunks stay in 32 bits until the last
+      const bool first = row0 == 0, last = row0 + n == c.n, own = c.dweight_type == TT_F32;
+      const int vec = vec_of(c.dweight, c.dweight_stride, c.dweight_type);
+      Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, word, vec};
+      int32_t type = c.dweight_type;
+      if (!last && !own) {
+        o.dst = ws + p.acc;
+        o.dst_stride = p.width;
+        type = TT_F32;
+      }
+      if (first ? c.accumulate : own) {
+        o.src = c.dweight;
+        o.src_stride = c.dweight_stride;
+        o.src_type = c.dweight_type;
+      } else if (!first) {
+        o.src = ws + p.acc;
+        o.src_stride = p.width;
+      }
+      if (!product<true>(bf16, gm, hc, p.split_w, sums, p.width, type, o, c.status, stream)) return false;
+    }
+  }
+  if (c.n == 0 && c.dweight && !c.accumulate) {
+    const Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, nullptr, vec_of(c.dweight, c.dweight_stride, c.dweight_type)};
+    with_type(c.dweight_type, [&](auto t) { join<decltype(t)>(nullptr, 0, up(c.dim, 8), o, stream); });
+  }
+  return true;
+}
+
+tt_status run_linear(const Call &c, void *d_workspace, int64_t workspace_bytes, cudaStream_t stream, const char *what) {
+  if (!type_ok(c.type) || c.n < 0 || !vocab_ok(c.vocab) || c.dim < 1 || c.dim > MAX_WIDTH || c.hidden_stride < c.dim ||
+      c.weight_stride < c.dim || !optional_ok(c.hidden, type_size(c.type)) || !optional_ok(c.targets, 4) || !optional_ok(c.loss, 4) ||
+      !optional_ok(c.lse, 4) || !optional_ok(c.lse_in, 4) || !optional_ok(c.row_grads, 4) || !optional_ok(c.status, 4) ||
+      !array_ok(c.weight, type_size(c.type)))
+    return TT_ERR_INVALID_ARG;
+  if (c.dhidden && (c.dhidden_stride < c.dim || !array_ok(c.dhidden, type_size(c.type)))) return TT_ERR_INVALID_ARG;
+  if (c.dweight && (c.dweight_stride < c.dim || (c.dweight_type != TT_F32 && c.dweight_type != c.type) ||
+                    !array_ok(c.dweight, type_size(c.dweight_type))))
+    return TT_ERR_INVALID_ARG;
+  if (c.n > TT_MAX_IDS) return TT_ERR_CAPACITY;
+  if (c.n > 0 && (!c.hidden || !c.targets || !(c.lse_in || c.loss))) return TT_ERR_INVALID_ARG;
+  if (c.n == 0 && !c.dweight) return TT_OK;
+  const Plan p = plan_of(c.n, c.vocab, c.dim, c.type, needs_pack(c.type, c.hidden, c.hidden_stride),
+                         needs_pack(c.type, c.weight, c.weight_stride), c.dhidden, c.dweight, c.dweight_type == TT_F32);
+  if (!d_workspace || !aligned(d_workspace, 256)) return TT_ERR_INVALID_ARG;
+  if (workspace_bytes < p.bytes) return TT_ERR_CAPACITY;
+  if (!run_chunks(c, p, (uint8_t *)d_workspace, stream)) {
+    const tt_status st = launched(what);
+    return st == TT_OK ? TT_ERR_CUDA : st;
+  }
+  return launched(what);
+}
+
+}  // namespace
+
+extern "C" tt_status tt_linear_loss(const void *d_hidden, const void *d_weight, int32_t type, int64_t n_rows, int64_t n_vocab,
+                                    int64_t dim, int64_t hidden_stride, int64_t weight_stride, const int32_t *d_targets,
+                                    float *d_loss, float *d_lse, const float *d_row_grads, void *d_dhidden, int64_t dhidden_stride,
+                                    void *d_dweight, int32_t dweight_type, int64_t dweight_stride, int32_t accumulate,
+                                    void *d_workspace, int64_t workspace_bytes, int32_t *d_status, tt_stream_t stream) {
+  const Call c{d_hidden, d_weight, type, n_rows, n_vocab, dim, hidden_stride, weight_stride, d_targets, d_loss, d_lse, nullptr,
+               d_row_grads, d_dhidden, d_dweight, dhidden_stride, dweight_type, dweight_stride, accumulate, d_status};
+  return run_linear(c, d_workspace, workspace_bytes, stream, "tt_linear_loss");
+}
+
+extern "C" tt_status tt_linear_loss_grad(const void *d_hidden, const void *d_weight, int32_t type, int64_t n_rows, int64_t n_vocab,
+                                         int64_t dim, int64_t hidden_stride, int64_t weight_stride, const int32_t *d_targets,
+                                         const float *d_lse, const float *d_row_grads, void *d_dhidden, int64_t dhidden_stride,
+                                         void *d_dweight, int32_t dweight_type, int64_t dweight_stride, int32_t accumulate,
+                                         void *d_workspace, int64_t workspace_bytes, int32_t *d_status, tt_stream_t stream) {
+  if ((n_rows > 0 && !d_lse) || (!d_dhidden && !d_dweight)) return TT_ERR_INVALID_ARG;
+  const Call c{d_hidden, d_weight, type, n_rows, n_vocab, dim, hidden_stride, weight_stride, d_targets, nullptr, nullptr, d_lse,
+               d_row_grads, d_dhidden, d_dweight, dhidden_stride, dweight_type, dweight_stride, accumulate, d_status};
+  return run_linear(c, d_workspace, workspace_bytes, stream, "tt_linear_loss_grad");
+}
+
+extern "C" int64_t tt_linear_loss_workspace(int64_t n_rows, int64_t n_vocab, int64_t dim, int32_t type, int32_t aligned_rows,
+                                            int32_t dweight_type, int32_t want_grad) {
+  if (!type_ok(type) || n_rows < 0 || n_rows > TT_MAX_IDS || !vocab_ok(n_vocab) || dim < 1 || dim > MAX_WIDTH ||
+      (want_grad && dweight_type != TT_F32 && dweight_type != type))
+    return -1;
+  const bool pack = type == TT_F32 || !aligned_rows;
+  return plan_of(n_rows, n_vocab, dim, type, pack, pack, want_grad != 0, want_grad != 0, dweight_type == TT_F32).bytes;
+}

@@ -31,15 +31,13 @@
 // gradients of the same stride and 817 into contiguous ones.
 #include <algorithm>
 
-#include "tt_ops.cuh"
+#include "tt_rows.cuh"
 
 using namespace tt::ops;
 
 namespace {
 
 constexpr int HELD = 104 * 1024;                 // bytes of a row a block holds: two blocks an SM
-constexpr float LOG2E = 1.44269504f;
-constexpr float LOWEST = -3.402823466e38f;
 constexpr float FAR = 128.f;                     // |lse| from where a probability would be off by 2^-18
 
 struct LossArgs {
@@ -51,53 +49,9 @@ struct LossArgs {
   int cluster, held;                             // blocks a row, vectors a block can hold
 };
 
-// A running maximum and the sum of exp(l - maximum).  The maximum stays within
-// the finite floats, so that a difference is NaN only where a logit is: +inf
-// adds +inf to the sum, -inf nothing.
-struct Running {
-  float m = LOWEST;
-  float2 s2 = make_float2(0, 0);                 // the sum in two halves
-  float s;                                       // and whole, from total() on
-  template <class T> __device__ __forceinline__ void add(uint4 r, T) {
-    constexpr int E = 16 / sizeof(T);
-    const float vm = vec_max(r, T{});
-    if (vm > m) raise(vm);
-    float v[E];
-    vec_f32(r, v, T{});
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
-      s2 = add2(s2, make_float2(ex2(y.x), ex2(y.y)));
-    }
-  }
-  __device__ __forceinline__ void add(float x) {
-    if (x > m) raise(x);
-    s2.x += ex2((x - m) * LOG2E);
-  }
-  __device__ __forceinline__ void raise(float vm) {
-    vm = fminf(vm, -LOWEST);
-    s2 = mul2(s2, ex2((m - vm) * LOG2E));
-    m = vm;
-  }
-  __device__ __forceinline__ void total() { s = s2.x + s2.y; }
-  __device__ __forceinline__ void join(float om, float os) {
-    const float nm = fmaxf(m, om);
-    s = s * ex2((m - nm) * LOG2E) + os * ex2((om - nm) * LOG2E);
-    m = nm;
-  }
-};
-
 // GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
 constexpr int U = 4;                             // vectors a thread takes at a time
 constexpr int UC = 4, AHEAD = 4;                 // vectors a group of copies, groups ahead
-
-// f(vector, whether all of the group's are there) for groups of `per` vectors
-// a thread between lo and hi: the tests of whole groups are left out.
-template <bool WHOLE> struct Whole { static constexpr bool value = WHOLE; };
-template <int THREADS, class F> __device__ __forceinline__ void groups(int lo, int hi, int per, F f) {
-  for (; lo + per * THREADS <= hi; lo += per * THREADS) f(lo + (int)threadIdx.x, Whole<true>{});
-  if (lo < hi) f(lo + (int)threadIdx.x, Whole<false>{});
-}
 
 template <class T, int GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, const T *logits, T *dlogits) {
@@ -142,7 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_loss(LossArgs a, co
   } else {
     // read by one thread, before any block can write to the row
     const float lt = there && rank == 0 && tid == 0 ? to_f32(l[t]) : 0.f;
-    Running run;
+    Running<false> run;
     if (GRAD == 1)
       groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
         copy_wait<AHEAD - 1>();

@@ -480,6 +480,118 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
                     const float *d_top_p, const float *d_min_p, int32_t *d_out_ids, float *d_out_logprobs,
                     int32_t *d_status, tt_stream_t stream);
 
+/*
+ * tt_linear_loss - next-token loss of hidden states through a model's head, and
+ * its gradients, without the matrix of logits:
+ *   l[i][j]    = sum_d hidden[i][d] * weight[j][d]
+ *   lse[i]     = log(sum_j exp(l[i][j]))
+ *   loss[i]    = lse[i] - l[i][targets[i]]
+ *   G[i][j]    = row_grads[i] * (exp(l[i][j] - lse[i]) - (j == targets[i]))
+ *   dhidden    = G * weight          dweight = G^T * hidden
+ *
+ * Products and sums are in 32 bits.  G is rounded to the type of hidden and weight
+ * before its own products (TT_F32: it is not; 32-bit operands are multiplied in
+ * parts whose neglected products are below 2^-24 of theirs).  With TT_F16 it is
+ * scaled by a power of two first, so that the largest |row_grads| of a chunk of rows
+ * becomes 2^14 there; what lies 2^-38 below that is lost.
+ *
+ *   d_hidden   device, type [n_rows][dim], rows hidden_stride apart.
+ *   d_weight   device, type [n_vocab][dim], rows weight_stride apart (the layout
+ *              of an embedding table).
+ *   n_rows     0 .. TT_MAX_IDS.    dim  1 .. 2^16.
+ *   d_targets  device, int32 [n_rows]; padding: the row's loss is zero and it adds
+ *              nothing to the gradients (its lse is computed).
+ *   d_loss     device, float [n_rows].    d_lse  the same, or NULL.
+ *   d_row_grads  device, float [n_rows]: the gradient that arrives at each loss;
+ *              NULL: 1 for every row.
+ *   d_dhidden  device, type [n_rows][dim], rows dhidden_stride apart, or NULL.
+ *   d_dweight  device, dweight_type (type or TT_F32) [n_vocab][dim], rows
+ *              dweight_stride apart, or NULL; with accumulate != 0 the gradient is
+ *              added to what it holds, else every row is written.
+ *   d_workspace  device, 256-byte aligned, workspace_bytes >=
+ *              tt_linear_loss_workspace(...), else TT_ERR_CAPACITY; its contents
+ *              before and after mean nothing.
+ * A target >= n_vocab is padding and sets TT_ERR_INVALID_ARG in d_status.  NaN or
+ * infinities in hidden or weight give NaN or infinities in what they enter.  A wait
+ * within a kernel that ran out sets TT_ERR_TIMEOUT in d_status, and the outputs then
+ * mean nothing.
+ */
+tt_status tt_linear_loss(const void *d_hidden, const void *d_weight, int32_t type, int64_t n_rows, int64_t n_vocab,
+                         int64_t dim, int64_t hidden_stride, int64_t weight_stride, const int32_t *d_targets,
+                         float *d_loss, float *d_lse, const float *d_row_grads, void *d_dhidden,
+                         int64_t dhidden_stride, void *d_dweight, int32_t dweight_type, int64_t dweight_stride,
+                         int32_t accumulate, void *d_workspace, int64_t workspace_bytes, int32_t *d_status,
+                         tt_stream_t stream);
+
+/* tt_linear_loss_grad - the gradients of tt_linear_loss alone, from the lse that it
+ * returned (for a gradient that is known only later); arguments as there.  lse's
+ * rounding, 2^-24 |lse|, is in each probability then. */
+tt_status tt_linear_loss_grad(const void *d_hidden, const void *d_weight, int32_t type, int64_t n_rows,
+                              int64_t n_vocab, int64_t dim, int64_t hidden_stride, int64_t weight_stride,
+                              const int32_t *d_targets, const float *d_lse, const float *d_row_grads,
+                              void *d_dhidden, int64_t dhidden_stride, void *d_dweight, int32_t dweight_type,
+                              int64_t dweight_stride, int32_t accumulate, void *d_workspace, int64_t workspace_bytes,
+                              int32_t *d_status, tt_stream_t stream);
+
+/* tt_linear_loss_workspace - bytes of scratch that tt_linear_loss and
+ * tt_linear_loss_grad need (host-side arithmetic only); -1 for sizes that they
+ * reject.  want_grad: 0 the loss alone (dweight_type is then not looked at), else
+ * with any of its gradients.  aligned_rows != 0: every row of hidden and weight
+ * starts on a 16-byte boundary; else, and with TT_F32, room for copies of both is
+ * in it. */
+int64_t tt_linear_loss_workspace(int64_t n_rows, int64_t n_vocab, int64_t dim, int32_t type, int32_t aligned_rows,
+                                 int32_t dweight_type, int32_t want_grad);
+
+/* The most entries of a row of tt_distill_loss. */
+#define TT_MAX_TEACHER 1024
+
+/*
+ * tt_distill_loss - distillation from a teacher's top logits: the divergence of
+ * each row of logits from them, at a temperature T, and its gradient:
+ *   q[i][:]       = softmax(teacher_logits[i][:] / T) over the row's entries
+ *   lse[i]        = log(sum_j exp(logits[i][j] / T))
+ *   loss[i]       = sum_e q[i][e] * (log(q[i][e]) - logits[i][teacher_ids[i][e]] / T + lse[i])
+ *   dlogits[i][j] = row_grads[i] / T * (exp(logits[i][j] / T - lse[i])
+ *                                       - sum of q[i][e] over the e with teacher_ids[i][e] == j)
+ * (the customary factor T^2 is the caller's, in row_grads).
+ *
+ *   d_logits   device, type [n_rows][n_vocab], rows logits_stride apart.
+ *   n_rows     0 .. TT_MAX_IDS.
+ *   d_teacher_ids  device, int32 [n_rows][k], rows ids_stride apart, in any order;
+ *              padding: no entry.  An ID that occurs more than once counts as
+ *              often.  An ID >= n_vocab is padding and sets TT_ERR_INVALID_ARG in
+ *              d_status.
+ *   d_teacher_logits  device, teacher_type [n_rows][k], rows teacher_stride apart:
+ *              logits, or logarithms of probabilities (q is normalised over the
+ *              entries); -inf: an entry without weight.
+ *   k          1 .. TT_MAX_TEACHER.
+ *   temperature  2^-64 .. 2^64.
+ *   d_loss     device, float [n_rows].    d_lse  the same, or NULL.
+ *   d_row_grads  device, float [n_rows]: the gradient that arrives at each loss;
+ *              NULL: 1 for every row.
+ *   d_dlogits  device, type [n_rows][n_vocab], rows dlogits_stride apart, or
+ *              NULL: no gradient.  May be d_logits itself with equal strides.
+ * A row without entries (all padding or -inf) has loss 0 and a zero gradient (its
+ * lse is computed).  An entry with q > 0 at a -inf logit makes the loss +inf; a row
+ * of logits that is -inf throughout has lse -inf, loss +inf and a zero gradient.
+ * NaN or +inf in a row, the teacher's included, give what the formulas then give in
+ * IEEE arithmetic.  Loss and gradient do not go through the 32-bit lse.
+ */
+tt_status tt_distill_loss(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab, int64_t logits_stride,
+                          const int32_t *d_teacher_ids, int64_t ids_stride, const void *d_teacher_logits,
+                          int32_t teacher_type, int64_t teacher_stride, int64_t k, float temperature, float *d_loss,
+                          float *d_lse, const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,
+                          int32_t *d_status, tt_stream_t stream);
+
+/* tt_distill_loss_grad - the gradient of tt_distill_loss alone, from the lse that it
+ * returned (for a gradient that is known only later); arguments as there.  lse's
+ * rounding, 2^-24 |lse|, is in each probability then. */
+tt_status tt_distill_loss_grad(const void *d_logits, int32_t type, int64_t n_rows, int64_t n_vocab,
+                               int64_t logits_stride, const int32_t *d_teacher_ids, int64_t ids_stride,
+                               const void *d_teacher_logits, int32_t teacher_type, int64_t teacher_stride, int64_t k,
+                               float temperature, const float *d_lse, const float *d_row_grads, void *d_dlogits,
+                               int64_t dlogits_stride, int32_t *d_status, tt_stream_t stream);
+
 /* tt_status_string - static English text for a status code. */
 const char *tt_status_string(tt_status s);
 
