@@ -28,7 +28,8 @@ using namespace tt::ops;
 constexpr int TILE = 256, HALF = 128, KB = 64;            // rows and columns of a tile, a block's part, contraction a stage
 constexpr int STAGES = 6, STAGE_BYTES = 2 * HALF * KB * 2;
 constexpr int EPI_WARPS = 8, THREADS = (4 + EPI_WARPS) * 32;
-constexpr int SHARED = STAGES * STAGE_BYTES + 1024;       // and what aligns the stages to 1024 bytes
+constexpr int OWN_BYTES = 4096;                            // shared memory of an epilogue's warp, for what it writes
+constexpr int SHARED = STAGES * STAGE_BYTES + EPI_WARPS * OWN_BYTES + 1024;   // and what aligns the stages to 1024 bytes
 constexpr int SMS = 152;
 constexpr uint32_t TRIES = 1u << 22;                      // of a wait, before the call gives up
 
@@ -38,6 +39,7 @@ struct Gemm {
   int pairs;                                              // of parts, listed in nibbles of pair_a and pair_b
   uint32_t pair_a, pair_b, idesc;
   int group;                                              // tile rows that are passed through together
+  const int32_t *only;                                    // or NULL: nothing is done unless only[0], for the tile rows i with only[1 + i]
   int32_t *status;
 };
 
@@ -117,6 +119,32 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t lead, uint32
   return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
+// 16 bytes of the warp's own shared memory: 32 rows of 128 bytes, swizzled as TMA's
+// 128-byte mode does, so that rows can be written and columns of chunks be read
+__device__ __forceinline__ uint32_t own_chunk(uint32_t own, int row, int chunk) { return own + row * 128 + ((chunk ^ (row & 7)) << 4); }
+__device__ __forceinline__ void own_write(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 own_read(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float own_float(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+// 32 rows of 64 16-bit elements from there to a matrix, by one thread; what lies outside is left out
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, int z, uint32_t own) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(own), "r"(x), "r"(y),
+               "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // how a block's half of an operand (128 rows by 64 of the contraction) is loaded
 // and described: K-major one box of 128 rows, MN-major two boxes of 64 rows
 template <bool MN> struct Operand {
@@ -152,12 +180,15 @@ __device__ __forceinline__ int2 blocks_of(const Gemm &g, int split) {
   return make_int2((int)((int64_t)g.k_blocks * split / g.splits), (int)((int64_t)g.k_blocks * (split + 1) / g.splits));
 }
 
-// Epi is called by each thread of the epilogue's warps as epi(row, column, split, half, load):
-// the row of the result that it has, the first of the 128 columns that it reads, and
-// load(c, v), which brings 32 of them from the c-th on and is called by whole warps.
+// Epi is called by the epilogue's warps as epi(row, column, split, own, load): the row of
+// the result that a thread has (consecutive ones in a warp), the first of the 128 columns
+// that it reads, the warp's own shared memory, and load(c, v), which brings 32 of the
+// columns from the c-th on and is called by whole warps.  epi.end() comes behind the last.
 template <bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
-    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Gemm g, const Epi epi) {
+    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Gemm g,
+           const __grid_constant__ Epi epi) {
+  if (g.only && !g.only[0]) return;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_bar[2 * STAGES + 4];
   __shared__ uint32_t s_tmem;
@@ -196,6 +227,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     uint32_t phase = 1;
     for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs) {
       const Place p = place_of(g, t);
+      if (g.only && !g.only[1 + p.m]) continue;
       const int2 kb = blocks_of(g, p.split);
       const int ra = p.m * TILE + rank * HALF, rb = p.n * TILE + rank * HALF;
       for (int i = 0; ok && i < g.pairs; ++i) {
@@ -216,8 +248,9 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     int i = 0;
-    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs, ++i) {
+    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs) {
       const Place p = place_of(g, t);
+      if (g.only && !g.only[1 + p.m]) continue;
       const int2 kb = blocks_of(g, p.split);
       const int count = (kb.y - kb.x) * g.pairs;
       if (!(ok = bar_wait(free_ + 8 * (i & 1), (i >> 1 & 1) ^ 1, &s_dead))) break;
@@ -237,12 +270,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
         }
       }
       if (ok) commit(done + 8 * (i & 1));
+      ++i;
     }
   } else if (warp >= 4) {
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     int i = 0;
-    for (int t = blockIdx.x / 2; t < n_tiles; t += n_pairs, ++i) {
+    const uint32_t own = stages + STAGES * STAGE_BYTES + (warp - 4) * OWN_BYTES;
+    for (int t = blockIdx.x / 2; t < n_tiles; t += n_pairs) {
       const Place p = place_of(g, t);
+      if (g.only && !g.only[1 + p.m]) continue;
       ok = bar_wait(done + 8 * (i & 1), i >> 1 & 1, &s_dead);
       if (!__all_sync(~0u, ok)) {
         ok = false;
@@ -250,12 +286,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t at = tmem + (i & 1) * TILE + half * HALF + ((uint32_t)(quarter * 32) << 16);
-      epi(p.m * TILE + (int)rank * HALF + quarter * 32 + lane, p.n * TILE + half * HALF, p.split, half,
+      epi(p.m * TILE + (int)rank * HALF + quarter * 32 + lane, p.n * TILE + half * HALF, p.split, own,
           [&](int c, float v[32]) { tmem_load32(at + c, v); });
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(in_block(free_ + 8 * (i & 1), 0));
+      ++i;
     }
+    epi.end();
   }
   if (!ok) {
     // what is under way (copies, products) ends by itself within this time
@@ -292,7 +330,7 @@ template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
 // other way round (its rows are the contraction).  False: an error, which is kept.
 template <bool A_MN, bool B_MN, class Epi>
 inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, int group, const Epi &epi, int32_t *status,
-                     cudaStream_t stream) {
+                     cudaStream_t stream, const int32_t *only = nullptr) {
   CUtensorMap ma, mb;
   if (encode_map(&ma, bf16, a, A_MN ? KB : HALF) != CUDA_SUCCESS || encode_map(&mb, bf16, b, B_MN ? KB : HALF) != CUDA_SUCCESS) return false;
   Gemm g;
@@ -307,6 +345,7 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   g.pair_b = a.parts == 1 ? 0 : 0x010120;
   g.idesc = idesc_of(bf16, A_MN, B_MN);
   g.group = group;
+  g.only = only;
   g.status = status;
   auto k = k_gemm<A_MN, B_MN, Epi>;
   if (allow_shared<GemmTag<A_MN, B_MN, Epi>>(k, SHARED)) return false;

@@ -48,51 +48,140 @@ constexpr int64_t KEPT = 1ll << 30;                        // bytes of G at a ti
 constexpr int64_t PARTIALS = 1ll << 28;                    // bytes of maxima and sums at a time
 constexpr int F16_UP = 14;                                 // G in 16 bits: the largest |g| becomes 2^14
 
-// what a row's gradient is made from: G = exp(l - from) * mul - g (j == t); t < 0: none
+// What a row's G is made from: G = exp(l - from) * mul - g (j == t); t < 0: zeros.
 struct RowInfo { float from, mul, g; int t; };
 
 // ------------------------------------------------------------ epilogues
+template <class T> using Element = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
+
+// 64 columns of a warp's rows to a matrix, T: float in three parts: a TMA store of 32
+// rows, from the warp's own memory.
+template <class T> __device__ __forceinline__ void put_box(const CUtensorMap *map, int row, int col, uint32_t own, float v[64], bool inside) {
+  using E = Element<T>;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < (sizeof(T) == 2 ? 1 : 3); ++p) {
+    if (lane == 0) stores_read();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own_write(own_chunk(own, lane, i), f32_vec(v + 8 * i, E{}));
+    fence_copies();
+    __syncwarp();
+    if (lane == 0 && inside) store_box(map, col, row, p, own);
+    if (sizeof(T) == 4 && p < 2) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+    }
+  }
+}
+
+// a running maximum and sum of 32 values, those of columns that are not there being -inf
+__device__ __forceinline__ void add32(const float v[32], float &m, float2 &s) {
+  float top = v[0];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+  top = fminf(top, -LOWEST);
+  if (top > m) {
+    s = mul2(s, ex2((m - top) * LOG2E));
+    m = top;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
+    s = add2(s, make_float2(ex2(y.x), ex2(y.y)));
+  }
+}
+__device__ __forceinline__ void cut32(float v[32], int n) {
+  if (n < 32)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -INF;
+}
+
 // The maximum and sum of each row and 128 columns, and the target's logit.  The
 // maximum stays within the finite floats, so that a difference is NaN only where a
 // logit is.
 struct StatsEpi {
   int n_rows, n_cols;
-  int64_t row0;                                            // the chunk's first row
   const int32_t *targets;
   float2 *part;                                            // [column halves][n_rows]
   float *target_logit;                                     // [n_rows]
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t, Load load) const {
     const bool mine = row < n_rows;
-    const int t = mine ? targets[row0 + row] : -1;
+    const int t = mine ? targets[row] : -1;
     float m = LOWEST;
     float2 s = make_float2(0, 0);
     for (int c = 0; c < HALF; c += 32) {
       float v[32];
       load(c, v);
       const int n = n_cols - col - c;                      // columns that are there
-      if (n < 32)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -INF;
+      cut32(v, n);
       if ((uint32_t)(t - col - c) < 32u)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i == t - col - c && i < n) target_logit[row] = v[i];
-      float top = v[0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-      top = fminf(top, -LOWEST);
-      if (top > m) {
-        s = mul2(s, ex2((m - top) * LOG2E));
-        m = top;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
-        s = add2(s, make_float2(ex2(y.x), ex2(y.y)));
-      }
+      add32(v, m, s);
     }
     if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = make_float2(m, s.x + s.y);
   }
+  __device__ __forceinline__ void end() const {}
+};
+
+// The same in one pass with what G is made from: powers exp(l - c), c the target's
+// logit, of which k_finish knows the sum, the row's exp(loss), later.  They are
+// written in the operands' type, whose range is a float's: precise for any loss that
+// is not absurd, and k_finish finds the rows for which they are not.  Where a sum
+// leaves the safe range, the columns are read once more with a maximum.
+template <class T> struct PowersEpi {
+  CUtensorMap map;
+  int n_rows, n_cols;
+  const int32_t *targets;
+  const float *from;                                       // [n_rows] c
+  float2 *part;                                            // [column halves][n_rows]
+  float *target_power;                                     // [n_rows]
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load) const {
+    const bool mine = row < n_rows;
+    const int t = mine ? targets[row] : -1;
+    const bool there = (uint32_t)t < (uint32_t)n_cols;
+    const float c0 = mine ? from[row] : 0.f;
+    float2 s = make_float2(0, 0);
+    for (int c = 0; c < HALF; c += 64) {
+      float v[64];
+      load(c, v);
+      load(c + 32, v + 32);
+      cut32(v, n_cols - col - c);
+      cut32(v + 32, n_cols - col - c - 32);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), c0, LOG2E);
+        v[i] = ex2(y.x);
+        v[i + 1] = ex2(y.y);
+        s = add2(s, make_float2(v[i], v[i + 1]));
+      }
+      if (there && (uint32_t)(t - col - c) < 64u)
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i == t - col - c) target_power[row] = v[i];
+      if (!there)
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = 0;
+      put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
+    }
+    float2 p = make_float2(c0, s.x + s.y);
+    const bool safe = p.y > 0x1p-100f && p.y < 0x1p100f;
+    if (__any_sync(~0u, mine && !safe)) {
+      float m = LOWEST;
+      s = make_float2(0, 0);
+      for (int c = 0; c < HALF; c += 32) {
+        float v[32];
+        load(c, v);
+        cut32(v, n_cols - col - c);
+        add32(v, m, s);
+      }
+      if (!safe) p = make_float2(m, s.x + s.y);
+    }
+    if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = p;
+  }
+  __device__ __forceinline__ void end() const { stores_read(); }
 };
 
 __device__ __forceinline__ float f16_up(const uint32_t *g_max) {
@@ -105,61 +194,43 @@ __device__ __forceinline__ float f16_up(const uint32_t *g_max) {
 // a mean's 1 / n: there G is scaled by a power of two that brings the largest |g| to
 // 2^14, and the gradients' epilogue takes it back.
 template <class T> struct GradEpi {
+  CUtensorMap map;
   int n_rows, n_cols;
   const RowInfo *info;
-  const uint32_t *g_max;
-  uint16_t *g;                                             // [parts][n_rows][stride]
-  int64_t stride, part_stride;
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
-    const bool mine = row < n_rows;
+  const uint32_t *g_max;                                   // or NULL
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load) const {
     RowInfo r = {0, 0, 0, -1};
-    if (mine) r = info[row];
-    if (sizeof(T) == 2 && g_max) {
+    if (row < n_rows) r = info[row];
+    if (g_max) {
       const float up = f16_up(g_max);
       r.mul *= up;
       r.g *= up;
     }
-    for (int c = 0; c < HALF; c += 32) {
-      float v[32];
+    for (int c = 0; c < HALF; c += 64) {
+      float v[64];
       load(c, v);
-      if (!mine || col + c >= stride) continue;
+      load(c + 32, v + 32);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < 64; i += 2) {
         float2 y = sub_mul2(make_float2(v[i], v[i + 1]), r.from, LOG2E);
         y = mul2(make_float2(ex2(y.x), ex2(y.y)), r.mul);
         v[i] = y.x;
         v[i + 1] = y.y;
       }
-      if ((uint32_t)(r.t - col - c) < 32u)
+      if (r.t >= 0 && (uint32_t)(r.t - col - c) < 64u)
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 64; ++i)
           if (i == r.t - col - c) v[i] -= r.g;
       if (r.t < 0)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0;
-      uint16_t *to = g + (int64_t)row * stride + col + c;
-      put(to, v);
+        for (int i = 0; i < 64; ++i) v[i] = 0;
+      put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
     }
   }
-  __device__ __forceinline__ void put(uint16_t *to, const float v[32]) const {
-    using E = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + i) = f32_vec(v + i, E{});
-    if (sizeof(T) == 4) {
-      float w[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + part_stride + i) = f32_vec(w + i, E{});
-#pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = w[i] - __bfloat162float(__float2bfloat16_rn(w[i]));
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4 *>(to + 2 * part_stride + i) = f32_vec(w + i, E{});
-    }
-  }
+  __device__ __forceinline__ void end() const { stores_read(); }
 };
 
-// Where a gradient goes: dst = sums * scale (+ src), T the type of dst.
+// Where a gradient goes: dst = sums * scale * the row's (+ src), T the type of dst.
 struct Target {
   int64_t n_rows, n_cols;
   void *dst;
@@ -168,7 +239,16 @@ struct Target {
   int64_t src_stride;
   int32_t src_type;
   const uint32_t *g_max;                                   // 16-bit floats: what scaled G, or NULL
+  const float *row_scale;                                  // or NULL; 0: a row of zeros, whatever the sums
   int vec;                                                 // rows of dst and src lie on 16-byte boundaries
+  __device__ __forceinline__ float scale() const { return g_max ? 1.f / f16_up(g_max) : 1.f; }
+  __device__ __forceinline__ float scaled(float x, int64_t row, float by) const {
+    if (row_scale) {
+      const float r = row_scale[row];
+      return r == 0 ? 0.f : x * r;
+    }
+    return x * by;
+  }
 };
 
 template <class S> __device__ __forceinline__ void add8(const void *src, int64_t at, float v[8], int n, bool vec) {
@@ -188,11 +268,11 @@ template <class S> __device__ __forceinline__ void add8(const void *src, int64_t
   }
 }
 
-template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t row, int64_t col, float v[8], float scale) {
+// n of eight columns of a row
+template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t row, int64_t col, float v[8], int n, float scale) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= scale;
+  for (int i = 0; i < 8; ++i) v[i] = o.scaled(v[i], row, scale);
   T *to = reinterpret_cast<T *>(o.dst) + row * o.dst_stride + col;
-  const int n = (int)min((int64_t)8, o.n_cols - col);
   const bool vec = o.vec && n == 8;
   if (o.src) {
     const int64_t at = row * o.src_stride + col;
@@ -209,101 +289,188 @@ template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t
   }
 }
 
+// Sums to a matrix of any alignment: through the warp's own memory, so that a warp
+// writes whole lines of a few rows at a time.
 template <class T> struct OutEpi {
   Target o;
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, int, Load load) const {
-    const float scale = o.g_max ? 1.f / f16_up(o.g_max) : 1.f;
+  int64_t split_rows;                                      // rows between the parts of a split contraction
+  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int split, uint32_t own, Load load) const {
+    const int lane = threadIdx.x & 31, row0 = row & ~31;
+    const float scale = o.scale();
+    Target to = o;
+    to.dst = reinterpret_cast<T *>(o.dst) + split * split_rows * o.dst_stride;
     for (int c = 0; c < HALF; c += 32) {
       float v[32];
       load(c, v);
-      if (row < o.n_rows)
+      const int n = (int)min((int64_t)32, o.n_cols - col - c), rows = (int)min((int64_t)32, o.n_rows - row0);
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          if (col + c + i < o.n_cols) put8<T>(o, row, col + c + i, v + i, scale);
-    }
-  }
-};
-
-// parts of a contraction's sums, [split][n_rows][stride] floats, stride a multiple of 8
-struct PartEpi {
-  int n_rows, stride;
-  float *part;
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int split, int, Load load) const {
-    for (int c = 0; c < HALF; c += 32) {
-      float v[32];
-      load(c, v);
-      if (row < n_rows)
+      for (int i = 0; i < 8; ++i) own_write(own_chunk(own, lane, i), f32_vec(v + 4 * i, float{}));
+      __syncwarp();
+      if (n <= 0 || rows <= 0) continue;
+      if (o.vec) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          if (col + c + i < stride) {
-            float4 *to = reinterpret_cast<float4 *>(part + ((int64_t)split * n_rows + row) * stride + col + c + i);
-            to[0] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            to[1] = make_float4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + lane / 4, k = lane % 4 * 8;
+          if (r >= rows || k >= n) continue;
+          float w[8];
+          vec_f32(own_read(own_chunk(own, r, k / 4)), w, float{});
+          vec_f32(own_read(own_chunk(own, r, k / 4 + 1)), w + 4, float{});
+          put8<T>(to, row0 + r, col + c + k, w, min(8, n - k), scale);
+        }
+      } else if (lane < n) {
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) {
+          const int64_t at = row0 + r, k = col + c + lane;
+          float x = o.scaled(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4), at, scale);
+          if (o.src) {
+            const int64_t from = at * o.src_stride + k;
+            x += o.src_type == TT_F32 ? reinterpret_cast<const float *>(o.src)[from]
+                 : o.src_type == TT_F16 ? to_f32(reinterpret_cast<const __half *>(o.src)[from])
+                                        : to_f32(reinterpret_cast<const __nv_bfloat16 *>(o.src)[from]);
           }
+          reinterpret_cast<T *>(to.dst)[at * o.dst_stride + k] = from_f32<T>(x);
+        }
+      }
     }
   }
+  __device__ __forceinline__ void end() const {}
 };
 
+// the parts of a split contraction, [split][n_rows][stride] floats, stride a multiple of 8
 template <class T> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
   const int64_t per = stride / 8, total = o.n_rows * per;
-  const float scale = o.g_max ? 1.f / f16_up(o.g_max) : 1.f;
+  const float scale = o.scale();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / per, col = (i - row * per) * 8;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const float4 *p = reinterpret_cast<const float4 *>(part + row * stride + col);
+    const int64_t step = o.n_rows * stride / 4;
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const float4 *p = reinterpret_cast<const float4 *>(part + ((int64_t)s * o.n_rows + row) * stride + col);
-      const float4 a = p[0], b = p[1];
+      const float4 a = p[s * step], b = p[s * step + 1];
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    if (col < o.n_cols) put8<T>(o, row, col, v, scale);
+    if (col < o.n_cols) put8<T>(o, row, col, v, (int)min((int64_t)8, o.n_cols - col), scale);
   }
 }
 
 // ------------------------------------------------------------ rows
-// Operands as TMA can read them: rows of whole 16-byte groups; floats in three parts.
-template <class T> __global__ void __launch_bounds__(256) k_pack(const T *x, int64_t n, int dim, int64_t x_stride, uint16_t *out, int stride) {
-  using E = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
+// n of eight elements
+template <class T> __device__ __forceinline__ void take8(const T *p, float v[8], int n, bool vec) {
+  if (vec && n == 8) {
+    Raw8<T> r;
+    load_raw(p, r);
+    raw_f32(r, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+  }
+}
+// eight elements as TMA reads them: floats in three parts
+template <class T> __device__ __forceinline__ void pack8(uint16_t *to, int64_t part_stride, float v[8]) {
+  using E = Element<T>;
+  *reinterpret_cast<uint4 *>(to) = f32_vec(v, E{});
+  if (sizeof(T) == 4)
+    for (int p = 1; p < 3; ++p) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
+      *reinterpret_cast<uint4 *>(to + p * part_stride) = f32_vec(v, E{});
+    }
+}
+
+// Operands as TMA can read them: rows of whole 16-byte groups.
+template <class T> __global__ void __launch_bounds__(256) k_pack(const T *x, int64_t n, int dim, int64_t x_stride, uint16_t *out, int stride, bool vec) {
   const int per = stride / 8;
   const int64_t total = n * per;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / per;
     const int col = (int)(i - row * per) * 8;
     float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = col + j < dim ? to_f32(x[row * x_stride + col + j]) : 0.f;
-    uint16_t *to = out + row * stride + col;
-    *reinterpret_cast<uint4 *>(to) = f32_vec(v, E{});
-    if (sizeof(T) == 4)
-      for (int p = 1; p < 3; ++p) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
-        *reinterpret_cast<uint4 *>(to + p * n * stride) = f32_vec(v, E{});
-      }
+    take8(x + row * x_stride + col, v, min(8, dim - col), vec);
+    pack8<T>(out + row * stride + col, n * stride, v);
   }
 }
 
-struct FinishArgs {
-  int n_rows, n_parts, n_vocab;
-  int64_t row0;
-  const float2 *part;
-  const float *target_logit, *row_grads, *lse_in;
+struct RowArgs {
+  int n_rows, n_parts, n_vocab, dim;                       // rows of the chunk, whose arrays the pointers point to
+  float2 *part;
+  const float *row_grads, *lse_in;
   const int32_t *targets;
   float *loss, *lse;
-  RowInfo *info;                                           // or NULL
+  float *target_logit, *target_power;                      // the latter NULL: no powers
+  RowInfo *info;                                           // or NULL: no gradients
+  float *row_scale, *hidden_scale;
   uint32_t *g_max;                                         // or NULL
-  int32_t *status;
+  int32_t *only, *status;
+  const void *hidden, *weight;
+  int64_t hidden_stride, weight_stride;
+  int hidden_vec, weight_vec;
+  uint16_t *scaled;                                        // hidden by its scale, [parts][n_rows][width]
+  int width;
+  uint16_t *g;
+  int64_t g_stride, g_part;
+  int parts;
 };
 
-__device__ __forceinline__ void row_info(const FinishArgs &a, int row, bool there, float from, float inverse, float lse) {
-  const float g = a.row_grads ? a.row_grads[a.row0 + row] : 1.f;
-  const bool none = !there || lse == -INF;
-  a.info[row] = RowInfo{from, g * inverse, g, none ? -1 : a.targets[a.row0 + row]};
-  if (a.g_max && !none && fabsf(g) < INF) atomicMax(a.g_max, __float_as_uint(fabsf(g)));
+// the target's logit of each row, a warp a row (0 for padding)
+template <class T> __global__ void __launch_bounds__(256) k_target(RowArgs a) {
+  const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (row >= a.n_rows) return;
+  const int32_t t = a.targets[row];
+  float sum = 0;
+  if ((uint32_t)t < (uint32_t)a.n_vocab) {
+    const T *h = (const T *)a.hidden + row * a.hidden_stride, *w = (const T *)a.weight + t * a.weight_stride;
+    for (int c = lane * 8; c < a.dim; c += 256) {
+      float x[8], y[8];
+      take8(h + c, x, min(8, a.dim - c), a.hidden_vec);
+      take8(w + c, y, min(8, a.dim - c), a.weight_vec);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], y[i], sum);
+    }
+  }
+  sum = warp_all(sum, OpSum{});
+  if (lane == 0) a.target_logit[row] = sum;
+}
+
+// What G and hidden's scaled copy are made from.  With powers: G is left without the
+// row's factor g / S (S their sum), which dhidden's rows and the copy of hidden for
+// dweight get.  Rows of a loss beyond 41, whose powers leave what is safe, ask for G to
+// be made anew from their maximum and sum, with all of their 256.
+__device__ __forceinline__ void row_info(const RowArgs &a, int row, bool there, float m, float s, float lse, float loss) {
+  const float g = a.row_grads ? a.row_grads[row] : 1.f;
+  const int t = a.targets[row];
+  RowInfo r = {m, __fdividef(1.f, s) * g, g, there && lse != -INF ? t : -1};
+  float row_scale = 1, hidden_scale = r.t >= 0 ? 1.f : 0.f;
+  if (a.target_power && r.t >= 0) {
+    if (loss <= 41.f) {
+      const float c = a.target_logit[row];
+      s *= ex2((m - c) * LOG2E);
+      r = RowInfo{c, 1.f, s, t};
+      row_scale = hidden_scale = g / s;
+      float x = a.target_power[row] - s;                   // the target's place in G
+      __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.g) + row * a.g_stride + t;
+      for (int p = 0; p < a.parts; ++p) {
+        to[p * a.g_part] = __float2bfloat16_rn(x);
+        x -= __bfloat162float(__float2bfloat16_rn(x));
+      }
+    } else {
+      r = RowInfo{m, __fdividef(1.f, s), 1.f, t};
+      row_scale = hidden_scale = g;
+      a.only[0] = a.only[1 + row / TILE] = 1;
+    }
+  } else if (a.target_power) {
+    row_scale = 0;
+  }
+  a.info[row] = r;
+  a.row_scale[row] = row_scale;
+  a.hidden_scale[row] = hidden_scale;
+  if (a.g_max && r.t >= 0 && fabsf(g) < INF) atomicMax(a.g_max, __float_as_uint(fabsf(g)));
 }
 
 // R rows a block: the parts of a row are joined by 256 / R threads
-template <int R> __global__ void __launch_bounds__(256) k_finish(FinishArgs a) {
+template <int R> __global__ void __launch_bounds__(256) k_finish(RowArgs a) {
   constexpr int EACH = 256 / R;
   __shared__ float2 box[256];
   const int r = threadIdx.x % R, j = threadIdx.x / R, row = blockIdx.x * R + r;
@@ -335,23 +502,42 @@ template <int R> __global__ void __launch_bounds__(256) k_finish(FinishArgs a) {
   }
   if (j || row >= a.n_rows) return;
   const float log_s = logf(s), lse = m + log_s;
-  const int32_t t = a.targets[a.row0 + row];
+  const int32_t t = a.targets[row];
   const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
   if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
-  if (a.lse) a.lse[a.row0 + row] = lse;
-  a.loss[a.row0 + row] = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
-  if (a.info) row_info(a, row, there, m, __fdividef(1.f, s), lse);
+  const float loss = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
+  if (a.lse) a.lse[row] = lse;
+  a.loss[row] = loss;
+  if (a.info) row_info(a, row, there, m, s, lse, loss);
 }
 
 // the same from an lse that the caller has
-__global__ void __launch_bounds__(256) k_info(FinishArgs a) {
+__global__ void __launch_bounds__(256) k_info(RowArgs a) {
   const int row = blockIdx.x * 256 + threadIdx.x;
   if (row >= a.n_rows) return;
-  const float lse = a.lse_in[a.row0 + row];
-  const int32_t t = a.targets[a.row0 + row];
+  const float lse = a.lse_in[row];
+  const int32_t t = a.targets[row];
   const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
   if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
-  row_info(a, row, there, lse, 1.f, lse);
+  row_info(a, row, there, lse, 1.f, lse, 0.f);
+}
+
+// Hidden by its rows' scale, for dweight (padding rows as zeros, whatever they hold); a
+// warp a row.
+template <class T> __global__ void __launch_bounds__(256) k_hidden(RowArgs a) {
+  const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (row >= a.n_rows) return;
+  const float scale = a.hidden_scale[row];
+  const T *h = (const T *)a.hidden + row * a.hidden_stride;
+  uint16_t *to = a.scaled + (int64_t)row * a.width;
+  const bool none = a.info[row].t < 0;
+  for (int c = lane * 8; c < a.width; c += 256) {
+    float v[8];
+    take8(h + c, v, min(8, a.dim - c), a.hidden_vec);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = none ? 0.f : v[i] * scale;
+    pack8<T>(to + c, (int64_t)a.n_rows * a.width, v);
+  }
 }
 
 // ------------------------------------------------------------ host
@@ -376,7 +562,7 @@ struct Call {
 struct Plan {
   int64_t chunk, width, g_stride;                          // rows; columns of packed operands and of G
   int split_h, split_w;
-  int64_t hidden, weight, part, target_logit, info, word, g, acc, sums, bytes;
+  int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
 };
 
 Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, bool pack_w, bool dh, bool dw, bool dw_f32) {
@@ -404,10 +590,11 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   p.hidden = take(pack_h ? n * p.width * 2 * parts : 0);
   p.weight = take(pack_w ? vocab * p.width * 2 * parts : 0);
   p.part = take(halves * 8 * p.chunk);
-  p.target_logit = take(4 * p.chunk);
-  p.word = take(4);
+  p.rows = take(4 * 4 * p.chunk);                          // target_logit, target_power, row_scale, hidden_scale
+  p.word = take(4 * (1 + (p.chunk + TILE - 1) / TILE));
   if (grad) {
     p.info = take(sizeof(RowInfo) * p.chunk);
+    p.scaled = take(dw ? p.chunk * p.width * 2 * parts : 0);
     p.g = take(p.g_stride * 2 * parts * p.chunk);
     p.acc = take(dw && !dw_f32 && p.chunk < n ? vocab * p.width * 4 : 0);
     int64_t sums = 0;
@@ -419,6 +606,10 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   return p;
 }
 
+// rows lie on 16-byte boundaries
+inline int vec_of(const void *p, int64_t stride, int32_t type) {
+  return aligned(p, 16) && stride * (int64_t)type_size(type) % 16 == 0;
+}
 inline bool rows_tma(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 inline bool needs_pack(int32_t type, const void *p, int64_t stride) { return type == TT_F32 || !rows_tma(p, stride); }
 
@@ -426,7 +617,7 @@ void pack(int32_t type, const void *x, int64_t n, int64_t dim, int64_t stride, v
   const unsigned blocks = (unsigned)std::min<int64_t>((n * (width / 8) + 255) / 256, SMS * 16);
   with_type(type, [&](auto t) {
     using T = decltype(t);
-    k_pack<T><<<blocks, 256, 0, stream>>>((const T *)x, n, (int)dim, stride, (uint16_t *)out, (int)width);
+    k_pack<T><<<blocks, 256, 0, stream>>>((const T *)x, n, (int)dim, stride, (uint16_t *)out, (int)width, vec_of(x, stride, type));
   });
 }
 
@@ -440,22 +631,42 @@ template <bool A_MN>
 bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sums, int64_t width, int32_t type, const Target &o,
              int32_t *status, cudaStream_t stream) {
   if (splits > 1) {
-    if (!run_gemm<A_MN, true>(bf16, a, b, splits, 8, PartEpi{(int)o.n_rows, (int)width, sums}, status, stream)) return false;
+    const Target part{o.n_rows, o.n_cols, sums, width, nullptr, 0, TT_F32, nullptr, nullptr, 1};
+    if (!run_gemm<A_MN, true>(bf16, a, b, splits, 8, OutEpi<float>{part, o.n_rows}, status, stream)) return false;
     with_type(type, [&](auto t) { join<decltype(t)>(sums, splits, width, o, stream); });
     return true;
   }
   bool ok = true;
-  with_type(type, [&](auto t) { ok = run_gemm<A_MN, true>(bf16, a, b, 1, 8, OutEpi<decltype(t)>{o}, status, stream); });
+  with_type(type, [&](auto t) { ok = run_gemm<A_MN, true>(bf16, a, b, 1, 8, OutEpi<decltype(t)>{o, 0}, status, stream); });
   return ok;
 }
 
-inline int vec_of(const void *p, int64_t stride, int32_t type) {
-  return aligned(p, 16) && stride * (int64_t)type_size(type) % 16 == 0;
+// the product of hidden and weight into powers, or into G; T: the operands' type
+template <class T> bool make_powers(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  PowersEpi<T> e{{}, r.n_rows, r.n_vocab, r.targets, r.target_logit, r.part, r.target_power};
+  if (encode_map(&e.map, true, g, 32) != CUDA_SUCCESS) return false;
+  return run_gemm<false, false>(true, h, w, 1, 16, e, r.status, stream);
+}
+template <class T> bool make_g(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  const bool bf16 = !std::is_same<T, __half>::value;
+  GradEpi<T> e{{}, r.n_rows, r.n_vocab, r.info, r.g_max};
+  if (encode_map(&e.map, bf16, g, 32) != CUDA_SUCCESS) return false;
+  return run_gemm<false, false>(bf16, h, w, 1, 16, e, r.status, stream, r.only);
+}
+
+void finish(const RowArgs &r, cudaStream_t stream) {
+  const int n = r.n_rows;
+  if (n >= 4096) k_finish<32><<<(n + 31) / 32, 256, 0, stream>>>(r);
+  else if (n >= 1024) k_finish<8><<<(n + 7) / 8, 256, 0, stream>>>(r);
+  else k_finish<1><<<n, 256, 0, stream>>>(r);
 }
 
 bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) {
   const int parts = c.type == TT_F32 ? 3 : 1;
+  const size_t size = type_size(c.type);
   const bool bf16 = c.type != TT_F16, grad = c.dhidden || c.dweight;
+  // a 16-bit float has no range for powers: the product runs twice, for lse and for G
+  const bool powers = grad && !c.lse_in && c.type != TT_F16;
   Matrix h{c.hidden, c.n, c.dim, c.hidden_stride, parts, 8}, w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
   if (needs_pack(c.type, c.hidden, c.hidden_stride)) {
     pack(c.type, c.hidden, c.n, c.dim, c.hidden_stride, ws + p.hidden, p.width, stream);
@@ -465,47 +676,84 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     pack(c.type, c.weight, c.vocab, c.dim, c.weight_stride, ws + p.weight, p.width, stream);
     w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
   }
-  RowInfo *info = grad ? (RowInfo *)(ws + p.info) : nullptr;
-  uint32_t *word = grad && c.type == TT_F16 ? (uint32_t *)(ws + p.word) : nullptr;
-  const int halves = (int)((c.vocab + HALF - 1) / HALF);
+  RowArgs r{};
+  r.n_parts = (int)((c.vocab + HALF - 1) / HALF);
+  r.n_vocab = (int)c.vocab;
+  r.dim = (int)c.dim;
+  r.part = (float2 *)(ws + p.part);
+  r.target_logit = (float *)(ws + p.rows);
+  r.row_scale = r.target_logit + 2 * p.chunk;
+  r.hidden_scale = r.target_logit + 3 * p.chunk;
+  r.status = c.status;
+  r.weight = c.weight;
+  r.hidden_stride = c.hidden_stride;
+  r.weight_stride = c.weight_stride;
+  r.hidden_vec = vec_of(c.hidden, c.hidden_stride, c.type);
+  r.weight_vec = vec_of(c.weight, c.weight_stride, c.type);
+  r.width = (int)p.width;
+  r.parts = parts;
+  r.g_stride = p.g_stride;
+  r.g_part = p.chunk * p.g_stride;
+  if (grad) {
+    r.info = (RowInfo *)(ws + p.info);
+    r.g = (uint16_t *)(ws + p.g);
+    if (c.dweight) r.scaled = (uint16_t *)(ws + p.scaled);
+    if (c.type == TT_F16) r.g_max = (uint32_t *)(ws + p.word);
+    if (powers) {
+      r.target_power = r.target_logit + p.chunk;
+      r.only = (int32_t *)(ws + p.word);
+    }
+  }
   for (int64_t row0 = 0; row0 < c.n; row0 += p.chunk) {
     const int n = (int)std::min(p.chunk, c.n - row0);
     Matrix hc = h;
     hc.p = (const uint16_t *)h.p + row0 * h.stride;
     hc.rows = n;
-    FinishArgs f{n, halves, (int)c.vocab, row0, (float2 *)(ws + p.part), (float *)(ws + p.target_logit), c.row_grads, c.lse_in,
-                 c.targets, c.loss, c.lse, info, word, c.status};
-    if (word && cudaMemsetAsync(word, 0, 4, stream) != cudaSuccess) return false;
+    r.n_rows = n;
+    r.hidden = (const uint8_t *)c.hidden + row0 * c.hidden_stride * size;
+    r.targets = c.targets + row0;
+    r.row_grads = c.row_grads ? c.row_grads + row0 : nullptr;
+    r.lse_in = c.lse_in ? c.lse_in + row0 : nullptr;
+    r.loss = c.loss ? c.loss + row0 : nullptr;
+    r.lse = c.lse ? c.lse + row0 : nullptr;
+    const Matrix g{r.g, n, c.vocab, p.g_stride, parts, r.g_part};
+    if ((r.g_max || r.only) && cudaMemsetAsync(ws + p.word, 0, 4 * (1 + (n + TILE - 1) / TILE), stream) != cudaSuccess) return false;
+    bool ok = true;
     if (c.lse_in) {
-      k_info<<<(n + 255) / 256, 256, 0, stream>>>(f);
+      k_info<<<(n + 255) / 256, 256, 0, stream>>>(r);
+    } else if (powers) {
+      auto run = [&](auto t) {
+        using T = decltype(t);
+        k_target<T><<<(n + 7) / 8, 256, 0, stream>>>(r);
+        ok = make_powers<T>(hc, w, g, r, stream);
+      };
+      if (c.type == TT_F32) run(float{});
+      else run(__nv_bfloat16{});
+      if (!ok) return false;
+      finish(r, stream);
     } else {
-      const StatsEpi e{n, (int)c.vocab, row0, c.targets, (float2 *)(ws + p.part), (float *)(ws + p.target_logit)};
+      const StatsEpi e{n, (int)c.vocab, r.targets, r.part, r.target_logit};
       if (!run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream)) return false;
-      if (n >= 4096) k_finish<32><<<(n + 31) / 32, 256, 0, stream>>>(f);
-      else if (n >= 1024) k_finish<8><<<(n + 7) / 8, 256, 0, stream>>>(f);
-      else k_finish<1><<<n, 256, 0, stream>>>(f);
+      finish(r, stream);
     }
     if (!grad) continue;
-    uint16_t *g = (uint16_t *)(ws + p.g);
-    const int64_t g_part = p.chunk * p.g_stride;
-    bool ok = true;
     with_type(c.type, [&](auto t) {
-      const GradEpi<decltype(t)> e{n, (int)c.vocab, info, word, g, p.g_stride, g_part};
-      ok = run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream);
+      using T = decltype(t);
+      ok = make_g<T>(hc, w, g, r, stream);
+      if (c.dweight) k_hidden<T><<<(n + 7) / 8, 256, 0, stream>>>(r);
     });
     if (!ok) return false;
-    const Matrix gm{g, n, c.vocab, p.g_stride, parts, g_part};
     float *sums = (float *)(ws + p.sums);
     if (c.dhidden) {
-      Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * type_size(c.type), c.dhidden_stride, nullptr, 0, TT_F32, word,
-               vec_of(c.dhidden, c.dhidden_stride, c.type)};
-      if (!product<false>(bf16, gm, w, p.split_h, sums, p.width, c.type, o, c.status, stream)) return false;
+      const Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * size, c.dhidden_stride, nullptr, 0, TT_F32, r.g_max,
+                     powers ? r.row_scale : nullptr, vec_of(c.dhidden, c.dhidden_stride, c.type)};
+      if (!product<false>(bf16, g, w, p.split_h, sums, p.width, c.type, o, c.status, stream)) return false;
     }
     if (c.dweight) {
       // the sums of several chunks stay in 32 bits until the last
       const bool first = row0 == 0, last = row0 + n == c.n, own = c.dweight_type == TT_F32;
       const int vec = vec_of(c.dweight, c.dweight_stride, c.dweight_type);
-      Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, word, vec};
+      Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, r.g_max, nullptr, vec};
       int32_t type = c.dweight_type;
       if (!last && !own) {
         o.dst = ws + p.acc;
@@ -520,11 +768,13 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
         o.src = ws + p.acc;
         o.src_stride = p.width;
       }
-      if (!product<true>(bf16, gm, hc, p.split_w, sums, p.width, type, o, c.status, stream)) return false;
+      const Matrix scaled{r.scaled, n, c.dim, p.width, parts, n * p.width};
+      if (!product<true>(bf16, g, scaled, p.split_w, sums, p.width, type, o, c.status, stream)) return false;
     }
   }
   if (c.n == 0 && c.dweight && !c.accumulate) {
-    const Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, nullptr, vec_of(c.dweight, c.dweight_stride, c.dweight_type)};
+    const Target o{c.vocab, c.dim, c.dweight, c.dweight_stride, nullptr, 0, TT_F32, nullptr, nullptr,
+                   vec_of(c.dweight, c.dweight_stride, c.dweight_type)};
     with_type(c.dweight_type, [&](auto t) { join<decltype(t)>(nullptr, 0, up(c.dim, 8), o, stream); });
   }
   return true;
