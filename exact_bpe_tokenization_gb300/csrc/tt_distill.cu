@@ -47,7 +47,33 @@ __device__ __forceinline__ float value_of(const DistillArgs &a, int64_t row, int
   return to_f32(reinterpret_cast<const __nv_bfloat16 *>(a.values)[at]);
 }
 
-struct OpMaxNan { __device__ float operator()(float a, float b) const { return a > b || a != a ? a : b; } };
+// The maximum and sum of a warp's, or of n entries of an array: the maximum first, so
+// that no sum waits for another.  (Joined in turn, what stands between reading a row and
+// writing its gradient took twice as long.)
+__device__ __forceinline__ float warp_top(float m) {
+  float top;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+  return top;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+__device__ __forceinline__ float2 warp_join(const Running<true> &r) {
+  const float top = warp_top(r.m);
+  return make_float2(top, warp_sum(r.s * ex2((r.m - top) * r.c)));
+}
+template <int N> __device__ __forceinline__ float2 join_all(const float2 *p, int n, float c) {
+  float top = LOWEST, s = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) top = fmaxf(top, p[i].x);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (i < n) s += p[i].y * ex2((p[i].x - top) * c);
+  return make_float2(top, s);
+}
 
 // GRAD: 0 the loss alone, 1 with its gradient, 2 the gradient from lse
 template <class T, int GRAD, int THREADS>
@@ -57,8 +83,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs
   int32_t *s_id = reinterpret_cast<int32_t *>(s_row + a.held);              // [k] the entries' IDs, -1: none
   float *s_q = reinterpret_cast<float *>(s_id + a.k), *s_x = s_q + a.k;     // [k] shares and logits
   int32_t *s_key = reinterpret_cast<int32_t *>(s_x + a.k), *s_first = s_key + a.slots;
-  __shared__ float2 s_warp[WARPS], s_blocks[8];
-  __shared__ float s_box[WARPS];
+  __shared__ float2 s_warp[2][WARPS];
+  __shared__ float2 s_blocks[8], s_terms[8 * WARPS];                        // what blocks tell all others, and warps the first block
   __shared__ int s_twice;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
@@ -71,9 +97,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs
   const uint4 *body = reinterpret_cast<const uint4 *>(l + part.lead) + first;
   // what is held comes by copies that run ahead; a thread reads its own
   auto fetch = [&](int v0) {
+    if (v0 - tid + UC * THREADS <= n_held) {
 #pragma unroll
-    for (int u = 0; u < UC; ++u)
-      if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+      for (int u = 0; u < UC; ++u) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+    } else {
+#pragma unroll
+      for (int u = 0; u < UC; ++u)
+        if (v0 + u * THREADS < n_held) copy_async(s_row + v0 + u * THREADS, body + v0 + u * THREADS);
+    }
     copy_group();
   };
   if (GRAD == 1) {
@@ -84,37 +115,97 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs
   const float x = lone >= 0 ? to_f32(l[lone]) : -INF;
   const float g_row = GRAD && a.row_grads ? a.row_grads[row] : 1.f;
 
-  // the teacher's entries: the maximum and sum of their softmax, and their logits
+  // The teacher's entries, and the maximum and sum of their softmax.  A thread's first
+  // entry is on its way while the row is summed.
+  Running<true> teacher, run;
+  teacher.c = run.c = a.c;
+  const int32_t *ids = a.ids + row * a.ids_stride;
   const int lo = part.lead + first * E, hi = lo + n * E;                    // this block's part of the row
   auto in_part = [&](int id) { return (id >= lo && id < hi) || (rank == 0 && (id < part.lead || id >= part.lead + part.vecs * E)); };
+  float x0 = 0;
+  const int id0 = tid < a.k ? ids[tid] : -1;
+  const float value0 = tid < a.k ? value_of(a, row, tid) : 0.f;
+  auto take = [&](int i, int id, float value) {
+    if (id >= a.n_vocab) {
+      if (rank == 0) op_status(a.status, TT_ERR_INVALID_ARG);
+      id = -1;
+    }
+    s_id[i] = max(id, -1);
+    s_q[i] = value;
+    if (id >= 0) teacher.add(value);
+  };
   if (tid == 0) s_twice = 0;
   for (int i = tid; i < a.slots; i += THREADS) {
     s_key[i] = -1;
     s_first[i] = 1 << 30;
   }
-  float top = -INF;
-  for (int i = tid; i < a.k; i += THREADS) {
-    int id = a.ids[row * a.ids_stride + i];
-    if (id >= a.n_vocab) {
-      if (rank == 0) op_status(a.status, TT_ERR_INVALID_ARG);
-      id = -1;
+  if (GRAD != 2) {
+    if (GRAD == 1)
+      groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
+        copy_wait<AHEAD - 1>();
+        fetch(v0 + AHEAD * UC * THREADS);
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+          if (whole.value || v0 + u * THREADS < n_held) run.add(s_row[v0 + u * THREADS], T{});
+      });
+    auto sum = [&](int from, int to) {
+      groups<THREADS>(from, to, U, [&](int v0, auto whole) {
+        uint4 r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (whole.value || v0 + u * THREADS < to) r[u] = __ldcs(body + v0 + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (whole.value || v0 + u * THREADS < to) run.add(r[u], T{});
+      });
+    };
+    if (GRAD == 0) {
+      // the logit of the thread's first entry is asked for when its ID is there, halfway
+      const int half = n / 2 / (U * THREADS) * (U * THREADS);
+      sum(0, half);
+      if (tid < a.k && id0 >= 0 && id0 < a.n_vocab && in_part(id0)) x0 = to_f32(l[id0]);
+      sum(half, n);
+    } else {
+      sum(n_held, n);
     }
-    const float v = id >= 0 ? value_of(a, row, i) : -INF;
-    s_id[i] = max(id, -1);
-    s_q[i] = v;
-    // read here, before any block can write to the row
-    s_x[i] = id >= 0 && ((GRAD != 2 && rank == 0) || (GRAD && in_part(id))) ? to_f32(l[id]) : 0.f;
-    top = OpMaxNan{}(top, v);
+    if (lone >= 0) run.add(x);
   }
-  top = block_all(top, OpMaxNan{}, s_box);
-  float mass = 0;
-  for (int i = tid; i < a.k; i += THREADS) mass += s_id[i] >= 0 ? ex2((s_q[i] - top) * a.c) : 0.f;
-  mass = block_all(mass, OpSum{}, s_box);
-  // nothing that the teacher gives any weight to
-  const bool none = top == -INF;
-  const float log_mass = logf(mass);
-  // slots are claimed by the entries of this block's part
-  if (GRAD) {
+  if (tid < a.k) take(tid, id0, value0);
+  for (int i = tid + THREADS; i < a.k; i += THREADS) take(i, ids[i], value_of(a, row, i));
+  run.total();
+  teacher.total();
+  float2 mine = warp_join(run), theirs = warp_join(teacher);
+  if (lane == 0) {
+    s_warp[0][warp] = mine;
+    s_warp[1][warp] = theirs;
+  }
+  __syncthreads();                               // (a thread's copies are there, and so are all others')
+  mine = join_all<WARPS>(s_warp[0], WARPS, a.c);
+  theirs = join_all<WARPS>(s_warp[1], WARPS, a.c);
+  const bool none = theirs.y == 0;               // nothing that the teacher gives any weight to
+
+  // The shares of the entries in this block's part of the row, which each of them lies in
+  // one block's of, and their terms of the loss, against this block's maximum.  The
+  // logits are read before any block can write to the row, from what is held if they are.
+  const float log_mass = logf(theirs.y), one = __fdividef(1.f, theirs.y);
+  float2 terms = make_float2(0, 0);              // the loss's, and the shares
+  for (int i = tid; i < a.k; i += THREADS) {
+    const int id = s_id[i];
+    if (id < 0) continue;
+    const float above = s_q[i] - theirs.x, q = ex2(above * a.c) * one;
+    s_q[i] = q;
+    if (!in_part(id)) continue;
+    const float xi = GRAD == 0 && i == tid                             ? x0
+                     : id >= lo && (id - lo) / E < n_held ? to_f32(reinterpret_cast<const T *>(s_row)[id - lo])
+                                                          : to_f32(l[id]);
+    s_x[i] = xi;
+    if (GRAD != 2 && q != 0) {
+      terms.x += q * (above * a.inv_t - log_mass - (xi - mine.x) * a.inv_t);
+      terms.y += q;
+    }
+  }
+  // An ID's slot is claimed by its first entry (while the cluster's blocks meet).
+  auto claim = [&]() {
     for (int i = tid; i < a.k; i += THREADS) {
       const int id = s_id[i];
       if (id < 0 || !in_part(id)) continue;
@@ -129,67 +220,48 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs
         at = (at + 1) & (a.slots - 1);
       }
     }
-  }
+  };
 
-  float lse, from, inverse = 1.f;                // probabilities are 2^(c (l - from)) * inverse
+  float lse, from, log_s = 0, inverse = 1.f;                // probabilities are 2^(c (l - from)) * inverse
   if (GRAD == 2) {
     lse = a.lse_in[row];
     from = 0;
+    claim();
   } else {
-    Running<true> run;
-    run.c = a.c;
-    if (GRAD == 1)
-      groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
-        copy_wait<AHEAD - 1>();
-        fetch(v0 + AHEAD * UC * THREADS);
-#pragma unroll
-        for (int u = 0; u < UC; ++u)
-          if (whole.value || v0 + u * THREADS < n_held) run.add(s_row[v0 + u * THREADS], T{});
-      });
-    groups<THREADS>(n_held, n, U, [&](int v0, auto whole) {
-      uint4 r[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (whole.value || v0 + u * THREADS < n) r[u] = __ldcs(body + v0 + u * THREADS);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (whole.value || v0 + u * THREADS < n) run.add(r[u], T{});
-    });
-    if (lone >= 0) run.add(x);
-    run.total();
-#pragma unroll
-    for (int o = 16; o; o >>= 1) run.join(__shfl_xor_sync(~0u, run.m, o), __shfl_xor_sync(~0u, run.s, o));
-    if (lane == 0) s_warp[warp] = make_float2(run.m, run.s);
-    __syncthreads();
-    run.m = LOWEST;
-    run.s = 0;
-    for (int w = 0; w < WARPS; ++w) run.join(s_warp[w].x, s_warp[w].y);
+    if (warp * 32 < a.k) terms = make_float2(warp_sum(terms.x), warp_sum(terms.y));
     if (a.cluster > 1) {
       cluster_wait();                            // all blocks have begun
-      if (tid < a.cluster) *of_block(&s_blocks[rank], tid) = make_float2(run.m, run.s);
-      cluster_sync();
-      run.m = LOWEST;
-      run.s = 0;
-      for (int b = 0; b < a.cluster; ++b) run.join(s_blocks[b].x, s_blocks[b].y);
+      if (tid < a.cluster) *of_block(&s_blocks[rank], tid) = mine;
+      if (lane == 0) *of_block(&s_terms[rank * WARPS + warp], 0) = terms;
+      cluster_arrive();
+      if (GRAD) claim();
+      cluster_wait();
+    } else {
+      if (tid == 0) s_blocks[0] = mine;
+      if (lane == 0) s_terms[warp] = terms;
+      if (GRAD) claim();
+      __syncthreads();
     }
-    const float log_s = logf(run.s);
-    from = run.m;
-    inverse = __fdividef(1.f, run.s);            // of 1 .. 2^20
-    lse = run.s == 0 ? -INF : run.m * a.inv_t + log_s;
-    if (rank == 0) {
-      float loss = 0;
-      for (int i = tid; i < a.k; i += THREADS) {
-        if (s_id[i] < 0) continue;
-        const float y = (s_q[i] - top) * a.c, q = ex2(y) * __fdividef(1.f, mass);
-        if (q != 0) loss += q * ((s_q[i] - top) * a.inv_t - log_mass - (s_x[i] - run.m) * a.inv_t + log_s);
-      }
-      loss = block_all(loss, OpSum{}, s_box);
-      if (tid == 0) {
-        if (a.lse_out) a.lse_out[row] = lse;
-        a.loss[row] = none ? 0.f : run.s == 0 ? INF : loss;
-      }
-    }
+    const float2 all = join_all<8>(s_blocks, a.cluster, a.c);
+    log_s = logf(all.y);
+    from = all.x;
+    inverse = __fdividef(1.f, all.y);            // of 1 .. 2^20
+    lse = all.y == 0 ? -INF : all.x * a.inv_t + log_s;
   }
+  // the row's loss, by the warp that is likely to have least to do
+  auto report = [&]() {
+    float loss = 0;
+    for (int i = lane; i < a.cluster * WARPS; i += 32) {
+      const float2 t = s_terms[i];
+      if (t.y != 0) loss += t.x + t.y * ((from - s_blocks[i / WARPS].x) * a.inv_t);
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) {
+      if (a.lse_out) a.lse_out[row] = lse;
+      a.loss[row] = none ? 0.f : lse == -INF ? INF : loss + log_s;
+    }
+  };
+  if (GRAD == 0 && rank == 0 && warp == WARPS - 1) report();
   if (GRAD) {
     T *d = dlogits + row * a.dlogits_stride;
     const bool zero = none || lse == -INF;
@@ -240,20 +312,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_distill(DistillArgs
         if (whole.value || v0 + u * THREADS < n) write(r[u], v0 + u * THREADS);
     });
     if (lone >= 0) d[lone] = from_f32<T>(zero ? 0.f : power(x) * factor);
+    if (GRAD == 1 && rank == 0 && warp == WARPS - 1) report();
     if (zero) return;
-    __syncthreads();                             // the part's gradients are written, the slots claimed
+    // the part's gradients are written, the slots claimed: warps without entries need not wait
+    if (warp * 32 >= a.k) {
+      asm volatile("barrier.cta.arrive 1, %0;" ::"n"(THREADS) : "memory");
+      return;
+    }
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
     const bool twice = s_twice;
     for (int i = tid; i < a.k; i += THREADS) {
       const int id = s_id[i];
       if (id < 0 || !in_part(id)) continue;
-      auto share = [&](int e) { return ex2((s_q[e] - top) * a.c) * __fdividef(1.f, mass); };
-      float q = share(i);
+      float q = s_q[i];
       if (twice) {
         int at = (int)((uint32_t)id * 2654435761u >> 16) & (a.slots - 1);
         while (s_key[at] != id) at = (at + 1) & (a.slots - 1);
         if (s_first[at] != i) continue;
         for (int e = i + 1; e < a.k; ++e)
-          if (s_id[e] == id) q += share(e);
+          if (s_id[e] == id) q += s_q[e];
       }
       d[id] = from_f32<T>((power(s_x[i]) * inverse - q) * g);
     }
@@ -265,15 +342,19 @@ template <class T, int GRAD, int THREADS> struct Tag {};
 template <class T, int GRAD, int THREADS>
 void run_rows_by(DistillArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
   const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
-  a.slots = 0;
-  if (GRAD)
-    for (a.slots = 32; a.slots < 2 * a.k;) a.slots *= 2;
-  const int extra = (a.k * 12 + a.slots * 8 + 15) / 16 * 16, held = std::min(HELD, SPACE - extra) / 16 * 16;
+  // the same blocks a row, and the same order of its sums, with the gradient and without
+  for (a.slots = 32; a.slots < 2 * a.k;) a.slots *= 2;
+  int extra = (a.k * 12 + a.slots * 8 + 15) / 16 * 16;
+  const int held = std::min(HELD, SPACE - extra) / (16 * THREADS) * (16 * THREADS);
   a.cluster = (int)std::min<int64_t>(8, (bytes + held - 1) / held);
   // few rows: spread each over more blocks, down to 16 KB a block, as for the next-token loss
   while (a.cluster <= 4 && n_rows * a.cluster * 2 <= 2 * 152 && bytes >= a.cluster * 2 * 16384) a.cluster *= 2;
   const int64_t each = ((bytes + 15) / 16 + a.cluster - 1) / a.cluster;
   a.held = GRAD == 1 ? (int)std::min<int64_t>(each, held / 16) : 0;
+  if (!GRAD) {
+    a.slots = 0;
+    extra = (a.k * 12 + 15) / 16 * 16;
+  }
   auto k = k_distill<T, GRAD, THREADS>;
   if (allow_shared<Tag<T, GRAD, THREADS>>(k, SPACE)) return;                // (the error is kept)
   launch_cluster(k, dim3((unsigned)(n_rows * a.cluster)), THREADS, (size_t)a.held * 16 + extra, a.cluster, false, stream, a,

@@ -36,6 +36,8 @@ constexpr uint32_t TRIES = 1u << 22;                      // of a wait, before t
 struct Gemm {
   int m_tiles, n_tiles, splits;                           // the contraction is cut into `splits` parts
   int k_blocks;                                           // of 64, the last filled up with zeros
+  int rows_a, rows_b;                                     // of the operands
+  uint32_t box_a;                                         // bytes of A a block loads a stage
   int pairs;                                              // of parts, listed in nibbles of pair_a and pair_b
   uint32_t pair_a, pair_b, idesc;
   int group;                                              // tile rows that are passed through together
@@ -230,13 +232,17 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
       if (g.only && !g.only[1 + p.m]) continue;
       const int2 kb = blocks_of(g, p.split);
       const int ra = p.m * TILE + rank * HALF, rb = p.n * TILE + rank * HALF;
+      // Rows that are not there are left out: what lies in their place enters only results
+      // of theirs.  (TMA reads the border again for each row beyond it: 152 SMs at one
+      // line of a single row took 124 us for 1 x 100256 x 2048 instead of 86.)
+      const uint32_t bytes = (1 + (p.m * TILE + HALF < g.rows_a)) * g.box_a + (1 + (p.n * TILE + HALF < g.rows_b)) * (STAGE_BYTES / 2);
       for (int i = 0; ok && i < g.pairs; ++i) {
         for (int k = kb.x; k < kb.y; ++k) {
           if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) break;
-          if (rank == 0) bar_expect(full + 8 * stage, 2 * STAGE_BYTES);
+          if (rank == 0) bar_expect(full + 8 * stage, bytes);
           const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
-          Operand<A_MN>::load(to, &map_a, ra, k * KB, g.pair_a >> (4 * i) & 15, bar);
-          Operand<B_MN>::load(to + STAGE_BYTES / 2, &map_b, rb, k * KB, g.pair_b >> (4 * i) & 15, bar);
+          if (ra < g.rows_a) Operand<A_MN>::load(to, &map_a, ra, k * KB, g.pair_a >> (4 * i) & 15, bar);
+          if (rb < g.rows_b) Operand<B_MN>::load(to + STAGE_BYTES / 2, &map_b, rb, k * KB, g.pair_b >> (4 * i) & 15, bar);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -332,10 +338,16 @@ template <bool A_MN, bool B_MN, class Epi>
 inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, int group, const Epi &epi, int32_t *status,
                      cudaStream_t stream, const int32_t *only = nullptr) {
   CUtensorMap ma, mb;
-  if (encode_map(&ma, bf16, a, A_MN ? KB : HALF) != CUDA_SUCCESS || encode_map(&mb, bf16, b, B_MN ? KB : HALF) != CUDA_SUCCESS) return false;
+  // few rows: a box no higher than they are
+  const int64_t rows_a = A_MN ? a.cols : a.rows, rows_b = B_MN ? b.cols : b.rows;
+  const uint32_t box = A_MN ? HALF : (uint32_t)std::min<int64_t>(HALF, (rows_a + 7) / 8 * 8);
+  if (encode_map(&ma, bf16, a, A_MN ? KB : box) != CUDA_SUCCESS || encode_map(&mb, bf16, b, B_MN ? KB : HALF) != CUDA_SUCCESS) return false;
   Gemm g;
-  g.m_tiles = (int)(((A_MN ? a.cols : a.rows) + TILE - 1) / TILE);
-  g.n_tiles = (int)(((B_MN ? b.cols : b.rows) + TILE - 1) / TILE);
+  g.rows_a = (int)rows_a;
+  g.rows_b = (int)rows_b;
+  g.box_a = box * KB * 2;
+  g.m_tiles = (int)((rows_a + TILE - 1) / TILE);
+  g.n_tiles = (int)((rows_b + TILE - 1) / TILE);
   g.k_blocks = (int)(((A_MN ? a.rows : a.cols) + KB - 1) / KB);
   g.splits = splits;
   // the products of parts whose orders add up to less than three, the smallest first (the
