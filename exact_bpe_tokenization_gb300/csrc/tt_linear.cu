@@ -75,27 +75,35 @@ template <class T> __device__ __forceinline__ void put_box(const CUtensorMap *ma
   }
 }
 
-// a running maximum and sum of 32 values, those of columns that are not there being -inf
-__device__ __forceinline__ void add32(const float v[32], float &m, float2 &s) {
-  float top = v[0];
+// a running maximum and sum, with 64 values of columns of which n are there (the others
+// become -inf); in several chains, since a warp has one other to wait with
+__device__ __forceinline__ void cut64(float v[64], int n) {
+  if (n < 64)
 #pragma unroll
-  for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-  top = fminf(top, -LOWEST);
-  if (top > m) {
-    s = mul2(s, ex2((m - top) * LOG2E));
-    m = top;
+    for (int i = 0; i < 64; ++i) v[i] = i < n ? v[i] : -INF;
+}
+__device__ __forceinline__ void add64(const float v[64], float &m, float2 s[2]) {
+  float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int i = 4; i < 64; i += 4)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top[j] = fmaxf(top[j], v[i + j]);
+  top[0] = fminf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), -LOWEST);
+  if (top[0] > m) {
+    const float by = ex2((m - top[0]) * LOG2E);
+    s[0] = mul2(s[0], by);
+    s[1] = mul2(s[1], by);
+    m = top[0];
   }
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
-    const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), m, LOG2E);
-    s = add2(s, make_float2(ex2(y.x), ex2(y.y)));
-  }
-}
-__device__ __forceinline__ void cut32(float v[32], int n) {
-  if (n < 32)
+  for (int i = 0; i < 64; i += 4)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -INF;
+    for (int j = 0; j < 2; ++j) {
+      const float2 y = sub_mul2(make_float2(v[i + 2 * j], v[i + 2 * j + 1]), m, LOG2E);
+      s[j] = add2(s[j], make_float2(ex2(y.x), ex2(y.y)));
+    }
 }
+__device__ __forceinline__ float total(const float2 s[2]) { return (s[0].x + s[0].y) + (s[1].x + s[1].y); }
 
 // The maximum and sum of each row and 128 columns, and the target's logit.  The
 // maximum stays within the finite floats, so that a difference is NaN only where a
@@ -105,23 +113,24 @@ struct StatsEpi {
   const int32_t *targets;
   float2 *part;                                            // [column halves][n_rows]
   float *target_logit;                                     // [n_rows]
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t, Load load) const {
+  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t, Load load, Release release) const {
     const bool mine = row < n_rows;
     const int t = mine ? targets[row] : -1;
     float m = LOWEST;
-    float2 s = make_float2(0, 0);
-    for (int c = 0; c < HALF; c += 32) {
-      float v[32];
+    float2 s[2] = {{0, 0}, {0, 0}};
+    for (int c = 0; c < HALF; c += 64) {
+      float v[64];
       load(c, v);
+      if (c) release();
       const int n = n_cols - col - c;                      // columns that are there
-      cut32(v, n);
-      if ((uint32_t)(t - col - c) < 32u)
+      cut64(v, n);
+      if ((uint32_t)(t - col - c) < 64u)
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 64; ++i)
           if (i == t - col - c && i < n) target_logit[row] = v[i];
-      add32(v, m, s);
+      add64(v, m, s);
     }
-    if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = make_float2(m, s.x + s.y);
+    if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = make_float2(m, total(s));
   }
   __device__ __forceinline__ void end() const {}
 };
@@ -138,24 +147,38 @@ template <class T> struct PowersEpi {
   const float *from;                                       // [n_rows] c
   float2 *part;                                            // [column halves][n_rows]
   float *target_power;                                     // [n_rows]
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load) const {
+  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load, Release release) const {
     const bool mine = row < n_rows;
     const int t = mine ? targets[row] : -1;
     const bool there = (uint32_t)t < (uint32_t)n_cols;
     const float c0 = mine ? from[row] : 0.f;
-    float2 s = make_float2(0, 0);
+    float2 s[2] = {{0, 0}, {0, 0}}, p;
     for (int c = 0; c < HALF; c += 64) {
       float v[64];
       load(c, v);
-      load(c + 32, v + 32);
-      cut32(v, n_cols - col - c);
-      cut32(v + 32, n_cols - col - c - 32);
+      cut64(v, n_cols - col - c);
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
         const float2 y = sub_mul2(make_float2(v[i], v[i + 1]), c0, LOG2E);
         v[i] = ex2(y.x);
         v[i + 1] = ex2(y.y);
-        s = add2(s, make_float2(v[i], v[i + 1]));
+        s[i / 2 & 1] = add2(s[i / 2 & 1], make_float2(v[i], v[i + 1]));
+      }
+      if (c) {
+        p = make_float2(c0, total(s));
+        const bool safe = p.y > 0x1p-100f && p.y < 0x1p100f;
+        if (__any_sync(~0u, mine && !safe)) {
+          float m = LOWEST;
+          float2 again[2] = {{0, 0}, {0, 0}};
+          for (int d = 0; d < HALF; d += 64) {
+            float w[64];
+            load(d, w);
+            cut64(w, n_cols - col - d);
+            add64(w, m, again);
+          }
+          if (!safe) p = make_float2(m, total(again));
+        }
+        release();
       }
       if (there && (uint32_t)(t - col - c) < 64u)
 #pragma unroll
@@ -165,19 +188,6 @@ template <class T> struct PowersEpi {
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i] = 0;
       put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
-    }
-    float2 p = make_float2(c0, s.x + s.y);
-    const bool safe = p.y > 0x1p-100f && p.y < 0x1p100f;
-    if (__any_sync(~0u, mine && !safe)) {
-      float m = LOWEST;
-      s = make_float2(0, 0);
-      for (int c = 0; c < HALF; c += 32) {
-        float v[32];
-        load(c, v);
-        cut32(v, n_cols - col - c);
-        add32(v, m, s);
-      }
-      if (!safe) p = make_float2(m, s.x + s.y);
     }
     if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = p;
   }
@@ -198,7 +208,7 @@ template <class T> struct GradEpi {
   int n_rows, n_cols;
   const RowInfo *info;
   const uint32_t *g_max;                                   // or NULL
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load) const {
+  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load, Release release) const {
     RowInfo r = {0, 0, 0, -1};
     if (row < n_rows) r = info[row];
     if (g_max) {
@@ -209,7 +219,7 @@ template <class T> struct GradEpi {
     for (int c = 0; c < HALF; c += 64) {
       float v[64];
       load(c, v);
-      load(c + 32, v + 32);
+      if (c) release();
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
         float2 y = sub_mul2(make_float2(v[i], v[i + 1]), r.from, LOG2E);
@@ -294,42 +304,58 @@ template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t
 template <class T> struct OutEpi {
   Target o;
   int64_t split_rows;                                      // rows between the parts of a split contraction
-  template <class Load> __device__ __forceinline__ void operator()(int row, int col, int split, uint32_t own, Load load) const {
+  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int split, uint32_t own, Load load, Release release) const {
     const int lane = threadIdx.x & 31, row0 = row & ~31;
     const float scale = o.scale();
     Target to = o;
     to.dst = reinterpret_cast<T *>(o.dst) + split * split_rows * o.dst_stride;
-    for (int c = 0; c < HALF; c += 32) {
-      float v[32];
+    for (int c = 0; c < HALF; c += 64) {
+      float v[64];
       load(c, v);
-      const int n = (int)min((int64_t)32, o.n_cols - col - c), rows = (int)min((int64_t)32, o.n_rows - row0);
-      __syncwarp();
+      if (c) release();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) own_write(own_chunk(own, lane, i), f32_vec(v + 4 * i, float{}));
-      __syncwarp();
-      if (n <= 0 || rows <= 0) continue;
-      if (o.vec) {
+      for (int h = 0; h < 64; h += 32) {
+        const int n = (int)min((int64_t)32, o.n_cols - col - c - h), rows = (int)min((int64_t)32, o.n_rows - row0);
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 8 + lane / 4, k = lane % 4 * 8;
-          if (r >= rows || k >= n) continue;
-          float w[8];
-          vec_f32(own_read(own_chunk(own, r, k / 4)), w, float{});
-          vec_f32(own_read(own_chunk(own, r, k / 4 + 1)), w + 4, float{});
-          put8<T>(to, row0 + r, col + c + k, w, min(8, n - k), scale);
-        }
-      } else if (lane < n) {
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r) {
-          const int64_t at = row0 + r, k = col + c + lane;
-          float x = o.scaled(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4), at, scale);
-          if (o.src) {
-            const int64_t from = at * o.src_stride + k;
-            x += o.src_type == TT_F32 ? reinterpret_cast<const float *>(o.src)[from]
-                 : o.src_type == TT_F16 ? to_f32(reinterpret_cast<const __half *>(o.src)[from])
-                                        : to_f32(reinterpret_cast<const __nv_bfloat16 *>(o.src)[from]);
+        for (int i = 0; i < 8; ++i) own_write(own_chunk(own, lane, i), f32_vec(v + h + 4 * i, float{}));
+        __syncwarp();
+        if (n <= 0 || rows <= 0) continue;
+        const int64_t to_col = col + c + h;
+        if (o.vec) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4, k = lane % 4 * 8;
+            if (r >= rows || k >= n) continue;
+            float w[8];
+            vec_f32(own_read(own_chunk(own, r, k / 4)), w, float{});
+            vec_f32(own_read(own_chunk(own, r, k / 4 + 1)), w + 4, float{});
+            put8<T>(to, row0 + r, to_col + k, w, min(8, n - k), scale);
           }
-          reinterpret_cast<T *>(to.dst)[at * o.dst_stride + k] = from_f32<T>(x);
+        } else if (lane < n) {
+          T *q = reinterpret_cast<T *>(to.dst) + row0 * o.dst_stride + to_col + lane;
+          if (rows == 32 && !o.src && !o.row_scale) {
+            // the common case, in few instructions an element (with the general one's 1023 x
+            // 200255 x 641 fp16's dweight took 311 us)
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              *q = from_f32<T>(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4) * scale);
+              q += o.dst_stride;
+            }
+          } else {
+            for (int r = 0; r < rows; ++r) {
+              const int64_t at = row0 + r;
+              float x = o.scaled(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4), at, scale);
+              if (o.src) {
+                const int64_t from = at * o.src_stride + to_col + lane;
+                x += o.src_type == TT_F32 ? reinterpret_cast<const float *>(o.src)[from]
+                     : o.src_type == TT_F16 ? to_f32(reinterpret_cast<const __half *>(o.src)[from])
+                                            : to_f32(reinterpret_cast<const __nv_bfloat16 *>(o.src)[from]);
+              }
+              *q = from_f32<T>(x);
+              q += o.dst_stride;
+            }
+          }
         }
       }
     }
