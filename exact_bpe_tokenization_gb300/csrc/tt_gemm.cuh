@@ -197,7 +197,6 @@ template <bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Gemm g,
            const __grid_constant__ Epi epi) {
-  if (g.only && !g.only[0]) return;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_bar[2 * STAGES + 4];
   __shared__ uint32_t s_tmem;
@@ -206,6 +205,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_rank();
   const uint32_t stages = (saddr(s_raw) + 1023) & ~1023u;
   const uint32_t full = saddr(s_bar), empty = full + 8 * STAGES, done = empty + 8 * STAGES, free_ = done + 16;
+  let_next_start();
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
       bar_init(full + 8 * i, 1);
@@ -227,7 +227,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t *)&s_tmem;
-  const int n_tiles = g.m_tiles * g.n_tiles * g.splits, n_pairs = gridDim.x / 2;
+  wait_for_last();                                        // all else is a matter of this block
+  const int n_tiles = g.only && !g.only[0] ? 0 : g.m_tiles * g.n_tiles * g.splits, n_pairs = gridDim.x / 2;
   bool ok = true;
 
   if (warp == 0 && lane == 0) {
@@ -345,6 +346,8 @@ inline uint32_t idesc_of(bool bf16, bool a_mn, bool b_mn) {
 
 template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
 
+// All launches of a call but its first are chained: a kernel's blocks start, and set
+// themselves up, while the one before ends.
 // D [rows of a][rows of b] = a * b^T over the contraction; with _MN the matrix lies the
 // other way round (its rows are the contraction).  False: an error, which is kept.
 template <bool A_MN, bool B_MN, class Epi>
@@ -375,7 +378,7 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   auto k = k_gemm<A_MN, B_MN, Epi>;
   if (allow_shared<GemmTag<A_MN, B_MN, Epi>>(k, SHARED)) return false;
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
-  k<<<2 * std::min(tiles, SMS / 2), THREADS, SHARED, stream>>>(ma, mb, g, epi);
+  launch_cluster(k, dim3(2 * std::min(tiles, SMS / 2)), THREADS, SHARED, 1, true, stream, ma, mb, g, epi);
   return true;
 }
 

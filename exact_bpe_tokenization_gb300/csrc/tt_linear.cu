@@ -365,6 +365,8 @@ template <class T> struct OutEpi {
 
 // the parts of a split contraction, [split][n_rows][stride] floats, stride a multiple of 8
 template <class T> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
+  let_next_start();
+  wait_for_last();
   const int64_t per = stride / 8, total = o.n_rows * per;
   const float scale = o.scale();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
@@ -372,7 +374,7 @@ template <class T> __global__ void __launch_bounds__(256) k_join(const float *pa
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const float4 *p = reinterpret_cast<const float4 *>(part + row * stride + col);
     const int64_t step = o.n_rows * stride / 4;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
       const float4 a = p[s * step], b = p[s * step + 1];
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
@@ -406,17 +408,63 @@ template <class T> __device__ __forceinline__ void pack8(uint16_t *to, int64_t p
     }
 }
 
-// Operands as TMA can read them: rows of whole 16-byte groups.
-template <class T> __global__ void __launch_bounds__(256) k_pack(const T *x, int64_t n, int dim, int64_t x_stride, uint16_t *out, int stride, bool vec) {
-  const int per = stride / 8;
-  const int64_t total = n * per;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t row = i / per;
-    const int col = (int)(i - row * per) * 8;
-    float v[8];
-    take8(x + row * x_stride + col, v, min(8, dim - col), vec);
-    pack8<T>(out + row * stride + col, n * stride, v);
-  }
+// A matrix as TMA can read it: rows of whole 16-byte groups.
+struct Pack {
+  const void *x;                                           // NULL: it can as it is
+  int64_t rows, stride;
+  int vec;
+  uint16_t *out;                                           // [parts][rows][width]
+};
+struct BeginArgs {
+  Pack hidden, weight;
+  int dim, width, n_vocab;
+  const void *h, *w;                                       // hidden and weight, whose targets' logits go to:
+  int64_t n_rows, h_stride, w_stride;
+  int h_vec, w_vec;
+  const int32_t *targets;
+  float *target_logit;                                     // [n_rows], or NULL: not wanted here
+  int32_t *words;                                          // and words to be cleared
+  int64_t n_words;
+};
+
+template <class T> __device__ __forceinline__ void pack_group(const Pack &p, int64_t i, int dim, int width) {
+  const int per = width / 8;
+  const int64_t row = i / per;
+  const int col = (int)(i - row * per) * 8;
+  float v[8];
+  take8((const T *)p.x + row * p.stride + col, v, min(8, dim - col), p.vec);
+  pack8<T>(p.out + row * width + col, p.rows * width, v);
+}
+
+// What a call begins with: operands laid out, the targets' logits (a warp a row, 0 for
+// padding), words cleared.
+template <class T> __global__ void __launch_bounds__(256) k_begin(BeginArgs a) {
+  let_next_start();
+  const int64_t id = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+  const int lane = threadIdx.x & 31;
+  for (int64_t i = id; i < a.n_words; i += step) a.words[i] = 0;
+  if (a.target_logit)
+    for (int64_t row = id / 32; row < a.n_rows; row += step / 32) {
+      const int32_t t = a.targets[row];
+      float sum = 0;
+      if ((uint32_t)t < (uint32_t)a.n_vocab) {
+        const T *h = (const T *)a.h + row * a.h_stride, *w = (const T *)a.w + t * a.w_stride;
+#pragma unroll 2
+        for (int c = lane * 8; c < a.dim; c += 256) {
+          float x[8], y[8];
+          take8(h + c, x, min(8, a.dim - c), a.h_vec);
+          take8(w + c, y, min(8, a.dim - c), a.w_vec);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(x[i], y[i], sum);
+        }
+      }
+      sum = warp_all(sum, OpSum{});
+      if (lane == 0) a.target_logit[row] = sum;
+    }
+  if (a.hidden.x)
+    for (int64_t i = id; i < a.hidden.rows * (a.width / 8); i += step) pack_group<T>(a.hidden, i, a.dim, a.width);
+  if (a.weight.x)
+    for (int64_t i = id; i < a.weight.rows * (a.width / 8); i += step) pack_group<T>(a.weight, i, a.dim, a.width);
 }
 
 struct RowArgs {
@@ -427,48 +475,29 @@ struct RowArgs {
   float *loss, *lse;
   float *target_logit, *target_power;                      // the latter NULL: no powers
   RowInfo *info;                                           // or NULL: no gradients
-  float *row_scale, *hidden_scale;
+  float *row_scale;
   uint32_t *g_max;                                         // or NULL
   int32_t *only, *status;
-  const void *hidden, *weight;
-  int64_t hidden_stride, weight_stride;
-  int hidden_vec, weight_vec;
-  uint16_t *scaled;                                        // hidden by its scale, [parts][n_rows][width]
+  const void *hidden;
+  int64_t hidden_stride;
+  int hidden_vec;
+  uint16_t *scaled;                                        // hidden by its scale, [parts][n_rows][width], or NULL
   int width;
   uint16_t *g;
   int64_t g_stride, g_part;
   int parts;
 };
 
-// the target's logit of each row, a warp a row (0 for padding)
-template <class T> __global__ void __launch_bounds__(256) k_target(RowArgs a) {
-  const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (row >= a.n_rows) return;
-  const int32_t t = a.targets[row];
-  float sum = 0;
-  if ((uint32_t)t < (uint32_t)a.n_vocab) {
-    const T *h = (const T *)a.hidden + row * a.hidden_stride, *w = (const T *)a.weight + t * a.weight_stride;
-    for (int c = lane * 8; c < a.dim; c += 256) {
-      float x[8], y[8];
-      take8(h + c, x, min(8, a.dim - c), a.hidden_vec);
-      take8(w + c, y, min(8, a.dim - c), a.weight_vec);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], y[i], sum);
-    }
-  }
-  sum = warp_all(sum, OpSum{});
-  if (lane == 0) a.target_logit[row] = sum;
-}
-
 // What G and hidden's scaled copy are made from.  With powers: G is left without the
 // row's factor g / S (S their sum), which dhidden's rows and the copy of hidden for
 // dweight get.  Rows of a loss beyond 41, whose powers leave what is safe, ask for G to
 // be made anew from their maximum and sum, with all of their 256.
-__device__ __forceinline__ void row_info(const RowArgs &a, int row, bool there, float m, float s, float lse, float loss) {
+// Returned is the scale of hidden's copy (none: a row of zeros).
+__device__ __forceinline__ float row_info(const RowArgs &a, int row, bool there, float m, float s, float lse, float loss, bool &none) {
   const float g = a.row_grads ? a.row_grads[row] : 1.f;
   const int t = a.targets[row];
   RowInfo r = {m, __fdividef(1.f, s) * g, g, there && lse != -INF ? t : -1};
-  float row_scale = 1, hidden_scale = r.t >= 0 ? 1.f : 0.f;
+  float row_scale = 1, hidden_scale = 1;
   if (a.target_power && r.t >= 0) {
     if (loss <= 41.f) {
       const float c = a.target_logit[row];
@@ -491,78 +520,88 @@ __device__ __forceinline__ void row_info(const RowArgs &a, int row, bool there, 
   }
   a.info[row] = r;
   a.row_scale[row] = row_scale;
-  a.hidden_scale[row] = hidden_scale;
   if (a.g_max && r.t >= 0 && fabsf(g) < INF) atomicMax(a.g_max, __float_as_uint(fabsf(g)));
+  none = r.t < 0;
+  return hidden_scale;
 }
 
-// R rows a block: the parts of a row are joined by 256 / R threads
-template <int R> __global__ void __launch_bounds__(256) k_finish(RowArgs a) {
+// R rows a block: the parts of a row are joined by 256 / R threads (or its lse is the
+// caller's), and then hidden's rows copied by their scale for dweight (padding rows as
+// zeros, whatever they hold).
+template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArgs a) {
   constexpr int EACH = 256 / R;
   __shared__ float2 box[256];
+  __shared__ float s_scale[R];
+  __shared__ int s_none[R];
+  let_next_start();
+  wait_for_last();
   const int r = threadIdx.x % R, j = threadIdx.x / R, row = blockIdx.x * R + r;
   float m = LOWEST, s = 0;
-  auto join = [&](float2 p) {
-    const float nm = fmaxf(m, p.x);
-    s = s * ex2((m - nm) * LOG2E) + p.y * ex2((p.x - nm) * LOG2E);
-    m = nm;
-  };
-  if (row < a.n_rows) {
-    const float2 *p = a.part + row;
-    int i = j;
-    for (; i + 3 * EACH < a.n_parts; i += 4 * EACH) {
-      float2 q[4];
+  if (a.lse_in) {
+    if (row < a.n_rows) m = a.lse_in[row];
+    s = 1;
+  } else {
+    auto join = [&](float2 p) {
+      const float nm = fmaxf(m, p.x);
+      s = s * ex2((m - nm) * LOG2E) + p.y * ex2((p.x - nm) * LOG2E);
+      m = nm;
+    };
+    if (row < a.n_rows) {
+      const float2 *p = a.part + row;
+      int i = j;
+      for (; i + 7 * EACH < a.n_parts; i += 8 * EACH) {
+        float2 q[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) q[u] = p[(int64_t)(i + u * EACH) * a.n_rows];
+        for (int u = 0; u < 8; ++u) q[u] = p[(int64_t)(i + u * EACH) * a.n_rows];
+        float top = q[0].x, sum = 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) join(q[u]);
+        for (int u = 1; u < 8; ++u) top = fmaxf(top, q[u].x);
+        top = fmaxf(top, LOWEST);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += q[u].y * ex2((q[u].x - top) * LOG2E);
+        join(make_float2(top, sum));
+      }
+      for (; i < a.n_parts; i += EACH) join(p[(int64_t)i * a.n_rows]);
     }
-    for (; i < a.n_parts; i += EACH) join(p[(int64_t)i * a.n_rows]);
-  }
-  box[threadIdx.x] = make_float2(m, s);
-  for (int k = EACH / 2; k; k /= 2) {
-    __syncthreads();
-    if (j < k) {
-      join(box[threadIdx.x + k * R]);
-      box[threadIdx.x] = make_float2(m, s);
+    box[threadIdx.x] = make_float2(m, s);
+    for (int k = EACH / 2; k; k /= 2) {
+      __syncthreads();
+      if (j < k) {
+        join(box[threadIdx.x + k * R]);
+        box[threadIdx.x] = make_float2(m, s);
+      }
     }
   }
-  if (j || row >= a.n_rows) return;
-  const float log_s = logf(s), lse = m + log_s;
-  const int32_t t = a.targets[row];
-  const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
-  if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
-  const float loss = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
-  if (a.lse) a.lse[row] = lse;
-  a.loss[row] = loss;
-  if (a.info) row_info(a, row, there, m, s, lse, loss);
-}
-
-// the same from an lse that the caller has
-__global__ void __launch_bounds__(256) k_info(RowArgs a) {
-  const int row = blockIdx.x * 256 + threadIdx.x;
-  if (row >= a.n_rows) return;
-  const float lse = a.lse_in[row];
-  const int32_t t = a.targets[row];
-  const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
-  if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
-  row_info(a, row, there, lse, 1.f, lse, 0.f);
-}
-
-// Hidden by its rows' scale, for dweight (padding rows as zeros, whatever they hold); a
-// warp a row.
-template <class T> __global__ void __launch_bounds__(256) k_hidden(RowArgs a) {
-  const int row = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (row >= a.n_rows) return;
-  const float scale = a.hidden_scale[row];
-  const T *h = (const T *)a.hidden + row * a.hidden_stride;
-  uint16_t *to = a.scaled + (int64_t)row * a.width;
-  const bool none = a.info[row].t < 0;
-  for (int c = lane * 8; c < a.width; c += 256) {
+  if (j == 0 && row < a.n_rows) {
+    const float log_s = logf(s), lse = m + log_s;
+    const int32_t t = a.targets[row];
+    const bool there = (uint32_t)t < (uint32_t)a.n_vocab;
+    if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
+    float loss = 0;
+    if (!a.lse_in) {
+      loss = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
+      if (a.lse) a.lse[row] = lse;
+      a.loss[row] = loss;
+    }
+    if (a.info) {
+      bool none;
+      s_scale[r] = row_info(a, row, there, m, s, lse, loss, none);
+      s_none[r] = none;
+    }
+  }
+  if (!a.scaled) return;
+  __syncthreads();
+  const int per = a.width / 8, rows = min(R, a.n_rows - blockIdx.x * R);
+  for (int i = threadIdx.x; i < rows * per; i += 256) {
+    const int k = i / per, c = (i - k * per) * 8;
+    const int64_t at = blockIdx.x * R + k;
     float v[8];
-    take8(h + c, v, min(8, a.dim - c), a.hidden_vec);
+    take8((const T *)a.hidden + at * a.hidden_stride + c, v, min(8, a.dim - c), a.hidden_vec);
+    const float scale = s_scale[k];
+    const bool none = s_none[k];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = none ? 0.f : v[i] * scale;
-    pack8<T>(to + c, (int64_t)a.n_rows * a.width, v);
+    for (int u = 0; u < 8; ++u) v[u] = none ? 0.f : v[u] * scale;
+    pack8<T>(a.scaled + at * a.width + c, (int64_t)a.n_rows * a.width, v);
   }
 }
 
@@ -588,6 +627,7 @@ struct Call {
 struct Plan {
   int64_t chunk, width, g_stride;                          // rows; columns of packed operands and of G
   int split_h, split_w;
+  int64_t words;                                           // 1 and one a tile row, for each chunk
   int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
 };
 
@@ -616,8 +656,9 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   p.hidden = take(pack_h ? n * p.width * 2 * parts : 0);
   p.weight = take(pack_w ? vocab * p.width * 2 * parts : 0);
   p.part = take(halves * 8 * p.chunk);
-  p.rows = take(4 * 4 * p.chunk);                          // target_logit, target_power, row_scale, hidden_scale
-  p.word = take(4 * (1 + (p.chunk + TILE - 1) / TILE));
+  p.rows = take(4 * (n + 2 * p.chunk));                    // target_logit of all rows, target_power, row_scale
+  p.words = (1 + (p.chunk + TILE - 1) / TILE) * ((n + p.chunk - 1) / p.chunk);
+  p.word = take(4 * p.words);
   if (grad) {
     p.info = take(sizeof(RowInfo) * p.chunk);
     p.scaled = take(dw ? p.chunk * p.width * 2 * parts : 0);
@@ -639,17 +680,9 @@ inline int vec_of(const void *p, int64_t stride, int32_t type) {
 inline bool rows_tma(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 inline bool needs_pack(int32_t type, const void *p, int64_t stride) { return type == TT_F32 || !rows_tma(p, stride); }
 
-void pack(int32_t type, const void *x, int64_t n, int64_t dim, int64_t stride, void *out, int64_t width, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)std::min<int64_t>((n * (width / 8) + 255) / 256, SMS * 16);
-  with_type(type, [&](auto t) {
-    using T = decltype(t);
-    k_pack<T><<<blocks, 256, 0, stream>>>((const T *)x, n, (int)dim, stride, (uint16_t *)out, (int)width, vec_of(x, stride, type));
-  });
-}
-
 template <class T> void join(const float *part, int splits, int64_t stride, const Target &o, cudaStream_t stream) {
   const unsigned blocks = (unsigned)std::min<int64_t>((o.n_rows * (stride / 8) + 255) / 256, SMS * 16);
-  k_join<T><<<blocks, 256, 0, stream>>>(part, splits, stride, o);
+  launch_cluster(k_join<T>, dim3(blocks), 256, 0, 1, true, stream, part, splits, stride, o);
 }
 
 // a gradient: the product a * b^T (their contraction lies across b's rows), to o
@@ -680,11 +713,11 @@ template <class T> bool make_g(const Matrix &h, const Matrix &w, const Matrix &g
   return run_gemm<false, false>(bf16, h, w, 1, 16, e, r.status, stream, r.only);
 }
 
-void finish(const RowArgs &r, cudaStream_t stream) {
+template <class T> void finish(const RowArgs &r, cudaStream_t stream) {
   const int n = r.n_rows;
-  if (n >= 4096) k_finish<32><<<(n + 31) / 32, 256, 0, stream>>>(r);
-  else if (n >= 1024) k_finish<8><<<(n + 7) / 8, 256, 0, stream>>>(r);
-  else k_finish<1><<<n, 256, 0, stream>>>(r);
+  if (n >= 4096) launch_cluster(k_finish<T, 8>, dim3((n + 7) / 8), 256, 0, 1, true, stream, r);
+  else if (n >= 512) launch_cluster(k_finish<T, 4>, dim3((n + 3) / 4), 256, 0, 1, true, stream, r);
+  else launch_cluster(k_finish<T, 1>, dim3(n), 256, 0, 1, true, stream, r);
 }
 
 bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) {
@@ -694,12 +727,13 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
   // a 16-bit float has no range for powers: the product runs twice, for lse and for G
   const bool powers = grad && !c.lse_in && c.type != TT_F16;
   Matrix h{c.hidden, c.n, c.dim, c.hidden_stride, parts, 8}, w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
+  BeginArgs begin{};
   if (needs_pack(c.type, c.hidden, c.hidden_stride)) {
-    pack(c.type, c.hidden, c.n, c.dim, c.hidden_stride, ws + p.hidden, p.width, stream);
+    begin.hidden = Pack{c.hidden, c.n, c.hidden_stride, vec_of(c.hidden, c.hidden_stride, c.type), (uint16_t *)(ws + p.hidden)};
     h = Matrix{ws + p.hidden, c.n, c.dim, p.width, parts, c.n * p.width};
   }
   if (needs_pack(c.type, c.weight, c.weight_stride)) {
-    pack(c.type, c.weight, c.vocab, c.dim, c.weight_stride, ws + p.weight, p.width, stream);
+    begin.weight = Pack{c.weight, c.vocab, c.weight_stride, vec_of(c.weight, c.weight_stride, c.type), (uint16_t *)(ws + p.weight)};
     w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
   }
   RowArgs r{};
@@ -708,14 +742,10 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
   r.dim = (int)c.dim;
   r.part = (float2 *)(ws + p.part);
   r.target_logit = (float *)(ws + p.rows);
-  r.row_scale = r.target_logit + 2 * p.chunk;
-  r.hidden_scale = r.target_logit + 3 * p.chunk;
+  r.row_scale = r.target_logit + c.n + p.chunk;
   r.status = c.status;
-  r.weight = c.weight;
   r.hidden_stride = c.hidden_stride;
-  r.weight_stride = c.weight_stride;
   r.hidden_vec = vec_of(c.hidden, c.hidden_stride, c.type);
-  r.weight_vec = vec_of(c.weight, c.weight_stride, c.type);
   r.width = (int)p.width;
   r.parts = parts;
   r.g_stride = p.g_stride;
@@ -726,16 +756,42 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     if (c.dweight) r.scaled = (uint16_t *)(ws + p.scaled);
     if (c.type == TT_F16) r.g_max = (uint32_t *)(ws + p.word);
     if (powers) {
-      r.target_power = r.target_logit + p.chunk;
+      r.target_power = r.target_logit + c.n;
       r.only = (int32_t *)(ws + p.word);
     }
   }
+  begin.dim = (int)c.dim;
+  begin.width = (int)p.width;
+  begin.n_vocab = (int)c.vocab;
+  begin.h = c.hidden;
+  begin.w = c.weight;
+  begin.n_rows = c.n;
+  begin.h_stride = c.hidden_stride;
+  begin.w_stride = c.weight_stride;
+  begin.h_vec = r.hidden_vec;
+  begin.w_vec = vec_of(c.weight, c.weight_stride, c.type);
+  begin.targets = c.targets;
+  if (powers) begin.target_logit = r.target_logit;
+  if (r.g_max || r.only) {
+    begin.words = (int32_t *)(ws + p.word);
+    begin.n_words = p.words;
+  }
+  const int64_t units = std::max(std::max(begin.hidden.x ? c.n * (p.width / 8) : 0, begin.weight.x ? c.vocab * (p.width / 8) : 0),
+                                 std::max(powers ? c.n * 32 : 0, begin.n_words));
+  if (units && c.n)
+    with_type(c.type, [&](auto t) {
+      k_begin<decltype(t)><<<(unsigned)std::min<int64_t>((units + 255) / 256, SMS * 16), 256, 0, stream>>>(begin);
+    });
   for (int64_t row0 = 0; row0 < c.n; row0 += p.chunk) {
     const int n = (int)std::min(p.chunk, c.n - row0);
     Matrix hc = h;
     hc.p = (const uint16_t *)h.p + row0 * h.stride;
     hc.rows = n;
+    int32_t *words = (int32_t *)(ws + p.word) + row0 / p.chunk * (1 + (p.chunk + TILE - 1) / TILE);
+    if (r.g_max) r.g_max = (uint32_t *)words;
+    if (r.only) r.only = words;
     r.n_rows = n;
+    r.target_logit = (float *)(ws + p.rows) + row0;
     r.hidden = (const uint8_t *)c.hidden + row0 * c.hidden_stride * size;
     r.targets = c.targets + row0;
     r.row_grads = c.row_grads ? c.row_grads + row0 : nullptr;
@@ -743,32 +799,22 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     r.loss = c.loss ? c.loss + row0 : nullptr;
     r.lse = c.lse ? c.lse + row0 : nullptr;
     const Matrix g{r.g, n, c.vocab, p.g_stride, parts, r.g_part};
-    if ((r.g_max || r.only) && cudaMemsetAsync(ws + p.word, 0, 4 * (1 + (n + TILE - 1) / TILE), stream) != cudaSuccess) return false;
     bool ok = true;
-    if (c.lse_in) {
-      k_info<<<(n + 255) / 256, 256, 0, stream>>>(r);
-    } else if (powers) {
-      auto run = [&](auto t) {
-        using T = decltype(t);
-        k_target<T><<<(n + 7) / 8, 256, 0, stream>>>(r);
-        ok = make_powers<T>(hc, w, g, r, stream);
-      };
-      if (c.type == TT_F32) run(float{});
-      else run(__nv_bfloat16{});
-      if (!ok) return false;
-      finish(r, stream);
-    } else {
+    if (powers) {
+      if (c.type == TT_F32) ok = make_powers<float>(hc, w, g, r, stream);
+      else ok = make_powers<__nv_bfloat16>(hc, w, g, r, stream);
+    } else if (!c.lse_in) {
       const StatsEpi e{n, (int)c.vocab, r.targets, r.part, r.target_logit};
-      if (!run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream)) return false;
-      finish(r, stream);
+      ok = run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream);
     }
-    if (!grad) continue;
+    if (!ok) return false;
     with_type(c.type, [&](auto t) {
       using T = decltype(t);
-      ok = make_g<T>(hc, w, g, r, stream);
-      if (c.dweight) k_hidden<T><<<(n + 7) / 8, 256, 0, stream>>>(r);
+      finish<T>(r, stream);
+      if (grad) ok = make_g<T>(hc, w, g, r, stream);
     });
     if (!ok) return false;
+    if (!grad) continue;
     float *sums = (float *)(ws + p.sums);
     if (c.dhidden) {
       const Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * size, c.dhidden_stride, nullptr, 0, TT_F32, r.g_max,
