@@ -367,7 +367,7 @@ template <class T> struct OutEpi {
 template <class T> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
   let_next_start();
   wait_for_last();
-  const int64_t per = stride / 8, total = o.n_rows * per;
+  const int64_t per = (o.n_cols + 7) / 8, total = o.n_rows * per;
   const float scale = o.scale();
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const int64_t row = i / per, col = (i - row * per) * 8;
@@ -380,7 +380,7 @@ template <class T> __global__ void __launch_bounds__(256) k_join(const float *pa
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    if (col < o.n_cols) put8<T>(o, row, col, v, (int)min((int64_t)8, o.n_cols - col), scale);
+    put8<T>(o, row, col, v, (int)min((int64_t)8, o.n_cols - col), scale);
   }
 }
 
@@ -636,7 +636,7 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   const int parts = type == TT_F32 ? 3 : 1;
   const bool grad = dh || dw;
   n = std::max<int64_t>(n, 1);
-  p.width = up(dim, 8);
+  p.width = up(dim, 64);                                   // whole 128-byte lines: a box's rows are one each
   p.g_stride = up(vocab, 64);
   const int64_t halves = (vocab + HALF - 1) / HALF;
   int64_t most = PARTIALS / (halves * 8);
@@ -681,7 +681,7 @@ inline bool rows_tma(const void *p, int64_t stride) { return aligned(p, 16) && s
 inline bool needs_pack(int32_t type, const void *p, int64_t stride) { return type == TT_F32 || !rows_tma(p, stride); }
 
 template <class T> void join(const float *part, int splits, int64_t stride, const Target &o, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)std::min<int64_t>((o.n_rows * (stride / 8) + 255) / 256, SMS * 16);
+  const unsigned blocks = (unsigned)std::min<int64_t>((o.n_rows * ((o.n_cols + 7) / 8) + 255) / 256, SMS * 16);
   launch_cluster(k_join<T>, dim3(blocks), 256, 0, 1, true, stream, part, splits, stride, o);
 }
 
