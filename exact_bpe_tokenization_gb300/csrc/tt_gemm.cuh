@@ -171,25 +171,39 @@ template <bool MN> struct Operand {
 
 // tile number -> its place: `group` tile rows are passed through together, column by
 // column, so that what runs at a time shares operands of both sides
-struct Place { int m, n, split; };
-__device__ __forceinline__ Place place_of(const Gemm &g, int t) {
-  const int per = g.m_tiles * g.n_tiles;
+struct Place {
+  int t, m, n, split;                                     // t: the tile's number, n_tiles for none
+  int first, last;                                        // blocks of the contraction
+};
+// the next tile of a pair of SMs at or behind number t.  (A thread that hands out work asks
+// for the next tile while the present one is computed: the divisions take longer than a block.)
+__device__ __forceinline__ Place place_of(const Gemm &g, int t, int n_tiles, int step) {
   Place p;
-  p.split = t / per;
-  t -= p.split * per;
-  const int first = t / (g.group * g.n_tiles) * g.group, rows = min(g.group, g.m_tiles - first);
-  t -= first * g.n_tiles;
-  p.m = first + t % rows;
-  p.n = t / rows;
+  p.split = p.first = 0;
+  p.last = g.k_blocks;
+  for (;; t += step) {
+    p.t = min(t, n_tiles);
+    if (t >= n_tiles) break;
+    int i = t;
+    const int per = g.m_tiles * g.n_tiles;
+    if (g.splits > 1) {
+      p.split = i / per;
+      i -= p.split * per;
+      p.first = (int)((int64_t)g.k_blocks * p.split / g.splits);
+      p.last = (int)((int64_t)g.k_blocks * (p.split + 1) / g.splits);
+    }
+    const int first = i / (g.group * g.n_tiles) * g.group, rows = min(g.group, g.m_tiles - first);
+    i -= first * g.n_tiles;
+    p.n = i / rows;
+    p.m = first + i - p.n * rows;
+    if (!g.only || g.only[1 + p.m]) break;
+  }
   return p;
 }
-__device__ __forceinline__ int2 blocks_of(const Gemm &g, int split) {
-  return make_int2((int)((int64_t)g.k_blocks * split / g.splits), (int)((int64_t)g.k_blocks * (split + 1) / g.splits));
-}
 
-// Epi is called by the epilogue's warps as epi(row, column, split, own, load, release): the
+// Epi is called by the epilogue's warps as epi(row, column, split, own, begun, load, release): the
 // row of the result that a thread has (consecutive ones in a warp), the first of the 128
-// columns that it reads, the warp's own shared memory, load(c, v), which brings 64 of the
+// columns that it reads, the warp's own shared memory, what epi.begin(row) gave before the tile was there, load(c, v), which brings 64 of the
 // columns from the c-th on, and release(), which follows the last of them: the next
 // products may overwrite them.  Both are called by whole warps.  epi.end() comes behind
 // the last tile.
@@ -235,17 +249,14 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     // copies: a stage is free when the products that read it are done
     int stage = 0;
     uint32_t phase = 1;
-    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs) {
-      const Place p = place_of(g, t);
-      if (g.only && !g.only[1 + p.m]) continue;
-      const int2 kb = blocks_of(g, p.split);
+    for (Place p = place_of(g, blockIdx.x / 2, n_tiles, n_pairs), next; ok && p.t < n_tiles; p = next) {
       const int ra = p.m * TILE + rank * HALF, rb = p.n * TILE + rank * HALF;
       // Rows that are not there are left out: what lies in their place enters only results
       // of theirs.  (TMA reads the border again for each row beyond it: 152 SMs at one
       // line of a single row took 124 us for 1 x 100256 x 2048 instead of 86.)
       const uint32_t bytes = (1 + (p.m * TILE + HALF < g.rows_a)) * g.box_a + (1 + (p.n * TILE + HALF < g.rows_b)) * (STAGE_BYTES / 2);
       for (int i = 0; ok && i < g.pairs; ++i) {
-        for (int k = kb.x; k < kb.y; ++k) {
+        for (int k = p.first; k < p.last; ++k) {
           if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) break;
           if (rank == 0) bar_expect(full + 8 * stage, bytes);
           const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
@@ -255,6 +266,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
             stage = 0;
             phase ^= 1;
           }
+          if (i == 0 && k == p.first) next = place_of(g, p.t + n_pairs, n_tiles, n_pairs);
         }
       }
     }
@@ -262,11 +274,8 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     int i = 0;
-    for (int t = blockIdx.x / 2; ok && t < n_tiles; t += n_pairs) {
-      const Place p = place_of(g, t);
-      if (g.only && !g.only[1 + p.m]) continue;
-      const int2 kb = blocks_of(g, p.split);
-      const int count = (kb.y - kb.x) * g.pairs;
+    for (Place p = place_of(g, blockIdx.x / 2, n_tiles, n_pairs), next; ok && p.t < n_tiles; p = next) {
+      const int count = (p.last - p.first) * g.pairs;
       if (!(ok = bar_wait(free_ + 8 * (i & 1), (i >> 1 & 1) ^ 1, &s_dead))) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + (i & 1) * TILE;
@@ -282,6 +291,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
           stage = 0;
           phase ^= 1;
         }
+        if (k == 0) next = place_of(g, p.t + n_pairs, n_tiles, n_pairs);
       }
       if (ok) commit(done + 8 * (i & 1));
       ++i;
@@ -290,9 +300,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     int i = 0;
     const uint32_t own = stages + STAGES * STAGE_BYTES + (warp - 4) * OWN_BYTES;
-    for (int t = blockIdx.x / 2; t < n_tiles; t += n_pairs) {
-      const Place p = place_of(g, t);
-      if (g.only && !g.only[1 + p.m]) continue;
+    for (Place p = place_of(g, blockIdx.x / 2, n_tiles, n_pairs), next; p.t < n_tiles; p = next) {
+      next = place_of(g, p.t + n_pairs, n_tiles, n_pairs);
+      const int row = p.m * TILE + (int)rank * HALF + quarter * 32 + lane;
+      const auto begun = epi.begin(row);
       ok = bar_wait(done + 8 * (i & 1), i >> 1 & 1, &s_dead);
       if (!__all_sync(~0u, ok)) {
         ok = false;
@@ -300,7 +311,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t at = tmem + (i & 1) * TILE + half * HALF + ((uint32_t)(quarter * 32) << 16);
-      epi(p.m * TILE + (int)rank * HALF + quarter * 32 + lane, p.n * TILE + half * HALF, p.split, own,
+      epi(row, p.n * TILE + half * HALF, p.split, own, begun,
           [&](int c, float v[64]) {
             tmem_load32(at + c, v);
             tmem_load32(at + c + 32, v + 32);

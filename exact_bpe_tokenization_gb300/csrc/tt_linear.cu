@@ -113,9 +113,10 @@ struct StatsEpi {
   const int32_t *targets;
   float2 *part;                                            // [column halves][n_rows]
   float *target_logit;                                     // [n_rows]
-  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t, Load load, Release release) const {
+  __device__ __forceinline__ int begin(int row) const { return row < n_rows ? targets[row] : -1; }
+  template <class Load, class Release>
+  __device__ __forceinline__ void operator()(int row, int col, int, uint32_t, int t, Load load, Release release) const {
     const bool mine = row < n_rows;
-    const int t = mine ? targets[row] : -1;
     float m = LOWEST;
     float2 s[2] = {{0, 0}, {0, 0}};
     for (int c = 0; c < HALF; c += 64) {
@@ -147,11 +148,14 @@ template <class T> struct PowersEpi {
   const float *from;                                       // [n_rows] c
   float2 *part;                                            // [column halves][n_rows]
   float *target_power;                                     // [n_rows]
-  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load, Release release) const {
+  struct Row { int t; float c; };
+  __device__ __forceinline__ Row begin(int row) const { return row < n_rows ? Row{targets[row], from[row]} : Row{-1, 0}; }
+  template <class Load, class Release>
+  __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Row r, Load load, Release release) const {
     const bool mine = row < n_rows;
-    const int t = mine ? targets[row] : -1;
+    const int t = r.t;
     const bool there = (uint32_t)t < (uint32_t)n_cols;
-    const float c0 = mine ? from[row] : 0.f;
+    const float c0 = r.c;
     float2 s[2] = {{0, 0}, {0, 0}}, p;
     for (int c = 0; c < HALF; c += 64) {
       float v[64];
@@ -208,7 +212,7 @@ template <class T> struct GradEpi {
   int n_rows, n_cols;
   const RowInfo *info;
   const uint32_t *g_max;                                   // or NULL
-  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, Load load, Release release) const {
+  __device__ __forceinline__ RowInfo begin(int row) const {
     RowInfo r = {0, 0, 0, -1};
     if (row < n_rows) r = info[row];
     if (g_max) {
@@ -216,6 +220,10 @@ template <class T> struct GradEpi {
       r.mul *= up;
       r.g *= up;
     }
+    return r;
+  }
+  template <class Load, class Release>
+  __device__ __forceinline__ void operator()(int row, int col, int, uint32_t own, RowInfo r, Load load, Release release) const {
     for (int c = 0; c < HALF; c += 64) {
       float v[64];
       load(c, v);
@@ -304,9 +312,10 @@ template <class T> __device__ __forceinline__ void put8(const Target &o, int64_t
 template <class T> struct OutEpi {
   Target o;
   int64_t split_rows;                                      // rows between the parts of a split contraction
-  template <class Load, class Release> __device__ __forceinline__ void operator()(int row, int col, int split, uint32_t own, Load load, Release release) const {
+  __device__ __forceinline__ float begin(int) const { return o.scale(); }
+  template <class Load, class Release>
+  __device__ __forceinline__ void operator()(int row, int col, int split, uint32_t own, float scale, Load load, Release release) const {
     const int lane = threadIdx.x & 31, row0 = row & ~31;
-    const float scale = o.scale();
     Target to = o;
     to.dst = reinterpret_cast<T *>(o.dst) + split * split_rows * o.dst_stride;
     for (int c = 0; c < HALF; c += 64) {
