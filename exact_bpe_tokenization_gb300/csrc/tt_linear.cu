@@ -372,24 +372,31 @@ template <class T> struct OutEpi {
   __device__ __forceinline__ void end() const {}
 };
 
-// the parts of a split contraction, [split][n_rows][stride] floats, stride a multiple of 8
-template <class T> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
+// The parts of a split contraction, [split][n_rows][stride] floats, stride a multiple of
+// 8: eight columns by SHARE threads, which have some of the parts each.
+template <class T, int SHARE> __global__ void __launch_bounds__(256) k_join(const float *part, int splits, int64_t stride, Target o) {
   let_next_start();
   wait_for_last();
+  constexpr int EACH = 256 / SHARE;
   const int64_t per = (o.n_cols + 7) / 8, total = o.n_rows * per;
   const float scale = o.scale();
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t row = i / per, col = (i - row * per) * 8;
+  const int share = threadIdx.x % SHARE;
+  const int64_t step = o.n_rows * stride / 4;
+  for (int64_t i0 = (int64_t)blockIdx.x * EACH; i0 < total; i0 += (int64_t)gridDim.x * EACH) {
+    const int64_t i = min(i0 + threadIdx.x / SHARE, total - 1), row = i / per, col = (i - row * per) * 8;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const float4 *p = reinterpret_cast<const float4 *>(part + row * stride + col);
-    const int64_t step = o.n_rows * stride / 4;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
+#pragma unroll 4
+    for (int s = share; s < splits; s += SHARE) {
       const float4 a = p[s * step], b = p[s * step + 1];
       v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    put8<T>(o, row, col, v, (int)min((int64_t)8, o.n_cols - col), scale);
+#pragma unroll
+    for (int o = SHARE / 2; o; o /= 2)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += __shfl_xor_sync(~0u, v[j], o);
+    if (share == 0 && i0 + threadIdx.x / SHARE < total) put8<T>(o, row, col, v, (int)min((int64_t)8, o.n_cols - col), scale);
   }
 }
 
@@ -689,9 +696,16 @@ inline int vec_of(const void *p, int64_t stride, int32_t type) {
 inline bool rows_tma(const void *p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
 inline bool needs_pack(int32_t type, const void *p, int64_t stride) { return type == TT_F32 || !rows_tma(p, stride); }
 
+// Few columns are few threads, which wait for one part after the other: four share them
+// (64 x 64 in 23 parts: 9 us, and 5 with four; 2047 x 1024 in 2 parts: 8, and 13 with four).
 template <class T> void join(const float *part, int splits, int64_t stride, const Target &o, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)std::min<int64_t>((o.n_rows * ((o.n_cols + 7) / 8) + 255) / 256, SMS * 16);
-  launch_cluster(k_join<T>, dim3(blocks), 256, 0, 1, true, stream, part, splits, stride, o);
+  const int64_t groups = o.n_rows * ((o.n_cols + 7) / 8);
+  auto run = [&](auto k, int share) {
+    const unsigned blocks = (unsigned)std::min<int64_t>((groups * share + 255) / 256, SMS * 16);
+    launch_cluster(k, dim3(blocks), 256, 0, 1, true, stream, part, splits, stride, o);
+  };
+  if (splits >= 8 && groups < SMS * 256) run(k_join<T, 4>, 4);
+  else run(k_join<T, 1>, 1);
 }
 
 // a gradient: the product a * b^T (their contraction lies across b's rows), to o
