@@ -10,10 +10,10 @@
 // memory of a cluster of blocks, summed on the way with a running maximum, and
 // turned into gradients from there.  The teacher's entries (at most 1024) stay beside
 // it: each block has their shares q, and the logits of those that lie in its part of
-// the row.  The gradient of the whole part is written first, without q; behind a
-// barrier of the block the entries' places are written once more.  An ID that occurs
-// more than once belongs to its first entry, which a small hash table in shared memory
-// finds: that entry adds the shares up, in their order.
+// the row.  The gradient of the whole part is written first, without q, and each thread
+// then writes the entries' places among those that it wrote once more: lists say which
+// those are.  (By the threads that had the entries, behind a barrier, 4096 x 100256 bf16
+// with 64 entries took 326 us; 302 so.)
 #include <algorithm>
 
 #include "tt_rows.cuh"
@@ -24,7 +24,6 @@ namespace {
 
 constexpr int SPACE = 112 * 1024;                // bytes of shared memory of a block: two blocks an SM
 constexpr int HELD = 104 * 1024;                 // the most of them for a row
-constexpr int TWICE = 1 << 30;                   // marks a slot's ID that more than one entry has
 constexpr int U = 4;                             // vectors a thread takes at a time
 constexpr int UC = 4, AHEAD = 4;                 // vectors a group of copies, groups ahead
 
@@ -33,7 +32,7 @@ struct DistillArgs {
   const int32_t *ids;
   const void *values;
   int32_t values_type;
-  int k, slots;                                  // entries a row, slots of the hash table (0: no gradient)
+  int k;                                         // entries a row
   float inv_t, c;                                // 1 / T and log2(e) / T
   float *loss, *lse_out;
   const float *lse_in, *row_grads;
@@ -87,10 +86,10 @@ __global__ void __launch_bounds__(THREADS, (GRAD && THREADS == 256 ? 1024 : 1536
   extern __shared__ uint4 s_row[];
   int32_t *s_id = reinterpret_cast<int32_t *>(s_row + a.held);              // [k] the entries' IDs, -1: none
   float *s_q = reinterpret_cast<float *>(s_id + a.k), *s_x = s_q + a.k;     // [k] shares and logits
-  int32_t *s_key = reinterpret_cast<int32_t *>(s_x + a.k), *s_first = s_key + a.slots;
+  int32_t *s_next = reinterpret_cast<int32_t *>(s_x + a.k);                 // [k] with the gradient: the next one in a thread's list
   __shared__ float2 s_warp[2][WARPS];
   __shared__ float2 s_blocks[8], s_terms[8 * WARPS];                        // what blocks tell all others, and warps the first block
-  __shared__ int s_twice;
+  __shared__ int32_t s_list[THREADS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
   if (GRAD != 2 && a.cluster > 1) cluster_arrive();
@@ -139,11 +138,7 @@ __global__ void __launch_bounds__(THREADS, (GRAD && THREADS == 256 ? 1024 : 1536
     s_q[i] = value;
     if (id >= 0) teacher.add(value);
   };
-  if (tid == 0) s_twice = 0;
-  for (int i = tid; i < a.slots; i += THREADS) {
-    s_key[i] = -1;
-    s_first[i] = 1 << 30;
-  }
+  if (GRAD) s_list[tid] = -1;
   if (GRAD != 2) {
     if (GRAD == 1)
       groups<THREADS>(0, n_held, UC, [&](int v0, auto whole) {
@@ -204,35 +199,22 @@ __global__ void __launch_bounds__(THREADS, (GRAD && THREADS == 256 ? 1024 : 1536
                      : id >= lo && (id - lo) / E < n_held ? to_f32(reinterpret_cast<const T *>(s_row)[id - lo])
                                                           : to_f32(l[id]);
     s_x[i] = xi;
+    if (GRAD) {
+      // the entry goes to the thread that will write its place in the gradient
+      const int v = (id - lo) / E;
+      const int owner = id >= lo && id < hi ? (v < n_held ? v : v - n_held) % THREADS : id < part.lead ? id : 16 + id - part.lead - part.vecs * E;
+      s_next[i] = atomicExch(&s_list[owner], i);
+    }
     if (GRAD != 2 && q != 0) {
       terms.x += q * (above * a.inv_t - log_mass - (xi - mine.x) * a.inv_t);
       terms.y += q;
     }
   }
-  // An ID's slot is claimed by its first entry (while the cluster's blocks meet).
-  auto claim = [&]() {
-    for (int i = tid; i < a.k; i += THREADS) {
-      const int id = s_id[i];
-      if (id < 0 || !in_part(id)) continue;
-      int at = (int)((uint32_t)id * 2654435761u >> 16) & (a.slots - 1);
-      for (int tries = 0; tries < a.slots; ++tries) {                       // (half of them at most are taken)
-        const int old = atomicCAS(&s_key[at], -1, id);
-        if (old == -1 || (old & ~TWICE) == id) {
-          atomicMin(&s_first[at], i);
-          if (old == id) s_key[at] = id | TWICE;
-          if (old != -1) s_twice = 1;
-          break;
-        }
-        at = (at + 1) & (a.slots - 1);
-      }
-    }
-  };
-
-  float lse, from, log_s = 0, inverse = 1.f;                // probabilities are 2^(c (l - from)) * inverse
+  float lse, from, log_s = 0, inverse = 1.f;     // probabilities are 2^(c (l - from)) * inverse
   if (GRAD == 2) {
     lse = a.lse_in[row];
     from = 0;
-    claim();
+    __syncthreads();                             // the lists are complete
   } else {
     if (warp * 32 < a.k) terms = make_float2(warp_sum(terms.x), warp_sum(terms.y));
     if (a.cluster > 1) {
@@ -240,12 +222,10 @@ __global__ void __launch_bounds__(THREADS, (GRAD && THREADS == 256 ? 1024 : 1536
       if (tid < a.cluster) *of_block(&s_blocks[rank], tid) = mine;
       if (lane == 0) *of_block(&s_terms[rank * WARPS + warp], 0) = terms;
       cluster_arrive();
-      if (GRAD) claim();
       cluster_wait();
     } else {
       if (tid == 0) s_blocks[0] = mine;
       if (lane == 0) s_terms[warp] = terms;
-      if (GRAD) claim();
       __syncthreads();
     }
     const float2 all = join_all<8>(s_blocks, a.cluster, a.c);
@@ -320,23 +300,22 @@ __global__ void __launch_bounds__(THREADS, (GRAD && THREADS == 256 ? 1024 : 1536
     if (lone >= 0) d[lone] = from_f32<T>(zero ? 0.f : power(x) * factor);
     if (GRAD == 1 && rank == 0 && warp == WARPS - 1) report();
     if (zero) return;
-    // the part's gradients are written, the slots claimed: warps without entries need not wait
-    if (warp * 32 >= a.k) {
-      asm volatile("barrier.cta.arrive 1, %0;" ::"n"(THREADS) : "memory");
-      return;
-    }
-    asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
-    const bool twice = s_twice;
-    for (int i = tid; i < a.k; i += THREADS) {
+    // The entries whose places this thread has written (the exchange above lies behind
+    // all that is read here).  All of an ID's are in the same list, and nearly always it
+    // is one; if not, their shares are added up in the entries' order, once.
+    for (int i = s_list[tid]; i >= 0; i = s_next[i]) {
       const int id = s_id[i];
-      if (id < 0 || !in_part(id)) continue;
+      if (id < 0) continue;                      // done
       float q = s_q[i];
+      bool twice = false;
+      for (int e = s_next[i]; e >= 0 && !twice; e = s_next[e]) twice = s_id[e] == id;
       if (twice) {
-        int at = (int)((uint32_t)id * 2654435761u >> 16) & (a.slots - 1);
-        while ((s_key[at] & ~TWICE) != id) at = (at + 1) & (a.slots - 1);
-        if (s_first[at] != i) continue;
-        for (int e = i + 1; e < (s_key[at] & TWICE ? a.k : 0); ++e)
-          if (s_id[e] == id) q += s_q[e];
+        q = 0;
+        for (int e = 0; e < a.k; ++e)
+          if (s_id[e] == id) {
+            q += s_q[e];
+            s_id[e] = -1;
+          }
       }
       d[id] = from_f32<T>((power(s_x[i]) * inverse - q) * g);
     }
@@ -349,18 +328,13 @@ template <class T, int GRAD, int THREADS>
 void run_rows_by(DistillArgs a, int64_t n_rows, const void *logits, void *dlogits, tt_stream_t stream) {
   const int64_t bytes = a.n_vocab * (int64_t)sizeof(T);
   // the same blocks a row, and the same order of its sums, with the gradient and without
-  for (a.slots = 32; a.slots < 2 * a.k;) a.slots *= 2;
-  int extra = (a.k * 12 + a.slots * 8 + 15) / 16 * 16;
+  const int extra = a.k * 16;
   const int held = std::min(HELD, SPACE - extra) / (16 * THREADS) * (16 * THREADS);
   a.cluster = (int)std::min<int64_t>(8, (bytes + held - 1) / held);
   // few rows: spread each over more blocks, down to 16 KB a block, as for the next-token loss
   while (a.cluster <= 4 && n_rows * a.cluster * 2 <= 2 * 152 && bytes >= a.cluster * 2 * 16384) a.cluster *= 2;
   const int64_t each = ((bytes + 15) / 16 + a.cluster - 1) / a.cluster;
   a.held = GRAD == 1 ? (int)std::min<int64_t>(each, held / 16) : 0;
-  if (!GRAD) {
-    a.slots = 0;
-    extra = (a.k * 12 + 15) / 16 * 16;
-  }
   auto k = k_distill<T, GRAD, THREADS>;
   if (allow_shared<Tag<T, GRAD, THREADS>>(k, SPACE)) return;                // (the error is kept)
   launch_cluster(k, dim3((unsigned)(n_rows * a.cluster)), THREADS, (size_t)a.held * 16 + extra, a.cluster, false, stream, a,
@@ -407,7 +381,7 @@ extern "C" tt_status tt_distill_loss(const void *d_logits, int32_t type, int64_t
                                      float *d_lse, const float *d_row_grads, void *d_dlogits, int64_t dlogits_stride,
                                      int32_t *d_status, tt_stream_t stream) {
   const DistillArgs a{n_vocab, logits_stride, dlogits_stride, ids_stride, teacher_stride, d_teacher_ids, d_teacher_logits, teacher_type,
-                      0, 0, 0, 0, d_loss, d_lse, nullptr, d_row_grads, d_status, 1, 0};
+                      0, 0, 0, d_loss, d_lse, nullptr, d_row_grads, d_status, 1, 0};
   return run_distill(d_logits, type, n_rows, k, temperature, a, d_dlogits, stream, "tt_distill_loss");
 }
 
@@ -418,6 +392,6 @@ extern "C" tt_status tt_distill_loss_grad(const void *d_logits, int32_t type, in
                                           int32_t *d_status, tt_stream_t stream) {
   if (n_rows > 0 && n_rows <= TT_MAX_IDS && (!d_lse || !d_dlogits)) return TT_ERR_INVALID_ARG;
   const DistillArgs a{n_vocab, logits_stride, dlogits_stride, ids_stride, teacher_stride, d_teacher_ids, d_teacher_logits, teacher_type,
-                      0, 0, 0, 0, nullptr, nullptr, d_lse, d_row_grads, d_status, 1, 0};
+                      0, 0, 0, nullptr, nullptr, d_lse, d_row_grads, d_status, 1, 0};
   return run_distill(d_logits, type, n_rows, k, temperature, a, d_dlogits, stream, "tt_distill_loss_grad");
 }

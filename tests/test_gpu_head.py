@@ -199,7 +199,7 @@ def test_linear_loss_without_rows(tt):
 def test_linear_loss_in_chunks(tt, kind, dwkind, accumulate):
     """More rows than are worked on at a time: the weight's gradient is summed over chunks."""
     kind, dwkind, g = KINDS[kind], KINDS[dwkind], gen(9)
-    n, vocab, dim = (2900 if kind != torch.float32 else 1100), 200256, 24
+    n, vocab, dim = (1100 if kind != torch.float32 else 400), 1 << 20, 24
     h, w, t = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.3), targets_of(n, vocab, 5)
     rg = torch.full((n,), 1 / 256, device="cuda")
     rg[:200] *= 16                                         # (chunks of different scales)

@@ -78,7 +78,7 @@ def test_linear_loss_workspace():
                 (4, 300, 16, 3, 1, 3, 1), (4, 300, 16, 2, 1, 1, 1)):
         assert f(*bad) == -1
     # bounded, however many the rows: a chunk of G, and the weight's sums in 32 bits between chunks
-    g, acc = 1 << 30, 100256 * 2048 * 4
+    g, acc = 2 << 30, 100256 * 2048 * 4
     assert f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_F32, 1) < 3 * g
     assert acc < f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_BF16, 1) < 3 * g + acc
     assert f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_BF16, 0) < 1 << 29
