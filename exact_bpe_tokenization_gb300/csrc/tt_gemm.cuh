@@ -31,7 +31,7 @@ constexpr int EPI_WARPS = 8, THREADS = (4 + EPI_WARPS) * 32;
 constexpr int OWN_BYTES = 4096;                            // shared memory of an epilogue's warp, for what it writes
 constexpr int SHARED = STAGES * STAGE_BYTES + EPI_WARPS * OWN_BYTES + 1024;   // and what aligns the stages to 1024 bytes
 constexpr int SMS = 152;
-constexpr uint32_t TRIES = 1u << 22;                      // of a wait, before the call gives up
+constexpr uint64_t PATIENCE = 4000000000ull;              // nanoseconds of a wait, before the call gives up
 
 struct Gemm {
   int m_tiles, n_tiles, splits;                           // the contraction is cut into `splits` parts
@@ -65,9 +65,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // false: the wait ran out, here or in another role of the block
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *dead) {
-  for (uint32_t i = 0; i < TRIES; ++i) {
+  uint64_t start, now;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+  for (uint32_t i = 0; i < 1u << 30; ++i) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 255) == 255 && *dead) return false;
+    if ((i & 63) == 63) {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (*dead || now - start > PATIENCE) break;
+    }
   }
   *dead = 1;
   return false;
@@ -149,6 +154,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, 
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

@@ -197,7 +197,7 @@ template <class T> struct PowersEpi {
     }
     if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = p;
   }
-  __device__ __forceinline__ void end() const { stores_read(); }
+  __device__ __forceinline__ void end() const { stores_done(); }
 };
 
 __device__ __forceinline__ float f16_up(const uint32_t *g_max) {
@@ -247,7 +247,7 @@ template <class T> struct GradEpi {
       put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
     }
   }
-  __device__ __forceinline__ void end() const { stores_read(); }
+  __device__ __forceinline__ void end() const { stores_done(); }
 };
 
 // Where a gradient goes: dst = sums * scale * the row's (+ src), T the type of dst.
@@ -454,10 +454,11 @@ template <class T> __device__ __forceinline__ void pack_group(const Pack &p, int
   pack8<T>(p.out + row * width + col, p.rows * width, v);
 }
 
-// What a call begins with: operands laid out, the targets' logits (a warp a row, 0 for
+// What a chunk of rows begins with: operands laid out, the targets' logits (a warp a row, 0 for
 // padding), words cleared.
 template <class T> __global__ void __launch_bounds__(256) k_begin(BeginArgs a) {
   let_next_start();
+  wait_for_last();
   const int64_t id = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
   const int lane = threadIdx.x & 31;
   for (int64_t i = id; i < a.n_words; i += step) a.words[i] = 0;
@@ -645,7 +646,7 @@ struct Call {
 struct Plan {
   int64_t chunk, width, g_stride;                          // rows; columns of packed operands and of G
   int split_h, split_w;
-  int64_t words;                                           // 1 and one a tile row, for each chunk
+  int64_t words;                                           // one, and one a tile row
   int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
 };
 
@@ -659,6 +660,7 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   const int64_t halves = (vocab + HALF - 1) / HALF;
   int64_t most = PARTIALS / (halves * 8);
   if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * parts));
+  if (pack_h || dw) most = std::min(most, KEPT / (p.width * 2 * parts));   // copies of hidden
   most = std::max<int64_t>(most / TILE * TILE, TILE);
   const int64_t chunks = (n + most - 1) / most;
   p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
@@ -671,11 +673,11 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
     at += up(bytes, 256);
     return here;
   };
-  p.hidden = take(pack_h ? n * p.width * 2 * parts : 0);
+  p.hidden = take(pack_h ? p.chunk * p.width * 2 * parts : 0);
   p.weight = take(pack_w ? vocab * p.width * 2 * parts : 0);
   p.part = take(halves * 8 * p.chunk);
-  p.rows = take(4 * (n + 2 * p.chunk));                    // target_logit of all rows, target_power, row_scale
-  p.words = (1 + (p.chunk + TILE - 1) / TILE) * ((n + p.chunk - 1) / p.chunk);
+  p.rows = take(4 * 3 * p.chunk);                          // target_logit, target_power, row_scale
+  p.words = 1 + (p.chunk + TILE - 1) / TILE;
   p.word = take(4 * p.words);
   if (grad) {
     p.info = take(sizeof(RowInfo) * p.chunk);
@@ -751,23 +753,16 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
   const bool bf16 = c.type != TT_F16, grad = c.dhidden || c.dweight;
   // a 16-bit float has no range for powers: the product runs twice, for lse and for G
   const bool powers = grad && !c.lse_in && c.type != TT_F16;
-  Matrix h{c.hidden, c.n, c.dim, c.hidden_stride, parts, 8}, w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
-  BeginArgs begin{};
-  if (needs_pack(c.type, c.hidden, c.hidden_stride)) {
-    begin.hidden = Pack{c.hidden, c.n, c.hidden_stride, vec_of(c.hidden, c.hidden_stride, c.type), (uint16_t *)(ws + p.hidden)};
-    h = Matrix{ws + p.hidden, c.n, c.dim, p.width, parts, c.n * p.width};
-  }
-  if (needs_pack(c.type, c.weight, c.weight_stride)) {
-    begin.weight = Pack{c.weight, c.vocab, c.weight_stride, vec_of(c.weight, c.weight_stride, c.type), (uint16_t *)(ws + p.weight)};
-    w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
-  }
+  Matrix w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
+  const bool pack_h = needs_pack(c.type, c.hidden, c.hidden_stride), pack_w = needs_pack(c.type, c.weight, c.weight_stride);
+  if (pack_w) w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
   RowArgs r{};
   r.n_parts = (int)((c.vocab + HALF - 1) / HALF);
   r.n_vocab = (int)c.vocab;
   r.dim = (int)c.dim;
   r.part = (float2 *)(ws + p.part);
   r.target_logit = (float *)(ws + p.rows);
-  r.row_scale = r.target_logit + c.n + p.chunk;
+  r.row_scale = r.target_logit + 2 * p.chunk;
   r.status = c.status;
   r.hidden_stride = c.hidden_stride;
   r.hidden_vec = vec_of(c.hidden, c.hidden_stride, c.type);
@@ -781,42 +776,27 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     if (c.dweight) r.scaled = (uint16_t *)(ws + p.scaled);
     if (c.type == TT_F16) r.g_max = (uint32_t *)(ws + p.word);
     if (powers) {
-      r.target_power = r.target_logit + c.n;
+      r.target_power = r.target_logit + p.chunk;
       r.only = (int32_t *)(ws + p.word);
     }
   }
+  BeginArgs begin{};
   begin.dim = (int)c.dim;
   begin.width = (int)p.width;
   begin.n_vocab = (int)c.vocab;
-  begin.h = c.hidden;
   begin.w = c.weight;
-  begin.n_rows = c.n;
   begin.h_stride = c.hidden_stride;
   begin.w_stride = c.weight_stride;
   begin.h_vec = r.hidden_vec;
   begin.w_vec = vec_of(c.weight, c.weight_stride, c.type);
-  begin.targets = c.targets;
   if (powers) begin.target_logit = r.target_logit;
   if (r.g_max || r.only) {
     begin.words = (int32_t *)(ws + p.word);
     begin.n_words = p.words;
   }
-  const int64_t units = std::max(std::max(begin.hidden.x ? c.n * (p.width / 8) : 0, begin.weight.x ? c.vocab * (p.width / 8) : 0),
-                                 std::max(powers ? c.n * 32 : 0, begin.n_words));
-  if (units && c.n)
-    with_type(c.type, [&](auto t) {
-      k_begin<decltype(t)><<<(unsigned)std::min<int64_t>((units + 255) / 256, SMS * 16), 256, 0, stream>>>(begin);
-    });
   for (int64_t row0 = 0; row0 < c.n; row0 += p.chunk) {
     const int n = (int)std::min(p.chunk, c.n - row0);
-    Matrix hc = h;
-    hc.p = (const uint16_t *)h.p + row0 * h.stride;
-    hc.rows = n;
-    int32_t *words = (int32_t *)(ws + p.word) + row0 / p.chunk * (1 + (p.chunk + TILE - 1) / TILE);
-    if (r.g_max) r.g_max = (uint32_t *)words;
-    if (r.only) r.only = words;
     r.n_rows = n;
-    r.target_logit = (float *)(ws + p.rows) + row0;
     r.hidden = (const uint8_t *)c.hidden + row0 * c.hidden_stride * size;
     r.targets = c.targets + row0;
     r.row_grads = c.row_grads ? c.row_grads + row0 : nullptr;
@@ -824,6 +804,19 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     r.loss = c.loss ? c.loss + row0 : nullptr;
     r.lse = c.lse ? c.lse + row0 : nullptr;
     const Matrix g{r.g, n, c.vocab, p.g_stride, parts, r.g_part};
+    Matrix hc{r.hidden, n, c.dim, c.hidden_stride, parts, 8};
+    if (pack_h) hc = Matrix{ws + p.hidden, n, c.dim, p.width, parts, n * p.width};
+    begin.hidden = Pack{pack_h ? r.hidden : nullptr, n, c.hidden_stride, r.hidden_vec, (uint16_t *)(ws + p.hidden)};
+    begin.weight = Pack{pack_w && row0 == 0 ? c.weight : nullptr, c.vocab, c.weight_stride, begin.w_vec, (uint16_t *)(ws + p.weight)};
+    begin.h = r.hidden;
+    begin.n_rows = n;
+    begin.targets = r.targets;
+    const int64_t units = std::max(std::max(begin.hidden.x ? n * (p.width / 8) : 0, begin.weight.x ? c.vocab * (p.width / 8) : 0),
+                                   std::max<int64_t>(powers ? n * 32ll : 0, begin.n_words));
+    if (units)
+      with_type(c.type, [&](auto t) {
+        launch_cluster(k_begin<decltype(t)>, dim3((unsigned)std::min<int64_t>((units + 255) / 256, SMS * 16)), 256, 0, 1, true, stream, begin);
+      });
     bool ok = true;
     if (powers) {
       if (c.type == TT_F32) ok = make_powers<float>(hc, w, g, r, stream);
@@ -918,7 +911,7 @@ extern "C" tt_status tt_linear_loss_grad(const void *d_hidden, const void *d_wei
                                          const float *d_lse, const float *d_row_grads, void *d_dhidden, int64_t dhidden_stride,
                                          void *d_dweight, int32_t dweight_type, int64_t dweight_stride, int32_t accumulate,
                                          void *d_workspace, int64_t workspace_bytes, int32_t *d_status, tt_stream_t stream) {
-  if ((n_rows > 0 && !d_lse) || (!d_dhidden && !d_dweight)) return TT_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!d_lse || (!d_dhidden && !d_dweight))) return TT_ERR_INVALID_ARG;
   const Call c{d_hidden, d_weight, type, n_rows, n_vocab, dim, hidden_stride, weight_stride, d_targets, nullptr, nullptr, d_lse,
                d_row_grads, d_dhidden, d_dweight, dhidden_stride, dweight_type, dweight_stride, accumulate, d_status};
   return run_linear(c, d_workspace, workspace_bytes, stream, "tt_linear_loss_grad");

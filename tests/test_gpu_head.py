@@ -192,6 +192,7 @@ def test_linear_loss_without_rows(tt):
     assert bool((kept == 3).all())
     tt.linear_loss_grad(h, w, t, lse, dweight=kept)
     assert not kept.any()
+    assert tt.linear_loss_grad(h, w, t, lse, dhidden=dh) == (dh, None)
 
 
 @pytest.mark.parametrize("kind,dwkind,accumulate", [("bf16", "bf16", False), ("bf16", "bf16", True), ("bf16", "f32", True),
@@ -268,8 +269,11 @@ def test_linear_loss_nan_and_infinities_stay_in_their_rows(tt, kind, value):
     t[7] = -1
     loss, lse, dh, dw = tt.linear_loss(h, w, t, rg, want_grad=True)
     assert loss[7] == 0 and not bool(dh[7].any()) and not bool(torch.isfinite(lse[7]))
-    if kind != torch.float32 or math.isnan(value):
-        check_linear([x[others] for x in (loss, lse, dh)], r)
+    check_linear([x[others] for x in (loss, lse, dh)] + [dw], r)
+    rg[7] = math.nan
+    dh, dw = tt.linear_loss_grad(h, w, t, torch.where(others, lse, math.nan), rg)
+    assert not bool(dh[7].any())
+    check_linear((None, None, dh[others], dw), r)
 
 
 @pytest.mark.parametrize("kind", KINDS)

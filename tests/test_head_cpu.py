@@ -82,6 +82,8 @@ def test_linear_loss_workspace():
     assert f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_F32, 1) < 3 * g
     assert acc < f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_BF16, 1) < 3 * g + acc
     assert f(1 << 20, 100256, 2048, tt.TT_BF16, 1, tt.TT_BF16, 0) < 1 << 29
+    assert f(1 << 28, 300, 2048, tt.TT_BF16, 1, tt.TT_F32, 1) < 4 * g      # (copies of hidden too)
+    assert f(1 << 28, 300, 2048, tt.TT_F32, 1, tt.TT_F32, 0) < 2 * g
     assert f(0, 300, 16, tt.TT_BF16, 1, tt.TT_BF16, 1) > 0
 
 
