@@ -406,18 +406,24 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
 
 // Parts to cut a contraction into, so that every pair of SMs has as much to do: the
 // least of the rounds of tiles, each of its blocks and a tile's start and end, and the
-// traffic of the parts (times in blocks of 64, 0.27 us).
+// traffic of the parts (times in blocks of 64, 0.27 us).  The tensor cores cut off the
+// sums at each step: operands of several parts, which are 32-bit values, are summed over
+// no more than 2048 at a time (dhidden of 100,000 tokens was off by 1.4e-5 of its size in one
+// sum, 7e-6 with 8192, 2.4e-6 so; plain 32-bit sums 2e-6).
+constexpr int64_t LONGEST = 2048;
 inline int choose_splits(int64_t m, int64_t n, int64_t k, int pairs) {
   const int64_t tiles = ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE), blocks = (k + KB - 1) / KB;
-  int best = 1;
+  const int64_t least_splits = pairs > 1 ? (k + LONGEST - 1) / LONGEST : 1;
+  const int64_t most = std::max<int64_t>(least_splits, std::min<int64_t>(std::min<int64_t>(32, blocks), blocks * pairs / 4));
+  int best = (int)least_splits;
   double least = 1e300;
-  for (int s = 1; s <= 32 && s <= blocks && s * 4 <= std::max<int64_t>(blocks * pairs, 4); ++s) {
+  for (int64_t s = least_splits; s <= most; ++s) {
     const int64_t rounds = (tiles * s + SMS / 2 - 1) / (SMS / 2);
     double cost = (double)rounds * ((double)((blocks + s - 1) / s) * pairs + 4);
     if (s > 1) cost += 12 + (double)s * m * n * 8 / 6.8e12 / 0.27e-6;
     if (cost < least * 0.99) {
       least = cost;
-      best = s;
+      best = (int)s;
     }
   }
   return best;
