@@ -624,6 +624,240 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
   }
 }
 
+// ------------------------------------------------------------ few rows of floats
+// Up to 64 rows of 32-bit values: laying out the weight in parts and multiplying 256 rows,
+// six times, would cost several times what reading it once costs (1 x 200256 x 2096: 1490
+// us for the loss; the weight alone is 247).  Here the weight goes by asynchronous copies
+// into shared memory, where ordinary 32-bit products, two at a time, take it from: XX us for
+// 1 row, XX for 8, XX for 32, XX for 64.  A warp has eight rows; warps that are left over
+// divide the contraction.
+constexpr int FEW = 64, FEW_STAGES = 4;
+constexpr int FEW_K = 32, FEW_ROW = FEW_K + 4;             // of the contraction a stage; floats a row of it in shared memory
+
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+// four floats of which n are there (the others become zeros) from any address
+__device__ __forceinline__ void copy4(float *to, const float *from, int n, bool vec) {
+  const uint32_t at = saddr(to);
+  if (vec) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(max(0, min(4, n)) * 4) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + 4 * i), "l"(from + (i < n ? i : 0)), "r"(i < n ? 4 : 0) : "memory");
+  }
+}
+
+// The logits of 128 tokens a block, and what becomes of them: MODE 0 maxima and sums,
+// 1 powers and their sums, 2 G (see the epilogues above).
+template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const float *weight, int64_t weight_stride, bool vec_w) {
+  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = (128 + ROWS) * FEW_ROW;
+  extern __shared__ uint4 s_few[];
+  float *stages = reinterpret_cast<float *>(s_few);
+  let_next_start();
+  wait_for_last();
+  if (MODE == 2 && a.only && !a.only[0]) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
+  const int col0 = blockIdx.x * 128, steps = (a.dim + FEW_K - 1) / FEW_K;
+  const float *hidden = (const float *)a.hidden;
+  auto fetch = [&](int step) {
+    if (step < steps) {
+      float *to = stages + step % FEW_STAGES * STAGE;
+      for (int i = tid; i < (128 + ROWS) * (FEW_K / 4); i += 256) {
+        const int r = i / (FEW_K / 4), c = i % (FEW_K / 4) * 4, k = step * FEW_K + c;
+        const bool w = r < 128, there = w ? col0 + r < a.n_vocab : r - 128 < a.n_rows;
+        const float *from = w ? weight + (int64_t)(col0 + r) * weight_stride + k : hidden + (r - 128) * a.hidden_stride + k;
+        const int n = there ? a.dim - k : 0;
+        copy4(to + r * FEW_ROW + c, n > 0 ? from : w ? weight : hidden, n, w ? vec_w : a.hidden_vec);
+      }
+    }
+    copy_group();
+  };
+#pragma unroll
+  for (int i = 0; i < FEW_STAGES - 1; ++i) fetch(i);
+  float2 acc[8][4];
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[m][j] = make_float2(0, 0);
+  for (int step = 0; step < steps; ++step) {
+    copy_wait<FEW_STAGES - 2>();
+    __syncthreads();
+    fetch(step + FEW_STAGES - 1);
+    const float *w = stages + step % FEW_STAGES * STAGE, *h = w + 128 * FEW_ROW + group * 8 * FEW_ROW;
+#pragma unroll
+    for (int k = share * (FEW_K / SHARES); k < (share + 1) * (FEW_K / SHARES); k += 4) {
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const float4 *>(w + (lane + 32 * j) * FEW_ROW + k);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const float4 y = *reinterpret_cast<const float4 *>(h + m * FEW_ROW + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[m][j] = fma2(make_float2(x[j].x, x[j].y), make_float2(y.x, y.y), acc[m][j]);
+          acc[m][j] = fma2(make_float2(x[j].z, x[j].w), make_float2(y.z, y.w), acc[m][j]);
+        }
+      }
+    }
+  }
+  // the shares' sums side by side: [share][row][128]
+  copy_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) stages[(share * ROWS + group * 8 + m) * 128 + lane + 32 * j] = acc[m][j].x + acc[m][j].y;
+  __syncthreads();
+  const int col = col0 + lane * 4;
+  for (int row = warp; row < a.n_rows; row += 8) {
+    float v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < SHARES; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(stages + (k * ROWS + row) * 128 + lane * 4);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i >= a.n_vocab) v[i] = -INF;
+    const int t = a.targets[row];
+    auto stats = [&]() {
+      float m = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), e = 0;
+      m = fminf(fmaxf(warp_all(m, OpMax{}), LOWEST), -LOWEST);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e += ex2((v[i] - m) * LOG2E);
+      return make_float2(m, warp_all(e, OpSum{}));
+    };
+    if (MODE == 0) {
+      if ((uint32_t)(t - col) < 4u && t < a.n_vocab)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == t - col) a.target_logit[row] = v[i];
+      const float2 p = stats();
+      if (lane == 0) a.part[(int64_t)blockIdx.x * a.n_rows + row] = p;
+      continue;
+    }
+    float g[4];
+    if (MODE == 1) {
+      const float c = a.target_logit[row];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = ex2((v[i] - c) * LOG2E);
+      float2 p = make_float2(c, warp_all((g[0] + g[1]) + (g[2] + g[3]), OpSum{}));
+      if (!(p.y > 0x1p-100f && p.y < 0x1p100f)) p = stats();
+      if (lane == 0) a.part[(int64_t)blockIdx.x * a.n_rows + row] = p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t >= 0 && col + i == t && t < a.n_vocab) a.target_power[row] = g[i];
+      if ((uint32_t)t >= (uint32_t)a.n_vocab)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = 0;
+    } else {
+      const RowInfo r = a.info[row];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = r.t < 0 ? 0.f : ex2((v[i] - r.from) * LOG2E) * r.mul - (col + i == r.t ? r.g : 0.f);
+    }
+    if (col >= a.g_stride) continue;
+    uint16_t *to = a.g + row * a.g_stride + col;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      *reinterpret_cast<uint2 *>(to + p * a.g_part) = make_uint2(f32_two<__nv_bfloat16>(g[0], g[1]), f32_two<__nv_bfloat16>(g[2], g[3]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] -= __bfloat162float(__float2bfloat16_rn(g[i]));
+    }
+  }
+}
+
+// dhidden's sums over a share of the tokens, by 128 columns a block: [share][n_rows][width]
+template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const float *weight, int64_t weight_stride, bool vec_w, int each, float *sums) {
+  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = FEW_K * 128 + FEW_K * ROWS;
+  extern __shared__ uint4 s_few[];
+  float *stages = reinterpret_cast<float *>(s_few);
+  let_next_start();
+  wait_for_last();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
+  const int col0 = blockIdx.x * 128, first = blockIdx.y * each, last = min(a.n_vocab, first + each), steps = (last - first + FEW_K - 1) / FEW_K;
+  // a stage: 32 tokens' 128 columns, and G of the rows and those tokens, [token][row]
+  auto fetch = [&](int step) {
+    if (step < steps) {
+      float *to = stages + step % FEW_STAGES * STAGE;
+      for (int i = tid; i < FEW_K * 32; i += 256) {
+        const int r = i / 32, c = i % 32 * 4, token = first + step * FEW_K + r;
+        const int n = token < last ? a.dim - col0 - c : 0;
+        copy4(to + r * 128 + c, n > 0 ? weight + token * weight_stride + col0 + c : weight, n, vec_w);
+      }
+    }
+    copy_group();
+  };
+  const int g_row = tid / 4, g_at = tid % 4 * 8;           // eight tokens of a row's G
+  uint4 part[3];
+  auto ask = [&](int step) {
+    const int token = first + step * FEW_K + g_at;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      part[p] = make_uint4(0, 0, 0, 0);
+      if (step < steps && g_row < min(ROWS, a.n_rows) && token < last) part[p] = *reinterpret_cast<const uint4 *>(a.g + p * a.g_part + g_row * a.g_stride + token);
+    }
+  };
+  auto give = [&](int step) {
+    if (step >= steps || g_row >= ROWS) return;
+    float *to = stages + step % FEW_STAGES * STAGE + FEW_K * 128 + g_row;
+    float v[8], w[8], x[8];
+    vec_f32(part[0], v, __nv_bfloat16{});
+    vec_f32(part[1], w, __nv_bfloat16{});
+    vec_f32(part[2], x, __nv_bfloat16{});
+    const int left = last - first - step * FEW_K - g_at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to[(g_at + i) * ROWS] = i < left ? v[i] + (w[i] + x[i]) : 0.f;
+  };
+#pragma unroll
+  for (int i = 0; i < FEW_STAGES - 1; ++i) fetch(i);
+  ask(0);
+  float2 acc[8][2];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) acc[m][0] = acc[m][1] = make_float2(0, 0);
+  for (int step = 0; step < steps; ++step) {
+    give(step);
+    ask(step + 1);
+    copy_wait<FEW_STAGES - 2>();
+    __syncthreads();
+    fetch(step + FEW_STAGES - 1);
+    const float *w = stages + step % FEW_STAGES * STAGE, *g = w + FEW_K * 128 + group * 8;
+#pragma unroll 4
+    for (int j = share; j < FEW_K; j += SHARES) {
+      const float4 x = *reinterpret_cast<const float4 *>(w + j * 128 + lane * 4);
+      const float4 y0 = *reinterpret_cast<const float4 *>(g + j * ROWS), y1 = *reinterpret_cast<const float4 *>(g + j * ROWS + 4);
+      const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        acc[m][0] = fma2(make_float2(x.x, x.y), make_float2(y[m], y[m]), acc[m][0]);
+        acc[m][1] = fma2(make_float2(x.z, x.w), make_float2(y[m], y[m]), acc[m][1]);
+      }
+    }
+  }
+  copy_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+    *reinterpret_cast<float4 *>(stages + (share * ROWS + group * 8 + m) * 128 + lane * 4) =
+        make_float4(acc[m][0].x, acc[m][0].y, acc[m][1].x, acc[m][1].y);
+  __syncthreads();
+  const int col = col0 + lane * 4;
+  for (int row = warp; row < a.n_rows; row += 8) {
+    float v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < SHARES; ++k) {
+      const float4 x = *reinterpret_cast<const float4 *>(stages + (k * ROWS + row) * 128 + lane * 4);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    }
+    if (col < a.width) *reinterpret_cast<float4 *>(sums + ((int64_t)blockIdx.y * a.n_rows + row) * a.width + col) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
 // ------------------------------------------------------------ host
 inline int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
@@ -650,8 +884,16 @@ struct Plan {
   int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
 };
 
+inline bool is_few(int64_t n, int32_t type) { return type == TT_F32 && n <= FEW; }
+// tokens a block of k_few_hidden takes: two blocks an SM, whole stages
+inline int64_t few_each(int64_t vocab, int64_t dim) {
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * SMS / ((dim + 127) / 128), (vocab + 255) / 256));
+  return up((vocab + splits - 1) / splits, FEW_K);
+}
+
 Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, bool pack_w, bool dh, bool dw, bool dw_f32) {
   Plan p{};
+  if (is_few(n, type)) pack_h = pack_w = false;
   const int parts = type == TT_F32 ? 3 : 1;
   const bool grad = dh || dw;
   n = std::max<int64_t>(n, 1);
@@ -665,7 +907,7 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   const int64_t chunks = (n + most - 1) / most;
   p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
   const int pairs = parts == 1 ? 1 : 6;
-  p.split_h = choose_splits(p.chunk, dim, vocab, pairs);
+  p.split_h = is_few(n, type) ? (int)((vocab + few_each(vocab, dim) - 1) / few_each(vocab, dim)) : choose_splits(p.chunk, dim, vocab, pairs);
   p.split_w = choose_splits(vocab, dim, p.chunk, pairs);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -685,7 +927,7 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
     p.g = take(p.g_stride * 2 * parts * p.chunk);
     p.acc = take(dw && !dw_f32 && p.chunk < n ? vocab * p.width * 4 : 0);
     int64_t sums = 0;
-    if (dh && p.split_h > 1) sums = std::max(sums, p.split_h * p.chunk * p.width * 4);
+    if (dh && (p.split_h > 1 || is_few(n, type))) sums = std::max(sums, p.split_h * p.chunk * p.width * 4);
     if (dw && p.split_w > 1) sums = std::max(sums, p.split_w * vocab * p.width * 4);
     p.sums = take(sums);
   }
@@ -727,6 +969,40 @@ bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sum
   return ok;
 }
 
+template <class T, int ROWS> struct FewTag {};
+// f(number of rows that there is a kernel for)
+template <class F> void with_rows(int n, F f) {
+  if (n <= 8) f(std::integral_constant<int, 8>{});
+  else if (n <= 16) f(std::integral_constant<int, 16>{});
+  else if (n <= 32) f(std::integral_constant<int, 32>{});
+  else f(std::integral_constant<int, 64>{});
+}
+template <int MODE> bool few_logits(const Call &c, const RowArgs &r, cudaStream_t stream) {
+  bool ok = true;
+  with_rows(r.n_rows, [&](auto rows) {
+    constexpr int ROWS = decltype(rows)::value;
+    const int shared = FEW_STAGES * (128 + ROWS) * FEW_ROW * 4;
+    auto k = k_few_logits<ROWS, MODE>;
+    if (!(ok = !allow_shared<FewTag<std::integral_constant<int, MODE>, ROWS>>(k, shared))) return;
+    launch_cluster(k, dim3(r.n_parts), 256, shared, 1, true, stream, r, (const float *)c.weight, c.weight_stride,
+                   vec_of(c.weight, c.weight_stride, TT_F32) != 0);
+  });
+  return ok;
+}
+bool few_hidden(const Call &c, const RowArgs &r, const Plan &p, float *sums, const Target &o, cudaStream_t stream) {
+  bool ok = true;
+  with_rows(r.n_rows, [&](auto rows) {
+    constexpr int ROWS = decltype(rows)::value;
+    const int shared = FEW_STAGES * FEW_K * (128 + ROWS) * 4;
+    auto k = k_few_hidden<ROWS>;
+    if (!(ok = !allow_shared<FewTag<float, ROWS>>(k, shared))) return;
+    launch_cluster(k, dim3((unsigned)((c.dim + 127) / 128), (unsigned)p.split_h), 256, shared, 1, true, stream, r, (const float *)c.weight,
+                   c.weight_stride, vec_of(c.weight, c.weight_stride, TT_F32) != 0, (int)few_each(c.vocab, c.dim), sums);
+  });
+  if (ok) join<float>(sums, p.split_h, p.width, o, stream);
+  return ok;
+}
+
 // the product of hidden and weight into powers, or into G; T: the operands' type
 template <class T> bool make_powers(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
   PowersEpi<T> e{{}, r.n_rows, r.n_vocab, r.targets, r.target_logit, r.part, r.target_power};
@@ -754,7 +1030,8 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
   // a 16-bit float has no range for powers: the product runs twice, for lse and for G
   const bool powers = grad && !c.lse_in && c.type != TT_F16;
   Matrix w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
-  const bool pack_h = needs_pack(c.type, c.hidden, c.hidden_stride), pack_w = needs_pack(c.type, c.weight, c.weight_stride);
+  const bool few = is_few(c.n, c.type);
+  const bool pack_h = !few && needs_pack(c.type, c.hidden, c.hidden_stride), pack_w = !few && needs_pack(c.type, c.weight, c.weight_stride);
   if (pack_w) w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
   RowArgs r{};
   r.n_parts = (int)((c.vocab + HALF - 1) / HALF);
@@ -819,8 +1096,11 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
       });
     bool ok = true;
     if (powers) {
-      if (c.type == TT_F32) ok = make_powers<float>(hc, w, g, r, stream);
+      if (few) ok = few_logits<1>(c, r, stream);
+      else if (c.type == TT_F32) ok = make_powers<float>(hc, w, g, r, stream);
       else ok = make_powers<__nv_bfloat16>(hc, w, g, r, stream);
+    } else if (few && !c.lse_in) {
+      ok = few_logits<0>(c, r, stream);
     } else if (!c.lse_in) {
       const StatsEpi e{n, (int)c.vocab, r.targets, r.part, r.target_logit};
       ok = run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream);
@@ -829,7 +1109,7 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     with_type(c.type, [&](auto t) {
       using T = decltype(t);
       finish<T>(r, stream);
-      if (grad) ok = make_g<T>(hc, w, g, r, stream);
+      if (grad) ok = few ? few_logits<2>(c, r, stream) : make_g<T>(hc, w, g, r, stream);
     });
     if (!ok) return false;
     if (!grad) continue;
@@ -837,7 +1117,9 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     if (c.dhidden) {
       const Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * size, c.dhidden_stride, nullptr, 0, TT_F32, r.g_max,
                      powers ? r.row_scale : nullptr, vec_of(c.dhidden, c.dhidden_stride, c.type)};
-      if (!product<false>(bf16, g, w, p.split_h, sums, p.width, c.type, o, c.status, stream)) return false;
+      if (few) ok = few_hidden(c, r, p, sums, o, stream);
+      else ok = product<false>(bf16, g, w, p.split_h, sums, p.width, c.type, o, c.status, stream);
+      if (!ok) return false;
     }
     if (c.dweight) {
       // the sums of several chunks stay in 32 bits until the last

@@ -87,7 +87,7 @@ def check_linear(out, r, dwkind=None):
 # around a tile's 256, a part's 128, a stage's 64, and 16 bytes
 SHAPES = [(1, 1, 1), (1, 300, 8), (2, 7, 3), (5, 129, 24), (33, 300, 64), (64, 4352, 64), (127, 128, 63), (128, 255, 65),
           (129, 256, 128), (255, 257, 40), (256, 512, 256), (257, 513, 257), (300, 1000, 641), (700, 2000, 72), (1030, 700, 16),
-          (4100, 260, 24), (40, 9000, 520)]
+          (4100, 260, 24), (40, 9000, 520), (8, 20000, 130), (9, 511, 1030), (17, 5000, 33), (65, 5000, 130)]
 
 
 @pytest.mark.parametrize("n,vocab,dim", SHAPES)
@@ -112,9 +112,10 @@ def test_linear_loss(tt, n, vocab, dim, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("hs,hshift,ws,wshift", [(48, 0, 48, 0), (41, 0, 40, 0), (40, 1, 40, 0), (40, 0, 43, 3), (47, 5, 49, 7), (56, 8, 64, 8)])
-def test_linear_loss_strides_and_alignments(tt, kind, hs, hshift, ws, wshift):
+@pytest.mark.parametrize("n,dim", [(70, 40), (50, 40), (11, 39)])
+def test_linear_loss_strides_and_alignments(tt, kind, hs, hshift, ws, wshift, n, dim):
     kind, g = KINDS[kind], gen(hs + ws)
-    n, vocab, dim = 70, 300, 40
+    vocab = 300
     h, w = rows_of(n, dim, kind, g, hs, hshift), rows_of(vocab, dim, kind, g, ws, wshift, 0.3)
     dh, dw = rows_of(n, dim, kind, g, hs, hshift), rows_of(vocab, dim, kind, g, ws, wshift)
     wide = rows_of(vocab, dim, torch.float32, g, ws, wshift)
@@ -166,10 +167,10 @@ def test_linear_loss_padding_and_invalid_targets(tt, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("wide", [False, True])
-@pytest.mark.parametrize("vocab", [300, 5000])
-def test_linear_loss_accumulates(tt, kind, wide, vocab):
+@pytest.mark.parametrize("n,vocab", [(300, 300), (300, 5000), (30, 5000)])
+def test_linear_loss_accumulates(tt, kind, wide, n, vocab):
     kind, g = KINDS[kind], gen(7)
-    n, dim = 300, 72
+    dim = 72
     h, w, t = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.2), targets_of(n, vocab, 4)
     dkind = torch.float32 if wide else kind
     before = (torch.randn(vocab, dim, generator=g, device="cuda") * 0.1).to(dkind)
@@ -220,11 +221,12 @@ def test_linear_loss_in_chunks(tt, kind, dwkind, accumulate):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("lift", [-300.0, -60.0, 60.0, 300.0])
-def test_linear_loss_far_from_zero(tt, kind, lift):
+@pytest.mark.parametrize("n", [300, 47])
+def test_linear_loss_far_from_zero(tt, kind, lift, n):
     """Rows whose logits lie far from zero, all of them or all but the target's, and rows
     of a spread beyond what 32-bit powers hold."""
     kind, g = KINDS[kind], gen(11)
-    n, vocab, dim = 300, 600, 32
+    vocab, dim = 600, 32
     h, w = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.3)
     h[:, 0] = 0
     w[:, 0] = 1
@@ -252,9 +254,10 @@ def test_linear_loss_of_equal_logits(tt, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_linear_loss_nan_and_infinities_stay_in_their_rows(tt, kind, value):
+@pytest.mark.parametrize("n", [300, 60])
+def test_linear_loss_nan_and_infinities_stay_in_their_rows(tt, kind, value, n):
     kind, g = KINDS[kind], gen(13)
-    n, vocab, dim = 300, 400, 24
+    vocab, dim = 400, 24
     h, w, t = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.3), targets_of(n, vocab, 9)
     rg = torch.full((n,), 1 / n, device="cuda")
     t[7] = 5
@@ -353,9 +356,10 @@ def test_linear_loss_on_other_streams(tt):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_linear_loss_in_a_graph(tt, kind):
+@pytest.mark.parametrize("n", [300, 30])
+def test_linear_loss_in_a_graph(tt, kind, n):
     kind, g = KINDS[kind], gen(19)
-    n, vocab, dim = 300, 1000, 40
+    vocab, dim = 1000, 40
     h, w, t = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.3), targets_of(n, vocab, 4)
     tt.linear_loss(h, w, t, want_grad=True)
     torch.cuda.synchronize()
