@@ -628,9 +628,10 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // Up to 64 rows of 32-bit values: laying out the weight in parts and multiplying 256 rows,
 // six times, would cost several times what reading it once costs (1 x 200256 x 2096: 1490
 // us for the loss; the weight alone is 247).  Here the weight goes by asynchronous copies
-// into shared memory, where ordinary 32-bit products, two at a time, take it from: XX us for
-// 1 row, XX for 8, XX for 32, XX for 64.  A warp has eight rows; warps that are left over
-// divide the contraction.
+// into shared memory, where ordinary 32-bit products, two at a time, take it from: 300 us for
+// 1 row and for 8, 404 for 16, 667 for 32, 1187 for 64 (the latter bound by the products: 60%
+// of their rate), where the tensor cores take 1500 for any number up to 256.  A warp has
+// eight rows; warps that are left over divide the contraction.
 constexpr int FEW = 64, FEW_STAGES = 4;
 constexpr int FEW_K = 32, FEW_ROW = FEW_K + 4;             // of the contraction a stage; floats a row of it in shared memory
 
@@ -665,15 +666,27 @@ template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_lo
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
   const int col0 = blockIdx.x * 128, steps = (a.dim + FEW_K - 1) / FEW_K;
   const float *hidden = (const float *)a.hidden;
+  // a thread copies four floats of every 32nd row: its places are found once
+  constexpr int COPIES = 4 + (ROWS + 31) / 32;
+  const int k0 = tid % 8 * 4;
+  const float *from[COPIES];
+  int left[COPIES];                                        // of the contraction behind its first
+#pragma unroll
+  for (int q = 0; q < COPIES; ++q) {
+    const int r = tid / 8 + 32 * (q & 3);
+    const bool w = q < 4, there = w ? col0 + r < a.n_vocab : r < a.n_rows;
+    left[q] = there ? a.dim - k0 : 0;
+    from[q] = w ? weight : hidden;
+    if (left[q] > 0) from[q] += w ? (col0 + r) * weight_stride + k0 : r * a.hidden_stride + k0;
+  }
   auto fetch = [&](int step) {
     if (step < steps) {
-      float *to = stages + step % FEW_STAGES * STAGE;
-      for (int i = tid; i < (128 + ROWS) * (FEW_K / 4); i += 256) {
-        const int r = i / (FEW_K / 4), c = i % (FEW_K / 4) * 4, k = step * FEW_K + c;
-        const bool w = r < 128, there = w ? col0 + r < a.n_vocab : r - 128 < a.n_rows;
-        const float *from = w ? weight + (int64_t)(col0 + r) * weight_stride + k : hidden + (r - 128) * a.hidden_stride + k;
-        const int n = there ? a.dim - k : 0;
-        copy4(to + r * FEW_ROW + c, n > 0 ? from : w ? weight : hidden, n, w ? vec_w : a.hidden_vec);
+      float *to = stages + step % FEW_STAGES * STAGE + tid / 8 * FEW_ROW + k0;
+#pragma unroll
+      for (int q = 0; q < COPIES; ++q) {
+        if (q >= 4 && ROWS < 32 && tid / 8 >= ROWS) break;
+        const int n = left[q] - step * FEW_K;
+        copy4(to + (q < 4 ? 32 * q : 128 + 32 * (q - 4)) * FEW_ROW, n > 0 ? from[q] + step * FEW_K : from[q], n, q < 4 ? vec_w : a.hidden_vec);
       }
     }
     copy_group();
@@ -690,7 +703,7 @@ template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_lo
     __syncthreads();
     fetch(step + FEW_STAGES - 1);
     const float *w = stages + step % FEW_STAGES * STAGE, *h = w + 128 * FEW_ROW + group * 8 * FEW_ROW;
-#pragma unroll
+#pragma unroll 1
     for (int k = share * (FEW_K / SHARES); k < (share + 1) * (FEW_K / SHARES); k += 4) {
       float4 x[4];
 #pragma unroll
@@ -785,10 +798,11 @@ template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowAr
   auto fetch = [&](int step) {
     if (step < steps) {
       float *to = stages + step % FEW_STAGES * STAGE;
-      for (int i = tid; i < FEW_K * 32; i += 256) {
-        const int r = i / 32, c = i % 32 * 4, token = first + step * FEW_K + r;
-        const int n = token < last ? a.dim - col0 - c : 0;
-        copy4(to + r * 128 + c, n > 0 ? weight + token * weight_stride + col0 + c : weight, n, vec_w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = tid / 32 + 8 * q, token = first + step * FEW_K + r;
+        const int n = token < last ? a.dim - col0 - lane * 4 : 0;
+        copy4(to + r * 128 + lane * 4, n > 0 ? weight + token * weight_stride + col0 + lane * 4 : weight, n, vec_w);
       }
     }
     copy_group();
