@@ -14,6 +14,12 @@
 // then writes the entries' places among those that it wrote once more: lists say which
 // those are.  (By the threads that had the entries, behind a barrier, 4096 x 100256 bf16
 // with 64 entries took 326 us; 302 so.)
+//
+// With gradients 4096 x 100256 bfloat16 and 64 entries take 302 us (1.64 GB, 80% of the
+// measured copy bandwidth; the next-token loss 288) and 1023 x 200255 floats and 37 entries
+// 303; the loss alone 140 us (86%), the gradient from lse 255.  What it takes beyond the
+// next-token loss is some 1500 cycles a block between reading and writing: the entries'
+// shares, their logits and two more sums over the warps.
 #include <algorithm>
 
 #include "tt_rows.cuh"

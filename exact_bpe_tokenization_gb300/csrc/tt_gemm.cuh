@@ -13,6 +13,14 @@
 // more leaves in shared memory with the 128-byte swizzle.  An operand may be a sum
 // of up to three parts (32-bit values split into bfloat16 ones): then the products
 // of the listed pairs of parts are added up.
+//
+// 64 of the contraction of a tile take 0.31 us at the clocks that the power limit leaves
+// (0.27 at the highest), a tile 0.45 us more.  The tensor pipe is active for 88% of the cycles
+// with a contraction of 2048 and 96% with one of 25,000; without its epilogue's work the
+// loss of 4096 x 100256 takes as long (862 us and 861).  Five stages instead of six are as
+// fast, and tile rows passed through by 8 or 4 instead of 16 take 2 and 4% longer.
+// Clusters of two pairs, with B's halves multicast, would leave 8 SMs idle, which they do not
+// fit.
 #pragma once
 #include <cuda.h>
 

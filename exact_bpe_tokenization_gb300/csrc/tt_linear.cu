@@ -5,12 +5,24 @@
 //   G_ij = g_i (exp(l_ij - lse_i) - (j == t_i)),  dH = G W,  dW = G^T H
 //
 // The products run on the tensor cores (tt_gemm.cuh), and what would be the logits
-// never leaves them: the first product's epilogue keeps a maximum and a sum of each
-// row and tile, k_finish joins them, and the second run of the same product turns its
-// tiles into G.  G is in the operands' type, the one place where less than 32 bits
-// stands between the logits and the gradients; a chunk of rows of it (2 GB) is kept at
-// a time.  32-bit operands are split into three bfloat16 parts each, whose products
-// are added in 32 bits: what is left out is below 2^-24.
+// never leaves them.  Three products are the least; each of them is bound by the tensor
+// cores under the power limit (4096 x 100256 x 2048 bf16: 850, 860 and 897 us alone, 1.95
+// to 1.87 PFLOP/s; the measured peak is 1.92).
+//   The loss alone: one product, whose epilogue keeps a maximum and a sum of each row and
+// 128 tokens; k_finish joins them.
+//   With gradients, from bfloat16 and float: the first product's epilogue writes powers
+// exp(l - l_t) in the operands' type, which has a float's range, and sums them.  S = exp(loss)
+// is known behind it, so G = (powers - S (j == t)) g / S needs no second product: the factor
+// g / S is a row's of dhidden, and goes into a copy of hidden for dweight (rounded there, a
+// second time beside G).  Rows of a loss beyond 41 have G made anew.  2.76 ms for the sizes
+// above, of which the products are 2.61; 3.0 from an lse, where all of G is made anew.
+//   From 16-bit floats, which lack the range, the first product runs twice, for lse and for G.
+// G is the one place where less than 32 bits stands between the logits and the gradients
+// (float: three bfloat16 parts, whose products are added in 32 bits; what is left out is
+// below 2^-24).  A chunk of rows of it is kept at a time.  dhidden's long sums are cut into
+// parts that k_join adds; dweight's over chunks are kept in 32 bits.
+//   One row is bound by reading the weight: 1 x 100256 x 2048 bf16 takes 76 us and k_finish
+// 5 (411 MB, 5.4 TB/s in the product: five and a fraction rounds of tiles take six).
 #include "tt_gemm.cuh"
 #include "tt_rows.cuh"
 
@@ -899,9 +911,10 @@ struct Plan {
 };
 
 inline bool is_few(int64_t n, int32_t type) { return type == TT_F32 && n <= FEW; }
-// tokens a block of k_few_hidden takes: two blocks an SM, whole stages
+// tokens a block of k_few_hidden takes: two blocks an SM, whole stages, 128 at least (64 x 4352
+// x 64 with all gradients, from a graph: 45 us with 256, 39 with 128)
 inline int64_t few_each(int64_t vocab, int64_t dim) {
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * SMS / ((dim + 127) / 128), (vocab + 255) / 256));
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * SMS / ((dim + 127) / 128), (vocab + 127) / 128));
   return up((vocab + splits - 1) / splits, FEW_K);
 }
 
