@@ -322,7 +322,8 @@ tt_status tt_pretokenize_batch(tt_tokenizer *h,
  *
  * What a model does with the IDs on either side of it: looks up their vectors
  * (tt_embed, and tt_embed_grad for training), scores its predictions against
- * them (tt_token_loss, tt_token_loss_grad) and draws new ones (tt_sample).
+ * them (tt_token_loss, tt_linear_loss and tt_distill_loss with their gradients) and
+ * draws new ones (tt_sample).
  * The paper has no counterpart.  They need no handle and keep no state:
  * everything a call reads or writes is the caller's, scratch included, so
  * calls on different streams are independent as long as their buffers are.
@@ -337,7 +338,7 @@ tt_status tt_pretokenize_batch(tt_tokenizer *h,
  *     statistics are in 32 bits or more, and results are rounded from there
  *     to their type (to nearest even).
  *   - IDs are int32.  A negative ID is padding: it stands for no token.
- *     n_vocab is 1 .. 2^20, as in tt_create; dim is 1 .. 2^24.
+ *     n_vocab is 1 .. 2^20, as in tt_create; dim is 1 .. 2^24 unless stated.
  *   - d_status (device, int32, may be NULL): a kernel that meets a value this
  *     header does not allow writes its tt_status there if the word is
  *     TT_OK (0); it is never cleared.  Such an ID, target or sampling row is
@@ -350,7 +351,7 @@ tt_status tt_pretokenize_batch(tt_tokenizer *h,
 typedef enum { TT_F32 = 0, TT_F16 = 1, TT_BF16 = 2 } tt_dtype;
 
 /* The most IDs of one tt_embed or tt_embed_grad call and the most rows of one
- * tt_token_loss, tt_token_loss_grad or tt_sample call; more are rejected with
+ * call of a loss, its gradient or tt_sample; more are rejected with
  * TT_ERR_CAPACITY. */
 #define TT_MAX_IDS (1 << 29)
 
@@ -489,11 +490,13 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  *   G[i][j]    = row_grads[i] * (exp(l[i][j] - lse[i]) - (j == targets[i]))
  *   dhidden    = G * weight          dweight = G^T * hidden
  *
- * Products and sums are in 32 bits.  G is rounded to the type of hidden and weight
- * before its own products (TT_F32: it is not; 32-bit operands are multiplied in
- * parts whose neglected products are below 2^-24 of theirs).  With TT_F16 it is
- * scaled by a power of two first, so that the largest |row_grads| of a chunk of rows
- * becomes 2^14 there; what lies 2^-38 below that is lost.
+ * Products and sums are in 32 bits.  Before its own products G is rounded to the type
+ * of hidden and weight, and with TT_BF16 hidden too, once it is scaled, for dweight.
+ * (TT_F32: neither is; more than 64 rows are multiplied in parts whose neglected
+ * products are below 2^-24 of theirs.)  With TT_F16 G is scaled by a power of two
+ * first, so that the largest |row_grads| of a chunk of rows becomes 2^14 there; what
+ * lies 2^-38 below that is lost.  The loss may differ in its last bits between calls
+ * with gradients and without.
  *
  *   d_hidden   device, type [n_rows][dim], rows hidden_stride apart.
  *   d_weight   device, type [n_vocab][dim], rows weight_stride apart (the layout
@@ -512,7 +515,8 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  *              tt_linear_loss_workspace(...), else TT_ERR_CAPACITY; its contents
  *              before and after mean nothing.
  * A target >= n_vocab is padding and sets TT_ERR_INVALID_ARG in d_status.  NaN or
- * infinities in hidden or weight give NaN or infinities in what they enter.  A wait
+ * infinities in hidden or weight give NaN or infinities in what they enter; those in
+ * padding rows of hidden enter their lse alone.  A wait
  * within a kernel that ran out sets TT_ERR_TIMEOUT in d_status, and the outputs then
  * mean nothing.
  */
