@@ -274,8 +274,12 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
       // of theirs.  (TMA reads the border again for each row beyond it: 152 SMs at one
       // line of a single row took 124 us for 1 x 100256 x 2048 instead of 86.)
       const uint32_t bytes = (1 + (p.m * TILE + HALF < g.rows_a)) * g.box_a + (1 + (p.n * TILE + HALF < g.rows_b)) * (STAGE_BYTES / 2);
-      for (int i = 0; ok && i < g.pairs; ++i) {
-        for (int k = p.first; k < p.last; ++k) {
+      // few pairs: all of a block of the contraction, whose second reading comes from L2
+      const bool by_block = g.pairs < 6;
+      const int blocks = p.last - p.first, outer = by_block ? blocks : g.pairs, inner = by_block ? g.pairs : blocks;
+      for (int u = 0; ok && u < outer; ++u) {
+        for (int v = 0; v < inner; ++v) {
+          const int i = by_block ? v : u, k = p.first + (by_block ? u : v);
           if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) break;
           if (rank == 0) bar_expect(full + 8 * stage, bytes);
           const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
@@ -396,11 +400,13 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   g.n_tiles = (int)((rows_b + TILE - 1) / TILE);
   g.k_blocks = (int)(((A_MN ? a.rows : a.cols) + KB - 1) / KB);
   g.splits = splits;
-  // the products of parts whose orders add up to less than three, the smallest first (the
-  // sums are cut off, not rounded, at each step: small ones lose less); the rest is below 2^-24
-  g.pairs = a.parts == 1 ? 1 : 6;
-  g.pair_a = a.parts == 1 ? 0 : 0x001102;
-  g.pair_b = a.parts == 1 ? 0 : 0x010120;
+  // The products of parts whose orders add up to less than three (two parts: two), the
+  // smallest first (the sums are cut off, not rounded, at each step: small ones lose less).
+  // Three parts each: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), the rest is below 2^-24; two and
+  // two: (1,0) (0,1) (0,0); two and one: (1,0) (0,0).
+  g.pairs = a.parts == 3 ? 6 : a.parts == 1 ? 1 : b.parts == 2 ? 3 : 2;
+  g.pair_a = g.pairs == 6 ? 0x001102 : g.pairs == 1 ? 0 : 0x001;
+  g.pair_b = g.pairs == 6 ? 0x010120 : g.pairs == 3 ? 0x010 : 0;
   g.idesc = idesc_of(bf16, A_MN, B_MN);
   g.group = group;
   g.only = only;
@@ -421,7 +427,7 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
 constexpr int64_t LONGEST = 2048;
 inline int choose_splits(int64_t m, int64_t n, int64_t k, int pairs) {
   const int64_t tiles = ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE), blocks = (k + KB - 1) / KB;
-  const int64_t least_splits = pairs > 1 ? (k + LONGEST - 1) / LONGEST : 1;
+  const int64_t least_splits = pairs == 6 ? (k + LONGEST - 1) / LONGEST : 1;
   const int64_t most = std::max<int64_t>(least_splits, std::min<int64_t>(std::min<int64_t>(32, blocks), blocks * pairs / 4));
   int best = (int)least_splits;
   double least = 1e300;

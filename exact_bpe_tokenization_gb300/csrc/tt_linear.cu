@@ -66,15 +66,13 @@ constexpr int F16_UP = 14;                                 // G in 16 bits: the 
 struct RowInfo { float from, mul, g; int t; };
 
 // ------------------------------------------------------------ epilogues
-template <class T> using Element = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
-
-// 64 columns of a warp's rows to a matrix, T: float in three parts: a TMA store of 32
-// rows, from the warp's own memory.
-template <class T> __device__ __forceinline__ void put_box(const CUtensorMap *map, int row, int col, uint32_t own, float v[64], bool inside) {
-  using E = Element<T>;
+// 64 columns of a warp's rows to a matrix in PARTS parts of type E (each the rest of those
+// before): a TMA store of 32 rows, from the warp's own memory.
+template <class E, int PARTS>
+__device__ __forceinline__ void put_box(const CUtensorMap *map, int row, int col, uint32_t own, float v[64], bool inside) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int p = 0; p < (sizeof(T) == 2 ? 1 : 3); ++p) {
+  for (int p = 0; p < PARTS; ++p) {
     if (lane == 0) stores_read();
     __syncwarp();
 #pragma unroll
@@ -82,9 +80,9 @@ template <class T> __device__ __forceinline__ void put_box(const CUtensorMap *ma
     fence_copies();
     __syncwarp();
     if (lane == 0 && inside) store_box(map, col, row, p, own);
-    if (sizeof(T) == 4 && p < 2) {
+    if (p < PARTS - 1) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+      for (int i = 0; i < 64; ++i) v[i] -= to_f32(from_f32<E>(v[i]));
     }
   }
 }
@@ -155,7 +153,7 @@ struct StatsEpi {
 // written in the operands' type, whose range is a float's: precise for any loss that
 // is not absurd, and k_finish finds the rows for which they are not.  Where a sum
 // leaves the safe range, the columns are read once more with a maximum.
-template <class T> struct PowersEpi {
+template <class E, int PARTS> struct PowersEpi {
   CUtensorMap map;
   int n_rows, n_cols;
   const int32_t *targets;
@@ -205,7 +203,7 @@ template <class T> struct PowersEpi {
       if (!there)
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i] = 0;
-      put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
+      put_box<E, PARTS>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
     }
     if (mine && col < n_cols) part[(int64_t)(col / HALF) * n_rows + row] = p;
   }
@@ -218,10 +216,10 @@ __device__ __forceinline__ float f16_up(const uint32_t *g_max) {
   return g > 0 ? exp2f((float)min(max(F16_UP - 1 - ilogbf(g), -100), 100)) : 1.f;
 }
 
-// G in the operands' type (T: float, three parts).  16-bit floats lack the range for
+// G, in the operands' type or in bfloat16 parts.  16-bit floats lack the range for
 // a mean's 1 / n: there G is scaled by a power of two that brings the largest |g| to
 // 2^14, and the gradients' epilogue takes it back.
-template <class T> struct GradEpi {
+template <class E, int PARTS> struct GradEpi {
   CUtensorMap map;
   int n_rows, n_cols;
   const RowInfo *info;
@@ -256,7 +254,7 @@ template <class T> struct GradEpi {
       if (r.t < 0)
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i] = 0;
-      put_box<T>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
+      put_box<E, PARTS>(&map, row & ~31, col + c, own, v, (row & ~31) < n_rows && col + c < n_cols);
     }
   }
   __device__ __forceinline__ void end() const { stores_done(); }
@@ -426,17 +424,16 @@ template <class T> __device__ __forceinline__ void take8(const T *p, float v[8],
     for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
   }
 }
-// eight elements as TMA reads them: floats in three parts
-template <class T> __device__ __forceinline__ void pack8(uint16_t *to, int64_t part_stride, float v[8]) {
-  using E = Element<T>;
+// eight elements as TMA reads them, in parts of type E
+template <class E> __device__ __forceinline__ void pack8(uint16_t *to, int64_t part_stride, float v[8], int parts) {
   *reinterpret_cast<uint4 *>(to) = f32_vec(v, E{});
-  if (sizeof(T) == 4)
-    for (int p = 1; p < 3; ++p) {
+  for (int p = 1; p < parts; ++p) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
-      *reinterpret_cast<uint4 *>(to + p * part_stride) = f32_vec(v, E{});
-    }
+    for (int j = 0; j < 8; ++j) v[j] -= to_f32(from_f32<E>(v[j]));
+    *reinterpret_cast<uint4 *>(to + p * part_stride) = f32_vec(v, E{});
+  }
 }
+template <class T> using Element = typename std::conditional<sizeof(T) == 2, T, __nv_bfloat16>::type;
 
 // A matrix as TMA can read it: rows of whole 16-byte groups.
 struct Pack {
@@ -463,7 +460,7 @@ template <class T> __device__ __forceinline__ void pack_group(const Pack &p, int
   const int col = (int)(i - row * per) * 8;
   float v[8];
   take8((const T *)p.x + row * p.stride + col, v, min(8, dim - col), p.vec);
-  pack8<T>(p.out + row * width + col, p.rows * width, v);
+  pack8<Element<T>>(p.out + row * width + col, p.rows * width, v, sizeof(T) == 2 ? 1 : 3);
 }
 
 // What a chunk of rows begins with: operands laid out, the targets' logits (a warp a row, 0 for
@@ -512,11 +509,12 @@ struct RowArgs {
   const void *hidden;
   int64_t hidden_stride;
   int hidden_vec;
-  uint16_t *scaled;                                        // hidden by its scale, [parts][n_rows][width], or NULL
+  uint16_t *scaled;                                        // hidden by its scale, [scaled_parts][n_rows][width], or NULL
+  int scaled_parts;
   int width;
   uint16_t *g;
   int64_t g_stride, g_part;
-  int parts;
+  int parts;                                               // of G
 };
 
 // What G and hidden's scaled copy are made from.  With powers: G is left without the
@@ -632,11 +630,13 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
     const bool none = s_none[k];
 #pragma unroll
     for (int u = 0; u < 8; ++u) v[u] = none ? 0.f : v[u] * scale;
-    pack8<T>(a.scaled + at * a.width + c, (int64_t)a.n_rows * a.width, v);
+    uint16_t *to = a.scaled + at * a.width + c;
+    if (a.scaled_parts == 3) pack8<__nv_bfloat16>(to, (int64_t)a.n_rows * a.width, v, 3);
+    else pack8<Element<T>>(to, (int64_t)a.n_rows * a.width, v, a.scaled_parts);
   }
 }
 
-// ------------------------------------------------------------ few rows of floats
+// ------------------------------------------------------------ few rows
 // Up to 64 rows of 32-bit values: laying out the weight in parts and multiplying 256 rows,
 // six times, would cost several times what reading it once costs (1 x 200256 x 2096: 1490
 // us for the loss; the weight alone is 247).  Here the weight goes by asynchronous copies
@@ -644,8 +644,11 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // 1 row and for 8, 404 for 16, 667 for 32, 1187 for 64 (the latter bound by the products: 60%
 // of their rate), where the tensor cores take 1500 for any number up to 256.  A warp has
 // eight rows; warps that are left over divide the contraction.
-constexpr int FEW = 64, FEW_STAGES = 4;
-constexpr int FEW_K = 32, FEW_ROW = FEW_K + 4;             // of the contraction a stage; floats a row of it in shared memory
+// Up to eight rows of 16-bit values take the same way, for their precision: the tensor cores
+// cut off their sums at each step, and a single token's loss may be a small difference of
+// large logits.  1 x 100256 x 2048 bf16: XX us, 78 by the tensor cores.
+constexpr int FEW = 64, FEW_16 = 8, FEW_STAGES = 4;
+constexpr int FEW_ROW = 128 + 16;                          // bytes of a row a stage, and as it lies in shared memory
 
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
@@ -654,34 +657,42 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
   return r;
 }
-// four floats of which n are there (the others become zeros) from any address
-__device__ __forceinline__ void copy4(float *to, const float *from, int n, bool vec) {
+// 16 bytes of elements of which n are there (the others become zeros) from any address
+template <class T> __device__ __forceinline__ void copy16(uint8_t *to, const T *from, int n, bool vec) {
+  constexpr int E = 16 / sizeof(T);
   const uint32_t at = saddr(to);
   if (vec) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(max(0, min(4, n)) * 4) : "memory");
-  } else {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(max(0, min(E, n)) * (int)sizeof(T)) : "memory");
+  } else if (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < E; ++i)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + 4 * i), "l"(from + (i < n ? i : 0)), "r"(i < n ? 4 : 0) : "memory");
+  } else {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(from[i]) : 0.f;
+    *reinterpret_cast<uint4 *>(to) = f32_vec(v, Element<T>{});
   }
 }
 
 // The logits of 128 tokens a block, and what becomes of them: MODE 0 maxima and sums,
 // 1 powers and their sums, 2 G (see the epilogues above).
-template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const float *weight, int64_t weight_stride, bool vec_w) {
-  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = (128 + ROWS) * FEW_ROW;
+template <class T, int ROWS, int MODE>
+__global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const T *weight, int64_t weight_stride, bool vec_w) {
+  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = (128 + ROWS) * FEW_ROW, E = 16 / sizeof(T), STEP = 128 / sizeof(T);
   extern __shared__ uint4 s_few[];
+  uint8_t *bytes = reinterpret_cast<uint8_t *>(s_few);
   float *stages = reinterpret_cast<float *>(s_few);
   let_next_start();
   wait_for_last();
   if (MODE == 2 && a.only && !a.only[0]) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
-  const int col0 = blockIdx.x * 128, steps = (a.dim + FEW_K - 1) / FEW_K;
-  const float *hidden = (const float *)a.hidden;
-  // a thread copies four floats of every 32nd row: its places are found once
+  const int col0 = blockIdx.x * 128, steps = (a.dim + STEP - 1) / STEP;
+  const T *hidden = (const T *)a.hidden;
+  // a thread copies 16 bytes of every 32nd row: its places are found once
   constexpr int COPIES = 4 + (ROWS + 31) / 32;
-  const int k0 = tid % 8 * 4;
-  const float *from[COPIES];
+  const int k0 = tid % 8 * E;
+  const T *from[COPIES];
   int left[COPIES];                                        // of the contraction behind its first
 #pragma unroll
   for (int q = 0; q < COPIES; ++q) {
@@ -693,12 +704,12 @@ template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_lo
   }
   auto fetch = [&](int step) {
     if (step < steps) {
-      float *to = stages + step % FEW_STAGES * STAGE + tid / 8 * FEW_ROW + k0;
+      uint8_t *to = bytes + step % FEW_STAGES * STAGE + tid / 8 * FEW_ROW + tid % 8 * 16;
 #pragma unroll
       for (int q = 0; q < COPIES; ++q) {
         if (q >= 4 && ROWS < 32 && tid / 8 >= ROWS) break;
-        const int n = left[q] - step * FEW_K;
-        copy4(to + (q < 4 ? 32 * q : 128 + 32 * (q - 4)) * FEW_ROW, n > 0 ? from[q] + step * FEW_K : from[q], n, q < 4 ? vec_w : a.hidden_vec);
+        const int n = left[q] - step * STEP;
+        copy16(to + (q < 4 ? 32 * q : 128 + 32 * (q - 4)) * FEW_ROW, n > 0 ? from[q] + step * STEP : from[q], n, q < 4 ? vec_w : a.hidden_vec);
       }
     }
     copy_group();
@@ -714,20 +725,20 @@ template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_lo
     copy_wait<FEW_STAGES - 2>();
     __syncthreads();
     fetch(step + FEW_STAGES - 1);
-    const float *w = stages + step % FEW_STAGES * STAGE, *h = w + 128 * FEW_ROW + group * 8 * FEW_ROW;
+    const uint8_t *w = bytes + step % FEW_STAGES * STAGE, *h = w + (128 + group * 8) * FEW_ROW;
 #pragma unroll 1
-    for (int k = share * (FEW_K / SHARES); k < (share + 1) * (FEW_K / SHARES); k += 4) {
-      float4 x[4];
+    for (int k = share * (8 / SHARES); k < (share + 1) * (8 / SHARES); ++k) {
+      float x[4][E];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const float4 *>(w + (lane + 32 * j) * FEW_ROW + k);
+      for (int j = 0; j < 4; ++j) vec_f32(*reinterpret_cast<const uint4 *>(w + (lane + 32 * j) * FEW_ROW + k * 16), x[j], T{});
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        const float4 y = *reinterpret_cast<const float4 *>(h + m * FEW_ROW + k);
+        float y[E];
+        vec_f32(*reinterpret_cast<const uint4 *>(h + m * FEW_ROW + k * 16), y, T{});
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[m][j] = fma2(make_float2(x[j].x, x[j].y), make_float2(y.x, y.y), acc[m][j]);
-          acc[m][j] = fma2(make_float2(x[j].z, x[j].w), make_float2(y.z, y.w), acc[m][j]);
-        }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < E; e += 2) acc[m][j] = fma2(make_float2(x[j][e], x[j][e + 1]), make_float2(y[e], y[e + 1]), acc[m][j]);
       }
     }
   }
@@ -798,9 +809,12 @@ template <int ROWS, int MODE> __global__ void __launch_bounds__(256, 2) k_few_lo
 }
 
 // dhidden's sums over a share of the tokens, by 128 columns a block: [share][n_rows][width]
-template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const float *weight, int64_t weight_stride, bool vec_w, int each, float *sums) {
-  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = FEW_K * 128 + FEW_K * ROWS;
+constexpr int FEW_K = 32;                                  // tokens a stage
+template <class T, int ROWS>
+__global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weight, int64_t weight_stride, bool vec_w, int each, float *sums) {
+  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, E = 16 / sizeof(T), ROW = 128 * sizeof(T), STAGE = FEW_K * (ROW + ROWS * 4);
   extern __shared__ uint4 s_few[];
+  uint8_t *bytes = reinterpret_cast<uint8_t *>(s_few);
   float *stages = reinterpret_cast<float *>(s_few);
   let_next_start();
   wait_for_last();
@@ -809,12 +823,12 @@ template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowAr
   // a stage: 32 tokens' 128 columns, and G of the rows and those tokens, [token][row]
   auto fetch = [&](int step) {
     if (step < steps) {
-      float *to = stages + step % FEW_STAGES * STAGE;
+      uint8_t *to = bytes + step % FEW_STAGES * STAGE;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = tid / 32 + 8 * q, token = first + step * FEW_K + r;
-        const int n = token < last ? a.dim - col0 - lane * 4 : 0;
-        copy4(to + r * 128 + lane * 4, n > 0 ? weight + token * weight_stride + col0 + lane * 4 : weight, n, vec_w);
+      for (int q = 0; q < FEW_K * ROW / 16 / 256; ++q) {
+        const int i = tid + 256 * q, r = i / (ROW / 16), c = i % (ROW / 16) * E, token = first + step * FEW_K + r;
+        const int n = token < last ? a.dim - col0 - c : 0;
+        copy16(to + i * 16, n > 0 ? weight + token * weight_stride + col0 + c : weight, n, vec_w);
       }
     }
     copy_group();
@@ -831,7 +845,7 @@ template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowAr
   };
   auto give = [&](int step) {
     if (step >= steps || g_row >= ROWS) return;
-    float *to = stages + step % FEW_STAGES * STAGE + FEW_K * 128 + g_row;
+    float *to = reinterpret_cast<float *>(bytes + step % FEW_STAGES * STAGE + FEW_K * ROW) + g_row;
     float v[8], w[8], x[8];
     vec_f32(part[0], v, __nv_bfloat16{});
     vec_f32(part[1], w, __nv_bfloat16{});
@@ -852,16 +866,24 @@ template <int ROWS> __global__ void __launch_bounds__(256, 2) k_few_hidden(RowAr
     copy_wait<FEW_STAGES - 2>();
     __syncthreads();
     fetch(step + FEW_STAGES - 1);
-    const float *w = stages + step % FEW_STAGES * STAGE, *g = w + FEW_K * 128 + group * 8;
+    const uint8_t *w = bytes + step % FEW_STAGES * STAGE;
+    const float *g = reinterpret_cast<const float *>(w + FEW_K * ROW) + group * 8;
 #pragma unroll 4
     for (int j = share; j < FEW_K; j += SHARES) {
-      const float4 x = *reinterpret_cast<const float4 *>(w + j * 128 + lane * 4);
+      float x[4];
+      if (sizeof(T) == 4) {
+        vec_f32(*reinterpret_cast<const uint4 *>(w + j * ROW + lane * 16), x, float{});
+      } else {
+        const uint2 two = *reinterpret_cast<const uint2 *>(w + j * ROW + lane * 8);
+        two_f32(two.x, x, Element<T>{});
+        two_f32(two.y, x + 2, Element<T>{});
+      }
       const float4 y0 = *reinterpret_cast<const float4 *>(g + j * ROWS), y1 = *reinterpret_cast<const float4 *>(g + j * ROWS + 4);
       const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        acc[m][0] = fma2(make_float2(x.x, x.y), make_float2(y[m], y[m]), acc[m][0]);
-        acc[m][1] = fma2(make_float2(x.z, x.w), make_float2(y[m], y[m]), acc[m][1]);
+        acc[m][0] = fma2(make_float2(x[0], x[1]), make_float2(y[m], y[m]), acc[m][0]);
+        acc[m][1] = fma2(make_float2(x[2], x[3]), make_float2(y[m], y[m]), acc[m][1]);
       }
     }
   }
@@ -910,7 +932,13 @@ struct Plan {
   int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
 };
 
-inline bool is_few(int64_t n, int32_t type) { return type == TT_F32 && n <= FEW; }
+inline bool is_few(int64_t n, int32_t type) { return n <= (type == TT_F32 ? FEW : FEW_16); }
+// Parts of G, and of hidden's scaled copy: rounded to 16 bits once each, a few rows' gradients
+// are off by up to the whole of such a rounding, where those of many rows average it (dweight of
+// 16 rows of bf16 by 3.3e-3 of its size, of 512 by 2.9e-3; a rounding of its own is 1.7e-3).
+// Up to 64 rows the second part is nearly free.
+inline int g_parts(int64_t n, int32_t type) { return type == TT_F32 || is_few(n, type) ? 3 : n <= FEW ? 2 : 1; }
+inline int scaled_parts(int64_t n, int32_t type) { return type == TT_F16 && !is_few(n, type) ? 1 : g_parts(n, type); }
 // tokens a block of k_few_hidden takes: two blocks an SM, whole stages, 128 at least (64 x 4352
 // x 64 with all gradients, from a graph: 45 us with 256, 39 with 128)
 inline int64_t few_each(int64_t vocab, int64_t dim) {
@@ -928,14 +956,15 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   p.g_stride = up(vocab, 64);
   const int64_t halves = (vocab + HALF - 1) / HALF;
   int64_t most = PARTIALS / (halves * 8);
-  if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * parts));
+  const int of_g = g_parts(n, type), of_h = scaled_parts(n, type);
+  if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * of_g));
   if (pack_h || dw) most = std::min(most, KEPT / (p.width * 2 * parts));   // copies of hidden
   most = std::max<int64_t>(most / TILE * TILE, TILE);
   const int64_t chunks = (n + most - 1) / most;
   p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
-  const int pairs = parts == 1 ? 1 : 6;
+  const int pairs = parts == 1 ? of_g : 6;
   p.split_h = is_few(n, type) ? (int)((vocab + few_each(vocab, dim) - 1) / few_each(vocab, dim)) : choose_splits(p.chunk, dim, vocab, pairs);
-  p.split_w = choose_splits(vocab, dim, p.chunk, pairs);
+  p.split_w = choose_splits(vocab, dim, p.chunk, of_g == 3 ? 6 : of_g * 2 - 1);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -950,8 +979,8 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   p.word = take(4 * p.words);
   if (grad) {
     p.info = take(sizeof(RowInfo) * p.chunk);
-    p.scaled = take(dw ? p.chunk * p.width * 2 * parts : 0);
-    p.g = take(p.g_stride * 2 * parts * p.chunk);
+    p.scaled = take(dw ? p.chunk * p.width * 2 * of_h : 0);
+    p.g = take(p.g_stride * 2 * of_g * p.chunk);
     p.acc = take(dw && !dw_f32 && p.chunk < n ? vocab * p.width * 4 : 0);
     int64_t sums = 0;
     if (dh && (p.split_h > 1 || is_few(n, type))) sums = std::max(sums, p.split_h * p.chunk * p.width * 4);
@@ -996,51 +1025,62 @@ bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sum
   return ok;
 }
 
-template <class T, int ROWS> struct FewTag {};
+template <class T, int ROWS, int MODE> struct FewTag {};
 // f(number of rows that there is a kernel for)
-template <class F> void with_rows(int n, F f) {
-  if (n <= 8) f(std::integral_constant<int, 8>{});
+template <class T, class F> void with_rows(int n, F f) {
+  if (sizeof(T) == 2 || n <= 8) f(std::integral_constant<int, 8>{});
   else if (n <= 16) f(std::integral_constant<int, 16>{});
   else if (n <= 32) f(std::integral_constant<int, 32>{});
   else f(std::integral_constant<int, 64>{});
 }
-template <int MODE> bool few_logits(const Call &c, const RowArgs &r, cudaStream_t stream) {
+template <class T, int MODE> bool few_logits(const Call &c, const RowArgs &r, cudaStream_t stream) {
   bool ok = true;
-  with_rows(r.n_rows, [&](auto rows) {
-    constexpr int ROWS = decltype(rows)::value;
-    const int shared = FEW_STAGES * (128 + ROWS) * FEW_ROW * 4;
-    auto k = k_few_logits<ROWS, MODE>;
-    if (!(ok = !allow_shared<FewTag<std::integral_constant<int, MODE>, ROWS>>(k, shared))) return;
-    launch_cluster(k, dim3(r.n_parts), 256, shared, 1, true, stream, r, (const float *)c.weight, c.weight_stride,
-                   vec_of(c.weight, c.weight_stride, TT_F32) != 0);
-  });
+  auto run = [&](auto rows) {
+    constexpr int ROWS = sizeof(T) == 2 ? 8 : decltype(rows)::value;
+    const int shared = FEW_STAGES * (128 + ROWS) * FEW_ROW;
+    auto k = k_few_logits<T, ROWS, MODE>;
+    if (!(ok = !allow_shared<FewTag<T, ROWS, MODE>>(k, shared))) return;
+    launch_cluster(k, dim3(r.n_parts), 256, shared, 1, true, stream, r, (const T *)c.weight, c.weight_stride,
+                   vec_of(c.weight, c.weight_stride, c.type) != 0);
+  };
+  with_rows<T>(r.n_rows, run);
   return ok;
 }
-bool few_hidden(const Call &c, const RowArgs &r, const Plan &p, float *sums, const Target &o, cudaStream_t stream) {
+template <class T> bool few_hidden(const Call &c, const RowArgs &r, const Plan &p, float *sums, const Target &o, cudaStream_t stream) {
   bool ok = true;
-  with_rows(r.n_rows, [&](auto rows) {
-    constexpr int ROWS = decltype(rows)::value;
-    const int shared = FEW_STAGES * FEW_K * (128 + ROWS) * 4;
-    auto k = k_few_hidden<ROWS>;
-    if (!(ok = !allow_shared<FewTag<float, ROWS>>(k, shared))) return;
-    launch_cluster(k, dim3((unsigned)((c.dim + 127) / 128), (unsigned)p.split_h), 256, shared, 1, true, stream, r, (const float *)c.weight,
-                   c.weight_stride, vec_of(c.weight, c.weight_stride, TT_F32) != 0, (int)few_each(c.vocab, c.dim), sums);
-  });
-  if (ok) join<float>(sums, p.split_h, p.width, o, stream);
+  auto run = [&](auto rows) {
+    constexpr int ROWS = sizeof(T) == 2 ? 8 : decltype(rows)::value;
+    const int shared = FEW_STAGES * FEW_K * (128 * (int)sizeof(T) + ROWS * 4);
+    auto k = k_few_hidden<T, ROWS>;
+    if (!(ok = !allow_shared<FewTag<T, ROWS, 3>>(k, std::max(shared, 64 * 128 * 4)))) return;
+    launch_cluster(k, dim3((unsigned)((c.dim + 127) / 128), (unsigned)p.split_h), 256, std::max(shared, 64 * 128 * 4), 1, true, stream, r,
+                   (const T *)c.weight, c.weight_stride, vec_of(c.weight, c.weight_stride, c.type) != 0, (int)few_each(c.vocab, c.dim), sums);
+  };
+  with_rows<T>(r.n_rows, run);
+  if (ok) join<T>(sums, p.split_h, p.width, o, stream);
   return ok;
 }
 
-// the product of hidden and weight into powers, or into G; T: the operands' type
-template <class T> bool make_powers(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
-  PowersEpi<T> e{{}, r.n_rows, r.n_vocab, r.targets, r.target_logit, r.part, r.target_power};
+// the product of hidden and weight into powers, or into G, in as many parts as g has
+template <class E, int PARTS> bool powers_to(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  PowersEpi<E, PARTS> e{{}, r.n_rows, r.n_vocab, r.targets, r.target_logit, r.part, r.target_power};
   if (encode_map(&e.map, true, g, 32) != CUDA_SUCCESS) return false;
   return run_gemm<false, false>(true, h, w, 1, 16, e, r.status, stream);
 }
-template <class T> bool make_g(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
-  const bool bf16 = !std::is_same<T, __half>::value;
-  GradEpi<T> e{{}, r.n_rows, r.n_vocab, r.info, r.g_max};
+bool make_powers(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  using B = __nv_bfloat16;
+  return g.parts == 1 ? powers_to<B, 1>(h, w, g, r, stream) : g.parts == 2 ? powers_to<B, 2>(h, w, g, r, stream) : powers_to<B, 3>(h, w, g, r, stream);
+}
+template <class E, int PARTS> bool g_to(const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  const bool bf16 = !std::is_same<E, __half>::value;
+  GradEpi<E, PARTS> e{{}, r.n_rows, r.n_vocab, r.info, r.g_max};
   if (encode_map(&e.map, bf16, g, 32) != CUDA_SUCCESS) return false;
   return run_gemm<false, false>(bf16, h, w, 1, 16, e, r.status, stream, r.only);
+}
+bool make_g(bool bf16, const Matrix &h, const Matrix &w, const Matrix &g, const RowArgs &r, cudaStream_t stream) {
+  using B = __nv_bfloat16;
+  if (!bf16) return g.parts == 1 ? g_to<__half, 1>(h, w, g, r, stream) : g_to<__half, 2>(h, w, g, r, stream);
+  return g.parts == 1 ? g_to<B, 1>(h, w, g, r, stream) : g.parts == 2 ? g_to<B, 2>(h, w, g, r, stream) : g_to<B, 3>(h, w, g, r, stream);
 }
 
 template <class T> void finish(const RowArgs &r, cudaStream_t stream) {
@@ -1053,11 +1093,11 @@ template <class T> void finish(const RowArgs &r, cudaStream_t stream) {
 bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) {
   const int parts = c.type == TT_F32 ? 3 : 1;
   const size_t size = type_size(c.type);
-  const bool bf16 = c.type != TT_F16, grad = c.dhidden || c.dweight;
+  const bool bf16 = c.type != TT_F16, grad = c.dhidden || c.dweight, few = is_few(c.n, c.type);
+  const int of_g = g_parts(c.n, c.type), of_h = scaled_parts(c.n, c.type);
   // a 16-bit float has no range for powers: the product runs twice, for lse and for G
-  const bool powers = grad && !c.lse_in && c.type != TT_F16;
+  const bool powers = grad && !c.lse_in && (c.type != TT_F16 || few);
   Matrix w{c.weight, c.vocab, c.dim, c.weight_stride, parts, 8};
-  const bool few = is_few(c.n, c.type);
   const bool pack_h = !few && needs_pack(c.type, c.hidden, c.hidden_stride), pack_w = !few && needs_pack(c.type, c.weight, c.weight_stride);
   if (pack_w) w = Matrix{ws + p.weight, c.vocab, c.dim, p.width, parts, c.vocab * p.width};
   RowArgs r{};
@@ -1071,14 +1111,15 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
   r.hidden_stride = c.hidden_stride;
   r.hidden_vec = vec_of(c.hidden, c.hidden_stride, c.type);
   r.width = (int)p.width;
-  r.parts = parts;
+  r.parts = of_g;
+  r.scaled_parts = of_h;
   r.g_stride = p.g_stride;
   r.g_part = p.chunk * p.g_stride;
   if (grad) {
     r.info = (RowInfo *)(ws + p.info);
     r.g = (uint16_t *)(ws + p.g);
     if (c.dweight) r.scaled = (uint16_t *)(ws + p.scaled);
-    if (c.type == TT_F16) r.g_max = (uint32_t *)(ws + p.word);
+    if (c.type == TT_F16 && !few) r.g_max = (uint32_t *)(ws + p.word);
     if (powers) {
       r.target_power = r.target_logit + p.chunk;
       r.only = (int32_t *)(ws + p.word);
@@ -1107,7 +1148,7 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     r.lse_in = c.lse_in ? c.lse_in + row0 : nullptr;
     r.loss = c.loss ? c.loss + row0 : nullptr;
     r.lse = c.lse ? c.lse + row0 : nullptr;
-    const Matrix g{r.g, n, c.vocab, p.g_stride, parts, r.g_part};
+    const Matrix g{r.g, n, c.vocab, p.g_stride, of_g, r.g_part};
     Matrix hc{r.hidden, n, c.dim, c.hidden_stride, parts, 8};
     if (pack_h) hc = Matrix{ws + p.hidden, n, c.dim, p.width, parts, n * p.width};
     begin.hidden = Pack{pack_h ? r.hidden : nullptr, n, c.hidden_stride, r.hidden_vec, (uint16_t *)(ws + p.hidden)};
@@ -1122,12 +1163,11 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
         launch_cluster(k_begin<decltype(t)>, dim3((unsigned)std::min<int64_t>((units + 255) / 256, SMS * 16)), 256, 0, 1, true, stream, begin);
       });
     bool ok = true;
-    if (powers) {
-      if (few) ok = few_logits<1>(c, r, stream);
-      else if (c.type == TT_F32) ok = make_powers<float>(hc, w, g, r, stream);
-      else ok = make_powers<__nv_bfloat16>(hc, w, g, r, stream);
-    } else if (few && !c.lse_in) {
-      ok = few_logits<0>(c, r, stream);
+    if (few) {
+      if (!c.lse_in)
+        with_type(c.type, [&](auto t) { ok = powers ? few_logits<decltype(t), 1>(c, r, stream) : few_logits<decltype(t), 0>(c, r, stream); });
+    } else if (powers) {
+      ok = make_powers(hc, w, g, r, stream);
     } else if (!c.lse_in) {
       const StatsEpi e{n, (int)c.vocab, r.targets, r.part, r.target_logit};
       ok = run_gemm<false, false>(bf16, hc, w, 1, 16, e, c.status, stream);
@@ -1136,7 +1176,7 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     with_type(c.type, [&](auto t) {
       using T = decltype(t);
       finish<T>(r, stream);
-      if (grad) ok = few ? few_logits<2>(c, r, stream) : make_g<T>(hc, w, g, r, stream);
+      if (grad) ok = few ? few_logits<T, 2>(c, r, stream) : make_g(bf16, hc, w, g, r, stream);
     });
     if (!ok) return false;
     if (!grad) continue;
@@ -1144,7 +1184,7 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     if (c.dhidden) {
       const Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * size, c.dhidden_stride, nullptr, 0, TT_F32, r.g_max,
                      powers ? r.row_scale : nullptr, vec_of(c.dhidden, c.dhidden_stride, c.type)};
-      if (few) ok = few_hidden(c, r, p, sums, o, stream);
+      if (few) with_type(c.type, [&](auto t) { ok = few_hidden<decltype(t)>(c, r, p, sums, o, stream); });
       else ok = product<false>(bf16, g, w, p.split_h, sums, p.width, c.type, o, c.status, stream);
       if (!ok) return false;
     }
@@ -1167,8 +1207,8 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
         o.src = ws + p.acc;
         o.src_stride = p.width;
       }
-      const Matrix scaled{r.scaled, n, c.dim, p.width, parts, n * p.width};
-      if (!product<true>(bf16, g, scaled, p.split_w, sums, p.width, type, o, c.status, stream)) return false;
+      const Matrix scaled{r.scaled, n, c.dim, p.width, of_h, n * p.width};
+      if (!product<true>(bf16 || few, g, scaled, p.split_w, sums, p.width, type, o, c.status, stream)) return false;
     }
   }
   if (c.n == 0 && c.dweight && !c.accumulate) {
