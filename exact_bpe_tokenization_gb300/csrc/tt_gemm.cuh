@@ -274,22 +274,27 @@ __global__ void __cluster_dims__(2) __launch_bounds__(THREADS, 1)
       // of theirs.  (TMA reads the border again for each row beyond it: 152 SMs at one
       // line of a single row took 124 us for 1 x 100256 x 2048 instead of 86.)
       const uint32_t bytes = (1 + (p.m * TILE + HALF < g.rows_a)) * g.box_a + (1 + (p.n * TILE + HALF < g.rows_b)) * (STAGE_BYTES / 2);
-      // few pairs: all of a block of the contraction, whose second reading comes from L2
-      const bool by_block = g.pairs < 6;
-      const int blocks = p.last - p.first, outer = by_block ? blocks : g.pairs, inner = by_block ? g.pairs : blocks;
-      for (int u = 0; ok && u < outer; ++u) {
-        for (int v = 0; v < inner; ++v) {
-          const int i = by_block ? v : u, k = p.first + (by_block ? u : v);
-          if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) break;
-          if (rank == 0) bar_expect(full + 8 * stage, bytes);
-          const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
-          if (ra < g.rows_a) Operand<A_MN>::load(to, &map_a, ra, k * KB, g.pair_a >> (4 * i) & 15, bar);
-          if (rb < g.rows_b) Operand<B_MN>::load(to + STAGE_BYTES / 2, &map_b, rb, k * KB, g.pair_b >> (4 * i) & 15, bar);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+      auto copy = [&](int i, int k) {
+        if (!(ok = bar_wait(empty + 8 * stage, phase, &s_dead))) return false;
+        if (rank == 0) bar_expect(full + 8 * stage, bytes);
+        const uint32_t bar = in_block(full + 8 * stage, 0), to = stages + stage * STAGE_BYTES;
+        if (ra < g.rows_a) Operand<A_MN>::load(to, &map_a, ra, k * KB, g.pair_a >> (4 * i) & 15, bar);
+        if (rb < g.rows_b) Operand<B_MN>::load(to + STAGE_BYTES / 2, &map_b, rb, k * KB, g.pair_b >> (4 * i) & 15, bar);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
+        return true;
+      };
+      if (g.pairs == 2 || g.pairs == 3) {
+        // all of a block of the contraction: its second reading comes from L2
+        for (int k = p.first; ok && k < p.last; ++k)
+          for (int i = 0; i < g.pairs; ++i)
+            if (!copy(i, k)) break;
+      } else {
+        for (int i = 0; ok && i < g.pairs; ++i)
+          for (int k = p.first; k < p.last; ++k)
+            if (!copy(i, k)) break;
       }
       next = place_of(g, p.t + n_pairs, n_tiles, n_pairs);
     }

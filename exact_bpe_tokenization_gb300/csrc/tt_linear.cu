@@ -647,8 +647,22 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // Up to eight rows of 16-bit values take the same way, for their precision: the tensor cores
 // cut off their sums at each step, and a single token's loss may be a small difference of
 // large logits.  1 x 100256 x 2048 bf16: XX us, 78 by the tensor cores.
-constexpr int FEW = 64, FEW_16 = 8, FEW_STAGES = 4;
-constexpr int FEW_ROW = 128 + 16;                          // bytes of a row a stage, and as it lies in shared memory
+constexpr int FEW = 64, FEW_16 = 4;
+// What a kernel for up to ROWS rows copies at a time, and how far ahead: few rows are little
+// work a stage, so that larger ones pay (of 128 bytes a token instead of 256, 8 x 100256 x
+// 2048 bf16 took 126 us).
+template <int ROWS> struct FewShape {
+  static constexpr int EACH = ROWS < 8 ? ROWS : 8;         // rows a warp
+  static constexpr int GROUPS = ROWS / EACH, SHARES = 8 / GROUPS;
+  static constexpr int BYTES = ROWS <= 8 ? 256 : 128, LINE = BYTES + 16;  // of a row of the operands, and as it lies in shared memory
+  static constexpr int STAGES = ROWS <= 8 ? 3 : 4;
+  static constexpr int TOKENS = ROWS <= 8 ? 64 : 32;       // of k_few_hidden
+  static constexpr int SHARED_LOGITS = STAGES * (128 + ROWS) * LINE;
+  template <class T> static constexpr int shared_hidden() {
+    const int a = STAGES * TOKENS * (128 * (int)sizeof(T) + ROWS * 4), b = SHARES * ROWS * 128 * 4;
+    return a > b ? a : b;
+  }
+};
 
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
@@ -679,7 +693,9 @@ template <class T> __device__ __forceinline__ void copy16(uint8_t *to, const T *
 // 1 powers and their sums, 2 G (see the epilogues above).
 template <class T, int ROWS, int MODE>
 __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const T *weight, int64_t weight_stride, bool vec_w) {
-  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, STAGE = (128 + ROWS) * FEW_ROW, E = 16 / sizeof(T), STEP = 128 / sizeof(T);
+  using S = FewShape<ROWS>;
+  constexpr int EACH = S::EACH, GROUPS = S::GROUPS, SHARES = S::SHARES, LINE = S::LINE, STAGES = S::STAGES, STAGE = (128 + ROWS) * LINE;
+  constexpr int E = 16 / sizeof(T), STEP = S::BYTES / sizeof(T), CHUNKS = S::BYTES / 16, PASS = 256 / CHUNKS;
   extern __shared__ uint4 s_few[];
   uint8_t *bytes = reinterpret_cast<uint8_t *>(s_few);
   float *stages = reinterpret_cast<float *>(s_few);
@@ -689,52 +705,53 @@ __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const T *weigh
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
   const int col0 = blockIdx.x * 128, steps = (a.dim + STEP - 1) / STEP;
   const T *hidden = (const T *)a.hidden;
-  // a thread copies 16 bytes of every 32nd row: its places are found once
-  constexpr int COPIES = 4 + (ROWS + 31) / 32;
-  const int k0 = tid % 8 * E;
+  // a thread copies 16 bytes of every PASS-th row: its places are found once
+  constexpr int OF_W = 128 / PASS, COPIES = OF_W + (ROWS + PASS - 1) / PASS;
+  const int k0 = tid % CHUNKS * E;
   const T *from[COPIES];
   int left[COPIES];                                        // of the contraction behind its first
 #pragma unroll
   for (int q = 0; q < COPIES; ++q) {
-    const int r = tid / 8 + 32 * (q & 3);
-    const bool w = q < 4, there = w ? col0 + r < a.n_vocab : r < a.n_rows;
+    const bool w = q < OF_W;
+    const int r = tid / CHUNKS + PASS * (w ? q : q - OF_W);
+    const bool there = w ? col0 + r < a.n_vocab : r < a.n_rows;
     left[q] = there ? a.dim - k0 : 0;
     from[q] = w ? weight : hidden;
     if (left[q] > 0) from[q] += w ? (col0 + r) * weight_stride + k0 : r * a.hidden_stride + k0;
   }
   auto fetch = [&](int step) {
     if (step < steps) {
-      uint8_t *to = bytes + step % FEW_STAGES * STAGE + tid / 8 * FEW_ROW + tid % 8 * 16;
+      uint8_t *to = bytes + step % STAGES * STAGE + tid / CHUNKS * LINE + tid % CHUNKS * 16;
 #pragma unroll
       for (int q = 0; q < COPIES; ++q) {
-        if (q >= 4 && ROWS < 32 && tid / 8 >= ROWS) break;
+        if (q >= OF_W && ROWS < PASS && tid / CHUNKS >= ROWS) break;
         const int n = left[q] - step * STEP;
-        copy16(to + (q < 4 ? 32 * q : 128 + 32 * (q - 4)) * FEW_ROW, n > 0 ? from[q] + step * STEP : from[q], n, q < 4 ? vec_w : a.hidden_vec);
+        copy16(to + (q < OF_W ? PASS * q : 128 + PASS * (q - OF_W)) * LINE, n > 0 ? from[q] + step * STEP : from[q], n, q < OF_W ? vec_w : a.hidden_vec);
       }
     }
     copy_group();
   };
 #pragma unroll
-  for (int i = 0; i < FEW_STAGES - 1; ++i) fetch(i);
-  float2 acc[8][4];
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  float2 acc[EACH][4];
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < EACH; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[m][j] = make_float2(0, 0);
   for (int step = 0; step < steps; ++step) {
-    copy_wait<FEW_STAGES - 2>();
+    copy_wait<STAGES - 2>();
     __syncthreads();
-    fetch(step + FEW_STAGES - 1);
-    const uint8_t *w = bytes + step % FEW_STAGES * STAGE, *h = w + (128 + group * 8) * FEW_ROW;
+    fetch(step + STAGES - 1);
+    const uint8_t *w = bytes + step % STAGES * STAGE, *h = w + (128 + group * EACH) * LINE;
 #pragma unroll 1
-    for (int k = share * (8 / SHARES); k < (share + 1) * (8 / SHARES); ++k) {
+    for (int k = share * (CHUNKS / SHARES); k < (share + 1) * (CHUNKS / SHARES); ++k) {
       float x[4][E];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vec_f32(*reinterpret_cast<const uint4 *>(w + (lane + 32 * j) * FEW_ROW + k * 16), x[j], T{});
+      for (int j = 0; j < 4; ++j) vec_f32(*reinterpret_cast<const uint4 *>(w + (lane + 32 * j) * LINE + k * 16), x[j], T{});
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
+      for (int m = 0; m < EACH; ++m) {
         float y[E];
-        vec_f32(*reinterpret_cast<const uint4 *>(h + m * FEW_ROW + k * 16), y, T{});
+        vec_f32(*reinterpret_cast<const uint4 *>(h + m * LINE + k * 16), y, T{});
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -746,9 +763,9 @@ __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const T *weigh
   copy_wait<0>();
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < EACH; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) stages[(share * ROWS + group * 8 + m) * 128 + lane + 32 * j] = acc[m][j].x + acc[m][j].y;
+    for (int j = 0; j < 4; ++j) stages[(share * ROWS + group * EACH + m) * 128 + lane + 32 * j] = acc[m][j].x + acc[m][j].y;
   __syncthreads();
   const int col = col0 + lane * 4;
   for (int row = warp; row < a.n_rows; row += 8) {
@@ -809,34 +826,35 @@ __global__ void __launch_bounds__(256, 2) k_few_logits(RowArgs a, const T *weigh
 }
 
 // dhidden's sums over a share of the tokens, by 128 columns a block: [share][n_rows][width]
-constexpr int FEW_K = 32;                                  // tokens a stage
 template <class T, int ROWS>
 __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weight, int64_t weight_stride, bool vec_w, int each, float *sums) {
-  constexpr int GROUPS = ROWS / 8, SHARES = 8 / GROUPS, E = 16 / sizeof(T), ROW = 128 * sizeof(T), STAGE = FEW_K * (ROW + ROWS * 4);
+  using S = FewShape<ROWS>;
+  constexpr int EACH = S::EACH, GROUPS = S::GROUPS, SHARES = S::SHARES, STAGES = S::STAGES, TOKENS = S::TOKENS;
+  constexpr int E = 16 / sizeof(T), ROW = 128 * sizeof(T), STAGE = TOKENS * (ROW + ROWS * 4);
   extern __shared__ uint4 s_few[];
   uint8_t *bytes = reinterpret_cast<uint8_t *>(s_few);
   float *stages = reinterpret_cast<float *>(s_few);
   let_next_start();
   wait_for_last();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
-  const int col0 = blockIdx.x * 128, first = blockIdx.y * each, last = min(a.n_vocab, first + each), steps = (last - first + FEW_K - 1) / FEW_K;
+  const int col0 = blockIdx.x * 128, first = blockIdx.y * each, last = min(a.n_vocab, first + each), steps = (last - first + TOKENS - 1) / TOKENS;
   // a stage: 32 tokens' 128 columns, and G of the rows and those tokens, [token][row]
   auto fetch = [&](int step) {
     if (step < steps) {
-      uint8_t *to = bytes + step % FEW_STAGES * STAGE;
+      uint8_t *to = bytes + step % STAGES * STAGE;
 #pragma unroll
-      for (int q = 0; q < FEW_K * ROW / 16 / 256; ++q) {
-        const int i = tid + 256 * q, r = i / (ROW / 16), c = i % (ROW / 16) * E, token = first + step * FEW_K + r;
+      for (int q = 0; q < TOKENS * ROW / 16 / 256; ++q) {
+        const int i = tid + 256 * q, r = i / (ROW / 16), c = i % (ROW / 16) * E, token = first + step * TOKENS + r;
         const int n = token < last ? a.dim - col0 - c : 0;
         copy16(to + i * 16, n > 0 ? weight + token * weight_stride + col0 + c : weight, n, vec_w);
       }
     }
     copy_group();
   };
-  const int g_row = tid / 4, g_at = tid % 4 * 8;           // eight tokens of a row's G
+  const int g_row = tid / (TOKENS / 8), g_at = tid % (TOKENS / 8) * 8;  // eight tokens of a row's G
   uint4 part[3];
   auto ask = [&](int step) {
-    const int token = first + step * FEW_K + g_at;
+    const int token = first + step * TOKENS + g_at;
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
       part[p] = make_uint4(0, 0, 0, 0);
@@ -845,31 +863,31 @@ __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weigh
   };
   auto give = [&](int step) {
     if (step >= steps || g_row >= ROWS) return;
-    float *to = reinterpret_cast<float *>(bytes + step % FEW_STAGES * STAGE + FEW_K * ROW) + g_row;
+    float *to = reinterpret_cast<float *>(bytes + step % STAGES * STAGE + TOKENS * ROW) + g_row;
     float v[8], w[8], x[8];
     vec_f32(part[0], v, __nv_bfloat16{});
     vec_f32(part[1], w, __nv_bfloat16{});
     vec_f32(part[2], x, __nv_bfloat16{});
-    const int left = last - first - step * FEW_K - g_at;
+    const int left = last - first - step * TOKENS - g_at;
 #pragma unroll
     for (int i = 0; i < 8; ++i) to[(g_at + i) * ROWS] = i < left ? v[i] + (w[i] + x[i]) : 0.f;
   };
 #pragma unroll
-  for (int i = 0; i < FEW_STAGES - 1; ++i) fetch(i);
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   ask(0);
-  float2 acc[8][2];
+  float2 acc[EACH][2];
 #pragma unroll
-  for (int m = 0; m < 8; ++m) acc[m][0] = acc[m][1] = make_float2(0, 0);
+  for (int m = 0; m < EACH; ++m) acc[m][0] = acc[m][1] = make_float2(0, 0);
   for (int step = 0; step < steps; ++step) {
     give(step);
     ask(step + 1);
-    copy_wait<FEW_STAGES - 2>();
+    copy_wait<STAGES - 2>();
     __syncthreads();
-    fetch(step + FEW_STAGES - 1);
-    const uint8_t *w = bytes + step % FEW_STAGES * STAGE;
-    const float *g = reinterpret_cast<const float *>(w + FEW_K * ROW) + group * 8;
+    fetch(step + STAGES - 1);
+    const uint8_t *w = bytes + step % STAGES * STAGE;
+    const float *g = reinterpret_cast<const float *>(w + TOKENS * ROW) + group * EACH;
 #pragma unroll 4
-    for (int j = share; j < FEW_K; j += SHARES) {
+    for (int j = share; j < TOKENS; j += SHARES) {
       float x[4];
       if (sizeof(T) == 4) {
         vec_f32(*reinterpret_cast<const uint4 *>(w + j * ROW + lane * 16), x, float{});
@@ -878,10 +896,16 @@ __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weigh
         two_f32(two.x, x, Element<T>{});
         two_f32(two.y, x + 2, Element<T>{});
       }
-      const float4 y0 = *reinterpret_cast<const float4 *>(g + j * ROWS), y1 = *reinterpret_cast<const float4 *>(g + j * ROWS + 4);
-      const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+      float y[EACH];
+      if (EACH == 2) {
+        const float2 two = *reinterpret_cast<const float2 *>(g + j * ROWS);
+        y[0] = two.x, y[1] = two.y;
+      } else {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < EACH; m += 4) vec_f32(*reinterpret_cast<const uint4 *>(g + j * ROWS + m), y + m, float{});
+      }
+#pragma unroll
+      for (int m = 0; m < EACH; ++m) {
         acc[m][0] = fma2(make_float2(x[0], x[1]), make_float2(y[m], y[m]), acc[m][0]);
         acc[m][1] = fma2(make_float2(x[2], x[3]), make_float2(y[m], y[m]), acc[m][1]);
       }
@@ -890,8 +914,8 @@ __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weigh
   copy_wait<0>();
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
-    *reinterpret_cast<float4 *>(stages + (share * ROWS + group * 8 + m) * 128 + lane * 4) =
+  for (int m = 0; m < EACH; ++m)
+    *reinterpret_cast<float4 *>(stages + (share * ROWS + group * EACH + m) * 128 + lane * 4) =
         make_float4(acc[m][0].x, acc[m][0].y, acc[m][1].x, acc[m][1].y);
   __syncthreads();
   const int col = col0 + lane * 4;
@@ -943,7 +967,7 @@ inline int scaled_parts(int64_t n, int32_t type) { return type == TT_F16 && !is_
 // x 64 with all gradients, from a graph: 45 us with 256, 39 with 128)
 inline int64_t few_each(int64_t vocab, int64_t dim) {
   const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * SMS / ((dim + 127) / 128), (vocab + 127) / 128));
-  return up((vocab + splits - 1) / splits, FEW_K);
+  return up((vocab + splits - 1) / splits, 64);
 }
 
 Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, bool pack_w, bool dh, bool dw, bool dw_f32) {
@@ -1028,7 +1052,9 @@ bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sum
 template <class T, int ROWS, int MODE> struct FewTag {};
 // f(number of rows that there is a kernel for)
 template <class T, class F> void with_rows(int n, F f) {
-  if (sizeof(T) == 2 || n <= 8) f(std::integral_constant<int, 8>{});
+  if (n <= 2) f(std::integral_constant<int, 2>{});
+  else if (sizeof(T) == 2 || n <= 4) f(std::integral_constant<int, 4>{});
+  else if (n <= 8) f(std::integral_constant<int, 8>{});
   else if (n <= 16) f(std::integral_constant<int, 16>{});
   else if (n <= 32) f(std::integral_constant<int, 32>{});
   else f(std::integral_constant<int, 64>{});
@@ -1036,8 +1062,8 @@ template <class T, class F> void with_rows(int n, F f) {
 template <class T, int MODE> bool few_logits(const Call &c, const RowArgs &r, cudaStream_t stream) {
   bool ok = true;
   auto run = [&](auto rows) {
-    constexpr int ROWS = sizeof(T) == 2 ? 8 : decltype(rows)::value;
-    const int shared = FEW_STAGES * (128 + ROWS) * FEW_ROW;
+    constexpr int ROWS = sizeof(T) == 2 && decltype(rows)::value > 4 ? 4 : decltype(rows)::value;
+    const int shared = FewShape<ROWS>::SHARED_LOGITS;
     auto k = k_few_logits<T, ROWS, MODE>;
     if (!(ok = !allow_shared<FewTag<T, ROWS, MODE>>(k, shared))) return;
     launch_cluster(k, dim3(r.n_parts), 256, shared, 1, true, stream, r, (const T *)c.weight, c.weight_stride,
@@ -1049,11 +1075,11 @@ template <class T, int MODE> bool few_logits(const Call &c, const RowArgs &r, cu
 template <class T> bool few_hidden(const Call &c, const RowArgs &r, const Plan &p, float *sums, const Target &o, cudaStream_t stream) {
   bool ok = true;
   auto run = [&](auto rows) {
-    constexpr int ROWS = sizeof(T) == 2 ? 8 : decltype(rows)::value;
-    const int shared = FEW_STAGES * FEW_K * (128 * (int)sizeof(T) + ROWS * 4);
+    constexpr int ROWS = sizeof(T) == 2 && decltype(rows)::value > 4 ? 4 : decltype(rows)::value;
+    const int shared = FewShape<ROWS>::template shared_hidden<T>();
     auto k = k_few_hidden<T, ROWS>;
-    if (!(ok = !allow_shared<FewTag<T, ROWS, 3>>(k, std::max(shared, 64 * 128 * 4)))) return;
-    launch_cluster(k, dim3((unsigned)((c.dim + 127) / 128), (unsigned)p.split_h), 256, std::max(shared, 64 * 128 * 4), 1, true, stream, r,
+    if (!(ok = !allow_shared<FewTag<T, ROWS, 3>>(k, shared))) return;
+    launch_cluster(k, dim3((unsigned)((c.dim + 127) / 128), (unsigned)p.split_h), 256, shared, 1, true, stream, r,
                    (const T *)c.weight, c.weight_stride, vec_of(c.weight, c.weight_stride, c.type) != 0, (int)few_each(c.vocab, c.dim), sums);
   };
   with_rows<T>(r.n_rows, run);
