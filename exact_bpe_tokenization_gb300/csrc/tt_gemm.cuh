@@ -383,6 +383,8 @@ inline uint32_t idesc_of(bool bf16, bool a_mn, bool b_mn) {
   return 1u << 4 | type << 7 | type << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (TILE >> 3) << 17 | (TILE >> 4) << 24;
 }
 
+inline int pairs_of(int a, int b) { return a == 3 ? 6 : a + b - 1; }
+
 template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
 
 // All launches of a call but its first are chained: a kernel's blocks start, and set
@@ -408,10 +410,10 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   // The products of parts whose orders add up to less than three (two parts: two), the
   // smallest first (the sums are cut off, not rounded, at each step: small ones lose less).
   // Three parts each: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), the rest is below 2^-24; two and
-  // two: (1,0) (0,1) (0,0); two and one: (1,0) (0,0).
-  g.pairs = a.parts == 3 ? 6 : a.parts == 1 ? 1 : b.parts == 2 ? 3 : 2;
-  g.pair_a = g.pairs == 6 ? 0x001102 : g.pairs == 1 ? 0 : 0x001;
-  g.pair_b = g.pairs == 6 ? 0x010120 : g.pairs == 3 ? 0x010 : 0;
+  // two: (1,0) (0,1) (0,0); two and one: (1,0) (0,0); one and two: (0,1) (0,0).
+  g.pairs = pairs_of((int)a.parts, (int)b.parts);
+  g.pair_a = g.pairs == 6 ? 0x001102 : a.parts == 2 ? 0x001 : 0;
+  g.pair_b = g.pairs == 6 ? 0x010120 : g.pairs == 3 ? 0x010 : b.parts == 2 ? 0x001 : 0;
   g.idesc = idesc_of(bf16, A_MN, B_MN);
   g.group = group;
   g.only = only;

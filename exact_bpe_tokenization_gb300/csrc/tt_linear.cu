@@ -14,15 +14,16 @@
 // exp(l - l_t) in the operands' type, which has a float's range, and sums them.  S = exp(loss)
 // is known behind it, so G = (powers - S (j == t)) g / S needs no second product: the factor
 // g / S is a row's of dhidden, and goes into a copy of hidden for dweight (rounded there, a
-// second time beside G).  Rows of a loss beyond 41 have G made anew.  2.76 ms for the sizes
+// second time beside G: dweight is off by 2.1e-3 to 2.4e-3 of its size with many rows, 1.7e-3
+// being its own rounding; up to 64 rows both keep a second part).  Rows of a loss beyond 41 have G made anew.  2.76 ms for the sizes
 // above, of which the products are 2.61; 3.0 from an lse, where all of G is made anew.
 //   From 16-bit floats, which lack the range, the first product runs twice, for lse and for G.
 // G is the one place where less than 32 bits stands between the logits and the gradients
 // (float: three bfloat16 parts, whose products are added in 32 bits; what is left out is
 // below 2^-24).  A chunk of rows of it is kept at a time.  dhidden's long sums are cut into
 // parts that k_join adds; dweight's over chunks are kept in 32 bits.
-//   One row is bound by reading the weight: 1 x 100256 x 2048 bf16 takes 76 us and k_finish
-// 5 (411 MB, 5.4 TB/s in the product: five and a fraction rounds of tiles take six).
+//   Few rows are bound by reading the weight, and have kernels of their own below: 1 x 100256
+// x 2048 bf16 takes 74 us with k_finish (411 MB, 5.9 TB/s in the product).
 #include "tt_gemm.cuh"
 #include "tt_rows.cuh"
 
@@ -535,6 +536,12 @@ __device__ __forceinline__ float row_info(const RowArgs &a, int row, bool there,
       row_scale = hidden_scale = g / s;
       float x = a.target_power[row] - s;                   // the target's place in G
       __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.g) + row * a.g_stride + t;
+      // The row's largest term by far: what G's rounding does to it in a single part, the
+      // row's factor takes back, which costs the others no more than their own roundings
+      // (dhidden's error 2.4e-3 -> 1.7e-3 of its size, the rounding of the result; dweight's of
+      // 512 rows 2.9e-3 -> 2.3e-3).
+      const float whole = __bfloat162float(__float2bfloat16_rn(x)), back = x / whole;
+      if (a.parts == 1 && fabsf(back - 1.f) < 0.01f) row_scale = hidden_scale = row_scale * back;
       for (int p = 0; p < a.parts; ++p) {
         to[p * a.g_part] = __float2bfloat16_rn(x);
         x -= __bfloat162float(__float2bfloat16_rn(x));
@@ -640,13 +647,15 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // Up to 64 rows of 32-bit values: laying out the weight in parts and multiplying 256 rows,
 // six times, would cost several times what reading it once costs (1 x 200256 x 2096: 1490
 // us for the loss; the weight alone is 247).  Here the weight goes by asynchronous copies
-// into shared memory, where ordinary 32-bit products, two at a time, take it from: 300 us for
-// 1 row and for 8, 404 for 16, 667 for 32, 1187 for 64 (the latter bound by the products: 60%
-// of their rate), where the tensor cores take 1500 for any number up to 256.  A warp has
-// eight rows; warps that are left over divide the contraction.
-// Up to eight rows of 16-bit values take the same way, for their precision: the tensor cores
+// into shared memory, where ordinary 32-bit products, two at a time, take it from: 254 us for
+// 1 row, 258 for 4, 270 for 8, 404 for 16, 667 for 32, 1184 for 64 (the latter bound by the
+// products: 60% of their rate), where the tensor cores take 1500 for any number up to 256.
+// A warp has eight rows, or the two or four that there are; warps that are left over divide
+// the contraction.
+// Up to four rows of 16-bit values take the same way, for their precision: the tensor cores
 // cut off their sums at each step, and a single token's loss may be a small difference of
-// large logits.  1 x 100256 x 2048 bf16: XX us, 78 by the tensor cores.
+// large logits (of 1e-4, off by a fiftieth of itself; 3.5e-4 so).  1 x 100256 x 2048 bf16: 74
+// us, 82 by the tensor cores; 4 rows 86 and 82; 8 rows would take 129.
 constexpr int FEW = 64, FEW_16 = 4;
 // What a kernel for up to ROWS rows copies at a time, and how far ahead: few rows are little
 // work a stage, so that larger ones pay (of 128 bytes a token instead of 256, 8 x 100256 x
@@ -957,10 +966,9 @@ struct Plan {
 };
 
 inline bool is_few(int64_t n, int32_t type) { return n <= (type == TT_F32 ? FEW : FEW_16); }
-// Parts of G, and of hidden's scaled copy: rounded to 16 bits once each, a few rows' gradients
-// are off by up to the whole of such a rounding, where those of many rows average it (dweight of
-// 16 rows of bf16 by 3.3e-3 of its size, of 512 by 2.9e-3; a rounding of its own is 1.7e-3).
-// Up to 64 rows the second part is nearly free.
+// Parts of G, and of hidden's scaled copy.  Rounded to 16 bits once each, the gradients of few
+// rows are off by up to the whole of such a rounding, where those of many rows average it;
+// up to 64 rows a second part of both is nearly free.
 inline int g_parts(int64_t n, int32_t type) { return type == TT_F32 || is_few(n, type) ? 3 : n <= FEW ? 2 : 1; }
 inline int scaled_parts(int64_t n, int32_t type) { return type == TT_F16 && !is_few(n, type) ? 1 : g_parts(n, type); }
 // tokens a block of k_few_hidden takes: two blocks an SM, whole stages, 128 at least (64 x 4352
@@ -988,7 +996,7 @@ Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, b
   p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
   const int pairs = parts == 1 ? of_g : 6;
   p.split_h = is_few(n, type) ? (int)((vocab + few_each(vocab, dim) - 1) / few_each(vocab, dim)) : choose_splits(p.chunk, dim, vocab, pairs);
-  p.split_w = choose_splits(vocab, dim, p.chunk, of_g == 3 ? 6 : of_g * 2 - 1);
+  p.split_w = choose_splits(vocab, dim, p.chunk, pairs_of(of_g, of_h));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;

@@ -491,12 +491,13 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  *   dhidden    = G * weight          dweight = G^T * hidden
  *
  * Products and sums are in 32 bits.  Before its own products G is rounded to the type
- * of hidden and weight, and with TT_BF16 hidden too, once it is scaled, for dweight.
- * (TT_F32: neither is; more than 64 rows are multiplied in parts whose neglected
- * products are below 2^-24 of theirs.)  With TT_F16 G is scaled by a power of two
- * first, so that the largest |row_grads| of a chunk of rows becomes 2^14 there; what
- * lies 2^-38 below that is lost.  The loss may differ in its last bits between calls
- * with gradients and without.
+ * of hidden and weight, and with TT_BF16 hidden too, once it is scaled, for dweight; up
+ * to 64 rows both keep twice as many bits.  (TT_F32: neither is rounded; more than 64
+ * rows are multiplied in parts whose neglected products are below 2^-24 of theirs.)
+ * With TT_F16 and more than 4 rows G is scaled by a power of two first, so that the
+ * largest |row_grads| of a chunk of rows becomes 2^14 there; what lies 2^-38 below
+ * that is lost.  The loss may differ in its last bits between calls with gradients and
+ * without.
  *
  *   d_hidden   device, type [n_rows][dim], rows hidden_stride apart.
  *   d_weight   device, type [n_vocab][dim], rows weight_stride apart (the layout

@@ -50,15 +50,16 @@ def linear_bounds(r):
     # few roundings, a sum of interleaved parts
     lse = worst + EPS * (2 * r["lse"].abs() + 4 * r["logits"].abs().amax(1) + 24 + vocab / 64)
     loss = 2 * worst + lse
-    # a probability: its logit's error and lse's, exp's argument; what rounds G (or the two
-    # factors that it is split into for dweight)
+    # a probability: its logit's error and lse's, exp's argument; what rounds G, a row's factor
+    # (which may make up for its target's rounding, of as much), and for dweight the factor's
+    # product with hidden
     p = r["p"] * torch.expm1(logit + (lse + 2 * worst + EPS * (4 * r["logits"].abs().amax(1) + 8))[:, None])
     dG = p * r["g"].abs()[:, None] + r["G"].abs() * (4 * EPS)
     unit = UNIT[kind] if kind != torch.float32 else 0.0
     # scaled 16-bit floats: what lies below their least values
     low = r["g"].abs().max() * 2.0**-37 if kind == torch.float16 else 0.0
-    over_h = dG + r["G"].abs() * unit + low
-    over_w = dG + r["G"].abs() * (2 * unit + unit * unit) + low
+    over_h = dG + r["G"].abs() * (2 * unit + unit * unit) + low
+    over_w = dG + r["G"].abs() * (3 * unit + 4 * unit * unit) + low
     dh = over_h @ w.abs() + product_bound(r["G"].abs() @ w.abs(), vocab, kind) * 1.01
     dw = over_w.T @ h.abs() + product_bound(r["G"].abs().T @ h.abs(), n, kind) * 1.01
     return loss, lse, dh, dw
