@@ -282,14 +282,19 @@ struct Target {
   }
 };
 
+// eight elements by plain loads: what chained kernels read may have been written by the
+// kernel before, so that none of it is declared constant
+template <class T> __device__ __forceinline__ void plain8(const T *p, float v[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+  raw_f32(r, v);
+}
 template <class S> __device__ __forceinline__ void add8(const void *src, int64_t at, float v[8], int n, bool vec) {
   const S *p = reinterpret_cast<const S *>(src) + at;
   if (vec) {
-    Raw8<S> r;
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(S) / 2); ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
     float w[8];
-    raw_f32(r, w);
+    plain8(p, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += w[i];
   } else {
@@ -417,9 +422,7 @@ template <class T, int SHARE> __global__ void __launch_bounds__(256) k_join(cons
 // n of eight elements
 template <class T> __device__ __forceinline__ void take8(const T *p, float v[8], int n, bool vec) {
   if (vec && n == 8) {
-    Raw8<T> r;
-    load_raw(p, r);
-    raw_f32(r, v);
+    plain8(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;

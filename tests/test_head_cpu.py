@@ -129,6 +129,18 @@ def test_distill_loss_sizes():
     distill_grad(n=0, x=None, ids=None, v=None, lse=None, dx=None)
 
 
+def test_chained_kernels_read_nothing_as_constant():
+    """tt_linear.cu's kernels start while the one before still writes, which may be the
+    caller's own: what they read goes by plain loads and copies, never by the read-only path."""
+    import os
+    csrc = os.path.join(os.path.dirname(tt.__file__), "csrc")
+    for name in ("tt_linear.cu", "tt_gemm.cuh"):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            text = f.read()
+        for word in ("__ldg", "load_raw", "ld.global.nc", "__restrict__"):
+            assert word not in text, (name, word)
+
+
 # ------------------------------------------------------------ the torch helpers
 
 torch = pytest.importorskip("torch")
