@@ -15,8 +15,9 @@
 // is known behind it, so G = (powers - S (j == t)) g / S needs no second product: the factor
 // g / S is a row's of dhidden, and goes into a copy of hidden for dweight (rounded there, a
 // second time beside G: dweight is off by 2.1e-3 to 2.4e-3 of its size with many rows, 1.7e-3
-// being its own rounding; up to 64 rows both keep a second part).  Rows of a loss beyond 41 have G made anew.  2.76 ms for the sizes
-// above, of which the products are 2.61; 3.0 from an lse, where all of G is made anew.
+// being its own rounding; up to 64 rows both keep a second part).  Rows of a loss beyond 41
+// have G made anew.  2.76 ms for the sizes above, of which the products are 2.61; 3.0 from an
+// lse, where all of G is made anew.
 //   From 16-bit floats, which lack the range, the first product runs twice, for lse and for G.
 // G is the one place where less than 32 bits stands between the logits and the gradients
 // (float: three bfloat16 parts, whose products are added in 32 bits; what is left out is
