@@ -24,21 +24,18 @@
 #pragma once
 #include <cuda.h>
 
-#include <algorithm>
-
 #include "tt_ops.cuh"
+#include "tt_plan.h"
 
 namespace tt {
 namespace gemm {
 
 using namespace tt::ops;
 
-constexpr int TILE = 256, HALF = 128, KB = 64;            // rows and columns of a tile, a block's part, contraction a stage
 constexpr int STAGES = 6, STAGE_BYTES = 2 * HALF * KB * 2;
 constexpr int EPI_WARPS = 8, THREADS = (4 + EPI_WARPS) * 32;
 constexpr int OWN_BYTES = 4096;                            // shared memory of an epilogue's warp, for what it writes
 constexpr int SHARED = STAGES * STAGE_BYTES + EPI_WARPS * OWN_BYTES + 1024;   // and what aligns the stages to 1024 bytes
-constexpr int SMS = 152;
 constexpr uint64_t PATIENCE = 4000000000ull;              // nanoseconds of a wait, before the call gives up
 
 struct Gemm {
@@ -383,14 +380,13 @@ inline uint32_t idesc_of(bool bf16, bool a_mn, bool b_mn) {
   return 1u << 4 | type << 7 | type << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (TILE >> 3) << 17 | (TILE >> 4) << 24;
 }
 
-inline int pairs_of(int a, int b) { return a == 3 ? 6 : a + b - 1; }
-
 template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
 
 // All launches of a call but its first are chained: a kernel's blocks start, and set
 // themselves up, while the one before ends.
 // D [rows of a][rows of b] = a * b^T over the contraction; with _MN the matrix lies the
-// other way round (its rows are the contraction).  False: an error, which is kept.
+// other way round (its rows are the contraction).  False: an error, which is kept, or more
+// parts of the contraction than it has blocks.
 template <bool A_MN, bool B_MN, class Epi>
 inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, int group, const Epi &epi, int32_t *status,
                      cudaStream_t stream, const int32_t *only = nullptr) {
@@ -406,6 +402,7 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   g.m_tiles = (int)((rows_a + TILE - 1) / TILE);
   g.n_tiles = (int)((rows_b + TILE - 1) / TILE);
   g.k_blocks = (int)(((A_MN ? a.rows : a.cols) + KB - 1) / KB);
+  if (splits > g.k_blocks) return false;
   g.splits = splits;
   // The products of parts whose orders add up to less than three (two parts: two), the
   // smallest first (the sums are cut off, not rounded, at each step: small ones lose less).
@@ -423,31 +420,6 @@ inline bool run_gemm(bool bf16, const Matrix &a, const Matrix &b, int splits, in
   const int tiles = g.m_tiles * g.n_tiles * g.splits;
   launch_cluster(k, dim3(2 * std::min(tiles, SMS / 2)), THREADS, SHARED, 1, true, stream, ma, mb, g, epi);
   return true;
-}
-
-// Parts to cut a contraction into, so that every pair of SMs has as much to do: the
-// least of the rounds of tiles, each of its blocks and a tile's start and end, and the
-// traffic of the parts (times in blocks of 64, 0.27 us).  The tensor cores cut off the
-// sums at each step: operands of several parts, which are 32-bit values, are summed over
-// no more than 2048 at a time (dhidden of 100,000 tokens was off by 1.4e-5 of its size in one
-// sum, 7e-6 with 8192, 2.4e-6 so; plain 32-bit sums 2e-6).
-constexpr int64_t LONGEST = 2048;
-inline int choose_splits(int64_t m, int64_t n, int64_t k, int pairs) {
-  const int64_t tiles = ((m + TILE - 1) / TILE) * ((n + TILE - 1) / TILE), blocks = (k + KB - 1) / KB;
-  const int64_t least_splits = pairs == 6 ? (k + LONGEST - 1) / LONGEST : 1;
-  const int64_t most = std::max<int64_t>(least_splits, std::min<int64_t>(std::min<int64_t>(32, blocks), blocks * pairs / 4));
-  int best = (int)least_splits;
-  double least = 1e300;
-  for (int64_t s = least_splits; s <= most; ++s) {
-    const int64_t rounds = (tiles * s + SMS / 2 - 1) / (SMS / 2);
-    double cost = (double)rounds * ((double)((blocks + s - 1) / s) * pairs + 4);
-    if (s > 1) cost += 12 + (double)s * m * n * 8 / 6.8e12 / 0.27e-6;
-    if (cost < least * 0.99) {
-      least = cost;
-      best = (int)s;
-    }
-  }
-  return best;
 }
 
 }  // namespace gemm

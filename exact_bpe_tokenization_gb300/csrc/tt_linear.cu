@@ -30,6 +30,7 @@
 
 using namespace tt::ops;
 using namespace tt::gemm;
+using namespace tt::linear;
 
 namespace tt {
 namespace gemm {
@@ -57,15 +58,7 @@ CUresult encode_map(CUtensorMap *map, bool bf16, const Matrix &m, uint32_t box_r
 
 namespace {
 
-constexpr int64_t MAX_WIDTH = 1 << 16;
-// Bytes of G at a time.  Fewer and larger chunks read and write the 32-bit sums of dweight
-// less often: 16400 x 100256 x 2048 bf16 takes 12.5 ms with 1 GB, 12.1 with 2, 11.9 with 4.
-constexpr int64_t KEPT = 2ll << 30;
-constexpr int64_t PARTIALS = 1ll << 28;                    // bytes of maxima and sums at a time
 constexpr int F16_UP = 14;                                 // G in 16 bits: the largest |g| becomes 2^14
-
-// What a row's G is made from: G = exp(l - from) * mul - g (j == t); t < 0: zeros.
-struct RowInfo { float from, mul, g; int t; };
 
 // ------------------------------------------------------------ epilogues
 // 64 columns of a warp's rows to a matrix in PARTS parts of type E (each the rest of those
@@ -660,7 +653,7 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // cut off their sums at each step, and a single token's loss may be a small difference of
 // large logits (of 1e-4, off by a fiftieth of itself; 3.5e-4 so).  1 x 100256 x 2048 bf16: 74
 // us, 82 by the tensor cores; 4 rows 86 and 82; 8 rows would take 129.
-constexpr int FEW = 64, FEW_16 = 4;
+
 // What a kernel for up to ROWS rows copies at a time, and how far ahead: few rows are little
 // work a stage, so that larger ones pay (of 128 bytes a token instead of 256, 8 x 100256 x
 // 2048 bf16 took 126 us).
@@ -944,8 +937,6 @@ __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weigh
 }
 
 // ------------------------------------------------------------ host
-inline int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
 struct Call {
   const void *hidden, *weight;
   int32_t type;
@@ -960,72 +951,6 @@ struct Call {
   int accumulate;
   int32_t *status;
 };
-
-// what lies where in the workspace, in bytes, and how the rows are cut into chunks
-struct Plan {
-  int64_t chunk, width, g_stride;                          // rows; columns of packed operands and of G
-  int split_h, split_w;
-  int64_t words;                                           // one, and one a tile row
-  int64_t hidden, weight, part, rows, word, info, scaled, g, acc, sums, bytes;
-};
-
-inline bool is_few(int64_t n, int32_t type) { return n <= (type == TT_F32 ? FEW : FEW_16); }
-// Parts of G, and of hidden's scaled copy.  Rounded to 16 bits once each, the gradients of few
-// rows are off by up to the whole of such a rounding, where those of many rows average it;
-// up to 64 rows a second part of both is nearly free.
-inline int g_parts(int64_t n, int32_t type) { return type == TT_F32 || is_few(n, type) ? 3 : n <= FEW ? 2 : 1; }
-inline int scaled_parts(int64_t n, int32_t type) { return type == TT_F16 && !is_few(n, type) ? 1 : g_parts(n, type); }
-// tokens a block of k_few_hidden takes: two blocks an SM, whole stages, 128 at least (64 x 4352
-// x 64 with all gradients, from a graph: 45 us with 256, 39 with 128)
-inline int64_t few_each(int64_t vocab, int64_t dim) {
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * SMS / ((dim + 127) / 128), (vocab + 127) / 128));
-  return up((vocab + splits - 1) / splits, 64);
-}
-
-Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pack_h, bool pack_w, bool dh, bool dw, bool dw_f32) {
-  Plan p{};
-  if (is_few(n, type)) pack_h = pack_w = false;
-  const int parts = type == TT_F32 ? 3 : 1;
-  const bool grad = dh || dw;
-  n = std::max<int64_t>(n, 1);
-  p.width = up(dim, 64);                                   // whole 128-byte lines: a box's rows are one each
-  p.g_stride = up(vocab, 64);
-  const int64_t halves = (vocab + HALF - 1) / HALF;
-  int64_t most = PARTIALS / (halves * 8);
-  const int of_g = g_parts(n, type), of_h = scaled_parts(n, type);
-  if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * of_g));
-  if (pack_h || dw) most = std::min(most, KEPT / (p.width * 2 * parts));   // copies of hidden
-  most = std::max<int64_t>(most / TILE * TILE, TILE);
-  const int64_t chunks = (n + most - 1) / most;
-  p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));
-  const int pairs = parts == 1 ? of_g : 6;
-  p.split_h = is_few(n, type) ? (int)((vocab + few_each(vocab, dim) - 1) / few_each(vocab, dim)) : choose_splits(p.chunk, dim, vocab, pairs);
-  p.split_w = choose_splits(vocab, dim, p.chunk, pairs_of(of_g, of_h));
-  int64_t at = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t here = at;
-    at += up(bytes, 256);
-    return here;
-  };
-  p.hidden = take(pack_h ? p.chunk * p.width * 2 * parts : 0);
-  p.weight = take(pack_w ? vocab * p.width * 2 * parts : 0);
-  p.part = take(halves * 8 * p.chunk);
-  p.rows = take(4 * 3 * p.chunk);                          // target_logit, target_power, row_scale
-  p.words = 1 + (p.chunk + TILE - 1) / TILE;
-  p.word = take(4 * p.words);
-  if (grad) {
-    p.info = take(sizeof(RowInfo) * p.chunk);
-    p.scaled = take(dw ? p.chunk * p.width * 2 * of_h : 0);
-    p.g = take(p.g_stride * 2 * of_g * p.chunk);
-    p.acc = take(dw && !dw_f32 && p.chunk < n ? vocab * p.width * 4 : 0);
-    int64_t sums = 0;
-    if (dh && (p.split_h > 1 || is_few(n, type))) sums = std::max(sums, p.split_h * p.chunk * p.width * 4);
-    if (dw && p.split_w > 1) sums = std::max(sums, p.split_w * vocab * p.width * 4);
-    p.sums = take(sums);
-  }
-  p.bytes = std::max<int64_t>(at, 256);
-  return p;
-}
 
 // rows lie on 16-byte boundaries
 inline int vec_of(const void *p, int64_t stride, int32_t type) {
@@ -1050,6 +975,7 @@ template <class T> void join(const float *part, int splits, int64_t stride, cons
 template <bool A_MN>
 bool product(bool bf16, const Matrix &a, const Matrix &b, int splits, float *sums, int64_t width, int32_t type, const Target &o,
              int32_t *status, cudaStream_t stream) {
+  splits = splits_of(splits, b.rows);
   if (splits > 1) {
     const Target part{o.n_rows, o.n_cols, sums, width, nullptr, 0, TT_F32, nullptr, nullptr, 1};
     if (!run_gemm<A_MN, true>(bf16, a, b, splits, 8, OutEpi<float>{part, o.n_rows}, status, stream)) return false;

@@ -1,0 +1,44 @@
+"""The losses of a model's head on the GPU where their kernels' ways part: short last
+chunks with divided contractions, small losses of large logits, gradients of one kind
+alone, weights with infinities and NaN, the size of the gradients' errors.  Against the
+64-bit forms of head_plain.py."""
+import math
+
+import pytest
+
+import head_plain as plain
+from test_gpu_head import DTYPES, KINDS, gen, rows_of, status_word, targets_of, tt, within  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("last", [1, 65])
+def test_linear_loss_short_last_chunk_of_a_divided_contraction(tt, last):  # noqa: F811
+    """Floats, chunks of 2304 rows, whose contraction for dweight is cut into two parts, and a
+    last chunk of one block of it, or two.  A product of large values goes ahead, so that no
+    tensor memory is zero by chance."""
+    g = gen(1)
+    vocab, dim, n = 151936, 64, 8 * 2304 + last
+    h, w = rows_of(n, dim, torch.float32, g), rows_of(vocab, dim, torch.float32, g, scale=0.1)
+    t = torch.randint(-1, vocab, (n,), generator=g, device="cuda", dtype=torch.int32)
+    rg = torch.rand(n, generator=g, device="cuda") / n
+    tt.linear_loss(h[:3000], w, t[:3000], torch.full((3000,), 1e6, device="cuda"), want_grad=True)
+    st = status_word()
+    loss, lse, dh, dw = tt.linear_loss(h, w, t, rg, want_grad=True, status=st)
+    exact = torch.empty_like(lse)
+    want, bound = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda"), 0
+    for a in range(0, n, 2304):
+        rows = slice(a, a + 2304)
+        r = plain.linear(h[rows], w, t[rows], rg[rows])
+        b = plain.linear_bounds(r)
+        for got, x, e in zip((loss, lse, dh), (r["loss"], r["lse"], r["dh"]), b):
+            within(got[rows], x, plain.rounded(e, x, torch.float32))
+        exact[rows] = r["lse"]
+        want += r["dw"]
+        bound = bound + b[3] + plain.EPS * want.abs() * 2  # (each chunk's sums are added in 32 bits)
+        del r, b
+    within(dw, want, plain.rounded(bound, want, torch.float32), "dweight")
+    later = tt.linear_loss_grad(h, w, t, exact, rg, dweight=torch.empty_like(dw), status=st)[1]
+    within(later, want, plain.rounded(bound, want, torch.float32), "dweight from lse")
+    assert st.item() == 0

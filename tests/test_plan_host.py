@@ -1,0 +1,54 @@
+"""How a call of tt_linear_loss is cut up (csrc/tt_plan.h), compiled for the host:
+parts of contractions, chunks of rows, scratch."""
+import ctypes
+import os
+import random
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+F32, F16, BF16 = range(3)
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("plan") / "libplan_host.so")
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-o", so, os.path.join(HERE, "plan_host.cpp")])
+    lib = ctypes.CDLL(so)
+    lib.plan_host.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 6 + [ctypes.c_void_p]
+    lib.plan_host_splits.argtypes = [ctypes.c_int, ctypes.c_int64]
+
+    def call(n, vocab, dim, kind, pack_h=False, pack_w=False, dh=True, dw=True, dw_f32=False):
+        """(rows of a chunk, parts of dhidden's contraction, of dweight's, bytes)"""
+        out = (ctypes.c_int64 * 4)()
+        lib.plan_host(n, vocab, dim, kind, pack_h, pack_w, dh, dw, dw_f32, out)
+        return tuple(out)
+    call.splits = lib.plan_host_splits
+    return call
+
+
+def sizes(count, seed):
+    rng = random.Random(seed)
+    for _ in range(count):
+        vocab = rng.choice([300, 4352, 50257, 100256, 128256, 151936, 200256, 1 << 20, int(2 ** rng.uniform(0, 20))])
+        yield int(2 ** rng.uniform(0, 24)), vocab, rng.choice([64, int(2 ** rng.uniform(0, 16))]), rng.choice([F32, F16, BF16])
+
+
+def test_every_part_of_a_contraction_has_a_block(plan):
+    """A part without one would be a tile that nothing is multiplied for, left with what its
+    tensor memory held before: float, 151,936 tokens, 18,433 rows are chunks of 2304, two
+    parts each, and a last one of a single row."""
+    assert plan(18433, 151936, 64, F32, True, True)[:3] == (2304, 75, 2)
+    short = 0
+    for n, vocab, dim, kind in list(sizes(20000, 1)) + [(18433 + i, 151936, 64, F32) for i in range(66)]:
+        chunk, split_h, split_w, _ = plan(n, vocab, dim, kind, kind == F32, kind == F32)
+        last = n - (n - 1) // chunk * chunk
+        for planned, k in ((split_h, vocab), (split_w, min(n, chunk)), (split_w, last)):
+            if k == vocab and n <= (64 if kind == F32 else 4):
+                continue                                   # (dhidden of few rows: parts of tokens, another kernel's)
+            blocks, parts = (k + 63) // 64, plan.splits(planned, k)
+            assert parts >= 1
+            assert all(blocks * i // parts < blocks * (i + 1) // parts for i in range(parts)), (n, vocab, dim, kind, k)
+            short += parts < planned
+    assert short > 60                                      # (the last chunks of the sizes above)
