@@ -97,7 +97,10 @@ inline Plan plan_of(int64_t n, int64_t vocab, int64_t dim, int32_t type, bool pa
   int64_t most = PARTIALS / (halves * 8);
   const int of_g = g_parts(n, type), of_h = scaled_parts(n, type);
   if (grad) most = std::min(most, KEPT / (p.g_stride * 2 * of_g));
-  if (pack_h || dw) most = std::min(most, KEPT / (p.width * 2 * parts));   // copies of hidden
+  // Copies of hidden, whether or not this call needs them: the chunk comes from the sizes
+  // alone, so that no call needs more than the one with copies and with both gradients,
+  // which is the one that tt_linear_loss_workspace knows.
+  most = std::min(most, KEPT / (p.width * 2 * parts));
   most = std::max<int64_t>(most / TILE * TILE, TILE);
   const int64_t chunks = (n + most - 1) / most;
   p.chunk = std::min(n, up((n + chunks - 1) / chunks, TILE));

@@ -42,3 +42,23 @@ def test_linear_loss_short_last_chunk_of_a_divided_contraction(tt, last):  # noq
     later = tt.linear_loss_grad(h, w, t, exact, rg, dweight=torch.empty_like(dw), status=st)[1]
     within(later, want, plain.rounded(bound, want, torch.float32), "dweight from lse")
     assert st.item() == 0
+
+
+def test_linear_loss_dhidden_alone_needs_no_more_scratch_than_asked(tt):  # noqa: F811
+    """A width above the vocabulary's size, and so many rows that they are worked on in chunks."""
+    n, vocab, dim = 143337, 7471, 7504
+    g = gen(2)
+    h = torch.empty(n, dim, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, n, 20000):
+        h[a:a + 20000] = torch.randn(len(h[a:a + 20000]), dim, generator=g, device="cuda")
+    w, t = rows_of(vocab, dim, torch.bfloat16, g, scale=0.01), targets_of(n, vocab, 3)
+    need = tt.tt_linear_loss_workspace(n, vocab, dim, tt.TT_BF16, 1, tt.TT_F32, 1)
+    space = torch.empty(need, dtype=torch.uint8, device="cuda")
+    loss, lse, dh, _ = tt.linear_loss(h, w, t, dhidden=torch.empty_like(h), workspace=space)
+    later = tt.linear_loss_grad(h, w, t, lse, dhidden=torch.empty_like(h), workspace=space)[0]
+    at = torch.tensor([0, 1, 71679, 71680, 71936, n - 2, n - 1], device="cuda")
+    r = plain.linear(h[at], w, t[at], torch.ones(len(at), device="cuda"))
+    b = plain.linear_bounds(r)
+    for got, want, e, kind in ((loss, r["loss"], b[0], torch.float32), (lse, r["lse"], b[1], torch.float32),
+                               (dh, r["dh"], b[2], torch.bfloat16), (later, r["dh"], b[2], torch.bfloat16)):
+        within(got[at], want, plain.rounded(e, want, kind))

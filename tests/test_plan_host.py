@@ -52,3 +52,30 @@ def test_every_part_of_a_contraction_has_a_block(plan):
             assert all(blocks * i // parts < blocks * (i + 1) // parts for i in range(parts)), (n, vocab, dim, kind, k)
             short += parts < planned
     assert short > 60                                      # (the last chunks of the sizes above)
+
+
+def test_no_call_needs_more_scratch_than_is_asked_for(plan):
+    """tt_linear_loss_workspace knows whether gradients are wanted, not which, and whether
+    copies are, not of what: 143,337 rows of bf16, 7,471 tokens, a width of 7,504 and dhidden
+    alone wanted more than both gradients."""
+    cases = list(sizes(1000, 2)) + [(143337, 7471, 7504, BF16), (13513788, 44, 1832, BF16), (240000, 4352, 4416, BF16)]
+    rng = random.Random(3)
+    for _ in range(1000):                                  # widths above the vocabulary
+        dim = int(2 ** rng.uniform(6, 16))
+        cases.append((int(2 ** rng.uniform(10, 24)), rng.randrange(1, dim + 1), dim, rng.choice([F32, F16, BF16])))
+    for n, vocab, dim, kind in cases:
+        for pack in ((True,) if kind == F32 else (False, True)):
+            packs = [(True, True)] if kind == F32 else [(True, True), (True, False), (False, True)] if pack else [(False, False)]
+            alone = plan(n, vocab, dim, kind, pack, pack, False, False)
+            assert all(plan(n, vocab, dim, kind, *p, False, False)[3] <= alone[3] for p in packs)
+            for wide in {False, kind == F32}:
+                most = plan(n, vocab, dim, kind, pack, pack, True, True, wide)
+                for p in packs:
+                    for dh, dw in ((True, True), (True, False), (False, True)):
+                        for dhidden_alone in ((False, True) if not dw else (wide,)):  # (no dweight: its type is not looked at)
+                            got = plan(n, vocab, dim, kind, *p, dh, dw, dhidden_alone)
+                            assert got[0] == most[0] and got[3] <= most[3], (n, vocab, dim, kind, p, dh, dw)
+            floats = plan(n, vocab, dim, kind, pack, pack, True, True, True)  # (16 bits into a float dweight)
+            for p in packs:
+                for dh, dw in ((True, True), (True, False), (False, True)):
+                    assert plan(n, vocab, dim, kind, *p, dh, dw, True)[3] <= floats[3], (n, vocab, dim, kind, p, dh, dw)
