@@ -558,6 +558,22 @@ __device__ __forceinline__ float row_info(const RowArgs &a, int row, bool there,
   return hidden_scale;
 }
 
+// The loss of a row.  With powers against c, the target's 32-bit logit, what is there is S
+// and the target's own power, of the same product's logits: their ratio is the loss's power,
+// and neither c nor what the tensor cores cut off every logit of the row stands in it.  (As
+// (m - c) + log(S) it was off by what they cut off the logits alone: 8e-4 at logits of 300, so
+// that a confident row's loss was below zero.)  S is a sum of powers, the target's among
+// them, and no rounding brings a sum of such terms below one of them: no loss is negative.
+__device__ __forceinline__ float row_loss(const RowArgs &a, int row, float m, float s, float log_s) {
+  const float c = a.target_logit[row];
+  if (a.target_power) {
+    const float p = a.target_power[row];
+    // (1 but for what the sums of c and of the product cut off; infinities and NaN go on below)
+    if (p > 0x1p-16f && p < 0x1p16f) return m == c ? log1pf((s - p) / p) : (m - c) + (log_s - logf(p));
+  }
+  return (m - c) + log_s;
+}
+
 // R rows a block: the parts of a row are joined by 256 / R threads (or its lse is the
 // caller's), and then hidden's rows copied by their scale for dweight (padding rows as
 // zeros, whatever they hold).
@@ -612,7 +628,7 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
     if (!there && t >= 0) op_status(a.status, TT_ERR_INVALID_ARG);
     float loss = 0;
     if (!a.lse_in) {
-      loss = !there ? 0.f : lse == -INF ? INF : (m - a.target_logit[row]) + log_s;
+      loss = !there ? 0.f : lse == -INF ? INF : row_loss(a, row, m, s, log_s);
       if (a.lse) a.lse[row] = lse;
       a.loss[row] = loss;
     }

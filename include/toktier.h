@@ -497,7 +497,7 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  * With TT_F16 and more than 4 rows G is scaled by a power of two first, so that the
  * largest |row_grads| of a chunk of rows becomes 2^14 there; what lies 2^-38 below
  * that is lost.  The loss may differ in its last bits between calls with gradients and
- * without.
+ * without; it is never below zero.
  *
  *   d_hidden   device, type [n_rows][dim], rows hidden_stride apart.
  *   d_weight   device, type [n_vocab][dim], rows weight_stride apart (the layout

@@ -62,3 +62,30 @@ def test_linear_loss_dhidden_alone_needs_no_more_scratch_than_asked(tt):  # noqa
     for got, want, e, kind in ((loss, r["loss"], b[0], torch.float32), (lse, r["lse"], b[1], torch.float32),
                                (dh, r["dh"], b[2], torch.bfloat16), (later, r["dh"], b[2], torch.bfloat16)):
         within(got[at], want, plain.rounded(e, want, kind))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [600, 300, 40, 4])
+@pytest.mark.parametrize("lift", [18.0, 300.0])
+def test_linear_loss_of_confident_rows(tt, kind, n, lift):  # noqa: F811
+    """Rows that give their target nearly all: losses of some 1e-4, small differences of
+    logits of 18 and 300, whose products are sums of terms of one sign.  What such sums lose
+    is in every logit of a row alike, so that a loss is off by a share of itself and by what
+    the sum of powers loses; and no loss is below zero."""
+    kind, g = KINDS[kind], gen(3)
+    vocab, dim = 3000, 2048
+    u = torch.rand(dim, generator=g, device="cuda") + 0.5
+    h = (u * (1 + 0.01 * torch.randn(n, dim, generator=g, device="cuda"))).to(kind)
+    w = torch.randn(vocab, dim, generator=g, device="cuda") * 1e-3 + (lift - 17) / float(u.sum())
+    w[5] += 17 / float(u.sum())
+    w = w.to(kind)
+    w[vocab - 1] = 0                                       # (a token far below)
+    t = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    r = plain.linear(h, w, t, torch.ones(n, device="cuda"))
+    worst = plain.product_bound(h.double().abs() @ w.double().abs().T, dim, kind).amax(1)
+    bound = r["loss"] * torch.expm1(2 * worst + plain.EPS * (4 * lift + 64)) + plain.EPS * (24 + vocab / 64)
+    assert 1e-5 < float(r["loss"].min()) and float(r["loss"].max()) < 1e-2
+    for want_grad in (False, True):
+        loss = tt.linear_loss(h, w, t, want_grad=want_grad)[0]
+        within(loss, r["loss"], plain.rounded(bound, r["loss"], torch.float32), "loss, gradients %s" % want_grad)
+        assert not bool((loss < 0).any())
