@@ -270,7 +270,7 @@ struct Target {
   __device__ __forceinline__ float scaled(float x, int64_t row, float by) const {
     if (row_scale) {
       const float r = row_scale[row];
-      return r == 0 ? 0.f : x * r;
+      return r == 0 ? 0.f : x * r * by;
     }
     return x * by;
   }
@@ -361,6 +361,12 @@ template <class T> struct OutEpi {
 #pragma unroll
             for (int r = 0; r < 32; ++r) {
               *q = from_f32<T>(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4) * scale);
+              q += o.dst_stride;
+            }
+          } else if (rows == 32 && !o.src) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+              *q = from_f32<T>(o.scaled(own_float(own_chunk(own, r, lane / 4) + (lane & 3) * 4), row0 + r, scale));
               q += o.dst_stride;
             }
           } else {
@@ -548,8 +554,8 @@ __device__ __forceinline__ float row_info(const RowArgs &a, int row, bool there,
       row_scale = hidden_scale = g;
       a.only[0] = a.only[1 + row / TILE] = 1;
     }
-  } else if (a.target_power) {
-    row_scale = 0;
+  } else if (r.t < 0) {
+    row_scale = 0;                                         // (G's zeros would not do: weight may hold NaN)
   }
   a.info[row] = r;
   a.row_scale[row] = row_scale;
@@ -1163,7 +1169,7 @@ bool run_chunks(const Call &c, const Plan &p, uint8_t *ws, cudaStream_t stream) 
     float *sums = (float *)(ws + p.sums);
     if (c.dhidden) {
       const Target o{n, c.dim, (uint8_t *)c.dhidden + row0 * c.dhidden_stride * size, c.dhidden_stride, nullptr, 0, TT_F32, r.g_max,
-                     powers ? r.row_scale : nullptr, vec_of(c.dhidden, c.dhidden_stride, c.type)};
+                     r.row_scale, vec_of(c.dhidden, c.dhidden_stride, c.type)};
       if (few) with_type(c.type, [&](auto t) { ok = few_hidden<decltype(t)>(c, r, p, sums, o, stream); });
       else ok = product<false>(bf16, g, w, p.split_h, sums, p.width, c.type, o, c.status, stream);
       if (!ok) return false;

@@ -517,7 +517,8 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  *              before and after mean nothing.
  * A target >= n_vocab is padding and sets TT_ERR_INVALID_ARG in d_status.  NaN or
  * infinities in hidden or weight give NaN or infinities in what they enter; those in
- * padding rows of hidden enter their lse alone.  A wait
+ * padding rows of hidden enter their lse alone, and dhidden's padding rows are zero
+ * whatever weight holds.  A wait
  * within a kernel that ran out sets TT_ERR_TIMEOUT in d_status, and the outputs then
  * mean nothing.
  */

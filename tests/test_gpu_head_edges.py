@@ -89,3 +89,21 @@ def test_linear_loss_of_confident_rows(tt, kind, n, lift):  # noqa: F811
         loss = tt.linear_loss(h, w, t, want_grad=want_grad)[0]
         within(loss, r["loss"], plain.rounded(bound, r["loss"], torch.float32), "loss, gradients %s" % want_grad)
         assert not bool((loss < 0).any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("n,vocab,dim", [(600, 300, 32), (600, 300, 33), (300, 5000, 33), (60, 300, 32), (4, 300, 32)])
+def test_linear_loss_padding_rows_are_zero_whatever_the_weight_holds(tt, kind, value, n, vocab, dim):  # noqa: F811
+    """NaN and infinities of the weight reach the rows that have a target, none that have not."""
+    kind, g = KINDS[kind], gen(4)
+    h, w, t = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=0.3), targets_of(n, vocab, 4)
+    t[0], t[n - 1] = -1, 7
+    w[7, 3] = value
+    rg = torch.full((n,), 1 / n, device="cuda")
+    none = t < 0
+    loss, lse, dh, _ = tt.linear_loss(h, w, t, rg, dhidden=torch.full_like(h, 5))
+    assert not bool(loss[none].any()) and not bool(dh[none].any())
+    assert not bool(torch.isfinite(dh[~none][:, 3]).any()) and not bool(torch.isfinite(loss[n - 1]))
+    dh = tt.linear_loss_grad(h, w, t, torch.zeros_like(lse), rg, dhidden=torch.full_like(h, 5))[0]
+    assert not bool(dh[none].any()) and not bool(torch.isfinite(dh[~none][:, 3]).any())
