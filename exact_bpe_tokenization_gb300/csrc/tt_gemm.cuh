@@ -36,7 +36,6 @@ constexpr int STAGES = 6, STAGE_BYTES = 2 * HALF * KB * 2;
 constexpr int EPI_WARPS = 8, THREADS = (4 + EPI_WARPS) * 32;
 constexpr int OWN_BYTES = 4096;                            // shared memory of an epilogue's warp, for what it writes
 constexpr int SHARED = STAGES * STAGE_BYTES + EPI_WARPS * OWN_BYTES + 1024;   // and what aligns the stages to 1024 bytes
-constexpr uint64_t PATIENCE = 4000000000ull;              // nanoseconds of a wait, before the call gives up
 
 struct Gemm {
   int m_tiles, n_tiles, splits;                           // the contraction is cut into `splits` parts
@@ -70,13 +69,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // false: the wait ran out, here or in another role of the block
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *dead) {
-  uint64_t start, now;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(start));
+  uint64_t now;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+  Patience patience(now);
   for (uint32_t i = 0; i < 1u << 30; ++i) {
     if (bar_try(bar, parity)) return true;
     if ((i & 63) == 63) {
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-      if (*dead || now - start > PATIENCE) break;
+      if (*dead || patience.over(now)) break;
     }
   }
   *dead = 1;

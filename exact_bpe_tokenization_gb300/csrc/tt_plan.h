@@ -1,6 +1,6 @@
 // tt_plan.h - how a call of tt_linear_loss is cut up: tiles of its products, parts of
-// their contractions, chunks of rows, and what lies where in the workspace.  Host
-// arithmetic alone, which tests compile without CUDA.
+// their contractions, chunks of rows, and what lies where in the workspace; and when a
+// wait within a kernel has run out.  Arithmetic alone, which tests compile without CUDA.
 #pragma once
 #include <stdint.h>
 
@@ -13,6 +13,27 @@ namespace gemm {
 
 constexpr int TILE = 256, HALF = 128, KB = 64;            // rows and columns of a tile, a block's part, contraction a stage
 constexpr int SMS = 152;
+
+// How long a wait within a kernel has taken, from looks at a clock that goes on while the
+// kernel does not run (a context switched out, a debugger, a machine put to sleep): a gap
+// between two looks counts for a quarter of a second at most, so that a wait of which nobody
+// looked for minutes has not run out.
+constexpr uint64_t PATIENCE = 4000000000ull, GAP = PATIENCE / 16;  // nanoseconds
+#ifdef __CUDACC__
+#define TT_BOTH __host__ __device__ __forceinline__
+#else
+#define TT_BOTH inline
+#endif
+struct Patience {
+  uint64_t last, waited;
+  TT_BOTH explicit Patience(uint64_t now) : last(now), waited(0) {}
+  TT_BOTH bool over(uint64_t now) {
+    const uint64_t gap = now - last;
+    waited += gap < GAP ? gap : GAP;
+    last = now;
+    return waited > PATIENCE;
+  }
+};
 
 inline int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 

@@ -14,6 +14,14 @@ void plan_host(int64_t n, int64_t vocab, int64_t dim, int32_t type, int pack_h, 
   out[3] = p.bytes;
 }
 
+// the first of n looks at the clock at which a wait has run out, or n
+int plan_host_patience(const uint64_t *looks, int n) {
+  Patience p(looks[0]);
+  for (int i = 1; i < n; ++i)
+    if (p.over(looks[i])) return i;
+  return n;
+}
+
 int plan_host_splits(int planned, int64_t k) { return splits_of(planned, k); }
 
 }

@@ -25,6 +25,8 @@ def plan(tmp_path_factory):
         lib.plan_host(n, vocab, dim, kind, pack_h, pack_w, dh, dw, dw_f32, out)
         return tuple(out)
     call.splits = lib.plan_host_splits
+    lib.plan_host_patience.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    call.patience = lambda looks: lib.plan_host_patience((ctypes.c_uint64 * len(looks))(*looks), len(looks))
     return call
 
 
@@ -79,3 +81,23 @@ def test_no_call_needs_more_scratch_than_is_asked_for(plan):
             for p in packs:
                 for dh, dw in ((True, True), (True, False), (False, True)):
                     assert plan(n, vocab, dim, kind, *p, dh, dw, True)[3] <= floats[3], (n, vocab, dim, kind, p, dh, dw)
+
+
+def test_a_wait_runs_out_by_the_time_that_it_was_looked_at(plan):
+    """Four seconds of a wait that is looked at all the time, however the looks lie; a clock
+    that went on while nothing ran (for minutes, in the midst of a wait) counts for a
+    quarter of a second."""
+    ms, start = 10**6, 1 << 60
+    for step in (ms // 100, ms, 100 * ms):
+        looks = [start + i * step for i in range(4000 * ms // step + 2)]
+        assert plan.patience(looks) == len(looks) - 1
+    for away in (1000 * ms, 4001 * ms, 600000 * ms, 1 << 62):
+        looks, now = [start], start
+        for i in range(8):                                 # eight times switched out, or put to sleep
+            now += away
+            looks.append(now)
+            looks += [now + j * ms for j in range(1, 100)]
+            now = looks[-1]
+        assert plan.patience(looks) == len(looks)
+    # nor does a wait whose looks lie far apart go on for ever
+    assert plan.patience([start + i * 1000 * ms for i in range(100)]) == 17
