@@ -107,3 +107,38 @@ def test_linear_loss_padding_rows_are_zero_whatever_the_weight_holds(tt, kind, v
     assert not bool(torch.isfinite(dh[~none][:, 3]).any()) and not bool(torch.isfinite(loss[n - 1]))
     dh = tt.linear_loss_grad(h, w, t, torch.zeros_like(lse), rg, dhidden=torch.full_like(h, 5))[0]
     assert not bool(dh[none].any()) and not bool(torch.isfinite(dh[~none][:, 3]).any())
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,vocab,dim", [(64, 5000, 136), (300, 5000, 136), (1030, 3000, 72), (2100, 4352, 256)])
+def test_linear_loss_size_of_the_gradients_errors(tt, kind, n, vocab, dim):  # noqa: F811
+    """The error of a gradient as a whole, which bounds on each element (worst cases, summed)
+    leave room for.  A rounding to nearest is off by as much as u / sqrt(3) of the value's size
+    in the mean (u half a spacing, relative, errors even within it; less for values inside a
+    binade), and the roundings are independent of each other and of the random hidden states
+    and weight that they meet, so that their shares add up as squares.  5% for chance: a norm of
+    10^4 elements and more.
+      The result's own rounding: 1.  G's: 1, or with bfloat16's powers the share of G that is not
+    the target's, twice (its rounding, and the row's factor that takes back the target's), and
+    for dweight hidden's copy: 1.  Up to 64 rows G and the copy have a second part: neither.
+    From an lse G is rounded as it is, and hidden's copy not."""
+    g = gen(5)
+    h, w = rows_of(n, dim, kind, g), rows_of(vocab, dim, kind, g, scale=2 / math.sqrt(dim))
+    t, rg = targets_of(n, vocab, 5), torch.full((n,), 1 / n, device="cuda")
+    r = plain.linear(h, w, t, rg)
+    there = (t >= 0).nonzero()[:, 0]
+    of_target = (r["G"][there, t[there].long()] ** 2).sum()
+    rest = float(1 - of_target / (r["G"] ** 2).sum())
+    one = plain.UNIT[kind] / math.sqrt(3) * 1.05
+
+    def size(got, want):
+        return float((got.double() - want).norm() / want.norm())
+    _, _, dh, dw = tt.linear_loss(h, w, t, rg, want_grad=True)
+    powers = kind == torch.bfloat16
+    of_g, of_copy = (0, 0) if n <= 64 else (2 * rest, 1) if powers else (1, 0)
+    assert size(dh, r["dh"]) <= one * math.sqrt(1 + of_g)
+    assert size(dw, r["dw"]) <= one * math.sqrt(1 + of_g + of_copy)
+    dh, dw = tt.linear_loss_grad(h, w, t, r["lse"].float(), rg)
+    of_g = 0 if n <= 64 else 1
+    assert size(dh, r["dh"]) <= one * math.sqrt(1 + of_g)
+    assert size(dw, r["dw"]) <= one * math.sqrt(1 + of_g)
