@@ -580,7 +580,9 @@ def linear_loss(hidden, weight, targets, row_grads=None, want_grad=False, dhidde
     weight as a third and fourth.  dhidden, dweight: where they go; with one of them
     given and not want_grad, the other is None and is not computed.  dweight may be
     float32; with accumulate it is added to.  workspace: a contiguous tensor of any type, of
-    tt_linear_loss_workspace() bytes (allocated if None)."""
+    tt_linear_loss_workspace() bytes (allocated if None).  status: without one, a wait
+    within a kernel that ran out (TT_ERR_TIMEOUT, all outputs then mean nothing) and targets
+    beyond the vocabulary go unnoticed."""
     return _linear(_torch or _load_torch(), hidden, weight, targets, row_grads, want_grad, dhidden, dweight, accumulate,
                    workspace, status, stream)
 

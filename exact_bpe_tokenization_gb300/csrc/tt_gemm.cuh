@@ -382,8 +382,9 @@ inline uint32_t idesc_of(bool bf16, bool a_mn, bool b_mn) {
 
 template <bool A_MN, bool B_MN, class Epi> struct GemmTag {};
 
-// All launches of a call but its first are chained: a kernel's blocks start, and set
-// themselves up, while the one before ends.
+// All launches of a call are chained, the first one to whatever the caller's stream has
+// before it: a kernel's blocks start, and set themselves up, while the one before ends, and
+// wait for all of it before they read or write memory.
 // D [rows of a][rows of b] = a * b^T over the contraction; with _MN the matrix lies the
 // other way round (its rows are the contraction).  False: an error, which is kept, or more
 // parts of the contraction than it has blocks.

@@ -16,15 +16,15 @@
 // g / S is a row's of dhidden, and goes into a copy of hidden for dweight (rounded there, a
 // second time beside G: dweight is off by 2.1e-3 to 2.4e-3 of its size with many rows, 1.7e-3
 // being its own rounding; up to 64 rows both keep a second part).  Rows of a loss beyond 41
-// have G made anew.  2.76 ms for the sizes above, of which the products are 2.61; 3.0 from an
-// lse, where all of G is made anew.
+// have G made anew.  2.76 to 3.19 ms for the sizes above, by the card and its clocks, of which
+// the products are 2.61 alone; 2.95 to 3.08 from an lse, where all of G is made anew.
 //   From 16-bit floats, which lack the range, the first product runs twice, for lse and for G.
 // G is the one place where less than 32 bits stands between the logits and the gradients
 // (float: three bfloat16 parts, whose products are added in 32 bits; what is left out is
 // below 2^-24).  A chunk of rows of it is kept at a time.  dhidden's long sums are cut into
 // parts that k_join adds; dweight's over chunks are kept in 32 bits.
 //   Few rows are bound by reading the weight, and have kernels of their own below: 1 x 100256
-// x 2048 bf16 takes 74 us with k_finish (411 MB, 5.9 TB/s in the product).
+// x 2048 bf16 takes 70 to 74 us with k_finish (411 MB, 6.1 TB/s in the product).
 #include "tt_gemm.cuh"
 #include "tt_rows.cuh"
 
@@ -666,19 +666,20 @@ template <class T, int R> __global__ void __launch_bounds__(256) k_finish(RowArg
 // Up to 64 rows of 32-bit values: laying out the weight in parts and multiplying 256 rows,
 // six times, would cost several times what reading it once costs (1 x 200256 x 2096: 1490
 // us for the loss; the weight alone is 247).  Here the weight goes by asynchronous copies
-// into shared memory, where ordinary 32-bit products, two at a time, take it from: 254 us for
-// 1 row, 258 for 4, 270 for 8, 404 for 16, 667 for 32, 1184 for 64 (the latter bound by the
-// products: 60% of their rate), where the tensor cores take 1500 for any number up to 256.
+// into shared memory, where ordinary 32-bit products, two at a time, take it from: 254 to 269 us
+// for 1 row, 258 to 272 for 4, 266 to 276 for 8, 404 for 16, 667 for 32, 1186 for 64 (the latter bound by the
+// products: 60% of their rate), where the tensor cores take 1510 to 1530 for any number up to 256.
 // A warp has eight rows, or the two or four that there are; warps that are left over divide
 // the contraction.
 // Up to four rows of 16-bit values take the same way, for their precision: the tensor cores
 // cut off their sums at each step, and a single token's loss may be a small difference of
-// large logits (of 1e-4, off by a fiftieth of itself; 3.5e-4 so).  1 x 100256 x 2048 bf16: 74
-// us, 82 by the tensor cores; 4 rows 86 and 82; 8 rows would take 129.
+// large logits (of 1e-4, off by a fiftieth of itself; 3.5e-4 so).  1 x 100256 x 2048 bf16: 70 to
+// 74 us, 82 by the tensor cores; 4 rows 82 to 86 and 82; 8 rows would take 129.
 
 // What a kernel for up to ROWS rows copies at a time, and how far ahead: few rows are little
-// work a stage, so that larger ones pay (of 128 bytes a token instead of 256, 8 x 100256 x
-// 2048 bf16 took 126 us).
+// work a stage, so that larger ones pay.  With 128 bytes a token and four stages instead of 256
+// and three, the loss of 1 and 4 x 100256 x 2048 bf16 takes 78 and 87 us instead of 73 and 84, of 1, 4 and
+// 8 x 200256 x 2096 floats 277, 279 and 296 instead of 264, 266 and 272.
 template <int ROWS> struct FewShape {
   static constexpr int EACH = ROWS < 8 ? ROWS : 8;         // rows a warp
   static constexpr int GROUPS = ROWS / EACH, SHARES = 8 / GROUPS;
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(256, 2) k_few_hidden(RowArgs a, const T *weigh
   wait_for_last();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp % GROUPS, share = warp / GROUPS;
   const int col0 = blockIdx.x * 128, first = blockIdx.y * each, last = min(a.n_vocab, first + each), steps = (last - first + TOKENS - 1) / TOKENS;
-  // a stage: 32 tokens' 128 columns, and G of the rows and those tokens, [token][row]
+  // a stage: TOKENS tokens' 128 columns, and G of the rows and those tokens, [token][row]
   auto fetch = [&](int step) {
     if (step < steps) {
       uint8_t *to = bytes + step % STAGES * STAGE;
@@ -1069,6 +1070,11 @@ bool make_g(bool bf16, const Matrix &h, const Matrix &w, const Matrix &g, const 
   return g.parts == 1 ? g_to<B, 1>(h, w, g, r, stream) : g.parts == 2 ? g_to<B, 2>(h, w, g, r, stream) : g_to<B, 3>(h, w, g, r, stream);
 }
 
+// Rows a block of k_finish: a row alone has more threads for its parts, several read whole
+// lines of them.  For 100,256 tokens (784 parts), in us, the loss alone / with hidden's copy of
+// 2048, by 1, 4 and 8 rows a block: 300 rows 6/8, 6/10, 6/13; 512 rows 6.5/8.0, 6.5/9.4,
+// 6.8/12.6; 1024 rows 10.7/13.4, 6.5/10.3, 7.0/13.1; 2048 rows 15/20, 7.2/11.3, 7.4/13.9; 4096
+// rows 28/35, 11.7/18.9, 9.0/16.4.
 template <class T> void finish(const RowArgs &r, cudaStream_t stream) {
   const int n = r.n_rows;
   if (n >= 4096) launch_cluster(k_finish<T, 8>, dim3((n + 7) / 8), 256, 0, 1, true, stream, r);

@@ -41,7 +41,12 @@ inline int pairs_of(int a, int b) { return a == 3 ? 6 : a + b - 1; }
 
 // Parts to cut a contraction into, so that every pair of SMs has as much to do: the
 // least of the rounds of tiles, each of its blocks and a tile's start and end, and the
-// traffic of the parts (times in blocks of 64, 0.27 us).  The tensor cores cut off the
+// traffic of the parts (times in blocks of 64, 0.27 us).  What it chooses, against one part and
+// the best other number tried of 2, 3, 4 and 8, in us of a call from lse: dhidden of 1023 x 20001 x
+// 640 bf16 59 (123; 65 with 4), of 1023 x 200255 x 641 fp16 507 (1154; 542 with 4), of 2047 x
+// 4352 x 1024 floats 155 (196; 150 with 2), of 300 x 20001 x 640 floats 148 (586; 160 with 8);
+// dweight of the same 60, 531, 149 and 145, which are one part's (94, 985, 159, 171 with 2).
+//   The tensor cores cut off the
 // sums at each step: operands of several parts, which are 32-bit values, are summed over
 // no more than 2048 at a time (dhidden of 100,000 tokens was off by 1.4e-5 of its size in one
 // sum, 7e-6 with 8192, 2.4e-6 so; plain 32-bit sums 2e-6).

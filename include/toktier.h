@@ -490,14 +490,20 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  *   G[i][j]    = row_grads[i] * (exp(l[i][j] - lse[i]) - (j == targets[i]))
  *   dhidden    = G * weight          dweight = G^T * hidden
  *
- * Products and sums are in 32 bits.  Before its own products G is rounded to the type
- * of hidden and weight, and with TT_BF16 hidden too, once it is scaled, for dweight; up
- * to 64 rows both keep twice as many bits.  (TT_F32: neither is rounded; more than 64
- * rows are multiplied in parts whose neglected products are below 2^-24 of theirs.)
- * With TT_F16 and more than 4 rows G is scaled by a power of two first, so that the
- * largest |row_grads| of a chunk of rows becomes 2^14 there; what lies 2^-38 below
- * that is lost.  The loss may differ in its last bits between calls with gradients and
+ * Products and sums are in 32 bits.  With more than 4 rows (TT_F32: 64) they run on the
+ * tensor cores, which cut the last bits of a sum off every 16 terms: what that loses grows
+ * with the length of a sum (about 1e-6 of a logit with a dim of 2048 and 3e-5 with 2^16; with
+ * TT_F32 sums over n_vocab and n_rows are cut into parts of at most 2048, which are added up
+ * in 32 bits).  The loss may differ in its last bits between calls with gradients and
  * without; it is never below zero.
+ * Before its own products G is rounded to the type of hidden and weight, and with TT_BF16
+ * hidden too, once it is scaled, for dweight; up to 64 rows both keep twice as many bits.
+ * (TT_F32: neither is rounded; more than 64 rows are multiplied in parts whose neglected
+ * products are below 2^-24 of theirs.)  With TT_BF16 and more than 64 rows, what G's rounding
+ * does at the target's place, up to 2^-8 of it, a factor of the whole row takes back.  With
+ * TT_F16 and more than 4 rows G is scaled by a power of two first, so that the largest
+ * |row_grads| of a chunk of rows is brought to 2^13 .. 2^14; what lies 2^-28 below that keeps
+ * fewer than 11 bits, and what lies 2^-38 below it is lost.
  *
  *   d_hidden   device, type [n_rows][dim], rows hidden_stride apart.
  *   d_weight   device, type [n_vocab][dim], rows weight_stride apart (the layout
@@ -518,9 +524,9 @@ tt_status tt_sample(const void *d_logits, int32_t type, int64_t n_rows, int64_t 
  * A target >= n_vocab is padding and sets TT_ERR_INVALID_ARG in d_status.  NaN or
  * infinities in hidden or weight give NaN or infinities in what they enter; those in
  * padding rows of hidden enter their lse alone, and dhidden's padding rows are zero
- * whatever weight holds.  A wait
- * within a kernel that ran out sets TT_ERR_TIMEOUT in d_status, and the outputs then
- * mean nothing.
+ * whatever weight holds.  A wait within a kernel that ran out (after four seconds
+ * without an end to copies or products of microseconds) sets TT_ERR_TIMEOUT in
+ * d_status, and the outputs then mean nothing; without d_status that cannot be told.
  */
 tt_status tt_linear_loss(const void *d_hidden, const void *d_weight, int32_t type, int64_t n_rows, int64_t n_vocab,
                          int64_t dim, int64_t hidden_stride, int64_t weight_stride, const int32_t *d_targets,
@@ -544,7 +550,11 @@ tt_status tt_linear_loss_grad(const void *d_hidden, const void *d_weight, int32_
  * reject.  want_grad: 0 the loss alone (dweight_type is then not looked at), else
  * with any of its gradients.  aligned_rows != 0: every row of hidden and weight
  * starts on a 16-byte boundary; else, and with TT_F32, room for copies of both is
- * in it. */
+ * in it (TT_F32 and more than 64 rows: of 6 bytes a value).  With gradients there is G of the
+ * rows that are worked on at a time (2 GB at most, or 256 rows), a scaled copy of them, and
+ * sums of contractions that are cut into parts: with TT_F32 those of dhidden take at least
+ * n_vocab / 2048 (rounded up) times these rows times dim floats, 2.5 GB of the 9.3 for 4096 x
+ * 200,256 x 4096, and nothing bounds them but the sizes. */
 int64_t tt_linear_loss_workspace(int64_t n_rows, int64_t n_vocab, int64_t dim, int32_t type, int32_t aligned_rows,
                                  int32_t dweight_type, int32_t want_grad);
 

@@ -83,6 +83,19 @@ def test_no_call_needs_more_scratch_than_is_asked_for(plan):
                     assert plan(n, vocab, dim, kind, *p, dh, dw, True)[3] <= floats[3], (n, vocab, dim, kind, p, dh, dw)
 
 
+def test_scratch_of_floats_with_gradients(plan):
+    """What the header says of it: copies of 6 bytes a value, G of 2 GB at most or 256 rows, and
+    sums of dhidden's parts of 2048 tokens, which nothing bounds but the sizes."""
+    for n, vocab, dim in ((4096, 200256, 4096), (1024, 200256, 2112), (70, 1 << 20, 64), (3000, 4352, 1024)):
+        rows, split_h, split_w, need = plan(n, vocab, dim, F32, True, True, True, True, True)
+        g = (vocab + 63) // 64 * 64 * 6 * rows
+        assert split_h >= (vocab + 2047) // 2048 and (g <= 2 << 30 or rows == 256)
+        sums = 4 * dim * max(split_h * rows, split_w * vocab if split_w > 1 else 0)
+        least = 6 * dim * (vocab + 2 * rows) + g + sums
+        assert least <= need <= 1.05 * least + (vocab + 127) // 128 * 8 * rows
+    assert plan(4096, 200256, 4096, F32, True, True, True, True, True)[3] == 9328072960
+
+
 def test_a_wait_runs_out_by_the_time_that_it_was_looked_at(plan):
     """Four seconds of a wait that is looked at all the time, however the looks lie; a clock
     that went on while nothing ran (for minutes, in the midst of a wait) counts for a
