@@ -58,7 +58,7 @@ CUresult encode_map(CUtensorMap *map, bool bf16, const Matrix &m, uint32_t box_r
 
 namespace {
 
-constexpr int F16_UP = 14;                                 // G in 16 bits: the largest |g| becomes 2^14
+constexpr int F16_UP = 14;                                 // G in 16 bits: the largest |g| is brought to 2^13 .. 2^14
 
 // ------------------------------------------------------------ epilogues
 // 64 columns of a warp's rows to a matrix in PARTS parts of type E (each the rest of those
@@ -212,7 +212,7 @@ __device__ __forceinline__ float f16_up(const uint32_t *g_max) {
 }
 
 // G, in the operands' type or in bfloat16 parts.  16-bit floats lack the range for
-// a mean's 1 / n: there G is scaled by a power of two that brings the largest |g| to
+// a mean's 1 / n: there G is scaled by a power of two that brings the largest |g| to 2^13 ..
 // 2^14, and the gradients' epilogue takes it back.
 template <class E, int PARTS> struct GradEpi {
   CUtensorMap map;
